@@ -32,7 +32,8 @@ import torch
 __all__ = ["SdmError", "sdm_fwd", "sdm_fwd_noalloc", "sdm_fwd_phase1", "sdm_fwd_phase2", "sdm_bwd", "sdm_write_read", "bwd_workspace_bytes", "chunk_mats", "chunk_records", "wy_solve", "product_key_topk", "product_key_topk_backward",
            "workspace_bytes", "plan",
            "library_path",
-           "SDM_ERRORS"]
+           "SDM_ERRORS", "gated_delta_fwd", "gated_delta_step", "gated_delta_bwd", "gated_delta_rule",
+           "gated_delta_workspace_bytes", "layer_norm_fwd", "layer_norm_bwd", "layer_norm"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.environ.get("SDM_LIBRARY", os.path.join(_HERE, "libsdm.so"))
@@ -117,6 +118,7 @@ def _load():
             lib.sdm_bwd_workspace_bytes.restype = ctypes.c_size_t
             lib.sdm_bwd.argtypes = [i32, i32, p, p, p, p, i32, p, p, p, p, p, i32, p]
             lib.sdm_bwd.restype = ctypes.c_int
+            dense.bind(lib)
             lib.sdm_error_string.argtypes = [ctypes.c_int]
             lib.sdm_error_string.restype = ctypes.c_char_p
             lib.sdm_last_error.argtypes = []
@@ -586,3 +588,8 @@ def product_key_topk_backward(lin: torch.Tensor, grad_val: torch.Tensor, factors
     _check_rc(lib, lib.sdm_product_key_topk_backward(rows, _ptr(lin), _ptr(grad_val), _DTYPES[grad_val.dtype], fac,
                                                      len(factors), kk, _ptr(graw), ctypes.byref(ex)))
     return graw
+
+
+from . import dense  # noqa: E402  (it takes its helpers from above)
+from .dense import (gated_delta_bwd, gated_delta_fwd, gated_delta_rule, gated_delta_step,  # noqa: E402
+                    gated_delta_workspace_bytes, layer_norm, layer_norm_bwd, layer_norm_fwd)

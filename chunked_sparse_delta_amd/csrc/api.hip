@@ -14,6 +14,8 @@
 #include "common.h"
 #include "wy_impl.h"
 #include "backward.h"
+#include "delta.h"
+#include "host.h"
 
 namespace sdm {
 hipError_t phase1_prepare();
@@ -41,11 +43,10 @@ int phase2_mode(const ChunkLayout &L, int C, int nv, int V, int es, int64_t M, i
 
 using namespace sdm;
 
-namespace {
+namespace sdm {
 
 thread_local char g_err[512] = "";
 
-int fail(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int code, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -57,6 +58,10 @@ int fail(int code, const char *fmt, ...) {
 int hip_fail(hipError_t e, const char *what) {
     return fail(SDM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace sdm
+
+namespace {
 
 // The scratch of sdm_fwd_noalloc: a file-scope device array, one copy per GPU the library
 // runs on, held until the process ends. In host code its name is a host-side stand-in, not
@@ -104,6 +109,8 @@ int device_info(DeviceInfo **out) {
         if ((e = wy_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (solve)");
         if ((e = part_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (phase 1, partitioned)");
         if ((e = bwd_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (backward)");
+        if ((e = delta_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (gated delta)");
+        if ((e = delta_bwd_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (gated delta backward)");
         void *sp = nullptr;
         if ((e = hipGetSymbolAddress(&sp, HIP_SYMBOL(scratch))) != hipSuccess)
             return hip_fail(e, "hipGetSymbolAddress (static scratch)");
@@ -116,7 +123,16 @@ int device_info(DeviceInfo **out) {
     return SDM_OK;
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace
+
+int sdm::device_cus(int *cus) {
+    DeviceInfo *d = nullptr;
+    const int rc = device_info(&d);
+    if (rc == SDM_OK) *cus = d->cus;
+    return rc;
+}
+
+namespace {
 
 int key_bits(int64_t M) {
     int bits = 0;
@@ -754,8 +770,6 @@ namespace {
 struct BwdSizes {
     size_t snap, lead, part, pairs, work, total;
 };
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // snap_es: bytes per saved element (4 float32, 2 bfloat16 snapshot rows)
 BwdSizes bwd_sizes(int32_t P, int32_t T, int32_t W, int32_t R, int32_t hd, int64_t M, int32_t dtype, bool shared,

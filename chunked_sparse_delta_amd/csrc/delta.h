@@ -1,0 +1,53 @@
+// The dense gated delta rule: what its kernels and host entry points share.
+#pragma once
+
+#include "common.h"
+
+namespace sdm {
+
+// A [P, T, heads, width] view (strides in elements).
+struct Rows {
+    const void *data;
+    int64_t sp, st, sh;
+};
+
+struct DeltaArgs {
+    Rows q, k, v;
+    const float *beta, *g;       // [P, T, Hv]
+    const float *state;          // [.., Hv, K, V] or null
+    float *state_out;            // or null
+    const int32_t *valid;        // [P] or null
+    const int32_t *ids;          // [P] or null (step)
+    int64_t slots;               // states (step)
+    void *out;                   // [P, T, Hv, V]
+    int32_t P, T, Hk, Hv, K, V;
+    float scale;
+};
+
+__device__ __forceinline__ int delta_valid(const DeltaArgs &a, int p) {
+    return a.valid ? max(0, min(a.valid[p], a.T)) : a.T;
+}
+
+// The chunked kernels' workspace: chunk n = (stream * Hv + head) * Nt + chunk.
+struct DeltaWs {
+    float *X, *Pm;      // [n][C][C]
+    float *U, *Y;       // [n][C][V]  (backward)
+    float *S, *dS;      // [n][K][V]  start states, gradients of the end states (backward)
+    int32_t Nt;
+    bool backward;      // X is computed for the backward (delta_beta_safe)
+};
+
+struct DeltaGrads {
+    const void *go;          // [P, T, Hv, V]
+    const float *gstate;     // [P, Hv, K, V] or null
+    void *q, *k, *v;
+    float *beta, *g, *state; // state or null
+};
+
+hipError_t delta_prepare();
+hipError_t delta_bwd_prepare();
+hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16, bool save, hipStream_t st);
+hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &g, bool is_bf16, hipStream_t st);
+hipError_t launch_delta_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st);
+
+}  // namespace sdm

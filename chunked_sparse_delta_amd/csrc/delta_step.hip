@@ -1,0 +1,151 @@
+// The gated delta rule token by token, for single tokens and a few at once.
+//
+// With r = k S and s = q S of the state before the token, a = exp(g) and c = q k:
+//     u = beta (v - a r),   out = scale (a s + c u),   S = a S + k u
+// so both products and c need the old state only and share one reduction.
+//
+// Bound by memory: a state is 4 K V bytes read and written once per call, against 2 (2 K + 2 V)
+// of bfloat16 rows. A wavefront owns CW columns of one state and keeps them in registers
+// through all tokens: CW / VW lanes side by side hold VW columns each of RG = 64 VW / CW rows
+// at a time, so a load instruction fetches RG row pieces of CW columns, and the reduction over
+// the rows is RG-way across lanes. Wavefronts share nothing.
+#include "delta.h"
+
+namespace sdm {
+
+namespace {
+
+// Sum over the lanes whose index differs in the bits from `low` up.
+template <int LOW> __device__ __forceinline__ float rows_sum(float x) {
+#pragma unroll
+    for (int m = LOW; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
+    return x;
+}
+
+// The lane's VW columns of a state row of which `cols` are left: one load or store at any element address where all are.
+constexpr int VW = 4;
+typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ void cols_load(const float *p, int cols, float (&o)[VW]) {
+    if (cols >= VW) {
+        const f4u x = *reinterpret_cast<const f4u *>(p);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) o[j] = x[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) o[j] = j < cols ? p[j] : 0.0f;
+    }
+}
+__device__ __forceinline__ void cols_store(float *p, int cols, const float (&o)[VW]) {
+    if (cols >= VW) *reinterpret_cast<f4u *>(p) = f4u{o[0], o[1], o[2], o[3]};
+    else {
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+            if (j < cols) p[j] = o[j];
+    }
+}
+
+template <typename T, int CW, int RPL>
+__global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
+    constexpr int LPR = CW / VW, RG = 64 / LPR;      // lanes per row piece, rows at a time
+    const int lane = threadIdx.x & 63;
+    const int slices = (a.V + CW - 1) / CW;
+    const int64_t wave = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (wave >= int64_t(a.P) * a.Hv * slices) return;
+    const int slice = int(wave % slices);
+    const int h = int(wave / slices % a.Hv), p = int(wave / slices / a.Hv);
+    const int hk = h / (a.Hv / a.Hk);
+    const int rg = lane / LPR, c0 = slice * CW + lane % LPR * VW;
+    const int cols = a.V - c0;                       // left from c0 on, <= 0 for lanes past the state
+    T *out = static_cast<T *>(a.out) + (int64_t(p) * a.T * a.Hv + h) * a.V + c0;
+    const int64_t so = int64_t(a.Hv) * a.V;
+    const int64_t slot = a.ids ? int64_t(a.ids[p]) : p;
+    const bool idle = slot < 0 || slot >= a.slots;
+    const int n = idle ? 0 : delta_valid(a, p);
+    auto put = [&](int t, const float (&o)[VW]) {
+        if (rg == 0) {
+#pragma unroll
+            for (int j = 0; j < VW; ++j)
+                if (j < cols) out[t * so + j] = from_f32<T>(o[j]);
+        }
+    };
+    const float zero[VW] = {};
+    for (int t = n; t < a.T; ++t) put(t, zero);
+    if (idle || (n == 0 && a.state == a.state_out)) return;
+
+    const int64_t s0 = (slot * a.Hv + h) * a.K * a.V + c0;
+    float S[RPL][VW];
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        const int row = i * RG + rg;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) S[i][j] = 0.0f;
+        if (row < a.K) cols_load(a.state + s0 + int64_t(row) * a.V, cols, S[i]);
+    }
+    const T *kp = static_cast<const T *>(a.k.data) + p * a.k.sp + hk * a.k.sh;
+    const T *qp = static_cast<const T *>(a.q.data) + p * a.q.sp + hk * a.q.sh;
+    const T *vp = static_cast<const T *>(a.v.data) + p * a.v.sp + h * a.v.sh + c0;
+    const float *bp = a.beta + int64_t(p) * a.T * a.Hv + h, *gp = a.g + int64_t(p) * a.T * a.Hv + h;
+    for (int t = 0; t < n; ++t) {
+        float kk[RPL], r[VW] = {}, s[VW] = {}, c = 0.0f, v[VW] = {};
+        const float beta = bp[int64_t(t) * a.Hv], decay = expf(gp[int64_t(t) * a.Hv]);
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+            if (j < cols) v[j] = to_f32(vp[t * a.v.st + j]);
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) {
+            const int row = i * RG + rg;
+            kk[i] = row < a.K ? to_f32(kp[t * a.k.st + row]) : 0.0f;
+            const float qq = row < a.K ? to_f32(qp[t * a.q.st + row]) : 0.0f;
+            c = fmaf(qq, kk[i], c);
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+                r[j] = fmaf(kk[i], S[i][j], r[j]);
+                s[j] = fmaf(qq, S[i][j], s[j]);
+            }
+        }
+        c = rows_sum<LPR>(c);
+        float u[VW], o[VW];
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+            r[j] = rows_sum<LPR>(r[j]);
+            s[j] = rows_sum<LPR>(s[j]);
+            u[j] = beta * (v[j] - decay * r[j]);
+            o[j] = a.scale * fmaf(c, u[j], decay * s[j]);
+        }
+        put(t, o);
+#pragma unroll
+        for (int i = 0; i < RPL; ++i)
+#pragma unroll
+            for (int j = 0; j < VW; ++j) S[i][j] = fmaf(kk[i], u[j], decay * S[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        const int row = i * RG + rg;
+        if (row < a.K) cols_store(a.state_out + s0 + int64_t(row) * a.V, cols, S[i]);
+    }
+}
+
+template <typename T, int CW, int RPL> hipError_t step_go(const DeltaArgs &a, hipStream_t st) {
+    const int64_t waves = int64_t(a.P) * a.Hv * ((a.V + CW - 1) / CW);
+    hipLaunchKernelGGL((delta_step_kernel<T, CW, RPL>), dim3(unsigned((waves + 3) / 4)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+// The fewest rows per lane that hold K.
+template <typename T, int CW> hipError_t step_rows(const DeltaArgs &a, hipStream_t st) {
+    constexpr int RG = 64 * VW / CW;
+    if (a.K <= 64) return step_go<T, CW, 64 / RG>(a, st);
+    if (a.K <= 128) return step_go<T, CW, 128 / RG>(a, st);
+    return step_go<T, CW, 256 / RG>(a, st);
+}
+template <typename T> hipError_t step_pick(const DeltaArgs &a, int cus, hipStream_t st) {
+    if (int64_t(a.P) * a.Hv * ((a.V + 31) / 32) >= 8 * cus) return step_rows<T, 32>(a, st);
+    return step_rows<T, 16>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_delta_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st) {
+    return is_bf16 ? step_pick<bf16>(a, cus, st) : step_pick<float>(a, cus, st);
+}
+
+}  // namespace sdm
