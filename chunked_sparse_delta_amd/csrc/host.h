@@ -6,7 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "sdm.h"
+#include "sdm_dense.h"
 
 namespace sdm {
 

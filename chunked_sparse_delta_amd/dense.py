@@ -1,4 +1,4 @@
-"""The dense gated delta rule and layer norm: the binding of libsdm.so's entry points of these (include/sdm.h).
+"""The dense gated delta rule and layer norm: the binding of libsdm.so's entry points of these (include/sdm_dense.h).
 
     out = gated_delta_fwd(state, k, v, beta, log_decay, q)       # sequences; state advanced in place
     out = gated_delta_step(state, k, v, beta, log_decay, q)      # one or a few tokens, a pool of states
