@@ -28,13 +28,14 @@ __device__ __forceinline__ int delta_valid(const DeltaArgs &a, int p) {
     return a.valid ? max(0, min(a.valid[p], a.T)) : a.T;
 }
 
-// The chunked kernels' workspace: chunk n = (stream * Hv + head) * Nt + chunk.
+// The chunked kernels' workspace: chunk n = (stream * Hv + head) * Nt + chunk. U, Y, S and dS are
+// kept as the accumulators hold them: [n][16-column group of V][32-row block][lane][8 rows].
 struct DeltaWs {
-    float *X, *Pm;      // [n][C][C]
-    float *U, *Y;       // [n][C][V]  (backward)
-    float *S, *dS;      // [n][K][V]  start states, gradients of the end states (backward)
+    unsigned char *mats;   // [n] ChunkMats
+    float *U, *Y;          // rows: the chunk's tokens (backward)
+    float *S, *dS;         // rows: the padded head_dim; start states, gradients of the end states (backward)
     int32_t Nt;
-    bool backward;      // X is computed for the backward (delta_beta_safe)
+    bool backward;         // X is computed for the backward (delta_beta_safe)
 };
 
 struct DeltaGrads {
@@ -44,9 +45,14 @@ struct DeltaGrads {
     float *beta, *g, *state; // state or null
 };
 
+// Padded head_dim of the chunked kernels, and tokens of a chunk.
+inline int delta_kp(int K) { return K <= 64 ? 64 : K <= 128 ? 128 : 256; }
+inline int delta_chunk(int K) { return K <= 128 ? 64 : 32; }
+
 hipError_t delta_prepare();
 hipError_t delta_bwd_prepare();
-hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16, bool save, hipStream_t st);
+hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16, hipStream_t st);
+size_t delta_mats_bytes(int K, bool is_bf16, bool backward);   // of a chunk
 hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &g, bool is_bf16, hipStream_t st);
 hipError_t launch_delta_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st);
 

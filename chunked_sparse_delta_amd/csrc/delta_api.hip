@@ -1,6 +1,5 @@
 // Host entry points of the dense gated delta rule: argument checks, workspace layout, launches.
 #include "delta.h"
-#include "delta_tile.h"
 #include "host.h"
 
 using namespace sdm;
@@ -61,24 +60,24 @@ int check_delta_inputs(const sdm_delta_shape *s, const sdm_rows *q, const sdm_ro
 // Lays the workspace out from `base` (NULL: only its size).
 size_t layout(const sdm_delta_shape *s, bool backward, void *base, DeltaWs *ws) {
     const size_t C = size_t(delta_chunk(s->head_dim)), Nt = (size_t(s->tokens) + C - 1) / C;
-    const size_t n = size_t(s->streams) * size_t(s->value_heads) * Nt, V = size_t(s->value_dim), K = size_t(s->head_dim);
+    const size_t n = size_t(s->streams) * size_t(s->value_heads) * Nt;
+    const size_t VP = (size_t(s->value_dim) + 15) / 16 * 16, KP = size_t(delta_kp(s->head_dim));
     char *p = static_cast<char *>(base);
     size_t at = 0;
-    auto take = [&](size_t floats) {
-        float *x = p ? reinterpret_cast<float *>(p + at) : nullptr;
-        at += align256(floats * 4);
+    auto take = [&](size_t bytes) {
+        char *x = p ? p + at : nullptr;
+        at += align256(bytes);
         return x;
     };
     DeltaWs w{};
     w.Nt = int32_t(Nt);
     w.backward = backward;
-    w.X = take(n * C * C);
-    w.Pm = take(n * C * C);
+    w.mats = reinterpret_cast<unsigned char *>(take(n * delta_mats_bytes(s->head_dim, s->dtype == SDM_BF16, backward)));
     if (backward) {
-        w.U = take(n * C * V);
-        w.Y = take(n * C * V);
-        w.S = take(n * K * V);
-        w.dS = take(n * K * V);
+        w.U = reinterpret_cast<float *>(take(n * C * VP * 4));
+        w.Y = reinterpret_cast<float *>(take(n * C * VP * 4));
+        w.S = reinterpret_cast<float *>(take(n * KP * VP * 4));
+        w.dS = reinterpret_cast<float *>(take(n * KP * VP * 4));
     }
     if (ws) *ws = w;
     return at < 256 ? 256 : at;
@@ -122,7 +121,7 @@ int sdm_gated_delta_fwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_r
     if ((rc = device_cus(&cus))) return rc;
     a.state_out = state_out;
     a.out = out;
-    const hipError_t e = launch_delta_fwd(a, ws, s->dtype == SDM_BF16, false, static_cast<hipStream_t>(exec->stream));
+    const hipError_t e = launch_delta_fwd(a, ws, s->dtype == SDM_BF16, static_cast<hipStream_t>(exec->stream));
     return e == hipSuccess ? SDM_OK : hip_fail(e, "gated delta launch");
 }
 

@@ -18,295 +18,397 @@
 //
 // U / beta is the write error; where beta is (nearly) 0 the backward's own X and U are computed
 // with beta 1e-20 instead, which changes no other result, so that it still is.
-#include "delta_tile.h"
+#include "delta_walk.h"
 
 namespace sdm {
 
 namespace {
 
-template <int C, int KP> struct BackLds {
-    static constexpr int LK = KP + 4, LC = C + 4;
-    float k[C * LK], q[C * LK], X[C * LC], P[C * LC];
-    Gates<C> g;
-};
+// The readings' gradient as rows.
+__device__ __forceinline__ Rows grad_rows(const DeltaArgs &a, const DeltaGrads &d) {
+    return {d.go, int64_t(a.T) * a.Hv * a.V, int64_t(a.Hv) * a.V, a.V};
+}
 
 template <typename T, int C, int KP>
 __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
-    using Lds = BackLds<C, KP>;
-    constexpr int LK = Lds::LK, LC = Lds::LC, NT = C / 16, KT = KP / 16;
+    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32;
+    using W = Walk<T, C, KP, 3, true>;
     extern __shared__ __align__(16) unsigned char raw[];
-    Lds &s = *reinterpret_cast<Lds *>(raw);
-    const int slices = (a.V + 63) / 64;
+    typename W::Lds &s = *reinterpret_cast<typename W::Lds *>(raw);
+    const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
     const int slice = blockIdx.x % slices, ph = blockIdx.x / slices, h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lc = lane & 15, lg = lane >> 4;
-    const int col = slice * 64 + wv * 16 + lc;
+    const int cg = slice * 4 + wv, col = cg * 16 + lc;
     const bool in = col < a.V;
-    const int n = delta_valid(a, p);
-    const int64_t so = int64_t(ph) * a.K * a.V + col;
-    const int64_t os = int64_t(a.Hv) * a.V, oo = (int64_t(p) * a.T * a.Hv + h) * a.V + col;
-    const T *go = static_cast<const T *>(d.go) + oo;
-    T *dv = static_cast<T *>(d.v) + oo;
-    dt4 S[KT];
-#pragma unroll
-    for (int i = 0; i < KT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = i * 16 + 4 * lg + r;
-            S[i][r] = in && row < a.K && d.gstate ? d.gstate[so + int64_t(row) * a.V] : 0.0f;
-        }
-    for (int c = (n + C - 1) / C - 1; c >= 0; --c) {
-        const int t0 = c * C, live = min(C, n - t0);
+    const int n = delta_valid(a, p), Nc = (n + C - 1) / C;
+    T *dv = static_cast<T *>(d.v) + (int64_t(p) * a.T * a.Hv + h) * a.V + col;
+    const int64_t os = int64_t(a.Hv) * a.V;
+    dt4 S[KB][2];
+    load_state<KB>(S, d.gstate, ph, a.K, a.V, col);
+    W w(a, ws, p, h, hk, ph, cg, grad_rows(a, d), h);
+    if (Nc > 0) {
+        w.load(Nc - 1, n);
+        w.store(s, Nc - 1, n);
+        __syncthreads();
+    }
+    for (int c = Nc - 1; c >= 0; --c) {
+        const int t0 = c * C;
+        if (c > 0) w.load(c - 1, n);
         const int64_t nc = int64_t(ph) * ws.Nt + c;
-        load_tile<T, C, KP, LK>(a.k, p, hk, t0, live, a.K, s.k);
-        load_tile<T, C, KP, LK>(a.q, p, hk, t0, live, a.K, s.q);
-        load_mat<C, C, LC>(ws.X + nc * C * C, s.X);
-        load_mat<C, C, LC>(ws.Pm + nc * C * C, s.P);
-        load_gates<C>(a, p, h, t0, live, s.g);
-        __syncthreads();
+        save_blocks<KB>(ws.dS, nc, VG, cg, S);
+        const Gates<C> &g = s.m.g;
+        dt4 x[TB][2] = {};
 #pragma unroll
-        for (int i = 0; i < KT; ++i)
+        for (int kb = 0; kb < KB; ++kb) {
+            const Frag<3> fs = split<3>(S[kb][0], S[kb][1]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = i * 16 + 4 * lg + r;
-                if (in && row < a.K) ws.dS[nc * a.K * a.V + int64_t(row) * a.V + col] = S[i][r];
-            }
-        dt4 O[NT], U[NT], Y[NT];
+            for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = t * 16 + 4 * lg + r;
-                O[t][r] = in && row < live ? to_f32(go[(t0 + row) * os]) : 0.0f;
-            }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            dt4 x{};
-#pragma unroll
-            for (int i = 0; i < KT; ++i) x = tile_mma(tile_row(s.k, LK, t * 16, i * 16), S[i], x);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] *= s.g.eL[t * 16 + 4 * lg + r];
-#pragma unroll
-            for (int i = t; i < NT; ++i) x = tile_mma(tile_col(s.P, LC, i * 16, t * 16), O[i], x);
-            U[t] = x;
+                for (int e = 0; e < 2; ++e) x[tb][e] = mma<3>(read_rows<NI>(s.k[0][tb][kb], W::kStride, e), fs, x[tb][e]);
         }
+        dt4 o[TB][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            Y[t] = dt4{};
+        for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-            for (int i = t; i < NT; ++i) Y[t] = tile_mma(tile_col(s.X, LC, i * 16, t * 16), U[i], Y[t]);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = t * 16 + 4 * lg + r;
-                if (in) ws.Y[(nc * C + row) * a.V + col] = Y[t][r];
-                const float y = s.g.beta[row] * Y[t][r];
-                if (in && row < live) dv[(t0 + row) * os] = from_f32<T>(y);
-                O[t][r] *= a.scale * s.g.eG[row];
-                Y[t][r] = -s.g.eG[row] * y;
+            for (int e = 0; e < 2; ++e) {
+                o[tb][e] = w.value(s, tb, e);
+                x[tb][e] *= *reinterpret_cast<const dt4 *>(g.eL + tb * 32 + lg * 8 + e * 4);
             }
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
+        for (int ib = 0; ib < TB; ++ib) {
+            const Frag<NI> fo = split<NI>(o[ib][0], o[ib][1]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[i][r] *= s.g.last;
+            for (int tb = 0; tb <= ib; ++tb)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                S[i] = tile_mma(tile_col(s.q, LK, t * 16, i * 16), O[t], S[i]);
-                S[i] = tile_mma(tile_col(s.k, LK, t * 16, i * 16), Y[t], S[i]);
-            }
+                for (int e = 0; e < 2; ++e)
+                    x[tb][e] = mma<3>(read_cols<3>(s.m.P[0][ib + tb], kTri<C> * kBlk, e), fo, x[tb][e]);
         }
-        __syncthreads();
+        dt4 Y[TB][2] = {};
+#pragma unroll
+        for (int ib = 0; ib < TB; ++ib) {
+            const Frag<3> fu = split<3>(x[ib][0], x[ib][1]);
+#pragma unroll
+            for (int tb = 0; tb <= ib; ++tb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    Y[tb][e] = mma<3>(read_cols<3>(s.m.X[0][ib + tb], kTri<C> * kBlk, e), fu, Y[tb][e]);
+        }
+        save_blocks<TB>(ws.Y, nc, VG, cg, Y);
+        const float last = g.last;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) S[kb][e] *= last;
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = tb * 32 + lg * 8 + e * 4;
+                const dt4 b = *reinterpret_cast<const dt4 *>(g.beta + t), eG = *reinterpret_cast<const dt4 *>(g.eG + t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y = b[i] * Y[tb][e][i];
+                    if (in && t0 + t + i < n) dv[(t0 + t + i) * os] = from_f32<T>(y);
+                    o[tb][e][i] *= a.scale * eG[i];
+                    Y[tb][e][i] = -eG[i] * y;
+                }
+            }
+            const Frag<3> fo = split<3>(o[tb][0], o[tb][1]), fy = split<3>(Y[tb][0], Y[tb][1]);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    S[kb][e] = mma<3>(read_cols<NI>(s.q[0][tb][kb], W::kStride, e), fo, S[kb][e]);
+                    S[kb][e] = mma<3>(read_cols<NI>(s.k[0][tb][kb], W::kStride, e), fy, S[kb][e]);
+                }
+        }
+        if (c > 0) {
+            __syncthreads();
+            w.store(s, c - 1, n);
+            __syncthreads();
+        }
     }
     for (int t = n + lg; t < a.T; t += 4)
         if (in) dv[t * os] = from_f32<T>(0.0f);
-    if (d.state) {
-#pragma unroll
-        for (int i = 0; i < KT; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = i * 16 + 4 * lg + r;
-                if (in && row < a.K) d.state[so + int64_t(row) * a.V] = S[i][r];
-            }
-    }
+    store_state<KB>(S, d.state, ph, a.K, a.V, col);
 }
 
-// V columns of the state, the readings' gradient, U and Y are taken VB at a time.
-constexpr int VB = 32, LV = VB + 4;
-
-template <int C, int KP> struct GradLds {
-    static constexpr int LK = KP + 4, LC = C + 4;
+// Every chunk of a key head at once. The gradients of q and k are computed transposed (rows:
+// head_dim, columns: tokens), so that a lane's accumulators are eight neighbours of an output row;
+// U, Y, S and dS lie in LDS transposed too (rows: columns of V, as the workspace holds them). V is
+// taken 32 columns at a time.
+template <typename T, int C, int KP> struct GradLds {
+    static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NM = NI == 1 ? 2 : 3;
     union {
         struct {
-            float go[C * LV], U[C * LV], Y[C * LV], S[KP * LV], dS[KP * LV];
+            unsigned char go[NI][TB][kBlk], U[3][TB][kBlk], Y[3][TB][kBlk], S[3][KB][kBlk], dS[3][KB][kBlk];
         };
         struct {
-            float k[C * LK], q[C * LK];
+            unsigned char k[NI][TB][KB][kBlk], q[NI][TB][KB][kBlk];
+            unsigned char Mq[NM][kTri<C>][kBlk], Ma[NM][kTri<C>][kBlk];   // scale D dP and D dA, rows: token i
+            float M[C * (C + 1)];                                        // dP P + dA A below the diagonal
         };
     };
-    float Mq[C * LC], Ma[C * LC];     // scale D dP and D dA
-    float M[C * (C + 1)];             // dP P + dA A below the diagonal
-    float ai[C], bj[C], ub[C];        // a_i, b_j, Y . U
-    double row[C], colm[C];           // sums of M
+    float ai[2][C], bj[2][C], ub[2][C];   // a_i, b_j, Y . U, in two parts
+    double row[C], colm[C], G[C];
     double cs[4];
     Gates<C> g;
 };
 
-// Sum over the 16 lanes of a row of accumulator blocks.
-__device__ __forceinline__ float lanes16(float x) {
+// G of a chunk again (delta_prep_kernel), by one wavefront.
+template <int C> __device__ __forceinline__ void chunk_G(const DeltaArgs &a, int p, int h, int t0, int live, double *G) {
+    const int lane = threadIdx.x & 63;
+    float g = lane < C && lane < live ? a.g[(int64_t(p) * a.T + t0 + lane) * a.Hv + h] : 0.0f;
+    if (g < -1e4f) g = -1e4f;
+    double x = double(g);
 #pragma unroll
-    for (int m = 8; m > 0; m >>= 1) x += __shfl_xor(x, m, 64);
-    return x;
+    for (int d = 1; d < C; d <<= 1) {
+        const double o = __shfl_up(x, d, 64);
+        if (lane >= d) x += o;
+    }
+    if (lane < C) G[lane] = x;
 }
 
 template <typename T, int C, int KP>
 __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
-    using Lds = GradLds<C, KP>;
-    constexpr int LK = Lds::LK, LC = Lds::LC, NT = C / 16, KT = KP / 16;
-    constexpr int CG = 4 / NT, CT = KT / CG;      // wavefronts side by side on a row of blocks, blocks of each
+    using Lds = GradLds<T, C, KP>;
+    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NT = C / 16, NM = Lds::NM;
+    constexpr int KG = 4 / NT, KW = KB / KG;        // wavefronts on the same tokens, their share of head_dim's blocks
+    constexpr int NJ = (kTri<C> * 2 + 3) / 4;       // tiles of pairs per wavefront
+    constexpr int kStride = TB * KB * kBlk;
     extern __shared__ __align__(16) unsigned char raw[];
     Lds &s = *reinterpret_cast<Lds *>(raw);
-    const int group = a.Hv / a.Hk;
+    const int group = a.Hv / a.Hk, VG = (a.V + 15) / 16;
     const int c = int(blockIdx.x % ws.Nt), ph = int(blockIdx.x / ws.Nt), hk = ph % a.Hk, p = ph / a.Hk;
     const int t0 = c * C, live = max(0, min(C, delta_valid(a, p) - t0));
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lc = lane & 15, lg = lane >> 4;
-    const int rt = wv % NT, ct0 = wv / NT * CT;   // this wavefront's rows and first column block of dq, dk
-    T *dq = static_cast<T *>(d.q), *dk = static_cast<T *>(d.k);
-    dt4 aq[CT] = {}, ak[CT] = {};
+    const int tb = wv % NT / 2, ta = wv % 2, kb0 = wv / NT * KW;     // this wavefront's tokens and blocks of dq, dk
+    const int tok = tb * 32 + block_row(lc, ta);                    // the lane's token
+    const Rows gr = grad_rows(a, d);
+    dt4 aq[KW][2] = {}, ak[KW][2] = {};
     for (int hh = 0; live > 0 && hh < group; ++hh) {
         const int h = hk * group + hh;
         const int64_t nc = (int64_t(p) * a.Hv + h) * ws.Nt + c;
-        const T *go = static_cast<const T *>(d.go) + (int64_t(p) * a.T + t0) * a.Hv * a.V + int64_t(h) * a.V;
-        load_gates<C>(a, p, h, t0, live, s.g);
-        // over V: dP, dA (blocks dealt to the wavefronts), do S0^T, Y S0^T, U dS1^T
-        constexpr int NP = (NT * (NT + 1) / 2 + 3) / 4;
-        dt4 dP[NP] = {}, dA[NP] = {}, oS[CT] = {}, yS[CT] = {}, uS[CT] = {};
+        const T *go = static_cast<const T *>(gr.data) + p * gr.sp + t0 * gr.st + h * gr.sh;
+        const ChunkMats<C, 3> *mats = reinterpret_cast<const ChunkMats<C, 3> *>(ws.mats) + nc;
+        if (tid < int(sizeof(Gates<C>) / 4)) reinterpret_cast<float *>(&s.g)[tid] = reinterpret_cast<const float *>(&mats->g)[tid];
+        if (wv == 3) chunk_G<C>(a, p, h, t0, live, s.G);
+        // over V: dP, dA (transposed: columns i, rows j), S do^T, S Y^T, dS U^T
+        dt4 dP[NJ][2] = {}, dA[NJ][2] = {}, oS[KW][2] = {}, yS[KW][2] = {}, uS[KW][2] = {};
         double cc = 0.0;
-        float ub = 0.0f;
-        for (int v0 = 0; v0 < a.V; v0 += VB) {
-            for (int i = tid; i < C * VB; i += 256) {
-                const int t = i / VB, v = i % VB;
-                const bool in = v0 + v < a.V;
-                s.go[t * LV + v] = in && t < live ? to_f32(go[int64_t(t) * a.Hv * a.V + v0 + v]) : 0.0f;
-                s.U[t * LV + v] = in ? ws.U[(nc * C + t) * a.V + v0 + v] : 0.0f;
-                s.Y[t * LV + v] = in ? ws.Y[(nc * C + t) * a.V + v0 + v] : 0.0f;
+        float ub[8] = {};
+        for (int vg = 0; vg < VG; vg += 2) {
+            for (int i = tid; i < C * 4; i += 256) {      // eights of do
+                const int t = i / 4, e = vg * 16 + i % 4 * 8, ce = min(e, a.V - 1);
+                Eight<T> x;
+                x.load(go + int64_t(min(t, live - 1)) * gr.st, ce, a.V);
+                x.fix(ce, a.V, t < live && e < a.V);
+                const Frag<NI> f = x.pieces();
+#pragma unroll
+                for (int n = 0; n < NI; ++n) *reinterpret_cast<db8 *>(s.go[n][t / 32] + block_at(t % 32, i % 4)) = f.p[n];
             }
-            for (int i = tid; i < KP * VB; i += 256) {
-                const int r = i / VB, v = i % VB;
-                const bool in = v0 + v < a.V && r < a.K;
-                const int64_t at = nc * a.K * a.V + int64_t(r) * a.V + v0 + v;
-                const float x = in ? ws.S[at] : 0.0f, y = in ? ws.dS[at] : 0.0f;
-                s.S[r * LV + v] = x;
-                s.dS[r * LV + v] = y;
-                cc += double(x * y);
+            for (int i = tid; i < TB * 128; i += 256) {   // eights of tokens of U and Y: one per thread
+                const int cg = i / (TB * 64), b = i / 64 % TB, row = cg * 16 + lc;
+                dt4 u[2] = {}, y[2] = {};
+                if (vg + cg < VG) {
+                    const int64_t at = (((nc * VG + vg + cg) * TB + b) * 64 + lane) * 8;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        u[e] = *reinterpret_cast<const dt4 *>(ws.U + at + e * 4);
+                        y[e] = *reinterpret_cast<const dt4 *>(ws.Y + at + e * 4);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ub[e] = fmaf(u[e / 4][e % 4], y[e / 4][e % 4], ub[e]);
+                const Frag<3> fu = split<3>(u[0], u[1]), fy = split<3>(y[0], y[1]);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    *reinterpret_cast<db8 *>(s.U[n][b] + block_at(row, lg)) = fu.p[n];
+                    *reinterpret_cast<db8 *>(s.Y[n][b] + block_at(row, lg)) = fy.p[n];
+                }
+            }
+            for (int i = tid; i < KB * 128; i += 256) {   // eights of head_dim of S and dS
+                const int cg = i / (KB * 64), b = i / 64 % KB, row = cg * 16 + lc;
+                dt4 x[2] = {}, y[2] = {};
+                if (vg + cg < VG) {
+                    const int64_t at = (((nc * VG + vg + cg) * KB + b) * 64 + lane) * 8;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = *reinterpret_cast<const dt4 *>(ws.S + at + e * 4);
+                        y[e] = *reinterpret_cast<const dt4 *>(ws.dS + at + e * 4);
+                    }
+                }
+                float m = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaf(x[e / 4][e % 4], y[e / 4][e % 4], m);
+                cc += double(m);
+                const Frag<3> fx = split<3>(x[0], x[1]), fy = split<3>(y[0], y[1]);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    *reinterpret_cast<db8 *>(s.S[n][b] + block_at(row, lg)) = fx.p[n];
+                    *reinterpret_cast<db8 *>(s.dS[n][b] + block_at(row, lg)) = fy.p[n];
+                }
             }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                const int i = wv + 4 * j;
-                if (i >= NT * (NT + 1) / 2) break;
-                int r = 0, q = i;
-                while (q > r) q -= ++r;
+            for (int j = 0; j < NJ; ++j) {    // tile e of the columns i, both tiles of the rows j
+                const int m = wv + 4 * j, b = m / 2, e = m & 1, bi = b > 0, bj = b == 2;
+                if (b >= kTri<C>) break;
+                const Frag<NI> fo = read_rows<NI>(s.go[0][bi], TB * kBlk, e);
+                const Frag<3> fy = read_cols<3>(s.Y[0][bi], TB * kBlk, e);
 #pragma unroll
-                for (int v = 0; v < VB; v += 16) {
-                    const dt4 u = tile_row(s.U, LV, q * 16, v);
-                    dP[j] = tile_mma(tile_row(s.go, LV, r * 16, v), u, dP[j]);
-                    dA[j] = tile_mma(tile_row(s.Y, LV, r * 16, v), u, dA[j]);
+                for (int x = 0; x < 2; ++x) {
+                    const Frag<3> fu = read_cols<3>(s.U[0][bj], TB * kBlk, x);
+                    dP[j][x] = mma<3>(fu, fo, dP[j][x]);
+                    dA[j][x] = mma<3>(fu, fy, dA[j][x]);
                 }
             }
+            const Frag<NI> fo = read_rows<NI>(s.go[0][tb], TB * kBlk, ta);
+            const Frag<3> fu = read_cols<3>(s.U[0][tb], TB * kBlk, ta), fy = read_cols<3>(s.Y[0][tb], TB * kBlk, ta);
 #pragma unroll
-            for (int v = 0; v < VB; v += 16) {
-                const dt4 o = tile_row(s.go, LV, rt * 16, v), y = tile_row(s.Y, LV, rt * 16, v),
-                          u = tile_row(s.U, LV, rt * 16, v);
+            for (int b = 0; b < KW; ++b)
 #pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    const dt4 S = tile_row(s.S, LV, (ct0 + j) * 16, v), dS = tile_row(s.dS, LV, (ct0 + j) * 16, v);
-                    oS[j] = tile_mma(o, S, oS[j]);
-                    yS[j] = tile_mma(y, S, yS[j]);
-                    uS[j] = tile_mma(u, dS, uS[j]);
+                for (int e = 0; e < 2; ++e) {
+                    const Frag<3> fs = read_cols<3>(s.S[0][kb0 + b], KB * kBlk, e);
+                    oS[b][e] = mma<3>(fs, fo, oS[b][e]);
+                    yS[b][e] = mma<3>(fs, fy, yS[b][e]);
+                    uS[b][e] = mma<3>(read_cols<3>(s.dS[0][kb0 + b], KB * kBlk, e), fu, uS[b][e]);
                 }
-            }
-            if (tid < C) {
-#pragma unroll
-                for (int v = 0; v < VB; ++v) ub = fmaf(s.Y[tid * LV + v], s.U[tid * LV + v], ub);
-            }
             __syncthreads();
         }
-        if (tid < C) s.ub[tid] = ub;
+        // Y . U of each token: over the 16 columns of a lane group, then the two column groups
+        if (tid < TB * 128) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                for (int m = 8; m > 0; m >>= 1) ub[e] += __shfl_xor(ub[e], m, 64);
+                if (lc == 0) s.ub[tid / (TB * 64)][tid / 64 % TB * 32 + lg * 8 + e] = ub[e];
+            }
+        }
 #pragma unroll
         for (int m = 32; m > 0; m >>= 1) cc += __shfl_xor(cc, m, 64);
         if (lane == 0) s.cs[wv] = cc;
-        load_tile<T, C, KP, LK>(a.k, p, hk, t0, live, a.K, s.k);
-        load_tile<T, C, KP, LK>(a.q, p, hk, t0, live, a.K, s.q);
-        for (int i = tid; i < C * LC; i += 256) s.Mq[i] = s.Ma[i] = 0.0f;
-        for (int i = tid; i < C; i += 256) s.ai[i] = s.bj[i] = 0.0f;
-        __syncthreads();
-        // D, P and A again, and the weights of k and q in the gradients
+        {
+            const T *kp = static_cast<const T *>(a.k.data) + p * a.k.sp + hk * a.k.sh + t0 * a.k.st;
+            const T *qp = static_cast<const T *>(a.q.data) + p * a.q.sp + hk * a.q.sh + t0 * a.q.st;
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-            const int i = wv + 4 * j;
-            if (i >= NT * (NT + 1) / 2) break;
-            int r = 0, q = i;
-            while (q > r) q -= ++r;
-            dt4 kk{}, qk{};
-            for (int x = 0; x < KP; x += 16) {
-                const dt4 b = tile_row(s.k, LK, q * 16, x);
-                kk = tile_mma(tile_row(s.k, LK, r * 16, x), b, kk);
-                qk = tile_mma(tile_row(s.q, LK, r * 16, x), b, qk);
-            }
-            const int col = q * 16 + lc;
+            for (int i = tid; i < C * KP / 8; i += 256) {
+                const int b = i / 128, r = i % 128 / 4, t = b / KB * 32 + r, e = b % KB * 32 + i % 4 * 8, at = b * kBlk + block_at(r, i % 4);
+                Eight<T> x, y;
+                x.load(kp + min(t, live - 1) * a.k.st, e, a.K);
+                y.load(qp + min(t, live - 1) * a.q.st, e, a.K);
+                x.fix(e, a.K, t < live);
+                y.fix(e, a.K, t < live);
+                const Frag<NI> fk = x.pieces(), fq = y.pieces();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = r * 16 + 4 * lg + e;
-                const float D = row >= col ? expf(float(s.g.G[row] - s.g.G[col])) : 0.0f;
-                const float wq = row >= col ? a.scale * (D * dP[j][e]) : 0.0f;
-                const float wa = row > col ? -s.g.beta[row] * (D * dA[j][e]) : 0.0f;
-                s.Mq[row * LC + col] = wq;
-                s.Ma[row * LC + col] = wa;
-                s.M[row * (C + 1) + col] = row > col ? fmaf(wq, qk[e], wa * kk[e]) : 0.0f;
+                for (int n = 0; n < NI; ++n) {
+                    *reinterpret_cast<db8 *>(&s.k[n][0][0][0] + at) = fk.p[n];
+                    *reinterpret_cast<db8 *>(&s.q[n][0][0][0] + at) = fq.p[n];
+                }
             }
         }
         __syncthreads();
+        // D, P and A again, and the weights of k and q in the gradients (accumulators: rows j, columns i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = rt * 16 + 4 * lg + r;
-            const float eG = s.g.eG[row], eL = s.g.eL[row], b = s.g.beta[row];
+        for (int j = 0; j < NJ; ++j) {
+            const int m = wv + 4 * j, b = m / 2, e = m & 1, bi = b > 0, bj = b == 2;
+            if (b >= kTri<C>) break;
+            dt4 kk[2] = {}, qk[2] = {};
+#pragma unroll
+            for (int x = 0; x < KB; ++x) {
+                const Frag<NI> fk = read_rows<NI>(s.k[0][bi][x], kStride, e), fq = read_rows<NI>(s.q[0][bi][x], kStride, e);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const Frag<NI> f = read_rows<NI>(s.k[0][bj][x], kStride, y);
+                    kk[y] = mma<3>(f, fk, kk[y]);
+                    qk[y] = mma<3>(f, fq, qk[y]);
+                }
+            }
+            const int i = bi * 32 + block_row(lc, e);
+            const double Gi = s.G[i];
+            const float beta = s.g.beta[i];
+            dt4 wq[2], wa[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int jj = bj * 32 + lg * 8 + y * 4 + r;
+                    const float D = i >= jj ? expf(float(Gi - s.G[jj])) : 0.0f;
+                    wq[y][r] = i >= jj ? a.scale * (D * dP[j][y][r]) : 0.0f;
+                    wa[y][r] = i > jj ? -beta * (D * dA[j][y][r]) : 0.0f;
+                    s.M[i * (C + 1) + jj] = i > jj ? fmaf(wq[y][r], qk[y][r], wa[y][r] * kk[y][r]) : 0.0f;
+                }
+            // a lane holds eight neighbours j of row i
+            const Frag<NM> fq = split<NM>(wq[0], wq[1]), fa = split<NM>(wa[0], wa[1]);
+#pragma unroll
+            for (int n = 0; n < NM; ++n) {
+                *reinterpret_cast<db8 *>(s.Mq[n][b] + block_at(block_row(lc, e), lg)) = fq.p[n];
+                *reinterpret_cast<db8 *>(s.Ma[n][b] + block_at(block_row(lc, e), lg)) = fa.p[n];
+            }
+        }
+        // the states' part of dq and dk, and its products with q and k
+        {
+            const float eG = s.g.eG[tok], eL = s.g.eL[tok], xo = a.scale * eG, xy = -(s.g.beta[tok] * eG);
             float ai = 0.0f, bj = 0.0f;
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                const int col = (ct0 + j) * 16 + lc;
-                const float k = s.k[row * LK + col], q = s.q[row * LK + col];
-                const float x = a.scale * (eG * oS[j][r]), y = -(b * eG) * yS[j][r], z = eL * uS[j][r];
-                ai += fmaf(x, q, y * k);
-                bj = fmaf(z, k, bj);
-                aq[j][r] += x;
-                ak[j][r] += y + z;
-            }
-            ai = lanes16(ai);
-            bj = lanes16(bj);
-            if constexpr (CG == 1) {
-                if (lc == 0) {
-                    s.ai[row] = ai;
-                    s.bj[row] = bj;
+            for (int b = 0; b < KW; ++b) {
+                dt4 k[2] = {}, q[2] = {};
+#pragma unroll
+                for (int n = NI - 1; n >= 0; --n) {
+                    const int at = n * kStride + (tb * KB + kb0 + b) * kBlk + block_at(tok % 32, lg);
+                    const du4 kw = *reinterpret_cast<const du4 *>(&s.k[0][0][0][0] + at);
+                    const du4 qw = *reinterpret_cast<const du4 *>(&s.q[0][0][0][0] + at);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int sh = e & 1 ? 0 : 16;
+                        k[e / 4][e % 4] += __uint_as_float((kw[e / 2] << sh) & 0xFFFF0000u);
+                        q[e / 4][e % 4] += __uint_as_float((qw[e / 2] << sh) & 0xFFFF0000u);
+                    }
                 }
-            } else if (lc == 0) {   // two wavefronts per row: the sum of two terms has one value
-                atomicAdd(&s.ai[row], ai);
-                atomicAdd(&s.bj[row], bj);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = xo * oS[b][e][r], y = xy * yS[b][e][r], z = eL * uS[b][e][r];
+                        ai += fmaf(x, q[e][r], y * k[e][r]);
+                        bj = fmaf(z, k[e][r], bj);
+                        aq[b][e][r] += x;
+                        ak[b][e][r] += y + z;
+                    }
+            }
+            ai += __shfl_xor(ai, 16, 64);
+            bj += __shfl_xor(bj, 16, 64);
+            ai += __shfl_xor(ai, 32, 64);
+            bj += __shfl_xor(bj, 32, 64);
+            if (lg == 0) {
+                s.ai[wv / NT][tok] = ai;
+                s.bj[wv / NT][tok] = bj;
             }
         }
+        __syncthreads();
+        // the pairs' part: the tokens as i (depth j up to them) and as j (depth i from them on)
 #pragma unroll
-        for (int j = 0; j < CT; ++j) {
-            const int c0 = (ct0 + j) * 16;
-            for (int t = 0; t < NT; ++t) {
-                const dt4 kt = tile_col(s.k, LK, t * 16, c0);
-                if (t <= rt) {
-                    aq[j] = tile_mma(tile_row(s.Mq, LC, rt * 16, t * 16), kt, aq[j]);
-                    ak[j] = tile_mma(tile_row(s.Ma, LC, rt * 16, t * 16), kt, ak[j]);
-                }
-                if (t >= rt) {
-                    ak[j] = tile_mma(tile_col(s.Ma, LC, t * 16, rt * 16), kt, ak[j]);
-                    ak[j] = tile_mma(tile_col(s.Mq, LC, t * 16, rt * 16), tile_col(s.q, LK, t * 16, c0), ak[j]);
-                }
+        for (int x = 0; x < TB; ++x) {
+            if (x <= tb) {
+                const Frag<NM> mq = read_rows<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta), ma = read_rows<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta);
+#pragma unroll
+                for (int b = 0; b < KW; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const Frag<NI> k = read_cols<NI>(s.k[0][x][kb0 + b], kStride, e);
+                        aq[b][e] = mma<NM>(k, mq, aq[b][e]);
+                        ak[b][e] = mma<NM>(k, ma, ak[b][e]);
+                    }
+            }
+            if (x >= tb) {
+                const Frag<NM> mq = read_cols<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta), ma = read_cols<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta);
+#pragma unroll
+                for (int b = 0; b < KW; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        ak[b][e] = mma<NM>(read_cols<NI>(s.q[0][x][kb0 + b], kStride, e), mq, ak[b][e]);
+                        ak[b][e] = mma<NM>(read_cols<NI>(s.k[0][x][kb0 + b], kStride, e), ma, ak[b][e]);
+                    }
             }
         }
         if (tid < C) {
@@ -323,41 +425,42 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
         if (tid < live) {
             const int m = tid;
             double x = double(s.g.last) * (s.cs[0] + s.cs[1] + s.cs[2] + s.cs[3]);
-            for (int i = 0; i < C; ++i) x += i >= m ? double(s.ai[i]) : double(s.bj[i]);
+            for (int i = 0; i < C; ++i) {
+                float y = i >= m ? s.ai[0][i] : s.bj[0][i];
+                if constexpr (KG > 1) y += i >= m ? s.ai[1][i] : s.bj[1][i];
+                x += double(y);
+            }
             for (int i = 0; i < m; ++i) x += s.colm[i] - s.row[i];   // pairs i >= m > j: those begun and not ended
             const int64_t at = (int64_t(p) * a.T + t0 + m) * a.Hv + h;
             d.g[at] = float(x);
-            d.beta[at] = s.ub[m] / delta_beta_safe(s.g.beta[m]);
+            d.beta[at] = (s.ub[0][m] + s.ub[1][m]) / delta_beta_safe(s.g.beta[m]);
         }
         __syncthreads();
     }
-    if (c * C >= a.T) return;
     const int rows = min(C, a.T - t0);
     for (int i = tid; i < rows * group; i += 256) {
         const int t = i / group, h = hk * group + i % group;
         const int64_t at = (int64_t(p) * a.T + t0 + t) * a.Hv + h;
         if (t >= live) d.g[at] = d.beta[at] = 0.0f;
     }
+    if (tok >= rows) return;
 #pragma unroll
-    for (int j = 0; j < CT; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = rt * 16 + 4 * lg + r, col = (ct0 + j) * 16 + lc;
-            if (row >= rows || col >= a.K) continue;
-            const int64_t at = ((int64_t(p) * a.T + t0 + row) * a.Hk + hk) * a.K + col;
-            dq[at] = from_f32<T>(row < live ? aq[j][r] : 0.0f);
-            dk[at] = from_f32<T>(row < live ? ak[j][r] : 0.0f);
-        }
+    for (int b = 0; b < KW; ++b) {
+        const int e0 = (kb0 + b) * 32 + lg * 8;
+        const int64_t at = ((int64_t(p) * a.T + t0 + tok) * a.Hk + hk) * a.K + e0;
+        put_eight(static_cast<T *>(d.q) + at, a.K - e0, aq[b][0], aq[b][1]);
+        put_eight(static_cast<T *>(d.k) + at, a.K - e0, ak[b][0], ak[b][1]);
+    }
 }
 
 template <typename T, int C, int KP>
 hipError_t bwd_go(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, hipStream_t st) {
     hipLaunchKernelGGL((delta_back_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hv * ((a.V + 63) / 64))), dim3(256),
-                       sizeof(BackLds<C, KP>), st, a, ws, d);
+                       sizeof(typename Walk<T, C, KP, 3, true>::Lds), st, a, ws, d);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || ws.Nt == 0) return e;
     hipLaunchKernelGGL((delta_grad_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hk * ws.Nt)), dim3(256),
-                       sizeof(GradLds<C, KP>), st, a, ws, d);
+                       sizeof(GradLds<T, C, KP>), st, a, ws, d);
     return hipGetLastError();
 }
 template <typename T>
@@ -369,13 +472,12 @@ hipError_t bwd_pick(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, 
     }
 }
 template <typename T, int C, int KP> hipError_t bwd_attr() {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_back_kernel<T, C, KP>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, sizeof(BackLds<C, KP>));
-    if (e == hipSuccess)
-        e = hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_grad_kernel<T, C, KP>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, sizeof(GradLds<C, KP>));
-    static_assert(sizeof(GradLds<C, KP>) <= 160 * 1024 && sizeof(BackLds<C, KP>) <= 160 * 1024, "LDS of a workgroup");
-    return e;
+    constexpr size_t lw = sizeof(typename Walk<T, C, KP, 3, true>::Lds), lg = sizeof(GradLds<T, C, KP>);
+    static_assert(lw <= kDeltaMaxLds && lg <= kDeltaMaxLds, "LDS of a workgroup");
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_back_kernel<T, C, KP>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lw);
+    return e != hipSuccess ? e : hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_grad_kernel<T, C, KP>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lg);
 }
 template <typename T> hipError_t bwd_attrs() {
     hipError_t e = bwd_attr<T, 64, 64>();
@@ -392,7 +494,7 @@ hipError_t delta_bwd_prepare() {
 }
 
 hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, bool is_bf16, hipStream_t st) {
-    const hipError_t e = launch_delta_fwd(a, ws, is_bf16, true, st);
+    const hipError_t e = launch_delta_fwd(a, ws, is_bf16, st);
     if (e != hipSuccess) return e;
     return is_bf16 ? bwd_pick<bf16>(a, ws, d, st) : bwd_pick<float>(a, ws, d, st);
 }
