@@ -9,10 +9,21 @@ namespace sdm {
 struct Rows {
     const void *data;
     int64_t sp, st, sh;
+    int32_t width;
+};
+constexpr int64_t kDeltaMaxStride = 1 << 24;   // of tokens: a chunk's offsets fit 32 bits
+
+// q or k as the chunked kernels take them: rows of the padded head_dim in bfloat16, `plane` elements
+// between the pieces of a float32 input (see delta_tile.h), every row 16-byte aligned. They are
+// the caller's rows where these are so, and copies otherwise; so with v (rows of a multiple of eight elements).
+struct KeyRows {
+    const bf16 *data;
+    int64_t plane, sp, st, sh;
 };
 
 struct DeltaArgs {
     Rows q, k, v;
+    KeyRows kk, qq;              // chunked kernels only; v is then regular too
     const float *beta, *g;       // [P, T, Hv]
     const float *state;          // [.., Hv, K, V] or null
     float *state_out;            // or null
@@ -39,7 +50,7 @@ struct DeltaWs {
 };
 
 struct DeltaGrads {
-    const void *go;          // [P, T, Hv, V]
+    Rows go;                 // [P, T, Hv, V]
     const float *gstate;     // [P, Hv, K, V] or null
     void *q, *k, *v;
     float *beta, *g, *state; // state or null
@@ -47,11 +58,16 @@ struct DeltaGrads {
 
 // Padded head_dim of the chunked kernels, and tokens of a chunk.
 inline int delta_kp(int K) { return K <= 64 ? 64 : K <= 128 ? 128 : 256; }
-inline int delta_chunk(int K) { return K <= 128 ? 64 : 32; }
+inline int delta_chunk(int K, bool is_bf16) { return is_bf16 && K <= 128 ? 64 : 32; }
 
 hipError_t delta_prepare();
 hipError_t delta_bwd_prepare();
 hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16, hipStream_t st);
+// Whether the chunked kernels can take the rows as they are, and the copies where they cannot (at `to`).
+bool delta_regular_keys(const Rows &r, bool is_bf16);
+bool delta_regular_values(const Rows &r, bool is_bf16);
+hipError_t launch_delta_copy_keys(const Rows &r, KeyRows *k, void *to, int P, int T, int H, bool is_bf16, hipStream_t st);
+hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool is_bf16, hipStream_t st);
 size_t delta_mats_bytes(int K, bool is_bf16, bool backward);   // of a chunk
 hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &g, bool is_bf16, hipStream_t st);
 hipError_t launch_delta_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st);

@@ -69,36 +69,29 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
         if (lane < C) {
             s.G[lane] = G;
             s.g.beta[lane] = in ? a.beta[at] : 0.0f;
-            s.g.eG[lane] = expf(float(G));
-            s.g.eL[lane] = expf(float(GL - G));
+            s.g.eG[lane] = in ? expf(float(G)) : 0.0f;
+            s.g.eL[lane] = in ? expf(float(GL - G)) : 0.0f;
         }
         if (lane == 0) s.g.last = expf(float(GL));
     }
     dt4 kk[NT] = {}, qk[NT] = {};
     if (wv < NT) {
-        const T *k = static_cast<const T *>(a.k.data) + p * a.k.sp + hk * a.k.sh + t0 * a.k.st;
-        const T *q = static_cast<const T *>(a.q.data) + p * a.q.sp + hk * a.q.sh + t0 * a.q.st;
+        const bf16 *k = a.kk.data + p * a.kk.sp + hk * a.kk.sh + t0 * a.kk.st;
+        const bf16 *q = a.qq.data + p * a.qq.sp + hk * a.qq.sh + t0 * a.qq.st;
+        // rows past the last valid token are cleared: their columns of X and P, and rows of P, are then 0
+        const int row = wv * 16 + lc;
 #pragma unroll
         for (int kb = 0; kb < KP / 32; ++kb) {
             const int d = kb * 32 + lg * 8;
-            Eight<T> x[NT], y;
-#pragma unroll
-            for (int ct = 0; ct < NT; ++ct)
-                if (ct <= wv) x[ct].load(k + min(ct * 16 + lc, live - 1) * a.k.st, d, a.K);
-            y.load(q + min(wv * 16 + lc, live - 1) * a.q.st, d, a.K);
-            y.fix(d, a.K, wv * 16 + lc < live);
-            Frag<NI> fk[NT];
-            const Frag<NI> fq = y.pieces();
+            Frag<NI> fk[NT], fa, fq = load_keys<NI>(q + (min(row, live - 1) * int(a.qq.st) + d), a.qq.plane);
+            if (row >= live) clear(fq);
 #pragma unroll
             for (int ct = 0; ct < NT; ++ct)
                 if (ct <= wv) {
-                    x[ct].fix(d, a.K, ct * 16 + lc < live);
-                    fk[ct] = x[ct].pieces();
+                    fk[ct] = load_keys<NI>(k + (min(ct * 16 + lc, live - 1) * int(a.kk.st) + d), a.kk.plane);
+                    if (ct * 16 + lc >= live) clear(fk[ct]);
+                    if (ct == wv) fa = fk[ct];
                 }
-            Frag<NI> fa;      // this wavefront's own rows of k
-#pragma unroll
-            for (int ct = 0; ct < NT; ++ct)
-                if (ct == wv) fa = fk[ct];
 #pragma unroll
             for (int ct = 0; ct < NT; ++ct)
                 if (ct <= wv) {
@@ -168,122 +161,229 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
 
 // Every column of the state evolves on its own: a wavefront keeps 16 columns of S in
 // accumulators through the whole sequence, and the four wavefronts of a workgroup share the
-// chunk's k, q, X and P in LDS. The next chunk's are loaded into registers under this one's products.
+// chunk's k, q, X and P in LDS. One wavefront per SIMD has nothing beside it to hide its waits: the
+// operands of each group of products are read from LDS before the group ahead of it.
 // SAVE: keeps U and each chunk's start state for the backward, and gives no output.
 template <typename T, int C, int KP, bool SAVE>
-__global__ __launch_bounds__(256) void delta_state_kernel(DeltaArgs a, DeltaWs ws) {
-    constexpr int NI = kPieces<T>, NP = kPPieces<T>(SAVE), KB = KP / 32, TB = C / 32;
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void delta_state_kernel(DeltaArgs a, DeltaWs ws) {
+    constexpr int NI = kPieces<T>, NP = kPPieces<T>(SAVE), KB = KP / 32, TB = C / 32, NTR = kTri<C>;
     constexpr int NS = NI == 1 ? 2 : 3;    // pieces of S and U that reach the readings only
     using W = Walk<T, C, KP, NP, !SAVE>;
     extern __shared__ __align__(16) unsigned char raw[];
-    typename W::Lds &s = *reinterpret_cast<typename W::Lds *>(raw);
+    typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
     const int slice = blockIdx.x % slices, ph = blockIdx.x / slices, h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lc = lane & 15, lg = lane >> 4;
     const int cg = slice * 4 + wv, col = cg * 16 + lc;
     const bool in = col < a.V;
     const int n = delta_valid(a, p), Nc = (n + C - 1) / C;
-    T *out = static_cast<T *>(a.out) + (int64_t(p) * a.T * a.Hv + h) * a.V + col;
+    const int oc = cg * 16 + lg * 4;   // readings come transposed: a lane holds four columns of the tokens block_row(lc, .)
+    T *out = static_cast<T *>(a.out) + (int64_t(p) * a.T * a.Hv + h) * a.V + oc;
     const int64_t os = int64_t(a.Hv) * a.V;
     dt4 S[KB][2];
     load_state<KB>(S, a.state, ph, a.K, a.V, col);
-    W w(a, ws, p, h, hk, ph, cg, a.v, h);
-    if (Nc > 0) {
-        w.load(0, n);
-        w.store(s, 0, n);
-        __syncthreads();
-    }
-    for (int c = 0; c < Nc; ++c) {
-        const int t0 = c * C;
-        if (c + 1 < Nc) w.load(c + 1, n);
-        const int64_t nc = int64_t(ph) * ws.Nt + c;
-        if constexpr (SAVE) save_blocks<KB>(ws.S, nc, VG, cg, S);
-        const Gates<C> &g = s.m.g;
-        dt4 x[TB][2] = {}, y[TB][2] = {};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            const Frag<3> fs = split<3>(S[kb][0], S[kb][1]);
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    x[tb][e] = mma<3>(read_rows<NI>(s.k[0][tb][kb], W::kStride, e), fs, x[tb][e]);
-                    if constexpr (!SAVE) y[tb][e] = mma<NS>(read_rows<NI>(s.q[0][tb][kb], W::kStride, e), fs, y[tb][e]);
-                }
-        }
-        Frag<3> fr[TB];
-#pragma unroll
-        for (int tb = 0; tb < TB; ++tb) {
-            dt4 r[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = tb * 32 + lg * 8 + e * 4;
-                const dt4 b = *reinterpret_cast<const dt4 *>(g.beta + t), eG = *reinterpret_cast<const dt4 *>(g.eG + t);
-                const dt4 v = w.value(s, tb, e);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    r[e][i] = (SAVE ? delta_beta_safe(b[i]) : b[i]) * (v[i] - eG[i] * x[tb][e][i]);
-                    y[tb][e][i] *= a.scale * eG[i];
-                }
-            }
-            fr[tb] = split<3>(r[0], r[1]);
-        }
-        dt4 U[TB][2];
+    const W w(a, ws, p, h, hk, ph, cg, a.v, n);
+    w.begin(bufs, 0);
+    dt4 y[TB][2] = {};
+    auto put = [&](int c) {
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                U[tb][e] = dt4{};
-#pragma unroll
-                for (int d = 0; d <= tb; ++d)
-                    U[tb][e] = mma<3>(read_rows<3>(s.m.X[0][tb + d], kTri<C> * kBlk, e), fr[d], U[tb][e]);
+                const int t = c * C + tb * 32 + block_row(lc, e);
+                if (t < n && oc < a.V) put_four(out + t * os, a.V - oc, y[tb][e]);
             }
-        if constexpr (SAVE) save_blocks<TB>(ws.U, nc, VG, cg, U);
-        else {
+    };
+    Frag<3> fs[KB];
 #pragma unroll
-            for (int d = 0; d < TB; ++d) {
-                const Frag<NS> fu = split<NS>(U[d][0], U[d][1]);
-#pragma unroll
-                for (int tb = d; tb < TB; ++tb)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        y[tb][e] = mma<NS>(read_rows<NP>(s.m.P[0][tb + d], kTri<C> * kBlk, e), fu, y[tb][e]);
-            }
+    for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
+    for (int c = 0; c < Nc; ++c) {
+        const typename W::Lds &s = bufs[c & (W::kBufs - 1)];
+        const Gates<C> &g = s.m.g;
+        if (!SAVE && c > 0) put(c - 1);    // late, so that no wait for what is on its way is a wait for these
+        w.ahead(bufs, c, c + 1);
+        // k S and q S
+        Frag<NI> A[2][TB][2];
+        auto rows_of = [&](Frag<NI>(&f)[TB][2], const unsigned char *m) {
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e) f[tb][e] = read_rows<NI>(m + tb * KB * kBlk, W::kStride, e);
+        };
+        rows_of(A[0], s.k[0][0][0]);
+        dt4 v[TB][2], b[TB][2], eG[TB][2];
+        float et[TB][2];             // exp(G) of the lane's tokens in the transposed readings
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = t0 + tb * 32 + lg * 8 + e * 4 + i;
-                        if (in && t < n) out[t * os] = from_f32<T>(y[tb][e][i]);
-                    }
+        for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = tb * 32 + lg * 8 + e * 4;
+                v[tb][e] = w.value(s, tb, e);
+                if (SAVE && !in) v[tb][e] = dt4{};
+                b[tb][e] = *reinterpret_cast<const dt4 *>(g.beta + t);
+                eG[tb][e] = *reinterpret_cast<const dt4 *>(g.eG + t);
+                et[tb][e] = g.eG[tb * 32 + block_row(lc, e)];
+            }
+        const int64_t nc = int64_t(ph) * ws.Nt + c;
+        if constexpr (SAVE) save_blocks<KB>(ws.S, nc, VG, cg, S);
+        dt4 x[TB][2] = {};
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) y[tb][0] = y[tb][1] = dt4{};
+        constexpr int KQ = SAVE ? KB : 2 * KB;
+        Frag<3> fx[2][2], fr[TB];    // X's blocks, a step ahead
+        auto x_of = [&](Frag<3>(&f)[2], int i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) f[e] = read_rows<3>(s.m.X[0][i], NTR * kBlk, e);
+        };
+#pragma unroll
+        for (int i = 0; i < KQ; ++i) {
+            if (i + 1 < KB) rows_of(A[(i + 1) & 1], s.k[0][0][i + 1]);
+            else if (i + 1 < KQ) rows_of(A[(i + 1) & 1], s.q[0][0][i + 1 - KB]);
+            else x_of(fx[0], 0);
+            lds_point();
+            if (i < KB) {
+                each_product<3, NI, 3>([&](int m, int l) {
+#pragma unroll
+                    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) x[tb][e] = mma1(A[i & 1][tb][e].p[m], fs[i % KB].p[l], x[tb][e]);
+                });
+            } else {
+                each_product<NS, NI, NS>([&](int m, int l) {
+#pragma unroll
+                    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) y[tb][e] = mma1(fs[i % KB].p[l], A[i & 1][tb][e].p[m], y[tb][e]);
+                });
+            }
+            if (i == KB - 1) {
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb) {
+                    dt4 r[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            r[e][j] = (SAVE ? delta_beta_safe(b[tb][e][j]) : b[tb][e][j]) * (v[tb][e][j] - eG[tb][e][j] * x[tb][e][j]);
+                    fr[tb] = split<3>(r[0], r[1]);
+                }
+            }
+            lds_point();
         }
+        // U = X r, then P U; block i of the lower triangle is row block i > 0, column block i == 2
+        dt4 U[TB][2] = {};
+        Frag<NP> fp[2][2];
+        auto p_of = [&](Frag<NP>(&f)[2], int i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) f[e] = read_rows<NP>(s.m.P[0][i], NTR * kBlk, e);
+        };
+        Frag<NI> fk[2][KB];          // blocks of k^T, half of a row block of them at a time
+        auto kt_of = [&](Frag<NI>(&f)[KB], int i) {
+#pragma unroll
+            for (int m = 0; m < KB; ++m) {
+                const int kb = i % 2 * (KB / 2) + m / 2;
+                f[m] = read_cols<NI>(s.k[0][i / 2][kb], W::kStride, m & 1);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NTR; ++i) {
+            if (i + 1 < NTR) x_of(fx[(i + 1) & 1], i + 1);
+            else if constexpr (!SAVE) p_of(fp[0], 0);
+            else kt_of(fk[0], 0);
+            lds_point();
+            each_product<3, 3, 3>([&](int m, int l) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) U[i > 0][e] = mma1(fx[i & 1][e].p[m], fr[i == 2].p[l], U[i > 0][e]);
+            });
+            lds_point();
+        }
+        Frag<3> fu[TB];
+        dt4 eL[TB][2];
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) eL[tb][e] = *reinterpret_cast<const dt4 *>(g.eL + tb * 32 + lg * 8 + e * 4);
         const float last = g.last;
+        if constexpr (SAVE) save_blocks<TB>(ws.U, nc, VG, cg, U);
+        else {
+            Frag<NS> fv[TB];
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) {
+                fv[tb] = split<NS>(U[tb][0], U[tb][1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) y[tb][e] *= a.scale * et[tb][e];
+            }
+#pragma unroll
+            for (int i = 0; i < NTR; ++i) {
+                if (i + 1 < NTR) p_of(fp[(i + 1) & 1], i + 1);
+                else kt_of(fk[0], 0);
+                lds_point();
+                each_product<NS, NP, NS>([&](int m, int l) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) y[i > 0][e] = mma1(fv[i == 2].p[l], fp[i & 1][e].p[m], y[i > 0][e]);
+                });
+                lds_point();
+            }
+        }
+        // S = e^{G_C} S + k^T (e^{G_C - G} U)
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) U[tb][e] *= eL[tb][e];
+            fu[tb] = split<3>(U[tb][0], U[tb][1]);
+        }
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) S[kb][e] *= last;
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb) {
+        for (int i = 0; i < 2 * TB; ++i) {
+            if (i + 1 < 2 * TB) kt_of(fk[(i + 1) & 1], i + 1);
+            lds_point();
+            each_product<3, NI, 3>([&](int x, int l) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) U[tb][e] *= *reinterpret_cast<const dt4 *>(g.eL + tb * 32 + lg * 8 + e * 4);
-            const Frag<3> fu = split<3>(U[tb][0], U[tb][1]);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) S[kb][e] = mma<3>(read_cols<NI>(s.k[0][tb][kb], W::kStride, e), fu, S[kb][e]);
+                for (int m = 0; m < KB; ++m) {
+                    const int kb = i % 2 * (KB / 2) + m / 2;
+                    S[kb][m & 1] = mma1(fk[i & 1][m].p[x], fu[i / 2].p[l], S[kb][m & 1]);
+                }
+            });
+            lds_point();
         }
-        if (c + 1 < Nc) {
-            __syncthreads();
-            w.store(s, c + 1, n);
-            __syncthreads();
-        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
+        w.turn(bufs, c + 1);
     }
     if constexpr (!SAVE) {
-        for (int t = n + lg; t < a.T; t += 4)
-            if (in) out[t * os] = from_f32<T>(0.0f);
+        if (Nc > 0) put(Nc - 1);
+        for (int t = n + lc; t < a.T; t += 16)
+            if (oc < a.V) put_four(out + t * os, a.V - oc, dt4{});
         store_state<KB>(S, a.state_out, ph, a.K, a.V, col);
+    }
+}
+
+// Rows of q or k as dense rows of KP elements, padded with zeros, a plane per piece: eight elements per thread.
+template <typename T> __global__ __launch_bounds__(256) void delta_copy_keys_kernel(Rows r, bf16 *out, int64_t rows, int tokens, int heads, int KP) {
+    const T *src = static_cast<const T *>(r.data);
+    const int per = KP / 8;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / per, t = row / heads % tokens, p = row / heads / tokens;
+        const int c = int(i % per) * 8, h = int(row % heads);
+        const T *x = src + p * r.sp + t * r.st + h * r.sh;
+        dt4 v[2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j / 4][j % 4] = c + j < r.width ? to_f32(x[c + j]) : 0.0f;
+        const Frag<kPieces<T>> f = split<kPieces<T>>(v[0], v[1]);
+#pragma unroll
+        for (int n = 0; n < kPieces<T>; ++n) *reinterpret_cast<db8 *>(out + n * rows * KP + row * KP + c) = f.p[n];
+    }
+}
+// Rows of v, or of the readings' gradient, as dense rows of VP elements, padded with zeros.
+template <typename T> __global__ __launch_bounds__(256) void delta_copy_values_kernel(Rows r, T *out, int64_t rows, int tokens, int heads, int VP) {
+    const T *src = static_cast<const T *>(r.data);
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * VP; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / VP, t = row / heads % tokens, p = row / heads / tokens;
+        const int c = int(i % VP), h = int(row % heads);
+        out[i] = c < r.width ? src[p * r.sp + t * r.st + h * r.sh + c] : from_f32<T>(0.0f);
     }
 }
 
@@ -297,22 +397,22 @@ template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const
         if (e != hipSuccess) return e;
     }
     if (ws.backward)
-        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, true>), grid, dim3(256), sizeof(typename Walk<T, C, KP, N1, false>::Lds), st, a, ws);
+        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, true>), grid, dim3(256), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
     else
-        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, false>), grid, dim3(256), sizeof(typename Walk<T, C, KP, N0, true>::Lds), st, a, ws);
+        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, false>), grid, dim3(256), (Walk<T, C, KP, N0, true>::kLds), st, a, ws);
     return hipGetLastError();
 }
 template <typename T> hipError_t fwd_pick(const DeltaArgs &a, const DeltaWs &ws, hipStream_t st) {
     switch (delta_kp(a.K)) {
-        case 64: return fwd_go<T, 64, 64>(a, ws, st);
-        case 128: return fwd_go<T, 64, 128>(a, ws, st);
+        case 64: return fwd_go<T, kChunk<T>, 64>(a, ws, st);
+        case 128: return fwd_go<T, kChunk<T>, 128>(a, ws, st);
         default: return fwd_go<T, 32, 256>(a, ws, st);
     }
 }
 
 template <typename T, int C, int KP> hipError_t fwd_attr() {
     constexpr int N0 = kPPieces<T>(false), N1 = kPPieces<T>(true);
-    constexpr size_t l0 = sizeof(typename Walk<T, C, KP, N0, true>::Lds), l1 = sizeof(typename Walk<T, C, KP, N1, false>::Lds);
+    constexpr size_t l0 = Walk<T, C, KP, N0, true>::kLds, l1 = Walk<T, C, KP, N1, false>::kLds;
     static_assert(l0 <= kDeltaMaxLds && l1 <= kDeltaMaxLds, "LDS of a workgroup");
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_state_kernel<T, C, KP, false>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, l0);
@@ -320,8 +420,8 @@ template <typename T, int C, int KP> hipError_t fwd_attr() {
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, l1);
 }
 template <typename T> hipError_t fwd_attrs() {
-    hipError_t e = fwd_attr<T, 64, 64>();
-    if (e == hipSuccess) e = fwd_attr<T, 64, 128>();
+    hipError_t e = fwd_attr<T, kChunk<T>, 64>();
+    if (e == hipSuccess) e = fwd_attr<T, kChunk<T>, 128>();
     if (e == hipSuccess) e = fwd_attr<T, 32, 256>();
     return e;
 }
@@ -337,9 +437,38 @@ hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16,
     return is_bf16 ? fwd_pick<bf16>(a, ws, st) : fwd_pick<float>(a, ws, st);
 }
 
+static bool rows_aligned(const Rows &r, int elements) {
+    return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.sp % elements == 0 && r.st % elements == 0 && r.sh % elements == 0;
+}
+bool delta_regular_keys(const Rows &r, bool is_bf16) { return is_bf16 && r.width == delta_kp(r.width) && rows_aligned(r, 8); }
+bool delta_regular_values(const Rows &r, bool is_bf16) { return r.width % 8 == 0 && rows_aligned(r, is_bf16 ? 8 : 4); }
+
+static unsigned copy_grid(int64_t threads) { return unsigned(threads / 256 + 1 < 8192 ? threads / 256 + 1 : 8192); }
+
+hipError_t launch_delta_copy_keys(const Rows &r, KeyRows *k, void *to, int P, int T, int H, bool is_bf16, hipStream_t st) {
+    const int KP = delta_kp(r.width);
+    const int64_t rows = int64_t(P) * T * H;
+    bf16 *out = static_cast<bf16 *>(to);
+    const dim3 grid(copy_grid(rows * (KP / 8)));
+    if (is_bf16) hipLaunchKernelGGL(delta_copy_keys_kernel<bf16>, grid, dim3(256), 0, st, r, out, rows, T, H, KP);
+    else hipLaunchKernelGGL(delta_copy_keys_kernel<float>, grid, dim3(256), 0, st, r, out, rows, T, H, KP);
+    *k = {out, rows * KP, int64_t(T) * H * KP, int64_t(H) * KP, KP};
+    return hipGetLastError();
+}
+
+hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool is_bf16, hipStream_t st) {
+    const int VP = (r->width + 7) / 8 * 8;
+    const int64_t rows = int64_t(P) * T * H;
+    const dim3 grid(copy_grid(rows * VP));
+    if (is_bf16) hipLaunchKernelGGL(delta_copy_values_kernel<bf16>, grid, dim3(256), 0, st, *r, static_cast<bf16 *>(to), rows, T, H, VP);
+    else hipLaunchKernelGGL(delta_copy_values_kernel<float>, grid, dim3(256), 0, st, *r, static_cast<float *>(to), rows, T, H, VP);
+    *r = {to, int64_t(T) * H * VP, int64_t(H) * VP, VP, VP};
+    return hipGetLastError();
+}
+
 size_t delta_mats_bytes(int K, bool is_bf16, bool backward) {
     const bool three = backward || !is_bf16;
-    if (delta_chunk(K) == 64) return three ? sizeof(ChunkMats<64, 3>) : sizeof(ChunkMats<64, 2>);
+    if (delta_chunk(K, is_bf16) == 64) return three ? sizeof(ChunkMats<64, 3>) : sizeof(ChunkMats<64, 2>);
     return three ? sizeof(ChunkMats<32, 3>) : sizeof(ChunkMats<32, 2>);
 }
 

@@ -19,6 +19,9 @@ int check_delta(const sdm_delta_shape *s) {
         return fail(SDM_ERR_RANGE, "head_dim must be <= 256 and value_dim <= 65536, got %d and %d", s->head_dim, s->value_dim);
     const int64_t heads = int64_t(s->streams) * s->value_heads;
     if (heads >= 1 << 24) return fail(SDM_ERR_RANGE, "streams * value_heads (%lld) must be below 2^24", (long long)heads);
+    if (int64_t(s->key_heads) * s->head_dim >= kDeltaMaxStride || int64_t(s->value_heads) * s->value_dim >= kDeltaMaxStride)
+        return fail(SDM_ERR_RANGE, "a token's rows must be below 2^24 elements: %d x %d and %d x %d", s->key_heads, s->head_dim,
+                    s->value_heads, s->value_dim);
     if (s->tokens > (1 << 30) || heads * (int64_t(s->tokens) / 16 + 1) >= int64_t(0x7fffffff) ||
         heads * ((s->value_dim + 15) / 16) >= int64_t(0x7fffffff))
         return fail(SDM_ERR_RANGE, "%d tokens of %lld heads are too many", s->tokens, (long long)heads);
@@ -43,24 +46,33 @@ int check_delta_inputs(const sdm_delta_shape *s, const sdm_rows *q, const sdm_ro
         if (!aligned(rows[i]->data, es)) return fail(SDM_ERR_ALIGN, "%s must be aligned to its element size", names[i]);
         if (rows[i]->stream < 0 || rows[i]->token < 0 || rows[i]->head < 0)
             return fail(SDM_ERR_SHAPE, "%s: strides must be >= 0", names[i]);
+        if (rows[i]->token >= kDeltaMaxStride) return fail(SDM_ERR_RANGE, "%s: the token stride must be below 2^24", names[i]);
     }
     if (s->tokens > 0 && (!beta || !log_decay)) return fail(SDM_ERR_NULL, "beta and log_decay must not be NULL");
     const void *f[] = {beta, log_decay, state, valid};
     for (const void *x : f)
         if (!aligned(x, 4)) return fail(SDM_ERR_ALIGN, "float32 and int32 arrays must be 4-byte aligned");
-    a->q = {q->data, q->stream, q->token, q->head};
-    a->k = {k->data, k->stream, k->token, k->head};
-    a->v = {v->data, v->stream, v->token, v->head};
+    a->q = {q->data, q->stream, q->token, q->head, s->head_dim};
+    a->k = {k->data, k->stream, k->token, k->head, s->head_dim};
+    a->v = {v->data, v->stream, v->token, v->head, s->value_dim};
     a->beta = beta; a->g = log_decay; a->state = state; a->valid = valid;
     a->P = s->streams; a->T = s->tokens; a->Hk = s->key_heads; a->Hv = s->value_heads;
     a->K = s->head_dim; a->V = s->value_dim; a->scale = s->scale;
     return SDM_OK;
 }
 
-// Lays the workspace out from `base` (NULL: only its size).
-size_t layout(const sdm_delta_shape *s, bool backward, void *base, DeltaWs *ws) {
-    const size_t C = size_t(delta_chunk(s->head_dim)), Nt = (size_t(s->tokens) + C - 1) / C;
-    const size_t n = size_t(s->streams) * size_t(s->value_heads) * Nt;
+// The workspace, and in it the room for copies of q, k, v and the readings' gradient.
+struct Layout {
+    DeltaWs ws;
+    void *q, *k, *v, *go;
+    size_t bytes;
+};
+
+// From `base` on (NULL: only the size counts).
+Layout layout(const sdm_delta_shape *s, bool backward, void *base) {
+    const bool b16 = s->dtype == SDM_BF16;
+    const size_t C = size_t(delta_chunk(s->head_dim, b16)), Nt = (size_t(s->tokens) + C - 1) / C;
+    const size_t n = size_t(s->streams) * size_t(s->value_heads) * Nt, rows = size_t(s->streams) * size_t(s->tokens);
     const size_t VP = (size_t(s->value_dim) + 15) / 16 * 16, KP = size_t(delta_kp(s->head_dim));
     char *p = static_cast<char *>(base);
     size_t at = 0;
@@ -69,28 +81,55 @@ size_t layout(const sdm_delta_shape *s, bool backward, void *base, DeltaWs *ws) 
         at += align256(bytes);
         return x;
     };
-    DeltaWs w{};
-    w.Nt = int32_t(Nt);
-    w.backward = backward;
-    w.mats = reinterpret_cast<unsigned char *>(take(n * delta_mats_bytes(s->head_dim, s->dtype == SDM_BF16, backward)));
+    auto floats = [&](size_t count) { return reinterpret_cast<float *>(take(count * 4)); };
+    Layout l{};
+    l.ws.Nt = int32_t(Nt);
+    l.ws.backward = backward;
+    l.ws.mats = reinterpret_cast<unsigned char *>(take(n * delta_mats_bytes(s->head_dim, b16, backward)));
     if (backward) {
-        w.U = reinterpret_cast<float *>(take(n * C * VP * 4));
-        w.Y = reinterpret_cast<float *>(take(n * C * VP * 4));
-        w.S = reinterpret_cast<float *>(take(n * KP * VP * 4));
-        w.dS = reinterpret_cast<float *>(take(n * KP * VP * 4));
+        l.ws.U = floats(n * C * VP);
+        l.ws.Y = floats(n * C * VP);
+        l.ws.S = floats(n * KP * VP);
+        l.ws.dS = floats(n * KP * VP);
     }
-    if (ws) *ws = w;
-    return at < 256 ? 256 : at;
+    const size_t keys = rows * size_t(s->key_heads) * KP * (b16 ? 2 : 6);
+    const size_t values = rows * size_t(s->value_heads) * ((size_t(s->value_dim) + 7) / 8 * 8) * (b16 ? 2 : 4);
+    l.q = take(keys);
+    l.k = take(keys);
+    l.v = take(values);
+    if (backward) l.go = take(values);
+    l.bytes = at < 256 ? 256 : at;
+    return l;
 }
 
-int take_workspace(const sdm_delta_shape *s, bool backward, const sdm_exec *exec, DeltaWs *ws) {
-    const size_t need = layout(s, backward, nullptr, nullptr);
+// Checks the workspace and makes the rows regular (go: NULL in the forward).
+int take_workspace(const sdm_delta_shape *s, DeltaArgs *a, Rows *go, const sdm_exec *exec, DeltaWs *ws) {
+    const size_t need = layout(s, go != nullptr, nullptr).bytes;
     if (!exec->workspace || exec->workspace_bytes < need)
         return fail(SDM_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu bytes needed",
                     exec->workspace ? exec->workspace_bytes : size_t(0), need);
     if (!aligned(exec->workspace, 256)) return fail(SDM_ERR_ALIGN, "workspace must be 256-byte aligned");
-    layout(s, backward, exec->workspace, ws);
-    return SDM_OK;
+    int cus = 0;
+    const int rc = device_cus(&cus);
+    if (rc) return rc;
+    const Layout l = layout(s, go != nullptr, exec->workspace);
+    *ws = l.ws;
+    if (a->T == 0) return SDM_OK;
+    const bool b16 = s->dtype == SDM_BF16;
+    const hipStream_t st = static_cast<hipStream_t>(exec->stream);
+    auto keys = [&](const Rows &r, KeyRows *k, void *to) {
+        if (!delta_regular_keys(r, b16)) return launch_delta_copy_keys(r, k, to, a->P, a->T, a->Hk, b16, st);
+        *k = {static_cast<const bf16 *>(r.data), 0, r.sp, r.st, r.sh};
+        return hipSuccess;
+    };
+    auto values = [&](Rows *r, void *to) {
+        return delta_regular_values(*r, b16) ? hipSuccess : launch_delta_copy_values(r, to, a->P, a->T, a->Hv, b16, st);
+    };
+    hipError_t e = keys(a->q, &a->qq, l.q);
+    if (e == hipSuccess) e = keys(a->k, &a->kk, l.k);
+    if (e == hipSuccess) e = values(&a->v, l.v);
+    if (e == hipSuccess && go) e = values(go, l.go);
+    return e == hipSuccess ? SDM_OK : hip_fail(e, "gated delta copy launch");
 }
 
 }  // namespace
@@ -99,7 +138,7 @@ extern "C" {
 
 size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *s, int32_t backward) {
     if (check_delta(s) != SDM_OK) return 0;
-    return layout(s, backward != 0, nullptr, nullptr);
+    return layout(s, backward != 0, nullptr).bytes;
 }
 
 int sdm_gated_delta_fwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
@@ -116,9 +155,7 @@ int sdm_gated_delta_fwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_r
     if (state && state_out && state != state_out && overlap(state, state_out, bytes))
         return fail(SDM_ERR_SHAPE, "state_out overlaps state without being it");
     DeltaWs ws{};
-    if ((rc = take_workspace(s, false, exec, &ws))) return rc;
-    int cus = 0;
-    if ((rc = device_cus(&cus))) return rc;
+    if ((rc = take_workspace(s, &a, nullptr, exec, &ws))) return rc;
     a.state_out = state_out;
     a.out = out;
     const hipError_t e = launch_delta_fwd(a, ws, s->dtype == SDM_BF16, static_cast<hipStream_t>(exec->stream));
@@ -173,10 +210,9 @@ int sdm_gated_delta_bwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_r
                          (grad_state_out && grad_state_out != grads->state && overlap(grad_state_out, grads->state, bytes))))
         return fail(SDM_ERR_SHAPE, "the state's gradient overlaps an input");
     DeltaWs ws{};
-    if ((rc = take_workspace(s, true, exec, &ws))) return rc;
-    int cus = 0;
-    if ((rc = device_cus(&cus))) return rc;
-    const DeltaGrads g{grad_out, grad_state_out, grads->q, grads->k, grads->v, grads->beta, grads->log_decay, grads->state};
+    Rows go{grad_out, int64_t(a.T) * a.Hv * a.V, int64_t(a.Hv) * a.V, a.V, a.V};
+    if ((rc = take_workspace(s, &a, &go, exec, &ws))) return rc;
+    const DeltaGrads g{go, grad_state_out, grads->q, grads->k, grads->v, grads->beta, grads->log_decay, grads->state};
     const hipError_t e = launch_delta_bwd(a, ws, g, s->dtype == SDM_BF16, static_cast<hipStream_t>(exec->stream));
     return e == hipSuccess ? SDM_OK : hip_fail(e, "gated delta backward launch");
 }

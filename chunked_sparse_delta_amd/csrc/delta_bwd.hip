@@ -24,17 +24,12 @@ namespace sdm {
 
 namespace {
 
-// The readings' gradient as rows.
-__device__ __forceinline__ Rows grad_rows(const DeltaArgs &a, const DeltaGrads &d) {
-    return {d.go, int64_t(a.T) * a.Hv * a.V, int64_t(a.Hv) * a.V, a.V};
-}
-
 template <typename T, int C, int KP>
-__global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void delta_back_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
     constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32;
     using W = Walk<T, C, KP, 3, true>;
     extern __shared__ __align__(16) unsigned char raw[];
-    typename W::Lds &s = *reinterpret_cast<typename W::Lds *>(raw);
+    typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
     const int slice = blockIdx.x % slices, ph = blockIdx.x / slices, h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lc = lane & 15, lg = lane >> 4;
@@ -45,15 +40,12 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, DeltaWs ws
     const int64_t os = int64_t(a.Hv) * a.V;
     dt4 S[KB][2];
     load_state<KB>(S, d.gstate, ph, a.K, a.V, col);
-    W w(a, ws, p, h, hk, ph, cg, grad_rows(a, d), h);
-    if (Nc > 0) {
-        w.load(Nc - 1, n);
-        w.store(s, Nc - 1, n);
-        __syncthreads();
-    }
-    for (int c = Nc - 1; c >= 0; --c) {
+    const W w(a, ws, p, h, hk, ph, cg, d.go, n);
+    w.begin(bufs, Nc - 1);
+    for (int c = Nc - 1, turn = 0; c >= 0; --c, ++turn) {
+        const typename W::Lds &s = bufs[turn & (W::kBufs - 1)];
         const int t0 = c * C;
-        if (c > 0) w.load(c - 1, n);
+        w.ahead(bufs, turn, c - 1);
         const int64_t nc = int64_t(ph) * ws.Nt + c;
         save_blocks<KB>(ws.dS, nc, VG, cg, S);
         const Gates<C> &g = s.m.g;
@@ -72,6 +64,7 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, DeltaWs ws
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 o[tb][e] = w.value(s, tb, e);
+                if (!in) o[tb][e] = dt4{};
                 x[tb][e] *= *reinterpret_cast<const dt4 *>(g.eL + tb * 32 + lg * 8 + e * 4);
             }
 #pragma unroll
@@ -94,6 +87,7 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, DeltaWs ws
                     Y[tb][e] = mma<3>(read_cols<3>(s.m.X[0][ib + tb], kTri<C> * kBlk, e), fu, Y[tb][e]);
         }
         save_blocks<TB>(ws.Y, nc, VG, cg, Y);
+        dt4 v[TB][2];
         const float last = g.last;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
@@ -107,10 +101,9 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, DeltaWs ws
                 const dt4 b = *reinterpret_cast<const dt4 *>(g.beta + t), eG = *reinterpret_cast<const dt4 *>(g.eG + t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float y = b[i] * Y[tb][e][i];
-                    if (in && t0 + t + i < n) dv[(t0 + t + i) * os] = from_f32<T>(y);
+                    v[tb][e][i] = b[i] * Y[tb][e][i];
                     o[tb][e][i] *= a.scale * eG[i];
-                    Y[tb][e][i] = -eG[i] * y;
+                    Y[tb][e][i] = -eG[i] * v[tb][e][i];
                 }
             }
             const Frag<3> fo = split<3>(o[tb][0], o[tb][1]), fy = split<3>(Y[tb][0], Y[tb][1]);
@@ -122,11 +115,8 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a, DeltaWs ws
                     S[kb][e] = mma<3>(read_cols<NI>(s.k[0][tb][kb], W::kStride, e), fy, S[kb][e]);
                 }
         }
-        if (c > 0) {
-            __syncthreads();
-            w.store(s, c - 1, n);
-            __syncthreads();
-        }
+        put_columns<T, TB>(dv + t0 * os, os, n - t0, in, v);
+        w.turn(bufs, c - 1);
     }
     for (int t = n + lg; t < a.T; t += 4)
         if (in) dv[t * os] = from_f32<T>(0.0f);
@@ -184,7 +174,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lc = lane & 15, lg = lane >> 4;
     const int tb = wv % NT / 2, ta = wv % 2, kb0 = wv / NT * KW;     // this wavefront's tokens and blocks of dq, dk
     const int tok = tb * 32 + block_row(lc, ta);                    // the lane's token
-    const Rows gr = grad_rows(a, d);
+    const Rows &gr = d.go;
     dt4 aq[KW][2] = {}, ak[KW][2] = {};
     for (int hh = 0; live > 0 && hh < group; ++hh) {
         const int h = hk * group + hh;
@@ -199,11 +189,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
         float ub[8] = {};
         for (int vg = 0; vg < VG; vg += 2) {
             for (int i = tid; i < C * 4; i += 256) {      // eights of do
-                const int t = i / 4, e = vg * 16 + i % 4 * 8, ce = min(e, a.V - 1);
-                Eight<T> x;
-                x.load(go + int64_t(min(t, live - 1)) * gr.st, ce, a.V);
-                x.fix(ce, a.V, t < live && e < a.V);
-                const Frag<NI> f = x.pieces();
+                const int t = i / 4, e = vg * 16 + i % 4 * 8;
+                Frag<NI> f = load_pieces(go + min(t, live - 1) * gr.st + min(e, gr.width - 8));
+                if (t >= live || e >= gr.width) clear(f);
 #pragma unroll
                 for (int n = 0; n < NI; ++n) *reinterpret_cast<db8 *>(s.go[n][t / 32] + block_at(t % 32, i % 4)) = f.p[n];
             }
@@ -289,17 +277,17 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
         for (int m = 32; m > 0; m >>= 1) cc += __shfl_xor(cc, m, 64);
         if (lane == 0) s.cs[wv] = cc;
         {
-            const T *kp = static_cast<const T *>(a.k.data) + p * a.k.sp + hk * a.k.sh + t0 * a.k.st;
-            const T *qp = static_cast<const T *>(a.q.data) + p * a.q.sp + hk * a.q.sh + t0 * a.q.st;
+            const bf16 *kp = a.kk.data + p * a.kk.sp + hk * a.kk.sh + t0 * a.kk.st;
+            const bf16 *qp = a.qq.data + p * a.qq.sp + hk * a.qq.sh + t0 * a.qq.st;
 #pragma unroll
             for (int i = tid; i < C * KP / 8; i += 256) {
                 const int b = i / 128, r = i % 128 / 4, t = b / KB * 32 + r, e = b % KB * 32 + i % 4 * 8, at = b * kBlk + block_at(r, i % 4);
-                Eight<T> x, y;
-                x.load(kp + min(t, live - 1) * a.k.st, e, a.K);
-                y.load(qp + min(t, live - 1) * a.q.st, e, a.K);
-                x.fix(e, a.K, t < live);
-                y.fix(e, a.K, t < live);
-                const Frag<NI> fk = x.pieces(), fq = y.pieces();
+                Frag<NI> fk = load_keys<NI>(kp + (min(t, live - 1) * int(a.kk.st) + e), a.kk.plane);
+                Frag<NI> fq = load_keys<NI>(qp + (min(t, live - 1) * int(a.qq.st) + e), a.qq.plane);
+                if (t >= live) {
+                    clear(fk);
+                    clear(fq);
+                }
 #pragma unroll
                 for (int n = 0; n < NI; ++n) {
                     *reinterpret_cast<db8 *>(&s.k[n][0][0][0] + at) = fk.p[n];
@@ -456,7 +444,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
 template <typename T, int C, int KP>
 hipError_t bwd_go(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, hipStream_t st) {
     hipLaunchKernelGGL((delta_back_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hv * ((a.V + 63) / 64))), dim3(256),
-                       sizeof(typename Walk<T, C, KP, 3, true>::Lds), st, a, ws, d);
+                       (Walk<T, C, KP, 3, true>::kLds), st, a, ws, d);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || ws.Nt == 0) return e;
     hipLaunchKernelGGL((delta_grad_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hk * ws.Nt)), dim3(256),
@@ -466,13 +454,13 @@ hipError_t bwd_go(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, hi
 template <typename T>
 hipError_t bwd_pick(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, hipStream_t st) {
     switch (delta_kp(a.K)) {
-        case 64: return bwd_go<T, 64, 64>(a, ws, d, st);
-        case 128: return bwd_go<T, 64, 128>(a, ws, d, st);
+        case 64: return bwd_go<T, kChunk<T>, 64>(a, ws, d, st);
+        case 128: return bwd_go<T, kChunk<T>, 128>(a, ws, d, st);
         default: return bwd_go<T, 32, 256>(a, ws, d, st);
     }
 }
 template <typename T, int C, int KP> hipError_t bwd_attr() {
-    constexpr size_t lw = sizeof(typename Walk<T, C, KP, 3, true>::Lds), lg = sizeof(GradLds<T, C, KP>);
+    constexpr size_t lw = Walk<T, C, KP, 3, true>::kLds, lg = sizeof(GradLds<T, C, KP>);
     static_assert(lw <= kDeltaMaxLds && lg <= kDeltaMaxLds, "LDS of a workgroup");
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_back_kernel<T, C, KP>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lw);
@@ -480,8 +468,8 @@ template <typename T, int C, int KP> hipError_t bwd_attr() {
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, lg);
 }
 template <typename T> hipError_t bwd_attrs() {
-    hipError_t e = bwd_attr<T, 64, 64>();
-    if (e == hipSuccess) e = bwd_attr<T, 64, 128>();
+    hipError_t e = bwd_attr<T, kChunk<T>, 64>();
+    if (e == hipSuccess) e = bwd_attr<T, kChunk<T>, 128>();
     if (e == hipSuccess) e = bwd_attr<T, 32, 256>();
     return e;
 }

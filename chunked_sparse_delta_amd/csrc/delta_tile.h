@@ -37,10 +37,30 @@ template <int N> struct Frag {
     db8 p[N];
 };
 
+// LDS accesses keep their side of this point (other instructions may cross): the operands of the
+// products to come are read before the products at hand, whose 16 cycles each hide the way to LDS.
+__device__ __forceinline__ void lds_point() { __builtin_amdgcn_sched_barrier(0x7F); }
+
+// x less its first 8 bits, for both halves of a pair `w` of such cuts, as one instruction each: w . (-1, 0) + x and
+// w . (0, -1) + x, which are exact. (The constants stay in registers: as an inline constant -1.0 the second one
+// would be taken for a pair of another type.)
+struct CutRest {
+    uint32_t lo, hi;
+    __device__ __forceinline__ CutRest() {
+        asm("s_mov_b32 %0, 0xbf80" : "=s"(lo));
+        asm("s_mov_b32 %0, 0xbf800000" : "=s"(hi));
+    }
+    __device__ __forceinline__ float operator()(uint32_t w, uint32_t which, float x) const {
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, w), __builtin_bit_cast(b2, which), x, false);
+    }
+};
+
 // Eight float32 values as N pieces.
 template <int N> __device__ __forceinline__ Frag<N> split(dt4 a, dt4 b) {
     Frag<N> f;
     float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    const CutRest rest;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         du4 w;
@@ -50,10 +70,9 @@ template <int N> __device__ __forceinline__ Frag<N> split(dt4 a, dt4 b) {
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t u = __float_as_uint(x[2 * j]), v = __float_as_uint(x[2 * j + 1]);
-                w[j] = __builtin_amdgcn_perm(v, u, 0x07060302);   // the high halves, u's low
-                x[2 * j] -= __uint_as_float(u & 0xFFFF0000u);
-                x[2 * j + 1] -= __uint_as_float(v & 0xFFFF0000u);
+                w[j] = __builtin_amdgcn_perm(__float_as_uint(x[2 * j + 1]), __float_as_uint(x[2 * j]), 0x07060302);   // the high halves
+                x[2 * j] = rest(w[j], rest.lo, x[2 * j]);
+                x[2 * j + 1] = rest(w[j], rest.hi, x[2 * j + 1]);
             }
         }
         f.p[i] = __builtin_bit_cast(db8, w);
@@ -69,6 +88,17 @@ template <int ORD, int NA, int NB> __device__ __forceinline__ dt4 mma(const Frag
         for (int j = NB - 1; j >= 0; --j)
             if (i + j < ORD) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], acc, 0, 0, 0);
     return acc;
+}
+
+__device__ __forceinline__ dt4 mma1(db8 a, db8 b, dt4 acc) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0); }
+// The same products, the smallest first, each for all the caller's blocks in turn (neighbouring instructions then do not
+// wait for each other).
+template <int ORD, int NA, int NB, typename F> __device__ __forceinline__ void each_product(F f) {
+#pragma unroll
+    for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = NB - 1; j >= 0; --j)
+            if (i + j < ORD) f(i, j);
 }
 
 // A operand: the rows of tile a of the block at `blk`; N pieces `stride` bytes apart.
@@ -97,103 +127,23 @@ template <int N> __device__ __forceinline__ Frag<N> read_cols(const unsigned cha
     return f;
 }
 
-// Eight elements of a row of `width` from column c on, zeros past its end, as one 16-byte load
-// (two for float32) at any element address: where the row ends inside it, the load starts at the row's last eight
-// elements and is shifted. The caller gives in = false for rows that are not there (p then has to be readable all the
-// same). Only rows narrower than eight elements are read one by one.
-template <typename T> struct Eight;
-template <> struct Eight<bf16> {
-    du4 x;
-    __device__ __forceinline__ void load(const bf16 *p, int c, int width) {
-        typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
-        if (width >= 8) {
-            const raw y = *reinterpret_cast<const raw *>(p + min(c, width - 8));
-            x = du4{y[0], y[1], y[2], y[3]};
-        } else {
+// Eight elements as pieces.
+__device__ __forceinline__ Frag<1> load_pieces(const bf16 *p) { return {{*reinterpret_cast<const db8 *>(p)}}; }
+__device__ __forceinline__ Frag<3> load_pieces(const float *p) {
+    return split<3>(*reinterpret_cast<const dt4 *>(p), *reinterpret_cast<const dt4 *>(p + 4));
+}
+// ... and those of a row of q or k.
+template <int N> __device__ __forceinline__ Frag<N> load_keys(const bf16 *p, int64_t plane) {
+    Frag<N> f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t lo = c + 2 * j < width ? p[c + 2 * j].bits : 0u;
-                const uint32_t hi = c + 2 * j + 1 < width ? p[c + 2 * j + 1].bits : 0u;
-                x[j] = lo | hi << 16;
-            }
-        }
-    }
-    // After the load: the shift, and zeros where there is nothing.
-    __device__ __forceinline__ void fix(int c, int width, bool in) {
-        if (width & 7) {
-            if (width >= 8) {
-                const int s = max(c - (width - 8), 0);       // elements to shift out
-                uint64_t lo = uint64_t(x[1]) << 32 | x[0], hi = uint64_t(x[3]) << 32 | x[2];
-                if (s >= 4) {
-                    lo = hi;
-                    hi = 0;
-                }
-                const int b = (s & 3) * 16;
-                if (b) {
-                    lo = lo >> b | hi << (64 - b);
-                    hi >>= b;
-                }
-                x = du4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
-            }
-        }
-        if (!in || c >= width) x = du4{0, 0, 0, 0};
-    }
-    __device__ __forceinline__ Frag<1> pieces() const { return {{__builtin_bit_cast(db8, x)}}; }
-    __device__ __forceinline__ void floats(dt4 &a, dt4 &b) const {
+    for (int i = 0; i < N; ++i) f.p[i] = *reinterpret_cast<const db8 *>(p + i * plane);
+    return f;
+}
+template <int N> __device__ __forceinline__ void clear(Frag<N> &f) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float l = __uint_as_float(x[j] << 16), h = __uint_as_float(x[j] & 0xFFFF0000u);
-            if (j < 2) {
-                a[2 * j] = l;
-                a[2 * j + 1] = h;
-            } else {
-                b[2 * j - 4] = l;
-                b[2 * j - 3] = h;
-            }
-        }
-    }
-};
-template <> struct Eight<float> {
-    dt4 a, b;
-    __device__ __forceinline__ void load(const float *p, int c, int width) {
-        typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
-        if (width >= 8) {
-            const float *s = p + min(c, width - 8);
-            const raw y = *reinterpret_cast<const raw *>(s), z = *reinterpret_cast<const raw *>(s + 4);
-            a = dt4{y[0], y[1], y[2], y[3]};
-            b = dt4{z[0], z[1], z[2], z[3]};
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = c + j < width ? p[c + j] : 0.0f;
-                if (j < 4) a[j] = v;
-                else b[j - 4] = v;
-            }
-        }
-    }
-    __device__ __forceinline__ void fix(int c, int width, bool in) {
-        if ((width & 7) && width >= 8) {
-            int s = max(c - (width - 8), 0);
-#pragma unroll
-            for (int bit = 4; bit; bit >>= 1)
-                if (s & bit) {
-                    float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float y = j + bit < 8 ? v[j + bit] : 0.0f;
-                        if (j < 4) a[j] = y;
-                        else b[j - 4] = y;
-                    }
-                }
-        }
-        if (!in || c >= width) a = b = dt4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    __device__ __forceinline__ Frag<3> pieces() const { return split<3>(a, b); }
-    __device__ __forceinline__ void floats(dt4 &x, dt4 &y) const {
-        x = a;
-        y = b;
-    }
-};
+    for (int i = 0; i < N; ++i) f.p[i] = __builtin_bit_cast(db8, du4{0, 0, 0, 0});
+}
+
 // Eight neighbours of an output row of which `left` are inside it: one 16-byte store (two for float32) at any element
 // address where all are.
 __device__ __forceinline__ void put_eight(bf16 *p, int left, dt4 a, dt4 b) {
@@ -219,13 +169,16 @@ __device__ __forceinline__ void put_eight(float *p, int left, dt4 a, dt4 b) {
 }
 // Pieces of an input element.
 template <typename T> constexpr int kPieces = sizeof(T) == 2 ? 1 : 3;
+// Tokens of a chunk where head_dim is at most 128 (32 above it): two chunks' operands in LDS at once.
+template <typename T> constexpr int kChunk = sizeof(T) == 2 ? 64 : 32;
 
 // The beta that the backward computes U with: its U / beta is the write error for every beta.
 __device__ __forceinline__ float delta_beta_safe(float b) { return fabsf(b) < 1e-20f ? 1e-20f : b; }
 
-// A chunk's gates, as delta_prep_kernel leaves them: beta, exp(G), exp(G_last - G) of every token, exp(G_last).
+// A chunk's gates, as delta_prep_kernel leaves them: beta, exp(G), exp(G_last - G) of every token (0 for padding tokens,
+// whose rows the kernels then need not clear), exp(G_last).
 template <int C> struct Gates {
-    float beta[C], eG[C], eL[C], last, pad[C == 64 ? 63 : 31];
+    float beta[C], eG[C], eL[C], last, pad[255 - 3 * C];
 };
 
 // What the prep kernel leaves of a chunk for the kernels that walk it: the lower 32 x 32
@@ -236,6 +189,7 @@ template <int C, int NP> struct ChunkMats {
     unsigned char P[NP][kTri<C>][kBlk];
     Gates<C> g;
 };
+static_assert(sizeof(ChunkMats<64, 2>) % 1024 == 0 && sizeof(ChunkMats<32, 3>) % 1024 == 0, "copied by the kilobyte");
 // Pieces of P: the forward's readings are all that P goes into there, and two are enough for those in bfloat16.
 template <typename T> constexpr int kPPieces(bool backward) { return backward || sizeof(T) == 4 ? 3 : 2; }
 

@@ -1,5 +1,5 @@
-// What the kernels that walk a sequence's chunks share: the chunk's operands in LDS, loaded into
-// registers a chunk ahead, and the state in accumulators.
+// What the kernels that walk a sequence's chunks share: the chunk's operands in LDS, copied there a
+// chunk ahead, and the state in accumulators.
 #pragma once
 
 #include "delta_tile.h"
@@ -8,91 +8,101 @@ namespace sdm {
 
 constexpr size_t kDeltaMaxLds = 160 * 1024 - 256;
 
+// A wavefront's 1 KB from per-lane addresses to consecutive LDS, without a register between. Written out, since the
+// compiler makes any later LDS read wait for its own form of it: Walk::arrive waits for these. (It has no result register,
+// and what the compiler waits for by count comes no later for more being on its way.)
+__device__ __forceinline__ void copy_to_lds(const void *src, const void *dst) {
+    const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)(dst)));
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"(src), "s"(__builtin_amdgcn_readfirstlane(at)) : "memory");
+}
+
 // T: the inputs' type; NP: pieces of P; Q: q is wanted too.
 template <typename T, int C, int KP, int NP, bool Q> struct Walk {
     static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32;
     static constexpr int kStride = TB * KB * kBlk;              // between the pieces of k (and of q)
-    static constexpr int KS = C * KP / 8 / 256;                 // eights of k per thread
-    static constexpr int MS = (sizeof(ChunkMats<C, NP>) / 16 + 255) / 256;
-    static constexpr int VS = C * 2 / 64;                       // eights of the wavefront's 16 columns of v per lane
+    static constexpr int KS = kStride / 1024 / 4;               // kilobytes of a piece of k per wavefront
+    static constexpr int MS = (sizeof(ChunkMats<C, NP>) / 1024 + 3) / 4;
+    static constexpr int RS = 16 * sizeof(T) / 16;              // 16-byte pieces of a row of v's 16 columns
+    static constexpr int VS = C * RS / 64;
     struct Lds {
         unsigned char k[NI][TB][KB][kBlk];
         unsigned char q[Q ? NI : 0][TB][KB][kBlk];
         ChunkMats<C, NP> m;
         T v[4][C][16];
     };
-    const T *kp, *qp, *vp;
+    static constexpr int kBufs = 2 * sizeof(Lds) <= kDeltaMaxLds ? 2 : 1;
+    static constexpr size_t kLds = kBufs * sizeof(Lds);
+    const bf16 *kp, *qp;
+    const T *vp;
     const unsigned char *mats;
-    int64_t ks, qs, vs;
-    int K, V, col0;
-    Eight<T> k[KS], q[Q ? KS : 1], v[VS];
-    du4 m[MS];
+    int64_t kplane, qplane, ks, qs, vs;
+    int col0, n, Nc;
 
     // Rows of `val` (v, or what takes its place) head vh; cg: the wavefront's group of 16 columns.
-    __device__ Walk(const DeltaArgs &a, const DeltaWs &ws, int p, int h, int hk, int ph, int cg, const Rows &val, int vh)
-        : kp(static_cast<const T *>(a.k.data) + p * a.k.sp + hk * a.k.sh),
-          qp(static_cast<const T *>(a.q.data) + p * a.q.sp + hk * a.q.sh),
-          vp(static_cast<const T *>(val.data) + p * val.sp + vh * val.sh),
-          mats(ws.mats + int64_t(ph) * ws.Nt * sizeof(ChunkMats<C, NP>)), ks(a.k.st), qs(a.q.st), vs(val.st), K(a.K), V(a.V),
-          col0(cg * 16) {}
-
-    // Rows past the last valid token are read from that token's place and put down as zeros.
-    __device__ __forceinline__ void load(int c, int n) {
-        const int t0 = c * C, top = n - 1 - t0, tid = threadIdx.x, lane = tid & 63;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            const int slot = tid + 256 * i, b = slot / 128, row = b / KB * 32 + slot % 128 / 4, d = b % KB * 32 + slot % 4 * 8;
-            const int64_t t = t0 + min(row, top);
-            k[i].load(kp + t * ks, d, K);
-            if constexpr (Q) q[i].load(qp + t * qs, d, K);
-        }
-#pragma unroll
-        for (int i = 0; i < VS; ++i) {
-            const int slot = lane + 64 * i;
-            v[i].load(vp + (t0 + min(slot / 2, top)) * vs, min(col0 + slot % 2 * 8, V - 1), V);
-        }
-        const unsigned char *src = mats + int64_t(c) * sizeof(ChunkMats<C, NP>);
-#pragma unroll
-        for (int i = 0; i < MS; ++i)
-            m[i] = *reinterpret_cast<const du4 *>(src + min(tid + 256 * i, int(sizeof(ChunkMats<C, NP>) / 16) - 1) * 16);
+    __device__ Walk(const DeltaArgs &a, const DeltaWs &ws, int p, int h, int hk, int ph, int cg, const Rows &val, int tokens)
+        : kp(a.kk.data + p * a.kk.sp + hk * a.kk.sh), qp(a.qq.data + p * a.qq.sp + hk * a.qq.sh),
+          vp(static_cast<const T *>(val.data) + p * val.sp + h * val.sh),
+          mats(ws.mats + int64_t(ph) * ws.Nt * sizeof(ChunkMats<C, NP>)), kplane(a.kk.plane), qplane(a.qq.plane), ks(a.kk.st),
+          qs(a.qq.st), vs(val.st), n(tokens), Nc((tokens + C - 1) / C) {
+        // columns past the row's end are read from its last ones: nothing that they reach is kept
+        const int piece = int(threadIdx.x) % RS * (16 / int(sizeof(T)));
+        col0 = min(cg * 16 + piece, val.width - 16 / int(sizeof(T)));
     }
-    __device__ __forceinline__ void store(Lds &s, int c, int n) {
-        const int top = n - 1 - c * C, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+
+    // Chunk c's operands, on their way to `s`. Rows past the last valid token are that token's: finite where it is, and met by
+    // gates of 0 everywhere.
+    __device__ __forceinline__ void load(Lds &s, int c) const {
+        const int t0 = c * C, top = n - 1 - t0, lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const bf16 *kc = kp + t0 * ks, *qc = qp + t0 * qs;
+        const T *vc = vp + t0 * vs;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
-            const int slot = tid + 256 * i, b = slot / 128, r = slot % 128 / 4, d = b % KB * 32 + slot % 4 * 8;
-            const bool in = b / KB * 32 + r <= top;
-            const int at = b * kBlk + block_at(r, slot % 4);
-            k[i].fix(d, K, in);
-            const Frag<NI> f = k[i].pieces();
+            const int slot = i * 256 + wv * 64 + lane, blk = slot / 128, r = slot % 128 / 4;
+            const int row = min(blk / KB * 32 + r, top), d = blk % KB * 32 + ((slot ^ (r >> 3)) & 3) * 8;
+            unsigned char *dk = &s.k[0][0][0][0] + (i * 256 + wv * 64) * 16;
 #pragma unroll
-            for (int e = 0; e < NI; ++e) *reinterpret_cast<db8 *>(&s.k[0][0][0][0] + e * kStride + at) = f.p[e];
+            for (int e = 0; e < NI; ++e) copy_to_lds(kc + e * kplane + (row * int(ks) + d), dk + e * kStride);
             if constexpr (Q) {
-                q[i].fix(d, K, in);
-                const Frag<NI> fq = q[i].pieces();
+                unsigned char *dq = &s.q[0][0][0][0] + (i * 256 + wv * 64) * 16;
 #pragma unroll
-                for (int e = 0; e < NI; ++e) *reinterpret_cast<db8 *>(&s.q[0][0][0][0] + e * kStride + at) = fq.p[e];
+                for (int e = 0; e < NI; ++e) copy_to_lds(qc + e * qplane + (row * int(qs) + d), dq + e * kStride);
             }
         }
 #pragma unroll
-        for (int i = 0; i < VS; ++i) {
-            const int slot = lane + 64 * i, d = col0 + slot % 2 * 8;
-            // the load was made at min(d, V - 1): a chunk that starts past the row's end holds nothing
-            v[i].fix(min(d, V - 1), V, slot / 2 <= top && d < V);
-            T *at = &s.v[wv][slot / 2][slot % 2 * 8];
-            if constexpr (sizeof(T) == 2) *reinterpret_cast<du4 *>(at) = v[i].x;
-            else {
-                *reinterpret_cast<dt4 *>(at) = v[i].a;
-                *reinterpret_cast<dt4 *>(at + 4) = v[i].b;
-            }
-        }
+        for (int i = 0; i < VS; ++i)
+            copy_to_lds(vc + (min((lane + 64 * i) / RS, top) * int(vs) + col0), reinterpret_cast<unsigned char *>(&s.v[wv][0][0]) + i * 1024);
+        const unsigned char *src = mats + int64_t(c) * sizeof(ChunkMats<C, NP>) + lane * 16;
 #pragma unroll
         for (int i = 0; i < MS; ++i) {
-            const int slot = tid + 256 * i;
-            if (slot < int(sizeof(ChunkMats<C, NP>) / 16)) reinterpret_cast<du4 *>(&s.m)[slot] = m[i];
+            const int kb = wv + 4 * i;
+            if (kb < int(sizeof(ChunkMats<C, NP>) / 1024)) copy_to_lds(src + kb * 1024, reinterpret_cast<unsigned char *>(&s.m) + kb * 1024);
         }
     }
-    // Rows tb * 32 + 8 g + 4 e + i, i = 0..3, of the wavefront's columns of v, column lane & 15.
+    __device__ __forceinline__ bool has(int c) const { return c >= 0 && c < Nc; }
+    static __device__ __forceinline__ void arrive() {   // everything on its way is there, for every wavefront
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+        __syncthreads();
+    }
+    // LDS holds the current chunk's operands. With two buffers the next chunk's are on their way to the other one meanwhile.
+    __device__ __forceinline__ void begin(Lds *bufs, int c) const {
+        if (!has(c)) return;
+        load(bufs[0], c);
+        arrive();
+    }
+    // At the start of the i-th chunk taken: `next` is the chunk after it.
+    __device__ __forceinline__ void ahead(Lds *bufs, int i, int next) const {
+        if constexpr (kBufs == 2)
+            if (has(next)) load(bufs[(i + 1) & 1], next);
+    }
+    // At its end.
+    __device__ __forceinline__ void turn(Lds *bufs, int next) const {
+        if constexpr (kBufs == 1) {
+            __syncthreads();
+            if (has(next)) load(bufs[0], next);
+        }
+        arrive();
+    }
     __device__ __forceinline__ dt4 value(const Lds &s, int tb, int e) const {
         const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, i = lane & 15, t = tb * 32 + g * 8 + e * 4;
         dt4 x;
@@ -108,6 +118,42 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
         return x;
     }
 };
+
+// Column `lane & 15` of the wavefront's 16 columns of a chunk's rows t0.. of `out` (token stride os), of which `live` are there.
+template <typename T, int TB>
+__device__ __forceinline__ void put_columns(T *out, int64_t os, int live, bool in, const dt4 (&y)[TB][2]) {
+    const int lg = (threadIdx.x & 63) >> 4;
+    if (!in) return;
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = tb * 32 + lg * 8 + e * 4 + i;
+                if (t < live) out[t * os] = from_f32<T>(y[tb][e][i]);
+            }
+}
+// Four neighbours of an output row of which `left` are inside it.
+__device__ __forceinline__ void put_four(bf16 *p, int left, dt4 x) {
+    typedef uint32_t raw __attribute__((ext_vector_type(2), aligned(2)));
+    const raw w = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3])};
+    if (left >= 4) *reinterpret_cast<raw *>(p) = w;
+    else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) p[j].bits = uint16_t(w[j / 2] >> (j & 1 ? 16 : 0));
+    }
+}
+__device__ __forceinline__ void put_four(float *p, int left, dt4 x) {
+    typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
+    if (left >= 4) *reinterpret_cast<raw *>(p) = raw{x[0], x[1], x[2], x[3]};
+    else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) p[j] = x[j];
+    }
+}
 
 // The wavefront's 16 columns of a [K, V] state, zeros past its ends and where there is none.
 template <int KB> __device__ __forceinline__ void load_state(dt4 (&S)[KB][2], const float *state, int ph, int K, int V, int col) {

@@ -25,14 +25,14 @@ typedef struct {
     int32_t key_heads;    /* Hk >= 1 */
     int32_t value_heads;  /* Hv, a multiple of Hk; P * Hv < 2^24 */
     int32_t head_dim;     /* K in 1..256 */
-    int32_t value_dim;    /* V in 1..65536 */
+    int32_t value_dim;    /* V in 1..65536; Hk * K and Hv * V below 2^24 */
     int32_t dtype;        /* sdm_dtype of q, k, v, out and their gradients */
     float scale;
 } sdm_delta_shape;
 
 /* A device [P, T, heads, width] array whose rows of `width` elements are dense; strides in
- * elements, >= 0 (slices of one fused projection need no copy). Rows need their element's
- * alignment only. */
+ * elements, >= 0, the token's below 2^24 (slices of one fused projection need no copy). Rows
+ * need their element's alignment only. */
 typedef struct {
     const void *data;
     int64_t stream;
