@@ -88,6 +88,8 @@ def library_path() -> str:
 
 def _load():
     global _lib
+    if _lib is not None:   # set once, when every signature is declared
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):

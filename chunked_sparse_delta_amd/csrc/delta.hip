@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
 // operands of each group of products are read from LDS before the group ahead of it.
 // SAVE: keeps U and each chunk's start state for the backward, and gives no output.
 template <typename T, int C, int KP, bool SAVE>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void delta_state_kernel(DeltaArgs a, DeltaWs ws) {
+__global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, DeltaWs ws) {
     constexpr int NI = kPieces<T>, NP = kPPieces<T>(SAVE), KB = KP / 32, TB = C / 32, NTR = kTri<C>;
     constexpr int NS = NI == 1 ? 2 : 3;    // pieces of S and U that reach the readings only
     using W = Walk<T, C, KP, NP, !SAVE>;
@@ -173,25 +173,41 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
     const int slice = blockIdx.x % slices, ph = blockIdx.x / slices, h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lc = lane & 15, lg = lane >> 4;
-    const int cg = slice * 4 + wv, col = cg * 16 + lc;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lc = lane & 15, lg = lane >> 4;
+    const int cg = slice * 4 + (wv & 3), col = cg * 16 + lc;
     const bool in = col < a.V;
     const int n = delta_valid(a, p), Nc = (n + C - 1) / C;
+    if (wv >= 4) {
+        typename W::Bring w(a, ws, p, h, hk, ph, cg, a.v, n);
+        w.run(bufs, 0, 1, Nc);
+        return;
+    }
     const int oc = cg * 16 + lg * 4;   // readings come transposed: a lane holds four columns of the tokens block_row(lc, .)
-    T *out = static_cast<T *>(a.out) + (int64_t(p) * a.T * a.Hv + h) * a.V + oc;
-    const int64_t os = int64_t(a.Hv) * a.V;
+    T *out = static_cast<T *>(a.out) + (int64_t(p) * a.T * a.Hv + h) * a.V;
+    const int os = a.Hv * a.V;
     dt4 S[KB][2];
     load_state<KB>(S, a.state, ph, a.K, a.V, col);
-    const W w(a, ws, p, h, hk, ph, cg, a.v, n);
-    w.begin(bufs, 0);
+    W::begin();
     dt4 y[TB][2] = {};
+    const int left = a.V - oc;
     auto put = [&](int c) {
+        T *o = out + int64_t(c) * C * os;
+        const int live = n - c * C;
+        if (live >= C) {
+            if (left >= 4) {
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) put_four(o + ((tb * 32 + block_row(lc, e)) * os + oc), 4, y[tb][e]);
+                return;
+            }
+        }
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int t = c * C + tb * 32 + block_row(lc, e);
-                if (t < n && oc < a.V) put_four(out + t * os, a.V - oc, y[tb][e]);
+                const int t = tb * 32 + block_row(lc, e);
+                if (t < live && left > 0) put_four(o + (t * os + oc), left, y[tb][e]);
             }
     };
     Frag<3> fs[KB];
@@ -200,8 +216,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int c = 0; c < Nc; ++c) {
         const typename W::Lds &s = bufs[c & (W::kBufs - 1)];
         const Gates<C> &g = s.m.g;
-        if (!SAVE && c > 0) put(c - 1);    // late, so that no wait for what is on its way is a wait for these
-        w.ahead(bufs, c, c + 1);
+        if (!SAVE && c > 0) put(c - 1);
         // k S and q S
         Frag<NI> A[2][TB][2];
         auto rows_of = [&](Frag<NI>(&f)[TB][2], const unsigned char *m) {
@@ -218,7 +233,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = tb * 32 + lg * 8 + e * 4;
-                v[tb][e] = w.value(s, tb, e);
+                v[tb][e] = W::value(s, tb, e);
                 if (SAVE && !in) v[tb][e] = dt4{};
                 b[tb][e] = *reinterpret_cast<const dt4 *>(g.beta + t);
                 eG[tb][e] = *reinterpret_cast<const dt4 *>(g.eG + t);
@@ -351,12 +366,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         }
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
-        w.turn(bufs, c + 1);
+        W::turn();
     }
     if constexpr (!SAVE) {
         if (Nc > 0) put(Nc - 1);
         for (int t = n + lc; t < a.T; t += 16)
-            if (oc < a.V) put_four(out + t * os, a.V - oc, dt4{});
+            if (left > 0) put_four(out + (int64_t(t) * os + oc), left, dt4{});
         store_state<KB>(S, a.state_out, ph, a.K, a.V, col);
     }
 }
@@ -397,9 +412,9 @@ template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const
         if (e != hipSuccess) return e;
     }
     if (ws.backward)
-        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, true>), grid, dim3(256), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
+        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, true>), grid, dim3(kWalkThreads), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
     else
-        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, false>), grid, dim3(256), (Walk<T, C, KP, N0, true>::kLds), st, a, ws);
+        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, false>), grid, dim3(kWalkThreads), (Walk<T, C, KP, N0, true>::kLds), st, a, ws);
     return hipGetLastError();
 }
 template <typename T> hipError_t fwd_pick(const DeltaArgs &a, const DeltaWs &ws, hipStream_t st) {

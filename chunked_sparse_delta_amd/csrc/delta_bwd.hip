@@ -25,98 +25,173 @@ namespace sdm {
 namespace {
 
 template <typename T, int C, int KP>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void delta_back_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
-    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32;
+__global__ __launch_bounds__(kWalkThreads) void delta_back_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
+    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NTR = kTri<C>;
     using W = Walk<T, C, KP, 3, true>;
     extern __shared__ __align__(16) unsigned char raw[];
     typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
     const int slice = blockIdx.x % slices, ph = blockIdx.x / slices, h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, lc = lane & 15, lg = lane >> 4;
-    const int cg = slice * 4 + wv, col = cg * 16 + lc;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lc = lane & 15, lg = lane >> 4;
+    const int cg = slice * 4 + (wv & 3), col = cg * 16 + lc;
     const bool in = col < a.V;
     const int n = delta_valid(a, p), Nc = (n + C - 1) / C;
+    if (wv >= 4) {
+        typename W::Bring w(a, ws, p, h, hk, ph, cg, d.go, n);
+        w.run(bufs, Nc - 1, -1, Nc);
+        return;
+    }
     T *dv = static_cast<T *>(d.v) + (int64_t(p) * a.T * a.Hv + h) * a.V + col;
     const int64_t os = int64_t(a.Hv) * a.V;
     dt4 S[KB][2];
     load_state<KB>(S, d.gstate, ph, a.K, a.V, col);
-    const W w(a, ws, p, h, hk, ph, cg, d.go, n);
-    w.begin(bufs, Nc - 1);
+    W::begin();
+    Frag<3> fs[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
     for (int c = Nc - 1, turn = 0; c >= 0; --c, ++turn) {
         const typename W::Lds &s = bufs[turn & (W::kBufs - 1)];
         const int t0 = c * C;
-        w.ahead(bufs, turn, c - 1);
         const int64_t nc = int64_t(ph) * ws.Nt + c;
         save_blocks<KB>(ws.dS, nc, VG, cg, S);
         const Gates<C> &g = s.m.g;
-        dt4 x[TB][2] = {};
+        // The products in this order, each group's operands read ahead of the group before it: P^T do, k dS, half of
+        // q^T do, X^T dU, the other half, k^T Y; the halves stand where dU and Y are being put together.
+        Frag<3> ft[2][2];            // a block of P^T or X^T
+        auto tri_of = [&](Frag<3>(&f)[2], const unsigned char *m) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            const Frag<3> fs = split<3>(S[kb][0], S[kb][1]);
+            for (int e = 0; e < 2; ++e) f[e] = read_cols<3>(m, NTR * kBlk, e);
+        };
+        Frag<NI> A[2][TB][2];        // a column block of k
+        auto rows_of = [&](Frag<NI>(&f)[TB][2], const unsigned char *m) {
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) x[tb][e] = mma<3>(read_rows<NI>(s.k[0][tb][kb], W::kStride, e), fs, x[tb][e]);
-        }
-        dt4 o[TB][2];
+                for (int e = 0; e < 2; ++e) f[tb][e] = read_rows<NI>(m + tb * KB * kBlk, W::kStride, e);
+        };
+        Frag<NI> fk[2][KB];          // half of a row block of k^T or q^T
+        auto cols_of = [&](Frag<NI>(&f)[KB], const unsigned char *m, int i) {
+#pragma unroll
+            for (int x = 0; x < KB; ++x) f[x] = read_cols<NI>(m + (i / 2 * KB + i % 2 * (KB / 2) + x / 2) * kBlk, W::kStride, x & 1);
+        };
+        tri_of(ft[0], s.m.P[0][0]);
+        dt4 o[TB][2], b[TB][2], eG[TB][2], eL[TB][2];
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                o[tb][e] = w.value(s, tb, e);
+                const int t = tb * 32 + lg * 8 + e * 4;
+                o[tb][e] = W::value(s, tb, e);
                 if (!in) o[tb][e] = dt4{};
-                x[tb][e] *= *reinterpret_cast<const dt4 *>(g.eL + tb * 32 + lg * 8 + e * 4);
+                b[tb][e] = *reinterpret_cast<const dt4 *>(g.beta + t);
+                eG[tb][e] = *reinterpret_cast<const dt4 *>(g.eG + t);
+                eL[tb][e] = *reinterpret_cast<const dt4 *>(g.eL + t);
             }
-#pragma unroll
-        for (int ib = 0; ib < TB; ++ib) {
-            const Frag<NI> fo = split<NI>(o[ib][0], o[ib][1]);
-#pragma unroll
-            for (int tb = 0; tb <= ib; ++tb)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    x[tb][e] = mma<3>(read_cols<3>(s.m.P[0][ib + tb], kTri<C> * kBlk, e), fo, x[tb][e]);
-        }
-        dt4 Y[TB][2] = {};
-#pragma unroll
-        for (int ib = 0; ib < TB; ++ib) {
-            const Frag<3> fu = split<3>(x[ib][0], x[ib][1]);
-#pragma unroll
-            for (int tb = 0; tb <= ib; ++tb)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    Y[tb][e] = mma<3>(read_cols<3>(s.m.X[0][ib + tb], kTri<C> * kBlk, e), fu, Y[tb][e]);
-        }
-        save_blocks<TB>(ws.Y, nc, VG, cg, Y);
-        dt4 v[TB][2];
         const float last = g.last;
+        Frag<NI> fo[TB];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int tb = 0; tb < TB; ++tb) fo[tb] = split<NI>(o[tb][0], o[tb][1]);
+        dt4 z[TB][2] = {}, x[TB][2] = {};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) S[kb][e] *= last;
+        for (int i = 0; i < NTR; ++i) {
+            if (i + 1 < NTR) tri_of(ft[(i + 1) & 1], s.m.P[0][i + 1]);
+            else rows_of(A[0], s.k[0][0][0]);
+            lds_point();
+            each_product<3, 3, NI>([&](int m, int l) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) z[i == 2][e] = mma1(ft[i & 1][e].p[m], fo[i > 0].p[l], z[i == 2][e]);
+            });
+            lds_point();
+        }
+#pragma unroll
+        for (int i = 0; i < KB; ++i) {
+            if (i + 1 < KB) rows_of(A[(i + 1) & 1], s.k[0][0][i + 1]);
+            else cols_of(fk[0], s.q[0][0][0], 0);
+            lds_point();
+            each_product<3, NI, 3>([&](int m, int l) {
+#pragma unroll
+                for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) x[tb][e] = mma1(A[i & 1][tb][e].p[m], fs[i].p[l], x[tb][e]);
+            });
+            lds_point();
+        }
+        Frag<3> fu[TB], fq[TB];
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int t = tb * 32 + lg * 8 + e * 4;
-                const dt4 b = *reinterpret_cast<const dt4 *>(g.beta + t), eG = *reinterpret_cast<const dt4 *>(g.eG + t);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[tb][e][i] = b[i] * Y[tb][e][i];
-                    o[tb][e][i] *= a.scale * eG[i];
-                    Y[tb][e][i] = -eG[i] * v[tb][e][i];
-                }
+                x[tb][e] = eL[tb][e] * x[tb][e] + z[tb][e];
+                o[tb][e] *= a.scale * eG[tb][e];
             }
-            const Frag<3> fo = split<3>(o[tb][0], o[tb][1]), fy = split<3>(Y[tb][0], Y[tb][1]);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    S[kb][e] = mma<3>(read_cols<NI>(s.q[0][tb][kb], W::kStride, e), fo, S[kb][e]);
-                    S[kb][e] = mma<3>(read_cols<NI>(s.k[0][tb][kb], W::kStride, e), fy, S[kb][e]);
-                }
+            fu[tb] = split<3>(x[tb][0], x[tb][1]);
+            fq[tb] = split<3>(o[tb][0], o[tb][1]);
         }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) S[kb][e] *= last;
+        auto add = [&](const Frag<NI>(&f)[KB], const Frag<3> &u, int i) {
+            each_product<3, NI, 3>([&](int m, int l) {
+#pragma unroll
+                for (int x = 0; x < KB; ++x) {
+                    dt4 &d = S[i % 2 * (KB / 2) + x / 2][x & 1];
+                    d = mma1(f[x].p[m], u.p[l], d);
+                }
+            });
+        };
+        dt4 Y[TB][2] = {};
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            if (i + 1 < TB) cols_of(fk[(i + 1) & 1], s.q[0][0][0], i + 1);
+            else tri_of(ft[0], s.m.X[0][0]);
+            lds_point();
+            add(fk[i & 1], fq[i / 2], i);
+            lds_point();
+        }
+#pragma unroll
+        for (int i = 0; i < NTR; ++i) {
+            if (i + 1 < NTR) tri_of(ft[(i + 1) & 1], s.m.X[0][i + 1]);
+            else cols_of(fk[0], s.q[0][0][0], TB);
+            lds_point();
+            each_product<3, 3, 3>([&](int m, int l) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) Y[i == 2][e] = mma1(ft[i & 1][e].p[m], fu[i > 0].p[l], Y[i == 2][e]);
+            });
+            lds_point();
+        }
+        dt4 v[TB][2];
+        Frag<3> fy[TB];
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+            dt4 y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                v[tb][e] = b[tb][e] * Y[tb][e];
+                y[e] = -eG[tb][e] * v[tb][e];
+            }
+            fy[tb] = split<3>(y[0], y[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            if (i + 1 < TB) cols_of(fk[(i + 1) & 1], s.q[0][0][0], TB + i + 1);
+            else cols_of(fk[(i + 1) & 1], s.k[0][0][0], 0);
+            lds_point();
+            add(fk[i & 1], fq[(TB + i) / 2], TB + i);
+            lds_point();
+        }
+        save_blocks<TB>(ws.Y, nc, VG, cg, Y);
         put_columns<T, TB>(dv + t0 * os, os, n - t0, in, v);
-        w.turn(bufs, c - 1);
+#pragma unroll
+        for (int i = 0; i < 2 * TB; ++i) {
+            if (i + 1 < 2 * TB) cols_of(fk[(TB + i + 1) & 1], s.k[0][0][0], i + 1);
+            lds_point();
+            add(fk[(TB + i) & 1], fy[i / 2], i);
+            lds_point();
+        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
+        W::turn();
     }
     for (int t = n + lg; t < a.T; t += 4)
         if (in) dv[t * os] = from_f32<T>(0.0f);
@@ -443,7 +518,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
 
 template <typename T, int C, int KP>
 hipError_t bwd_go(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, hipStream_t st) {
-    hipLaunchKernelGGL((delta_back_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hv * ((a.V + 63) / 64))), dim3(256),
+    hipLaunchKernelGGL((delta_back_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hv * ((a.V + 63) / 64))), dim3(kWalkThreads),
                        (Walk<T, C, KP, 3, true>::kLds), st, a, ws, d);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || ws.Nt == 0) return e;

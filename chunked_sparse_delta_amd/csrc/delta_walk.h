@@ -1,5 +1,5 @@
-// What the kernels that walk a sequence's chunks share: the chunk's operands in LDS, copied there a
-// chunk ahead, and the state in accumulators.
+// What the kernels that walk a sequence's chunks share: the chunk's operands in LDS, and the state in
+// accumulators.
 #pragma once
 
 #include "delta_tile.h"
@@ -8,22 +8,26 @@ namespace sdm {
 
 constexpr size_t kDeltaMaxLds = 160 * 1024 - 256;
 
-// A wavefront's 1 KB from per-lane addresses to consecutive LDS, without a register between. Written out, since the
-// compiler makes any later LDS read wait for its own form of it: Walk::arrive waits for these. (It has no result register,
-// and what the compiler waits for by count comes no later for more being on its way.)
-__device__ __forceinline__ void copy_to_lds(const void *src, const void *dst) {
-    const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)(dst)));
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-                 :: "v"(src), "s"(__builtin_amdgcn_readfirstlane(at)) : "memory");
+// A pointer that all lanes share, in scalar registers.
+template <typename T> __device__ __forceinline__ const T *uniform(const T *p) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(u)), hi = __builtin_amdgcn_readfirstlane(uint32_t(u >> 32));
+    return reinterpret_cast<const T *>(uint64_t(hi) << 32 | lo);
 }
+
+// Workgroups of eight wavefronts: four that compute, 16 columns of the state each, and four that
+// bring the chunks' operands from memory to LDS through their registers, a chunk ahead in LDS and another on its way. (The
+// computing ones have no registers for that, and the copy past the registers, global_load_lds, took 25 bytes a
+// cycle of a compute unit and LDS reads waited for it: 0.55 us of a chunk's 3.9.)
+constexpr int kWalkThreads = 512;
 
 // T: the inputs' type; NP: pieces of P; Q: q is wanted too.
 template <typename T, int C, int KP, int NP, bool Q> struct Walk {
     static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32;
     static constexpr int kStride = TB * KB * kBlk;              // between the pieces of k (and of q)
-    static constexpr int KS = kStride / 1024 / 4;               // kilobytes of a piece of k per wavefront
-    static constexpr int MS = (sizeof(ChunkMats<C, NP>) / 1024 + 3) / 4;
-    static constexpr int RS = 16 * sizeof(T) / 16;              // 16-byte pieces of a row of v's 16 columns
+    static constexpr int KS = kStride / 4096;                   // 16-byte eights of a piece of k per thread
+    static constexpr int kMats = sizeof(ChunkMats<C, NP>) / 16, MS = (kMats + 255) / 256;
+    static constexpr int RS = sizeof(T);                        // 16-byte pieces of a row of v's 16 columns
     static constexpr int VS = C * RS / 64;
     struct Lds {
         unsigned char k[NI][TB][KB][kBlk];
@@ -33,77 +37,95 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
     };
     static constexpr int kBufs = 2 * sizeof(Lds) <= kDeltaMaxLds ? 2 : 1;
     static constexpr size_t kLds = kBufs * sizeof(Lds);
-    const bf16 *kp, *qp;
-    const T *vp;
-    const unsigned char *mats;
-    int64_t kplane, qplane, ks, qs, vs;
-    int col0, n, Nc;
 
-    // Rows of `val` (v, or what takes its place) head vh; cg: the wavefront's group of 16 columns.
-    __device__ Walk(const DeltaArgs &a, const DeltaWs &ws, int p, int h, int hk, int ph, int cg, const Rows &val, int tokens)
-        : kp(a.kk.data + p * a.kk.sp + hk * a.kk.sh), qp(a.qq.data + p * a.qq.sp + hk * a.qq.sh),
-          vp(static_cast<const T *>(val.data) + p * val.sp + h * val.sh),
-          mats(ws.mats + int64_t(ph) * ws.Nt * sizeof(ChunkMats<C, NP>)), kplane(a.kk.plane), qplane(a.qq.plane), ks(a.kk.st),
-          qs(a.qq.st), vs(val.st), n(tokens), Nc((tokens + C - 1) / C) {
-        // columns past the row's end are read from its last ones: nothing that they reach is kept
-        const int piece = int(threadIdx.x) % RS * (16 / int(sizeof(T)));
-        col0 = min(cg * 16 + piece, val.width - 16 / int(sizeof(T)));
+    // Orders LDS only: nothing waits for loads or stores of memory on their way.
+    static __device__ __forceinline__ void barrier() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     }
 
-    // Chunk c's operands, on their way to `s`. Rows past the last valid token are that token's: finite where it is, and met by
-    // gates of 0 everywhere.
-    __device__ __forceinline__ void load(Lds &s, int c) const {
-        const int t0 = c * C, top = n - 1 - t0, lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const bf16 *kc = kp + t0 * ks, *qc = qp + t0 * qs;
-        const T *vc = vp + t0 * vs;
+    // The computing wavefronts' side: the i-th chunk taken is in buffer i & (kBufs - 1) after begin() and i times turn().
+    static __device__ __forceinline__ void begin() { barrier(); }
+    static __device__ __forceinline__ void turn() {
+        barrier();
+        if constexpr (kBufs == 1) barrier();
+    }
+
+    // The other side. val: v, or what takes its place; cg: the column group of the wavefront four before this one.
+    struct Bring {
+        const bf16 *kp, *qp;
+        const T *vp;
+        const unsigned char *mats;
+        int64_t kplane, qplane, ks, qs, vs;
+        int col0, n;
+        du4 k[NI][KS], q[Q ? NI : 1][Q ? KS : 1], v[VS], m[MS];
+
+        __device__ Bring(const DeltaArgs &a, const DeltaWs &ws, int p, int h, int hk, int ph, int cg, const Rows &val, int tokens)
+            : kp(uniform(a.kk.data + p * a.kk.sp + hk * a.kk.sh)), qp(uniform(a.qq.data + p * a.qq.sp + hk * a.qq.sh)),
+              vp(uniform(static_cast<const T *>(val.data) + p * val.sp + h * val.sh)),
+              mats(uniform(ws.mats + int64_t(ph) * ws.Nt * sizeof(ChunkMats<C, NP>))), kplane(a.kk.plane), qplane(a.qq.plane),
+              ks(a.kk.st), qs(a.qq.st), vs(val.st), n(tokens) {
+            // columns past the row's end are read from its last ones: nothing that they reach is kept
+            col0 = min(cg * 16 + int(threadIdx.x) % RS * (16 / int(sizeof(T))), val.width - 16 / int(sizeof(T)));
+        }
+        // Rows past the last valid token are read as that token's: finite where it is, and met by gates of 0 everywhere.
+        __device__ __forceinline__ void load(int c) {
+            const int top = n - 1 - c * C, tid = threadIdx.x & 255, lane = tid & 63;
+            const int64_t t0 = int64_t(c) * C;
+            const bf16 *kc = kp + t0 * ks, *qc = qp + t0 * qs;
+            const T *vc = vp + t0 * vs;
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            const int slot = i * 256 + wv * 64 + lane, blk = slot / 128, r = slot % 128 / 4;
-            const int row = min(blk / KB * 32 + r, top), d = blk % KB * 32 + ((slot ^ (r >> 3)) & 3) * 8;
-            unsigned char *dk = &s.k[0][0][0][0] + (i * 256 + wv * 64) * 16;
+            for (int i = 0; i < KS; ++i) {
+                const int slot = tid + 256 * i, row = min(slot / 128 / KB * 32 + slot % 128 / 4, top);
+                const int d = slot / 128 % KB * 32 + slot % 4 * 8;
 #pragma unroll
-            for (int e = 0; e < NI; ++e) copy_to_lds(kc + e * kplane + (row * int(ks) + d), dk + e * kStride);
-            if constexpr (Q) {
-                unsigned char *dq = &s.q[0][0][0][0] + (i * 256 + wv * 64) * 16;
+                for (int e = 0; e < NI; ++e) {
+                    k[e][i] = *reinterpret_cast<const du4 *>(kc + e * kplane + uint32_t(row * int(ks) + d));
+                    if constexpr (Q) q[e][i] = *reinterpret_cast<const du4 *>(qc + e * qplane + uint32_t(row * int(qs) + d));
+                }
+            }
 #pragma unroll
-                for (int e = 0; e < NI; ++e) copy_to_lds(qc + e * qplane + (row * int(qs) + d), dq + e * kStride);
+            for (int i = 0; i < VS; ++i)
+                v[i] = *reinterpret_cast<const du4 *>(vc + uint32_t(min((lane + 64 * i) / RS, top) * int(vs) + col0));
+            const unsigned char *src = mats + t0 / C * int64_t(sizeof(ChunkMats<C, NP>));
+#pragma unroll
+            for (int i = 0; i < MS; ++i) m[i] = *reinterpret_cast<const du4 *>(src + uint32_t(min(tid + 256 * i, kMats - 1)) * 16);
+        }
+        __device__ __forceinline__ void store(Lds &s) const {
+            const int tid = threadIdx.x & 255, lane = tid & 63, wv = tid >> 6;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                const int slot = tid + 256 * i, at = slot / 128 * kBlk + block_at(slot % 128 / 4, slot % 4);
+#pragma unroll
+                for (int e = 0; e < NI; ++e) {
+                    *reinterpret_cast<du4 *>(&s.k[0][0][0][0] + e * kStride + at) = k[e][i];
+                    if constexpr (Q) *reinterpret_cast<du4 *>(&s.q[0][0][0][0] + e * kStride + at) = q[e][i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VS; ++i) reinterpret_cast<du4 *>(&s.v[wv][0][0])[lane + 64 * i] = v[i];
+#pragma unroll
+            for (int i = 0; i < MS; ++i)
+                if (tid + 256 * i < kMats) reinterpret_cast<du4 *>(&s.m)[tid + 256 * i] = m[i];
+        }
+        // Chunks c0, c0 + dir, ..., `count` of them.
+        __device__ __forceinline__ void run(Lds *bufs, int c0, int dir, int count) {
+            if (count > 0) {
+                load(c0);
+                store(bufs[0]);
+            }
+            if (count > 1) load(c0 + dir);
+            barrier();
+            for (int i = 0; i < count; ++i) {
+                if constexpr (kBufs == 1) barrier();
+                if (i + 1 < count) store(bufs[(i + 1) & (kBufs - 1)]);
+                if (i + 2 < count) load(c0 + (i + 2) * dir);
+                barrier();
             }
         }
-#pragma unroll
-        for (int i = 0; i < VS; ++i)
-            copy_to_lds(vc + (min((lane + 64 * i) / RS, top) * int(vs) + col0), reinterpret_cast<unsigned char *>(&s.v[wv][0][0]) + i * 1024);
-        const unsigned char *src = mats + int64_t(c) * sizeof(ChunkMats<C, NP>) + lane * 16;
-#pragma unroll
-        for (int i = 0; i < MS; ++i) {
-            const int kb = wv + 4 * i;
-            if (kb < int(sizeof(ChunkMats<C, NP>) / 1024)) copy_to_lds(src + kb * 1024, reinterpret_cast<unsigned char *>(&s.m) + kb * 1024);
-        }
-    }
-    __device__ __forceinline__ bool has(int c) const { return c >= 0 && c < Nc; }
-    static __device__ __forceinline__ void arrive() {   // everything on its way is there, for every wavefront
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-        __syncthreads();
-    }
-    // LDS holds the current chunk's operands. With two buffers the next chunk's are on their way to the other one meanwhile.
-    __device__ __forceinline__ void begin(Lds *bufs, int c) const {
-        if (!has(c)) return;
-        load(bufs[0], c);
-        arrive();
-    }
-    // At the start of the i-th chunk taken: `next` is the chunk after it.
-    __device__ __forceinline__ void ahead(Lds *bufs, int i, int next) const {
-        if constexpr (kBufs == 2)
-            if (has(next)) load(bufs[(i + 1) & 1], next);
-    }
-    // At its end.
-    __device__ __forceinline__ void turn(Lds *bufs, int next) const {
-        if constexpr (kBufs == 1) {
-            __syncthreads();
-            if (has(next)) load(bufs[0], next);
-        }
-        arrive();
-    }
-    __device__ __forceinline__ dt4 value(const Lds &s, int tb, int e) const {
+    };
+    static __device__ __forceinline__ dt4 value(const Lds &s, int tb, int e) {
         const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4, i = lane & 15, t = tb * 32 + g * 8 + e * 4;
         dt4 x;
         if constexpr (sizeof(T) == 2) {

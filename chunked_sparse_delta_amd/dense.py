@@ -20,28 +20,20 @@ past it are padding, they leave the state alone and read 0. ``scale`` defaults t
 from __future__ import annotations
 
 import ctypes
-import math
+import struct
 
 import torch
 
-from . import _DTYPES, _Exec, _check_rc, _expect, _load, _ptr, _stream_ptr
+from . import _DTYPES, _check_rc, _expect, _load, _stream_ptr
 
 __all__ = ["gated_delta_fwd", "gated_delta_step", "gated_delta_bwd", "gated_delta_rule", "gated_delta_workspace_bytes",
            "layer_norm_fwd", "layer_norm_bwd", "layer_norm"]
 
-
-class _Shape(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int32) for n in ("streams", "tokens", "key_heads", "value_heads", "head_dim", "value_dim",
-                                               "dtype")] + [("scale", ctypes.c_float)]
-
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stream", ctypes.c_int64), ("token", ctypes.c_int64),
-                ("head", ctypes.c_int64)]
-
-
-class _DeltaGrads(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "beta", "log_decay", "state")]
+# The ABI's structures, packed: a call of a few microseconds' work notices what building ctypes objects costs.
+_SHAPE = struct.Struct("@7if").pack            # sdm_delta_shape
+_ROWS = struct.Struct("@P3q").pack             # sdm_rows
+_EXEC = struct.Struct("@PPNPiPi").pack         # sdm_exec
+_GRADS = struct.Struct("@6P").pack             # sdm_delta_grads
 
 
 def bind(lib) -> None:
@@ -61,85 +53,109 @@ def bind(lib) -> None:
         fn.restype = ctypes.c_int
 
 
-def _on(device: torch.device) -> None:
-    """Calls run on the current device: the tensors have to be there."""
+_current_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(device: torch.device) -> int:
+    """Calls run on the current device: the tensors have to be there. Returns its index."""
     if device.type != "cuda":
         raise ValueError(f"expected GPU tensors, got {device}")
-    if device.index is not None and device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    index = _current_device()
+    if device.index != index:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{index}")
+    return index
 
 
 def _used_on(stream, *tensors) -> None:
     """Tensors made here (on the current stream's pool) but used on the caller's stream stay whole until that work ends."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
-def _exec(stream, workspace=None) -> _Exec:
+def _exec(stream, index, workspace=None) -> bytes:
+    if stream is None:
+        s = _raw_stream(index) if _raw_stream is not None else _stream_ptr(None).value or 0
+    else:
+        s = stream.cuda_stream
     if workspace is None:
-        return _Exec(_stream_ptr(stream), None, 0, None, 0, None)
+        return _EXEC(s, 0, 0, 0, 0, 0, 0)
     if workspace.device.type != "cuda" or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
-    return _Exec(_stream_ptr(stream), workspace.data_ptr(), workspace.numel() * workspace.element_size(), None, 0, None)
+    return _EXEC(s, workspace.data_ptr(), workspace.numel() * workspace.element_size(), 0, 0, 0, 0)
 
 
-def _view(t: torch.Tensor, name: str, shape, dtype, device) -> _Rows:
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need(t, name, shape, dtype, dev) -> None:
+    """_expect's checks, without the words while they pass."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+        _expect(t, name, shape, dtype, dev)
+
+
+def _view(t, name, shape, dtype, dev) -> bytes:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, v on {device}")
-    s = t.stride()
-    if s[3] != 1 and shape[3] > 1:
-        raise ValueError(f"{name}: the last axis must be dense, its stride is {s[3]}")
-    return _Rows(t.data_ptr(), s[0], s[1], s[2])
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, v on {dev}")
+    p, tok, head, one = t.stride()
+    if one != 1 and shape[3] > 1:
+        raise ValueError(f"{name}: the last axis must be dense, its stride is {one}")
+    return _ROWS(t.data_ptr(), p, tok, head)
 
 
-def _rule_inputs(state, k, v, beta, log_decay, q, scale, valid_tokens):
+def _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens):
     if not isinstance(v, torch.Tensor) or not isinstance(k, torch.Tensor):
         raise TypeError("k and v must be torch tensors")
-    if v.dtype not in _DTYPES:
-        raise TypeError(f"v must be float32 or bfloat16, got {v.dtype}")
-    if v.dim() != 4 or k.dim() != 4:
-        raise ValueError(f"k and v must be [P, T, heads, width], got {tuple(k.shape)} and {tuple(v.shape)}")
-    dev = v.device
-    _on(dev)
-    P, T, Hv, V = v.shape
-    Hk, K = k.shape[2:]
+    dtype, dev, vs, ks = v.dtype, v.device, v.shape, k.shape
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"v must be float32 or bfloat16, got {dtype}")
+    if len(vs) != 4 or len(ks) != 4:
+        raise ValueError(f"k and v must be [P, T, heads, width], got {tuple(ks)} and {tuple(vs)}")
+    index = _on(dev)
+    P, T, Hv, V = vs
+    Hk, K = ks[2], ks[3]
     if Hk < 1 or Hv % Hk:
         raise ValueError(f"the value heads ({Hv}) must be a multiple of the key heads ({Hk})")
-    kr, qr = (_view(t, n, (P, T, Hk, K), v.dtype, dev) for t, n in ((k, "k"), (q, "q")))
-    vr = _view(v, "v", v.shape, v.dtype, dev)
-    for t, n in ((beta, "beta"), (log_decay, "log_decay")):
-        _expect(t, n, (P, T, Hv), torch.float32, dev)
+    keys, gates = (P, T, Hk, K), (P, T, Hv)
+    kr, qr, vr = _view(k, "k", keys, dtype, dev), _view(q, "q", keys, dtype, dev), _view(v, "v", vs, dtype, dev)
+    _need(beta, "beta", gates, torch.float32, dev)
+    _need(log_decay, "log_decay", gates, torch.float32, dev)
     if valid_tokens is not None:
-        _expect(valid_tokens, "valid_tokens", (P,), torch.int32, dev)
-    shape = _Shape(P, T, Hk, Hv, K, V, _DTYPES[v.dtype], K ** -0.5 if scale is None else float(scale))
-    return shape, qr, kr, vr, dev
+        _need(valid_tokens, "valid_tokens", (P,), torch.int32, dev)
+    shape = _SHAPE(P, T, Hk, Hv, K, V, code, K ** -0.5 if scale is None else scale)
+    return (P, Hv, K, V), shape, qr, kr, vr, dev, index
 
 
-def _out(out, v):
+def _out(out, v, stream):
     if out is None:
-        return torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    _expect(out, "out", tuple(v.shape), v.dtype, v.device)
+        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)   # dense whatever v's strides are
+        if stream is not None:
+            _used_on(stream, out)
+    else:
+        _need(out, "out", v.shape, v.dtype, v.device)
     return out
 
 
 def gated_delta_workspace_bytes(P: int, T: int, Hk: int, Hv: int, K: int, V: int, dtype: torch.dtype,
                                 backward: bool = False) -> int:
     """Bytes of scratch gated_delta_fwd (or gated_delta_bwd) needs; 0 for shapes they reject."""
-    return int(_load().sdm_gated_delta_workspace_bytes(ctypes.byref(_Shape(P, T, Hk, Hv, K, V, _DTYPES.get(dtype, -1), 1.0)),
-                                                       1 if backward else 0))
+    return _load().sdm_gated_delta_workspace_bytes(_SHAPE(P, T, Hk, Hv, K, V, _DTYPES.get(dtype, -1), 1.0), 1 if backward else 0)
 
 
-def _scratch(lib, shape, backward, device):
-    n = lib.sdm_gated_delta_workspace_bytes(ctypes.byref(shape), backward)
-    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
+def _scratch(lib, shape, backward, dev, stream):
+    ws = torch.empty(max(lib.sdm_gated_delta_workspace_bytes(shape, backward), 256), dtype=torch.uint8, device=dev)
+    if stream is not None:
+        _used_on(stream, ws)
+    return ws
 
 
 def gated_delta_fwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, log_decay: torch.Tensor,
@@ -150,23 +166,20 @@ def gated_delta_fwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
     is where ``state_out`` is given, which then gets the final state. ``state=None`` starts from zeros (the final state
     goes to ``state_out`` if given). ``workspace`` (uint8, GPU, gated_delta_workspace_bytes) is allocated if omitted."""
     lib = _load()
-    shape, qr, kr, vr, dev = _rule_inputs(state, k, v, beta, log_decay, q, scale, valid_tokens)
-    full = (shape.streams, shape.value_heads, shape.head_dim, shape.value_dim)
-    for t, n in ((state, "state"), (state_out, "state_out")):
-        if t is not None:
-            _expect(t, n, full, torch.float32, dev)
-    made = [] if out is not None else [0]
-    out = _out(out, v)
-    if made:
-        _used_on(stream, out)
+    full, shape, qr, kr, vr, dev, index = _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens)
+    if state is not None:
+        _need(state, "state", full, torch.float32, dev)
+    if state_out is None:
+        state_out = state
+    else:
+        _need(state_out, "state_out", full, torch.float32, dev)
+    out = _out(out, v, stream)
     if workspace is None:
-        workspace = _scratch(lib, shape, 0, dev)
-        _used_on(stream, workspace)
-    ex = _exec(stream, workspace)
-    rc = lib.sdm_gated_delta_fwd(ctypes.byref(shape), ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), _ptr(beta),
-                                 _ptr(log_decay), _ptr(state), _ptr(state if state_out is None else state_out),
-                                 _ptr(valid_tokens), _ptr(out), ctypes.byref(ex))
-    _check_rc(lib, rc)
+        workspace = _scratch(lib, shape, 0, dev, stream)
+    rc = lib.sdm_gated_delta_fwd(shape, qr, kr, vr, beta.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(state_out),
+                                 _ptr(valid_tokens), out.data_ptr(), _exec(stream, index, workspace))
+    if rc:
+        _check_rc(lib, rc)
     return out
 
 
@@ -180,26 +193,24 @@ def gated_delta_step(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta
     an idle stream, which reads 0; without it stream p has slot p. The states are advanced in place, or written to
     ``state_out`` (the same shape; slots that no stream names are left alone there)."""
     lib = _load()
-    shape, qr, kr, vr, dev = _rule_inputs(state, k, v, beta, log_decay, q, scale, valid_tokens)
+    full, shape, qr, kr, vr, dev, index = _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a [slots, Hv, K, V] tensor")
-    full = (state.shape[0], shape.value_heads, shape.head_dim, shape.value_dim)
-    _expect(state, "state", full, torch.float32, dev)
+    slots = state.shape[0]
+    pool = (slots, *full[1:])
+    _need(state, "state", pool, torch.float32, dev)
     if state_out is None:
         state_out = state
     else:
-        _expect(state_out, "state_out", full, torch.float32, dev)
+        _need(state_out, "state_out", pool, torch.float32, dev)
     if state_ids is not None:
-        _expect(state_ids, "state_ids", (shape.streams,), torch.int32, dev)
-    made = out is None
-    out = _out(out, v)
-    if made:
-        _used_on(stream, out)
-    ex = _exec(stream)
-    rc = lib.sdm_gated_delta_step(ctypes.byref(shape), ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), _ptr(beta),
-                                  _ptr(log_decay), _ptr(state), _ptr(state_out), _ptr(state_ids), full[0],
-                                  _ptr(valid_tokens), _ptr(out), ctypes.byref(ex))
-    _check_rc(lib, rc)
+        _need(state_ids, "state_ids", full[:1], torch.int32, dev)
+    out = _out(out, v, stream)
+    rc = lib.sdm_gated_delta_step(shape, qr, kr, vr, beta.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
+                                  state_out.data_ptr(), _ptr(state_ids), slots, _ptr(valid_tokens), out.data_ptr(),
+                                  _exec(stream, index))
+    if rc:
+        _check_rc(lib, rc)
     return out
 
 
@@ -211,33 +222,33 @@ def gated_delta_bwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
     gradient of the readings, ``grad_state`` (float32, optional) that of the final state. Returns dict(state, k, v, beta,
     log_decay, q): k, v and q in the inputs' dtype (sums over sharing heads in float32), the others float32."""
     lib = _load()
-    shape, qr, kr, vr, dev = _rule_inputs(state, k, v, beta, log_decay, q, scale, valid_tokens)
-    P, T, Hk, Hv, K, V = shape.streams, shape.tokens, shape.key_heads, shape.value_heads, shape.head_dim, shape.value_dim
-    _expect(grad_out, "grad_out", (P, T, Hv, V), v.dtype, dev)
+    full, shape, qr, kr, vr, dev, index = _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens)
+    _need(grad_out, "grad_out", v.shape, v.dtype, dev)
     for t, n in ((state, "state"), (grad_state, "grad_state")):
         if t is not None:
-            _expect(t, n, (P, Hv, K, V), torch.float32, dev)
+            _need(t, n, full, torch.float32, dev)
     f32 = dict(dtype=torch.float32, device=dev)
-    g = dict(state=torch.empty((P, Hv, K, V), **f32), k=torch.empty((P, T, Hk, K), dtype=v.dtype, device=dev),
-             v=torch.empty((P, T, Hv, V), dtype=v.dtype, device=dev), beta=torch.empty((P, T, Hv), **f32),
-             log_decay=torch.empty((P, T, Hv), **f32), q=torch.empty((P, T, Hk, K), dtype=v.dtype, device=dev))
-    _used_on(stream, *g.values())
+    g = dict(state=torch.empty(full, **f32), k=torch.empty(k.shape, dtype=k.dtype, device=dev),
+             v=torch.empty(v.shape, dtype=v.dtype, device=dev), beta=torch.empty_like(beta),
+             log_decay=torch.empty_like(log_decay), q=torch.empty(q.shape, dtype=q.dtype, device=dev))
+    if stream is not None:
+        _used_on(stream, *g.values())
     if workspace is None:
-        workspace = _scratch(lib, shape, 1, dev)
-        _used_on(stream, workspace)
-    gr = _DeltaGrads(*(g[n].data_ptr() for n in ("q", "k", "v", "beta", "log_decay", "state")))
-    ex = _exec(stream, workspace)
-    rc = lib.sdm_gated_delta_bwd(ctypes.byref(shape), ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), _ptr(beta),
-                                 _ptr(log_decay), _ptr(state), _ptr(valid_tokens), _ptr(grad_out), _ptr(grad_state),
-                                 ctypes.byref(gr), ctypes.byref(ex))
-    _check_rc(lib, rc)
+        workspace = _scratch(lib, shape, 1, dev, stream)
+    rc = lib.sdm_gated_delta_bwd(shape, qr, kr, vr, beta.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(valid_tokens),
+                                 grad_out.data_ptr(), _ptr(grad_state),
+                                 _GRADS(*(g[n].data_ptr() for n in ("q", "k", "v", "beta", "log_decay", "state"))),
+                                 _exec(stream, index, workspace))
+    if rc:
+        _check_rc(lib, rc)
     return g
 
 
 class _GatedDeltaRule(torch.autograd.Function):
     @staticmethod
     def forward(ctx, state, k, v, beta, log_decay, q, scale, valid_tokens):
-        final = torch.empty((v.shape[0], v.shape[2], k.shape[3], v.shape[3]), dtype=torch.float32, device=v.device)
+        P, _, Hv, V = v.shape
+        final = torch.empty((P, Hv, k.shape[3], V), dtype=torch.float32, device=v.device)
         out = gated_delta_fwd(state, k, v, beta, log_decay, q, scale=scale, valid_tokens=valid_tokens, state_out=final)
         ctx.save_for_backward(state, k, v, beta, log_decay, q, valid_tokens)
         ctx.scale = scale
@@ -265,25 +276,28 @@ def gated_delta_rule(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor
 
 # ---- layer norm ------------------------------------------------------------------------------------------------------
 
-def _norm_inputs(x, params):
+def _norm_inputs(x, weight, bias):
+    """rows, cols, x's and the parameters' dtype codes, the device index."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if x.dtype not in _DTYPES:
+    code, dev = _DTYPES.get(x.dtype), x.device
+    if code is None:
         raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"x must be [..., cols], got {tuple(x.shape)}")
-    _on(x.device)
+    index = _on(dev)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     N = x.shape[-1]
     wdtype = None
-    for t, n in params:
+    for t, n in ((weight, "weight"), (bias, "bias")):
         if t is not None:
-            if t.dtype not in _DTYPES or (wdtype is not None and t.dtype != wdtype):
-                raise TypeError(f"{n}: expected {wdtype or 'float32 or bfloat16'}, got {t.dtype}")
-            wdtype = t.dtype
-            _expect(t, n, (N,), wdtype, x.device)
-    return x.numel() // N, N, wdtype
+            if wdtype is None:
+                wdtype = t.dtype
+                if wdtype not in _DTYPES:
+                    raise TypeError(f"{n}: expected float32 or bfloat16, got {wdtype}")
+            _need(t, n, (N,), wdtype, dev)
+    return x.numel() // N, N, code, wdtype, index
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
@@ -291,18 +305,21 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     """Layer norm over the last axis of a contiguous x (float32 or bfloat16); weight and bias [cols] in x's dtype or
     float32, or None. Returns (y, mean, rstd); mean and rstd float32 [rows] are what layer_norm_bwd needs."""
     lib = _load()
-    rows, N, wdtype = _norm_inputs(x, ((weight, "weight"), (bias, "bias")))
-    made = out is None
-    if made:
+    rows, N, code, wdtype, index = _norm_inputs(x, weight, bias)
+    if out is None:
         out = torch.empty_like(x)
+        if stream is not None:
+            _used_on(stream, out)
     else:
-        _expect(out, "out", tuple(x.shape), x.dtype, x.device)
-    mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=x.device)
-    _used_on(stream, out if made else None, mean, rstd)
-    ex = _exec(stream)
-    rc = lib.sdm_layer_norm_fwd(rows, N, _ptr(x), _DTYPES[x.dtype], _ptr(weight), _ptr(bias),
-                                _DTYPES[wdtype or x.dtype], eps, _ptr(out), _ptr(mean), _ptr(rstd), ctypes.byref(ex))
-    _check_rc(lib, rc)
+        _need(out, "out", x.shape, x.dtype, x.device)
+    mean = x.new_empty((rows,), dtype=torch.float32)
+    rstd = torch.empty_like(mean)
+    if stream is not None:
+        _used_on(stream, mean, rstd)
+    rc = lib.sdm_layer_norm_fwd(rows, N, x.data_ptr(), code, _ptr(weight), _ptr(bias), code if wdtype is None else _DTYPES[wdtype],
+                                eps, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _exec(stream, index))
+    if rc:
+        _check_rc(lib, rc)
     return out, mean, rstd
 
 
@@ -312,30 +329,34 @@ def layer_norm_bwd(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, 
     """Backward of layer_norm_fwd: dict(x, weight, bias) of the gradients named in ``need``. The weight's and bias's are
     in ``weight_dtype`` (default: the weight's dtype, or x's)."""
     lib = _load()
-    rows, N, wdtype = _norm_inputs(x, ((weight, "weight"),))
+    rows, N, code, wdtype, index = _norm_inputs(x, weight, None)
     wdtype = weight_dtype or wdtype or x.dtype
     if wdtype not in _DTYPES or (weight is not None and weight.dtype != wdtype):
         raise TypeError(f"weight_dtype {wdtype} does not go with the weight")
     dev = x.device
-    _expect(grad_out, "grad_out", tuple(x.shape), x.dtype, dev)
-    for t, n in ((mean, "mean"), (rstd, "rstd")):
-        _expect(t, n, (rows,), torch.float32, dev)
-    if set(need) - {"x", "weight", "bias"}:
-        raise ValueError(f"need names x, weight and bias, got {need}")
-    g = {"x": torch.empty_like(x) if "x" in need else None}
-    for n in ("weight", "bias"):
-        g[n] = torch.empty((N,), dtype=wdtype, device=dev) if n in need else None
-    _used_on(stream, *g.values())
-    if workspace is None and (g["weight"] is not None or g["bias"] is not None):
-        workspace = torch.empty(lib.sdm_layer_norm_bwd_workspace_bytes(rows, N, _DTYPES[x.dtype]), dtype=torch.uint8,
-                                device=dev)
-        _used_on(stream, workspace)
-    ex = _exec(stream, workspace)
-    rc = lib.sdm_layer_norm_bwd(rows, N, _ptr(grad_out), _ptr(x), _DTYPES[x.dtype], _ptr(weight), _DTYPES[wdtype],
-                                _ptr(mean), _ptr(rstd), _ptr(g["x"]), _ptr(g["weight"]), _ptr(g["bias"]),
-                                ctypes.byref(ex))
-    _check_rc(lib, rc)
-    return {n: t for n, t in g.items() if t is not None}
+    _need(grad_out, "grad_out", x.shape, x.dtype, dev)
+    _need(mean, "mean", (rows,), torch.float32, dev)
+    _need(rstd, "rstd", (rows,), torch.float32, dev)
+    g = {}
+    for n in need:
+        if n == "x":
+            g[n] = torch.empty_like(x)
+        elif n in ("weight", "bias"):
+            g[n] = torch.empty((N,), dtype=wdtype, device=dev)
+        else:
+            raise ValueError(f"need names x, weight and bias, got {need}")
+    if workspace is None and ("weight" in g or "bias" in g):
+        workspace = torch.empty(lib.sdm_layer_norm_bwd_workspace_bytes(rows, N, code), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            _used_on(stream, workspace)
+    if stream is not None:
+        _used_on(stream, *g.values())
+    rc = lib.sdm_layer_norm_bwd(rows, N, grad_out.data_ptr(), x.data_ptr(), code, _ptr(weight), _DTYPES[wdtype],
+                                mean.data_ptr(), rstd.data_ptr(), _ptr(g.get("x")), _ptr(g.get("weight")), _ptr(g.get("bias")),
+                                _exec(stream, index, workspace))
+    if rc:
+        _check_rc(lib, rc)
+    return g
 
 
 class _LayerNorm(torch.autograd.Function):

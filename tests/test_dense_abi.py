@@ -44,19 +44,19 @@ class Delta:
     def run(self, form):
         from chunked_sparse_delta_amd import _Exec
         D, r, lib = self.dense, ctypes.byref, self.lib
-        sh = D._Shape(**self.shape)
-        q, k, v = (D._Rows(self.ptr[n], *self.stride) for n in "qkv")
-        need = lib.sdm_gated_delta_workspace_bytes(r(sh), 1 if form == "bwd" else 0)
+        sh = D._SHAPE(*self.shape.values())
+        q, k, v = (D._ROWS(self.ptr[n] or 0, *self.stride) for n in "qkv")
+        need = lib.sdm_gated_delta_workspace_bytes(sh, 1 if form == "bwd" else 0)
         ex = _Exec(None, self.ptr["ws"], max(need, 256) if self.ws_bytes is None else self.ws_bytes, None, 0, None)
         p = self.ptr
-        head = (r(sh), r(q), r(k), r(v), p["beta"], p["g"], p["state"])
+        head = (sh, q, k, v, p["beta"], p["g"], p["state"])
         if form == "fwd":
             rc = lib.sdm_gated_delta_fwd(*head, p["state_out"], p["valid"], p["out"], r(ex))
         elif form == "step":
             rc = lib.sdm_gated_delta_step(*head, p["state_out"], p["ids"], self.slots, p["valid"], p["out"], r(ex))
         else:
-            gr = D._DeltaGrads(*(p[n] for n in ("gq", "gk", "gv", "gbeta", "gg", "gstate")))
-            rc = lib.sdm_gated_delta_bwd(*head, p["valid"], p["go"], p["gs"], r(gr), r(ex))
+            gr = D._GRADS(*(p[n] or 0 for n in ("gq", "gk", "gv", "gbeta", "gg", "gstate")))
+            rc = lib.sdm_gated_delta_bwd(*head, p["valid"], p["go"], p["gs"], gr, r(ex))
         return rc, lib.sdm_last_error().decode()
 
 
