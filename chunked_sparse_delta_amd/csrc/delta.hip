@@ -52,74 +52,87 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
     const int t0 = c * C, live = min(C, delta_valid(a, p) - t0);
     if (live <= 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lc = lane & 15, lg = lane >> 4;
-    if (wv == 3) {
-        // G in 64 bits: its differences are as exact as the log-decays themselves however large it grew. A log-decay
-        // below -1e4 (-inf among them: it clears the state) counts as -1e4, whose exponential is 0 too.
-        const int64_t at = (int64_t(p) * a.T + t0 + lane) * a.Hv + h;
-        const bool in = lane < C && lane < live;
-        float g = in ? a.g[at] : 0.0f;
-        if (g < -1e4f) g = -1e4f;
-        double G = double(g);
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-            const double o = __shfl_up(G, d, 64);
-            if (lane >= d) G += o;
-        }
-        const double GL = __shfl(G, C - 1, 64);
-        if (lane < C) {
-            s.G[lane] = G;
-            s.g.beta[lane] = in ? a.beta[at] : 0.0f;
-            s.g.eG[lane] = in ? expf(float(G)) : 0.0f;
-            s.g.eL[lane] = in ? expf(float(GL - G)) : 0.0f;
-        }
-        if (lane == 0) s.g.last = expf(float(GL));
-    }
-    dt4 kk[NT] = {}, qk[NT] = {};
+    // every operand is on its way before the first product: row tile wv of q and row tiles 0 .. wv of k
+    const int row = wv * 16 + lc;
+    constexpr int KB = KP / 32;
+    Frag<NI> fk[NT][KB], fq[KB];
     if (wv < NT) {
         const bf16 *k = a.kk.data + p * a.kk.sp + hk * a.kk.sh + t0 * a.kk.st;
         const bf16 *q = a.qq.data + p * a.qq.sp + hk * a.qq.sh + t0 * a.qq.st;
-        // rows past the last valid token are cleared: their columns of X and P, and rows of P, are then 0
-        const int row = wv * 16 + lc;
 #pragma unroll
-        for (int kb = 0; kb < KP / 32; ++kb) {
+        for (int kb = 0; kb < KB; ++kb) {
             const int d = kb * 32 + lg * 8;
-            Frag<NI> fk[NT], fa, fq = load_keys<NI>(q + (min(row, live - 1) * int(a.qq.st) + d), a.qq.plane);
-            if (row >= live) clear(fq);
+            fq[kb] = load_keys<NI>(q + (min(row, live - 1) * int(a.qq.st) + d), a.qq.plane);
+#pragma unroll
+            for (int ct = 0; ct < NT; ++ct)
+                if (ct <= wv) fk[ct][kb] = load_keys<NI>(k + (min(ct * 16 + lc, live - 1) * int(a.kk.st) + d), a.kk.plane);
+        }
+    }
+    if (wv == (NT == 4 ? 0 : 3)) {      // the wavefront with the fewest products
+        const bool in = lane < C && lane < live;
+        const double G = chunk_G<C>(a, p, h, t0, live), GL = __shfl(G, C - 1, 64);
+        if (lane < C) {
+            s.G[lane] = G;
+            s.g.beta[lane] = in ? a.beta[(int64_t(p) * a.T + t0 + lane) * a.Hv + h] : 0.0f;
+            s.g.eG[lane] = in ? exp2_of(G) : 0.0f;
+            s.g.eL[lane] = in ? exp2_of(GL - G) : 0.0f;
+        }
+        if (lane == 0) s.g.last = exp2_of(GL);
+    }
+    dt4 kk[NT] = {}, qk[NT] = {};
+    if (wv < NT) {
+        // rows past the last valid token are cleared: their columns of X and P, and rows of P, are then 0
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            if (row >= live) clear(fq[kb]);
+            Frag<NI> fa;
 #pragma unroll
             for (int ct = 0; ct < NT; ++ct)
                 if (ct <= wv) {
-                    fk[ct] = load_keys<NI>(k + (min(ct * 16 + lc, live - 1) * int(a.kk.st) + d), a.kk.plane);
-                    if (ct * 16 + lc >= live) clear(fk[ct]);
-                    if (ct == wv) fa = fk[ct];
+                    if (ct * 16 + lc >= live) clear(fk[ct][kb]);
+                    if (ct == wv) fa = fk[ct][kb];
                 }
 #pragma unroll
             for (int ct = 0; ct < NT; ++ct)
                 if (ct <= wv) {
-                    kk[ct] = mma<3>(fa, fk[ct], kk[ct]);
-                    qk[ct] = mma<3>(fq, fk[ct], qk[ct]);
+                    kk[ct] = mma<3>(fa, fk[ct][kb], kk[ct]);
+                    qk[ct] = mma<3>(fq[kb], fk[ct][kb], qk[ct]);
                 }
         }
     }
-    __syncthreads();
+    lds_barrier();
     if (wv < NT) {
+        double Gr[4];
+        float b[4];
 #pragma unroll
-        for (int ct = 0; ct < NT; ++ct)
+        for (int r = 0; r < 4; ++r) {
+            const int row = wv * 16 + 4 * lg + r;
+            Gr[r] = s.G[row];
+            b[r] = ws.backward ? delta_beta_safe(s.g.beta[row]) : s.g.beta[row];
+        }
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct) {
+            const int col = ct * 16 + lc;
+            const double Gc = ct <= wv ? s.G[col] : 0.0;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = wv * 16 + 4 * lg + r, col = ct * 16 + lc;
-                const float D = row >= col ? expf(float(s.G[row] - s.G[col])) : 0.0f;
-                const float b = ws.backward ? delta_beta_safe(s.g.beta[row]) : s.g.beta[row];
-                s.L[row * LC + col] = row > col ? b * (D * kk[ct][r]) : 0.0f;
-                s.X[row * LC + col] = row >= col ? a.scale * (D * qk[ct][r]) : 0.0f;
+                const int row = wv * 16 + 4 * lg + r;
+                float l = 0.0f, x = 0.0f;
+                if (ct <= wv) {
+                    const float D = exp2_of(Gr[r] - Gc);
+                    l = row > col ? b[r] * (D * kk[ct][r]) : 0.0f;
+                    x = row >= col ? a.scale * (D * qk[ct][r]) : 0.0f;
+                }
+                s.L[row * LC + col] = l;
+                s.X[row * LC + col] = x;
             }
+        }
     }
-    __syncthreads();
+    lds_barrier();
     ChunkMats<C, NP> *out = reinterpret_cast<ChunkMats<C, NP> *>(ws.mats) + n;
     put_pieces<C, NP>(s.X, &out->P[0][0][0]);
     if (tid < int(sizeof(Gates<C>) / 4)) reinterpret_cast<float *>(&out->g)[tid] = reinterpret_cast<const float *>(&s.g)[tid];
-    __syncthreads();
-    for (int i = tid; i < C * LC; i += 256) s.X[i] = 0.0f;
-    __syncthreads();
+    lds_barrier();     // X's blocks above the diagonal stay the zeros that P has there
     // the inverse of I + L: the 16 x 16 diagonal blocks by substitution, one column per lane
     if (wv < NT && lane < 16) {
         const float *L = s.L + wv * 16 * (LC + 1);
@@ -130,31 +143,36 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
 #pragma unroll
             for (int j = 0; j < i; ++j) v = fmaf(-L[i * LC + j], x[j], v);
             x[i] = v;
-            s.X[(wv * 16 + i) * LC + wv * 16 + lane] = v;
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s.X[(wv * 16 + i) * LC + wv * 16 + lane] = x[i];
     }
-    __syncthreads();
-    // ... then [A 0; B D]^-1 = [A^-1 0; -D^-1 B A^-1 D^-1] of blocks of 16 and 32; B A^-1 takes B's place in L
+    lds_barrier();
+    // ... then [A 0; B D]^-1 = [A^-1 0; -D^-1 B A^-1 D^-1]: of blocks of 16, a wavefront each with B A^-1 in B's place,
+    auto put = [&](float *d, float sign, dt4 x) {
 #pragma unroll
-    for (int b = 1; b < NT; b *= 2) {
-        const int per = b * b, work = NT / (2 * b) * per;     // at most 4 blocks, one per wavefront
-        const int pair = wv / per, rt = pair * 2 * b + b + wv % per / b, ct = pair * 2 * b + wv % per % b;
+        for (int r = 0; r < 4; ++r) d[(4 * lg + r) * LC + lc] = sign * x[r];
+    };
+    if (wv < NT / 2) {
+        const int at = (wv * 32 + 16) * LC + wv * 32;
+        put(s.L + at, 1.0f, f32_mma(s.L + at, s.X + wv * 32 * (LC + 1), LC, dt4{}));
+        __builtin_amdgcn_wave_barrier();
+        put(s.X + at, -1.0f, f32_mma(s.X + at + 16, s.L + at, LC, dt4{}));
+    }
+    lds_barrier();
+    // ... and of blocks of 32, a 16 x 16 tile per wavefront, with B A^-1 in the block above the diagonal, which nobody reads.
+    if constexpr (C == 64) {
+        const int r0 = wv / 2 * 16, c0 = wv % 2 * 16;
+        dt4 x{};
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-            dt4 acc{};
-            if (wv < work)
-                for (int i = 0; i < b; ++i) {
-                    const int kb = pair * 2 * b + (pass ? b : 0) + i;
-                    acc = f32_mma((pass ? s.X : s.L) + rt * 16 * LC + kb * 16, (pass ? s.L : s.X) + kb * 16 * LC + ct * 16, LC, acc);
-                }
-            __syncthreads();
-            if (wv < work) {
-                float *d = (pass ? s.X : s.L) + (rt * 16 + 4 * lg) * LC + ct * 16 + lc;
+        for (int kb = 0; kb < 32; kb += 16) x = f32_mma(s.L + (32 + r0) * LC + kb, s.X + kb * LC + c0, LC, x);
+        put(s.X + r0 * LC + 32 + c0, 1.0f, x);
+        lds_barrier();
+        x = dt4{};
 #pragma unroll
-                for (int r = 0; r < 4; ++r) d[r * LC] = pass ? -acc[r] : acc[r];
-            }
-            __syncthreads();
-        }
+        for (int kb = 0; kb < 32; kb += 16) x = f32_mma(s.X + (32 + r0) * LC + 32 + kb, s.X + kb * LC + 32 + c0, LC, x);
+        put(s.X + (32 + r0) * LC + c0, -1.0f, x);
+        lds_barrier();
     }
     put_pieces<C, 3>(s.X, &out->X[0][0][0]);
 }

@@ -220,20 +220,6 @@ template <typename T, int C, int KP> struct GradLds {
     Gates<C> g;
 };
 
-// G of a chunk again (delta_prep_kernel), by one wavefront.
-template <int C> __device__ __forceinline__ void chunk_G(const DeltaArgs &a, int p, int h, int t0, int live, double *G) {
-    const int lane = threadIdx.x & 63;
-    float g = lane < C && lane < live ? a.g[(int64_t(p) * a.T + t0 + lane) * a.Hv + h] : 0.0f;
-    if (g < -1e4f) g = -1e4f;
-    double x = double(g);
-#pragma unroll
-    for (int d = 1; d < C; d <<= 1) {
-        const double o = __shfl_up(x, d, 64);
-        if (lane >= d) x += o;
-    }
-    if (lane < C) G[lane] = x;
-}
-
 template <typename T, int C, int KP>
 __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
     using Lds = GradLds<T, C, KP>;
@@ -257,7 +243,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
         const T *go = static_cast<const T *>(gr.data) + p * gr.sp + t0 * gr.st + h * gr.sh;
         const ChunkMats<C, 3> *mats = reinterpret_cast<const ChunkMats<C, 3> *>(ws.mats) + nc;
         if (tid < int(sizeof(Gates<C>) / 4)) reinterpret_cast<float *>(&s.g)[tid] = reinterpret_cast<const float *>(&mats->g)[tid];
-        if (wv == 3) chunk_G<C>(a, p, h, t0, live, s.G);
+        if (wv == 3) {
+            const double G = chunk_G<C>(a, p, h, t0, live);
+            if (lane < C) s.G[lane] = G;
+        }
         // over V: dP, dA (transposed: columns i, rows j), S do^T, S Y^T, dS U^T
         dt4 dP[NJ][2] = {}, dA[NJ][2] = {}, oS[KW][2] = {}, yS[KW][2] = {}, uS[KW][2] = {};
         double cc = 0.0;
@@ -312,7 +301,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
                     *reinterpret_cast<db8 *>(s.dS[n][b] + block_at(row, lg)) = fy.p[n];
                 }
             }
-            __syncthreads();
+            lds_barrier();
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {    // tile e of the columns i, both tiles of the rows j
                 const int m = wv + 4 * j, b = m / 2, e = m & 1, bi = b > 0, bj = b == 2;
@@ -337,7 +326,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
                     yS[b][e] = mma<3>(fs, fy, yS[b][e]);
                     uS[b][e] = mma<3>(read_cols<3>(s.dS[0][kb0 + b], KB * kBlk, e), fu, uS[b][e]);
                 }
-            __syncthreads();
+            lds_barrier();
         }
         // Y . U of each token: over the 16 columns of a lane group, then the two column groups
         if (tid < TB * 128) {
@@ -370,7 +359,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
                 }
             }
         }
-        __syncthreads();
+        lds_barrier();
         // D, P and A again, and the weights of k and q in the gradients (accumulators: rows j, columns i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -396,7 +385,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int jj = bj * 32 + lg * 8 + y * 4 + r;
-                    const float D = i >= jj ? expf(float(Gi - s.G[jj])) : 0.0f;
+                    const float D = i >= jj ? exp2_of(Gi - s.G[jj]) : 0.0f;
                     wq[y][r] = i >= jj ? a.scale * (D * dP[j][y][r]) : 0.0f;
                     wa[y][r] = i > jj ? -beta * (D * dA[j][y][r]) : 0.0f;
                     s.M[i * (C + 1) + jj] = i > jj ? fmaf(wq[y][r], qk[y][r], wa[y][r] * kk[y][r]) : 0.0f;
@@ -448,7 +437,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
                 s.bj[wv / NT][tok] = bj;
             }
         }
-        __syncthreads();
+        lds_barrier();
         // the pairs' part: the tokens as i (depth j up to them) and as j (depth i from them on)
 #pragma unroll
         for (int x = 0; x < TB; ++x) {
@@ -484,7 +473,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
             for (int i = j + 1; i < C; ++i) x += double(s.M[i * (C + 1) + j]);
             s.colm[j] = x;
         }
-        __syncthreads();
+        lds_barrier();
         if (tid < live) {
             const int m = tid;
             double x = double(s.g.last) * (s.cs[0] + s.cs[1] + s.cs[2] + s.cs[3]);
@@ -498,7 +487,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
             d.g[at] = float(x);
             d.beta[at] = (s.ub[0][m] + s.ub[1][m]) / delta_beta_safe(s.g.beta[m]);
         }
-        __syncthreads();
+        lds_barrier();
     }
     const int rows = min(C, a.T - t0);
     for (int i = tid; i < rows * group; i += 256) {

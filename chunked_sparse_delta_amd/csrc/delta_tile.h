@@ -37,6 +37,13 @@ template <int N> struct Frag {
     db8 p[N];
 };
 
+// A workgroup barrier that orders LDS only: nothing waits for loads or stores of memory on their way.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // LDS accesses keep their side of this point (other instructions may cross): the operands of the
 // products to come are read before the products at hand, whose 16 cycles each hide the way to LDS.
 __device__ __forceinline__ void lds_point() { __builtin_amdgcn_sched_barrier(0x7F); }
@@ -174,6 +181,23 @@ template <typename T> constexpr int kChunk = sizeof(T) == 2 ? 64 : 32;
 
 // The beta that the backward computes U with: its U / beta is the write error for every beta.
 __device__ __forceinline__ float delta_beta_safe(float b) { return fabsf(b) < 1e-20f ? 1e-20f : b; }
+
+// The running sum of a chunk's log-decays, over log 2 (so that exp2_of of a difference is the decay between two tokens), by one
+// wavefront: a token per lane. In 64 bits: differences are as exact as the log-decays themselves however large the sum
+// grew. A log-decay below -1e4 (-inf among them: it clears the state) counts as -1e4, whose exponential is 0 too.
+template <int C> __device__ __forceinline__ double chunk_G(const DeltaArgs &a, int p, int h, int t0, int live) {
+    const int lane = threadIdx.x & 63;
+    float g = lane < C && lane < live ? a.g[(int64_t(p) * a.T + t0 + lane) * a.Hv + h] : 0.0f;
+    if (g < -1e4f) g = -1e4f;
+    double G = double(g) * 1.4426950408889634;
+#pragma unroll
+    for (int d = 1; d < C; d <<= 1) {
+        const double o = __shfl_up(G, d, 64);
+        if (lane >= d) G += o;
+    }
+    return G;
+}
+__device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f(float(x)); }
 
 // A chunk's gates, as delta_prep_kernel leaves them: beta, exp(G), exp(G_last - G) of every token (0 for padding tokens,
 // whose rows the kernels then need not clear), exp(G_last).

@@ -38,18 +38,11 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
     static constexpr int kBufs = 2 * sizeof(Lds) <= kDeltaMaxLds ? 2 : 1;
     static constexpr size_t kLds = kBufs * sizeof(Lds);
 
-    // Orders LDS only: nothing waits for loads or stores of memory on their way.
-    static __device__ __forceinline__ void barrier() {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    }
-
     // The computing wavefronts' side: the i-th chunk taken is in buffer i & (kBufs - 1) after begin() and i times turn().
-    static __device__ __forceinline__ void begin() { barrier(); }
+    static __device__ __forceinline__ void begin() { lds_barrier(); }
     static __device__ __forceinline__ void turn() {
-        barrier();
-        if constexpr (kBufs == 1) barrier();
+        lds_barrier();
+        if constexpr (kBufs == 1) lds_barrier();
     }
 
     // The other side. val: v, or what takes its place; cg: the column group of the wavefront four before this one.
@@ -116,12 +109,12 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
                 store(bufs[0]);
             }
             if (count > 1) load(c0 + dir);
-            barrier();
+            lds_barrier();
             for (int i = 0; i < count; ++i) {
-                if constexpr (kBufs == 1) barrier();
+                if constexpr (kBufs == 1) lds_barrier();
                 if (i + 1 < count) store(bufs[(i + 1) & (kBufs - 1)]);
                 if (i + 2 < count) load(c0 + (i + 2) * dir);
-                barrier();
+                lds_barrier();
             }
         }
     };
