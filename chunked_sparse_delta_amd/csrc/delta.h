@@ -45,9 +45,15 @@ struct DeltaWs {
     unsigned char *mats;   // [n] ChunkMats
     float *U, *Y;          // rows: the chunk's tokens (backward)
     float *S, *dS;         // rows: the padded head_dim; start states, gradients of the end states (backward)
-    int32_t Nt;
+    // A sequence may be walked in `segs` segments of seg_chunks chunks at once (delta_segments): their start states [seg]
+    // [stream * Hv + head][KP][VP] and the maps from a segment's start state to its end state [seg][..][KP][KP].
+    float *seg_state, *seg_map;
+    int32_t Nt, segs, seg_chunks;
     bool backward;         // X is computed for the backward (delta_beta_safe)
 };
+
+// Segments of Nt chunks for `heads` states walked by `slices` workgroups each.
+int delta_segments(int64_t heads, int slices, int K, int Nt);
 
 struct DeltaGrads {
     Rows go;                 // [P, T, Hv, V]

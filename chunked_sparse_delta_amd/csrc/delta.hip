@@ -181,30 +181,49 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
 // accumulators through the whole sequence, and the four wavefronts of a workgroup share the
 // chunk's k, q, X and P in LDS. One wavefront per SIMD has nothing beside it to hide its waits: the
 // operands of each group of products are read from LDS before the group ahead of it.
-// SAVE: keeps U and each chunk's start state for the backward, and gives no output.
-template <typename T, int C, int KP, bool SAVE>
+// kRead gives the readings. kSave keeps U and each chunk's start state for the backward instead. kMap, for sequences
+// walked in segments at once: the segment's end state from a start state of zeros (the first's: from the caller's) and, in
+// workgroups of their own, what it makes of the columns of the identity, with v = 0: the two give a segment's end state from any
+// start state (delta_join_kernel).
+enum { kRead, kSave, kMap };
+template <typename T, int C, int KP, int MODE>
 __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, DeltaWs ws) {
+    constexpr bool SAVE = MODE == kSave, READ = MODE == kRead;
     constexpr int NI = kPieces<T>, NP = kPPieces<T>(SAVE), KB = KP / 32, TB = C / 32, NTR = kTri<C>;
     constexpr int NS = NI == 1 ? 2 : 3;    // pieces of S and U that reach the readings only
-    using W = Walk<T, C, KP, NP, !SAVE>;
+    using W = Walk<T, C, KP, NP, READ>;
     extern __shared__ __align__(16) unsigned char raw[];
     typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
-    const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
-    const int slice = blockIdx.x % slices, ph = blockIdx.x / slices, h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
+    const int vslices = (a.V + 63) / 64, VG = (a.V + 15) / 16, VP = VG * 16, heads = a.P * a.Hv;
+    const int slices = MODE == kMap ? vslices + KP / 64 : vslices, seg = blockIdx.x / (heads * slices);
+    const int block = blockIdx.x % (heads * slices), slice = block_slice(block, slices, heads);
+    const int ph = block_head(block, slices, heads), h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
+    const bool map = MODE == kMap && slice >= vslices;     // columns of the identity
+    if (map && seg == 0) return;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lc = lane & 15, lg = lane >> 4;
-    const int cg = slice * 4 + (wv & 3), col = cg * 16 + lc;
-    const bool in = col < a.V;
-    const int n = delta_valid(a, p), Nc = (n + C - 1) / C;
+    const int cg = (map ? slice - vslices : slice) * 4 + (wv & 3), col = cg * 16 + lc;
+    const bool in = !map && col < a.V;
+    const int n = delta_valid(a, p), Nc = (n + C - 1) / C, c0 = seg * ws.seg_chunks, c1 = min(c0 + ws.seg_chunks, Nc);
     if (wv >= 4) {
         typename W::Bring w(a, ws, p, h, hk, ph, cg, a.v, n);
-        w.run(bufs, 0, 1, Nc);
+        w.run(bufs, c0, 1, c1 - c0);
         return;
     }
+    float *seg_state = ws.seg_state + int64_t(seg) * heads * KP * VP;
     const int oc = cg * 16 + lg * 4;   // readings come transposed: a lane holds four columns of the tokens block_row(lc, .)
     T *out = static_cast<T *>(a.out) + (int64_t(p) * a.T * a.Hv + h) * a.V;
     const int os = a.Hv * a.V;
     dt4 S[KB][2];
-    load_state<KB>(S, a.state, ph, a.K, a.V, col);
+    if (seg == 0) load_state<KB>(S, a.state, ph, a.K, a.V, col);
+    else if (READ) load_state<KB>(S, seg_state, ph, KP, VP, col);
+    else {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[kb][e][r] = map && kb * 32 + lg * 8 + e * 4 + r == col ? 1.0f : 0.0f;
+    }
     W::begin();
     dt4 y[TB][2] = {};
     const int left = a.V - oc;
@@ -231,10 +250,10 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
     Frag<3> fs[KB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
-    for (int c = 0; c < Nc; ++c) {
-        const typename W::Lds &s = bufs[c & (W::kBufs - 1)];
+    for (int c = c0; c < c1; ++c) {
+        const typename W::Lds &s = bufs[(c - c0) & (W::kBufs - 1)];
         const Gates<C> &g = s.m.g;
-        if (!SAVE && c > 0) put(c - 1);
+        if (READ && c > c0) put(c - 1);
         // k S and q S
         Frag<NI> A[2][TB][2];
         auto rows_of = [&](Frag<NI>(&f)[TB][2], const unsigned char *m) {
@@ -252,7 +271,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
             for (int e = 0; e < 2; ++e) {
                 const int t = tb * 32 + lg * 8 + e * 4;
                 v[tb][e] = W::value(s, tb, e);
-                if (SAVE && !in) v[tb][e] = dt4{};
+                if (!READ && !in) v[tb][e] = dt4{};
                 b[tb][e] = *reinterpret_cast<const dt4 *>(g.beta + t);
                 eG[tb][e] = *reinterpret_cast<const dt4 *>(g.eG + t);
                 et[tb][e] = g.eG[tb * 32 + block_row(lc, e)];
@@ -262,7 +281,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
         dt4 x[TB][2] = {};
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb) y[tb][0] = y[tb][1] = dt4{};
-        constexpr int KQ = SAVE ? KB : 2 * KB;
+        constexpr int KQ = READ ? 2 * KB : KB;
         Frag<3> fx[2][2], fr[TB];    // X's blocks, a step ahead
         auto x_of = [&](Frag<3>(&f)[2], int i) {
 #pragma unroll
@@ -321,7 +340,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
 #pragma unroll
         for (int i = 0; i < NTR; ++i) {
             if (i + 1 < NTR) x_of(fx[(i + 1) & 1], i + 1);
-            else if constexpr (!SAVE) p_of(fp[0], 0);
+            else if constexpr (READ) p_of(fp[0], 0);
             else kt_of(fk[0], 0);
             lds_point();
             each_product<3, 3, 3>([&](int m, int l) {
@@ -338,7 +357,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
             for (int e = 0; e < 2; ++e) eL[tb][e] = *reinterpret_cast<const dt4 *>(g.eL + tb * 32 + lg * 8 + e * 4);
         const float last = g.last;
         if constexpr (SAVE) save_blocks<TB>(ws.U, nc, VG, cg, U);
-        else {
+        if constexpr (READ) {
             Frag<NS> fv[TB];
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
@@ -386,11 +405,53 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
         for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
         W::turn();
     }
-    if constexpr (!SAVE) {
-        if (Nc > 0) put(Nc - 1);
-        for (int t = n + lc; t < a.T; t += 16)
+    if constexpr (READ) {
+        if (c1 > c0) put(c1 - 1);
+        const int end = seg + 1 < ws.segs ? min(a.T, (c0 + ws.seg_chunks) * C) : a.T;
+        for (int t = max(n, c0 * C) + lc; t < end; t += 16)
             if (left > 0) put_four(out + (int64_t(t) * os + oc), left, dt4{});
-        store_state<KB>(S, a.state_out, ph, a.K, a.V, col);
+        // the segment with the last chunk; the first one where there is none
+        if (seg == (Nc > 0 ? (Nc - 1) / ws.seg_chunks : 0)) store_state<KB>(S, a.state_out, ph, a.K, a.V, col);
+    }
+    if constexpr (MODE == kMap) {
+        if (map) store_state<KB>(S, ws.seg_map + int64_t(seg) * heads * KP * KP, ph, KP, KP, col);
+        else store_state<KB>(S, seg_state + int64_t(heads) * KP * VP, ph, KP, VP, col);
+    }
+}
+
+// The segments' start states from their maps M and their end states from zeros N, in order: S_{i + 1} = M_i S_i + N_i. A
+// wavefront takes 16 columns; the next rows of M are on their way under the products.
+template <int KP> __global__ __launch_bounds__(256, 1) void delta_join_kernel(DeltaWs ws, int heads, int VP) {
+    constexpr int KB = KP / 32;
+    const int slices = (VP + 63) / 64, slice = blockIdx.x % slices, ph = blockIdx.x / slices;
+    const int lane = threadIdx.x & 63, lc = lane & 15, lg = lane >> 4, col = (slice * 4 + int(threadIdx.x >> 6)) * 16 + lc;
+    dt4 S[KB][2], N[KB][2];
+    load_state<KB>(S, ws.seg_state + int64_t(heads) * KP * VP, ph, KP, VP, col);
+    for (int i = 1; i + 1 < ws.segs; ++i) {
+        float *next = ws.seg_state + int64_t(i + 1) * heads * KP * VP;
+        load_state<KB>(N, next, ph, KP, VP, col);
+        Frag<3> fs[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
+        const float *M = ws.seg_map + (int64_t(i) * heads + ph) * KP * KP + lg * 8;
+        dt4 m[2][KB][2];
+        auto load = [&](dt4(&x)[KB][2], int t) {     // row tile t of M
+            const float *row = M + (t / 2 * 32 + block_row(lc, t & 1)) * KP;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) x[kb][e] = *reinterpret_cast<const dt4 *>(row + kb * 32 + e * 4);
+        };
+        load(m[0], 0);
+#pragma unroll
+        for (int t = 0; t < 2 * KB; ++t) {
+            if (t + 1 < 2 * KB) load(m[(t + 1) & 1], t + 1);
+            dt4 x[2] = {N[t / 2][t & 1], dt4{}};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) x[kb & 1] = mma<3>(split<3>(m[t & 1][kb][0], m[t & 1][kb][1]), fs[kb], x[kb & 1]);
+            S[t / 2][t & 1] = x[0] + x[1];
+        }
+        store_state<KB>(S, next, ph, KP, VP, col);
     }
 }
 
@@ -421,7 +482,7 @@ template <typename T> __global__ __launch_bounds__(256) void delta_copy_values_k
 }
 
 template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const DeltaWs &ws, hipStream_t st) {
-    const dim3 chunks(unsigned(int64_t(a.P) * a.Hv * ws.Nt)), grid(unsigned(int64_t(a.P) * a.Hv * ((a.V + 63) / 64)));
+    const dim3 chunks(unsigned(int64_t(a.P) * a.Hv * ws.Nt));
     constexpr int N0 = kPPieces<T>(false), N1 = kPPieces<T>(true);
     if (ws.Nt > 0) {
         if (ws.backward) hipLaunchKernelGGL((delta_prep_kernel<T, C, KP, N1>), chunks, dim3(256), 0, st, a, ws);
@@ -429,10 +490,19 @@ template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (ws.backward)
-        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, true>), grid, dim3(kWalkThreads), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
-    else
-        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, false>), grid, dim3(kWalkThreads), (Walk<T, C, KP, N0, true>::kLds), st, a, ws);
+    const unsigned heads = unsigned(a.P) * unsigned(a.Hv), slices = unsigned(a.V + 63) / 64;
+    if (ws.backward) {
+        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kSave>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
+        return hipGetLastError();
+    }
+    if (ws.segs > 1) {
+        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kMap>), dim3(heads * (slices + KP / 64) * unsigned(ws.segs - 1)), dim3(kWalkThreads),
+                           (Walk<T, C, KP, N0, false>::kLds), st, a, ws);
+        hipLaunchKernelGGL(delta_join_kernel<KP>, dim3(heads * slices), dim3(256), 0, st, ws, int(heads), (a.V + 15) / 16 * 16);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kRead>), dim3(heads * slices * unsigned(ws.segs)), dim3(kWalkThreads), (Walk<T, C, KP, N0, true>::kLds), st, a, ws);
     return hipGetLastError();
 }
 template <typename T> hipError_t fwd_pick(const DeltaArgs &a, const DeltaWs &ws, hipStream_t st) {
@@ -447,10 +517,12 @@ template <typename T, int C, int KP> hipError_t fwd_attr() {
     constexpr int N0 = kPPieces<T>(false), N1 = kPPieces<T>(true);
     constexpr size_t l0 = Walk<T, C, KP, N0, true>::kLds, l1 = Walk<T, C, KP, N1, false>::kLds;
     static_assert(l0 <= kDeltaMaxLds && l1 <= kDeltaMaxLds, "LDS of a workgroup");
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_state_kernel<T, C, KP, false>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, l0);
-    return e != hipSuccess ? e : hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_state_kernel<T, C, KP, true>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, l1);
+    auto set = [](auto kernel, size_t bytes) {
+        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    };
+    hipError_t e = set(&delta_state_kernel<T, C, KP, kRead>, l0);
+    if (e == hipSuccess) e = set(&delta_state_kernel<T, C, KP, kSave>, l1);
+    return e == hipSuccess ? set(&delta_state_kernel<T, C, KP, kMap>, Walk<T, C, KP, N0, false>::kLds) : e;
 }
 template <typename T> hipError_t fwd_attrs() {
     hipError_t e = fwd_attr<T, kChunk<T>, 64>();
@@ -497,6 +569,27 @@ hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool
     else hipLaunchKernelGGL(delta_copy_values_kernel<float>, grid, dim3(256), 0, st, *r, static_cast<float *>(to), rows, T, H, VP);
     *r = {to, int64_t(T) * H * VP, int64_t(H) * VP, VP, VP};
     return hipGetLastError();
+}
+
+// A workgroup walks a sequence's chunks one after the other, at a pace that hardly depends on the others: few states leave
+// most of the device idle. Walking segments at once costs the readings' walk again, once for the columns of the state and once
+// for those of the map, a third cheaper (no readings), and a join of about a chunk's time per segment.
+int delta_segments(int64_t heads, int slices, int K, int Nt) {
+    constexpr int64_t kCus = 256;
+    const int64_t wgs = heads * slices, maps = heads * (slices + delta_kp(K) / 64);
+    int best = 1;
+    double least = double(Nt);
+    if (wgs * 2 > kCus) return 1;
+    for (int g = 3; g <= 32 && Nt / g >= 4; ++g) {
+        const int64_t len = (Nt + g - 1) / g;
+        const int64_t a = (wgs + (g - 2) * maps + kCus - 1) / kCus, b = (wgs * g + kCus - 1) / kCus;
+        const double t = double(len) * (0.7 * double(a) + double(b)) + 1.2 * double(g) + 6.0;
+        if (t < 0.9 * least) {
+            least = t / 0.9 < least ? t : least;
+            best = g;
+        }
+    }
+    return best;
 }
 
 size_t delta_mats_bytes(int K, bool is_bf16, bool backward) {

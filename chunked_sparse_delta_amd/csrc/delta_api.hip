@@ -92,6 +92,13 @@ Layout layout(const sdm_delta_shape *s, bool backward, void *base) {
         l.ws.S = floats(n * KP * VP);
         l.ws.dS = floats(n * KP * VP);
     }
+    const size_t heads = size_t(s->streams) * size_t(s->value_heads);
+    l.ws.segs = backward ? 1 : delta_segments(int64_t(heads), (s->value_dim + 63) / 64, s->head_dim, int(Nt));
+    l.ws.seg_chunks = l.ws.segs > 1 ? int32_t((Nt + size_t(l.ws.segs) - 1) / size_t(l.ws.segs)) : int32_t(Nt);
+    if (l.ws.segs > 1) {
+        l.ws.seg_state = floats(size_t(l.ws.segs) * heads * KP * VP);
+        l.ws.seg_map = floats(size_t(l.ws.segs) * heads * KP * KP);
+    }
     const size_t keys = rows * size_t(s->key_heads) * KP * (b16 ? 2 : 6);
     const size_t values = rows * size_t(s->value_heads) * ((size_t(s->value_dim) + 7) / 8 * 8) * (b16 ? 2 : 4);
     l.q = take(keys);

@@ -31,7 +31,8 @@ __global__ __launch_bounds__(kWalkThreads) void delta_back_kernel(DeltaArgs a, D
     extern __shared__ __align__(16) unsigned char raw[];
     typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
-    const int slice = blockIdx.x % slices, ph = blockIdx.x / slices, h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
+    const int slice = block_slice(blockIdx.x, slices, a.P * a.Hv), ph = block_head(blockIdx.x, slices, a.P * a.Hv);
+    const int h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lc = lane & 15, lg = lane >> 4;
     const int cg = slice * 4 + (wv & 3), col = cg * 16 + lc;
     const bool in = col < a.V;

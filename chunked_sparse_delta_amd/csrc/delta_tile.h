@@ -205,6 +205,13 @@ template <int C> struct Gates {
     float beta[C], eG[C], eL[C], last, pad[255 - 3 * C];
 };
 
+// Slice and head of a block: the slices of a head, which read the same q and k, go to one XCD (blocks are dealt to the
+// eight in turn).
+__device__ __forceinline__ int block_slice(int b, int slices, int heads) { return (heads % kXcds ? b : b / kXcds) % slices; }
+__device__ __forceinline__ int block_head(int b, int slices, int heads) {
+    return heads % kXcds ? b / slices : b / kXcds / slices * kXcds + b % kXcds;
+}
+
 // What the prep kernel leaves of a chunk for the kernels that walk it: the lower 32 x 32
 // blocks of X and P in pieces (LDS images), and the gates.
 template <int C> constexpr int kTri = C == 64 ? 3 : 1;     // blocks (0, 0), (1, 0), (1, 1)

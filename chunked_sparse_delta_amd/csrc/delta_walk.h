@@ -171,9 +171,9 @@ __device__ __forceinline__ void put_four(float *p, int left, dt4 x) {
 }
 
 // The wavefront's 16 columns of a [K, V] state, zeros past its ends and where there is none.
-template <int KB> __device__ __forceinline__ void load_state(dt4 (&S)[KB][2], const float *state, int ph, int K, int V, int col) {
+template <int KB> __device__ __forceinline__ void load_state(dt4 (&S)[KB][2], const float *state, int64_t ph, int K, int V, int col) {
     const int lg = (threadIdx.x & 63) >> 4;
-    const float *src = state + int64_t(ph) * K * V + col;
+    const float *src = state + ph * K * V + col;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -184,10 +184,10 @@ template <int KB> __device__ __forceinline__ void load_state(dt4 (&S)[KB][2], co
                 S[kb][e][r] = state && col < V && row < K ? src[int64_t(row) * V] : 0.0f;
             }
 }
-template <int KB> __device__ __forceinline__ void store_state(const dt4 (&S)[KB][2], float *state, int ph, int K, int V, int col) {
+template <int KB> __device__ __forceinline__ void store_state(const dt4 (&S)[KB][2], float *state, int64_t ph, int K, int V, int col) {
     if (!state || col >= V) return;
     const int lg = (threadIdx.x & 63) >> 4;
-    float *dst = state + int64_t(ph) * K * V + col;
+    float *dst = state + ph * K * V + col;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
