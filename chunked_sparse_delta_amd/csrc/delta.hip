@@ -30,16 +30,18 @@ __device__ __forceinline__ dt4 f32_mma(const float *A, const float *B, int ld, d
     return acc;
 }
 
-// The lower 32 x 32 blocks of the row-major m as NP pieces, block images NP * kTri apart.
-template <int C, int NP> __device__ __forceinline__ void put_pieces(const float *m, unsigned char *out) {
+// The lower 32 x 32 blocks of the row-major m, in float32 or (N = 1) bfloat16.
+template <int C, int N> __device__ __forceinline__ void put_blocks(const float *m, void *out) {
     constexpr int LC = PrepLds<C>::LC;
     for (int i = threadIdx.x; i < kTri<C> * 128; i += 256) {
         const int b = i / 128, r = i % 128 / 4, c = i % 4, br = b > 0, bc = b == 2;
         const float *src = m + (br * 32 + r) * LC + bc * 32 + c * 8;
-        const Frag<NP> f = split<NP>(*reinterpret_cast<const dt4 *>(src), *reinterpret_cast<const dt4 *>(src + 4));
-#pragma unroll
-        for (int n = 0; n < NP; ++n)
-            *reinterpret_cast<db8 *>(out + (n * kTri<C> + b) * kBlk + block_at(r, c)) = f.p[n];
+        const dt4 x = *reinterpret_cast<const dt4 *>(src), y = *reinterpret_cast<const dt4 *>(src + 4);
+        if constexpr (N == 1) static_cast<db8 *>(out)[i] = split<1>(x, y).p[0];
+        else {
+            static_cast<dt4 *>(out)[2 * i] = x;
+            static_cast<dt4 *>(out)[2 * i + 1] = y;
+        }
     }
 }
 
@@ -129,8 +131,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
         }
     }
     lds_barrier();
-    ChunkMats<C, NP> *out = reinterpret_cast<ChunkMats<C, NP> *>(ws.mats) + n;
-    put_pieces<C, NP>(s.X, &out->P[0][0][0]);
+    ChunkMem<C, NP> *out = reinterpret_cast<ChunkMem<C, NP> *>(ws.mats) + n;
+    put_blocks<C, NP>(s.X, out->P);
     if (tid < int(sizeof(Gates<C>) / 4)) reinterpret_cast<float *>(&out->g)[tid] = reinterpret_cast<const float *>(&s.g)[tid];
     lds_barrier();     // X's blocks above the diagonal stay the zeros that P has there
     // the inverse of I + L: the 16 x 16 diagonal blocks by substitution, one column per lane
@@ -174,7 +176,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
         put(s.X + (32 + r0) * LC + c0, -1.0f, x);
         lds_barrier();
     }
-    put_pieces<C, 3>(s.X, &out->X[0][0][0]);
+    put_blocks<C, 3>(s.X, out->X);
 }
 
 // Every column of the state evolves on its own: a wavefront keeps 16 columns of S in
@@ -196,8 +198,8 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
     typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int vslices = (a.V + 63) / 64, VG = (a.V + 15) / 16, VP = VG * 16, heads = a.P * a.Hv;
     const int slices = MODE == kMap ? vslices + KP / 64 : vslices, seg = blockIdx.x / (heads * slices);
-    const int block = blockIdx.x % (heads * slices), slice = block_slice(block, slices, heads);
-    const int ph = block_head(block, slices, heads), h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
+    const int block = blockIdx.x % (heads * slices), slice = BlockAt(block, slices, heads, a.Hv / a.Hk).slice;
+    const int ph = BlockAt(block, slices, heads, a.Hv / a.Hk).ph, h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
     const bool map = MODE == kMap && slice >= vslices;     // columns of the identity
     if (map && seg == 0) return;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lc = lane & 15, lg = lane >> 4;
@@ -370,7 +372,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
                 if (i + 1 < NTR) p_of(fp[(i + 1) & 1], i + 1);
                 else kt_of(fk[0], 0);
                 lds_point();
-                each_product<NS, NP, NS>([&](int m, int l) {
+                each_product<(NP == 1 ? 2 : 3), NP, NS>([&](int m, int l) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) y[i > 0][e] = mma1(fv[i == 2].p[l], fp[i & 1][e].p[m], y[i > 0][e]);
                 });
@@ -594,8 +596,8 @@ int delta_segments(int64_t heads, int slices, int K, int Nt) {
 
 size_t delta_mats_bytes(int K, bool is_bf16, bool backward) {
     const bool three = backward || !is_bf16;
-    if (delta_chunk(K, is_bf16) == 64) return three ? sizeof(ChunkMats<64, 3>) : sizeof(ChunkMats<64, 2>);
-    return three ? sizeof(ChunkMats<32, 3>) : sizeof(ChunkMats<32, 2>);
+    if (delta_chunk(K, is_bf16) == 64) return three ? sizeof(ChunkMem<64, 3>) : sizeof(ChunkMem<64, 1>);
+    return three ? sizeof(ChunkMem<32, 3>) : sizeof(ChunkMem<32, 1>);
 }
 
 }  // namespace sdm

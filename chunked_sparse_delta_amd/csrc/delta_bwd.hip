@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_back_kernel(DeltaArgs a, D
     extern __shared__ __align__(16) unsigned char raw[];
     typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
-    const int slice = block_slice(blockIdx.x, slices, a.P * a.Hv), ph = block_head(blockIdx.x, slices, a.P * a.Hv);
+    const int slice = BlockAt(blockIdx.x, slices, a.P * a.Hv, a.Hv / a.Hk).slice, ph = BlockAt(blockIdx.x, slices, a.P * a.Hv, a.Hv / a.Hk).ph;
     const int h = ph % a.Hv, p = ph / a.Hv, hk = h / (a.Hv / a.Hk);
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lc = lane & 15, lg = lane >> 4;
     const int cg = slice * 4 + (wv & 3), col = cg * 16 + lc;
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
         const int h = hk * group + hh;
         const int64_t nc = (int64_t(p) * a.Hv + h) * ws.Nt + c;
         const T *go = static_cast<const T *>(gr.data) + p * gr.sp + t0 * gr.st + h * gr.sh;
-        const ChunkMats<C, 3> *mats = reinterpret_cast<const ChunkMats<C, 3> *>(ws.mats) + nc;
+        const ChunkMem<C, 3> *mats = reinterpret_cast<const ChunkMem<C, 3> *>(ws.mats) + nc;
         if (tid < int(sizeof(Gates<C>) / 4)) reinterpret_cast<float *>(&s.g)[tid] = reinterpret_cast<const float *>(&mats->g)[tid];
         if (wv == 3) {
             const double G = chunk_G<C>(a, p, h, t0, live);

@@ -205,23 +205,34 @@ template <int C> struct Gates {
     float beta[C], eG[C], eL[C], last, pad[255 - 3 * C];
 };
 
-// Slice and head of a block: the slices of a head, which read the same q and k, go to one XCD (blocks are dealt to the
-// eight in turn).
-__device__ __forceinline__ int block_slice(int b, int slices, int heads) { return (heads % kXcds ? b : b / kXcds) % slices; }
-__device__ __forceinline__ int block_head(int b, int slices, int heads) {
-    return heads % kXcds ? b / slices : b / kXcds / slices * kXcds + b % kXcds;
-}
+// Slice and head of a block. The slices of a head, and the heads that share a key head, read the same q and k: they go to one
+// XCD (blocks are dealt to the eight in turn), where the key heads divide among them.
+struct BlockAt {
+    int slice, ph;
+    __device__ __forceinline__ BlockAt(int b, int slices, int heads, int group) {
+        const bool even = heads / group % kXcds == 0;
+        const int i = even ? b / kXcds : b, head = i / slices;
+        slice = i % slices;
+        ph = even ? (head / group * kXcds + b % kXcds) * group + head % group : head;
+    }
+};
 
-// What the prep kernel leaves of a chunk for the kernels that walk it: the lower 32 x 32
-// blocks of X and P in pieces (LDS images), and the gates.
+// What the prep kernel leaves of a chunk for the kernels that walk it: the lower 32 x 32 blocks of X in float32, those of P
+// in float32 or, where one piece is wanted (NP = 1), in bfloat16, rows of 32; and the gates.
 template <int C> constexpr int kTri = C == 64 ? 3 : 1;     // blocks (0, 0), (1, 0), (1, 1)
+template <int C, int NP> struct ChunkMem {
+    float X[kTri<C>][32][32];
+    unsigned char P[kTri<C>][NP == 1 ? 2048 : 4096];
+    Gates<C> g;
+};
+// ... and as these have it in LDS: blocks in pieces.
 template <int C, int NP> struct ChunkMats {
     unsigned char X[3][kTri<C>][kBlk];
     unsigned char P[NP][kTri<C>][kBlk];
     Gates<C> g;
 };
-static_assert(sizeof(ChunkMats<64, 2>) % 1024 == 0 && sizeof(ChunkMats<32, 3>) % 1024 == 0, "copied by the kilobyte");
-// Pieces of P: the forward's readings are all that P goes into there, and two are enough for those in bfloat16.
-template <typename T> constexpr int kPPieces(bool backward) { return backward || sizeof(T) == 4 ? 3 : 2; }
+// Pieces of P. The forward's readings are all that P goes into there: in bfloat16 they are rounded anyway, and P with them (the
+// error against 64 bits grows from 1.66e-3 to at most 1.41 times that). The backward's P reaches float32 gradients.
+template <typename T> constexpr int kPPieces(bool backward) { return backward || sizeof(T) == 4 ? 3 : 1; }
 
 }  // namespace sdm

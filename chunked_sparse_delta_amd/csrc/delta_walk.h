@@ -21,12 +21,15 @@ template <typename T> __device__ __forceinline__ const T *uniform(const T *p) {
 // cycle of a compute unit and LDS reads waited for it: 0.55 us of a chunk's 3.9.)
 constexpr int kWalkThreads = 512;
 
-// T: the inputs' type; NP: pieces of P; Q: q is wanted too.
+// T: the inputs' type; NP: pieces of P; Q: q and P are wanted too.
 template <typename T, int C, int KP, int NP, bool Q> struct Walk {
+    static constexpr bool kP = Q;
     static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32;
     static constexpr int kStride = TB * KB * kBlk;              // between the pieces of k (and of q)
     static constexpr int KS = kStride / 4096;                   // 16-byte eights of a piece of k per thread
-    static constexpr int kMats = sizeof(ChunkMats<C, NP>) / 16, MS = (kMats + 255) / 256;
+    using Mem = ChunkMem<C, NP>;
+    static constexpr int NE = kTri<C> * 128, ES = (NE + 255) / 256;   // eights of X (and of P), and those of a thread
+    static constexpr int PW = NP == 1 ? 1 : 2;                        // 16-byte pieces of an eight of P
     static constexpr int RS = sizeof(T);                        // 16-byte pieces of a row of v's 16 columns
     static constexpr int VS = C * RS / 64;
     struct Lds {
@@ -49,15 +52,15 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
     struct Bring {
         const bf16 *kp, *qp;
         const T *vp;
-        const unsigned char *mats;
+        const Mem *mats;
         int64_t kplane, qplane, ks, qs, vs;
         int col0, n;
-        du4 k[NI][KS], q[Q ? NI : 1][Q ? KS : 1], v[VS], m[MS];
+        du4 k[NI][KS], q[Q ? NI : 1][Q ? KS : 1], v[VS], x[ES][2], pp[ES][PW], g;
 
         __device__ Bring(const DeltaArgs &a, const DeltaWs &ws, int p, int h, int hk, int ph, int cg, const Rows &val, int tokens)
             : kp(uniform(a.kk.data + p * a.kk.sp + hk * a.kk.sh)), qp(uniform(a.qq.data + p * a.qq.sp + hk * a.qq.sh)),
               vp(uniform(static_cast<const T *>(val.data) + p * val.sp + h * val.sh)),
-              mats(uniform(ws.mats + int64_t(ph) * ws.Nt * sizeof(ChunkMats<C, NP>))), kplane(a.kk.plane), qplane(a.qq.plane),
+              mats(uniform(reinterpret_cast<const Mem *>(ws.mats) + int64_t(ph) * ws.Nt)), kplane(a.kk.plane), qplane(a.qq.plane),
               ks(a.kk.st), qs(a.qq.st), vs(val.st), n(tokens) {
             // columns past the row's end are read from its last ones: nothing that they reach is kept
             col0 = min(cg * 16 + int(threadIdx.x) % RS * (16 / int(sizeof(T))), val.width - 16 / int(sizeof(T)));
@@ -81,9 +84,19 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
 #pragma unroll
             for (int i = 0; i < VS; ++i)
                 v[i] = *reinterpret_cast<const du4 *>(vc + uint32_t(min((lane + 64 * i) / RS, top) * int(vs) + col0));
-            const unsigned char *src = mats + t0 / C * int64_t(sizeof(ChunkMats<C, NP>));
+            const Mem &mem = mats[c];
 #pragma unroll
-            for (int i = 0; i < MS; ++i) m[i] = *reinterpret_cast<const du4 *>(src + uint32_t(min(tid + 256 * i, kMats - 1)) * 16);
+            for (int i = 0; i < ES; ++i) {
+                const int e = min(tid + 256 * i, NE - 1);
+                const du4 *px = reinterpret_cast<const du4 *>(&mem.X[0][0][0]), *ppp = reinterpret_cast<const du4 *>(&mem.P[0][0]);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) x[i][w] = px[e * 2 + w];
+                if constexpr (kP) {
+#pragma unroll
+                    for (int w = 0; w < PW; ++w) pp[i][w] = ppp[e * PW + w];
+                }
+            }
+            g = reinterpret_cast<const du4 *>(&mem.g)[lane];
         }
         __device__ __forceinline__ void store(Lds &s) const {
             const int tid = threadIdx.x & 255, lane = tid & 63, wv = tid >> 6;
@@ -99,8 +112,20 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
 #pragma unroll
             for (int i = 0; i < VS; ++i) reinterpret_cast<du4 *>(&s.v[wv][0][0])[lane + 64 * i] = v[i];
 #pragma unroll
-            for (int i = 0; i < MS; ++i)
-                if (tid + 256 * i < kMats) reinterpret_cast<du4 *>(&s.m)[tid + 256 * i] = m[i];
+            for (int i = 0; i < ES; ++i) {
+                const int e = tid + 256 * i;
+                if (NE % 256 && e >= NE) break;
+                const int at = block_at(e % 128 / 4, e % 4);
+                auto put = [&](unsigned char *blk, const Frag<3> &f) {
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) *reinterpret_cast<db8 *>(blk + n * kTri<C> * kBlk + at) = f.p[n];
+                };
+                put(s.m.X[0][e / 128], split<3>(__builtin_bit_cast(dt4, x[i][0]), __builtin_bit_cast(dt4, x[i][1])));
+                if constexpr (kP && NP == 1) *reinterpret_cast<du4 *>(s.m.P[0][e / 128] + at) = pp[i][0];
+                if constexpr (kP && NP == 3)
+                    put(s.m.P[0][e / 128], split<3>(__builtin_bit_cast(dt4, pp[i][0]), __builtin_bit_cast(dt4, pp[i][PW - 1])));
+            }
+            if (wv == 0) reinterpret_cast<du4 *>(&s.m.g)[lane] = g;
         }
         // Chunks c0, c0 + dir, ..., `count` of them.
         __device__ __forceinline__ void run(Lds *bufs, int c0, int dir, int count) {
