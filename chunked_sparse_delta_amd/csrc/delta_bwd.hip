@@ -199,177 +199,279 @@ __global__ __launch_bounds__(kWalkThreads) void delta_back_kernel(DeltaArgs a, D
     store_state<KB>(S, d.state, ph, a.K, a.V, col);
 }
 
-// Every chunk of a key head at once. The gradients of q and k are computed transposed (rows:
-// head_dim, columns: tokens), so that a lane's accumulators are eight neighbours of an output row;
-// U, Y, S and dS lie in LDS transposed too (rows: columns of V, as the workspace holds them). V is
-// taken 32 columns at a time.
+// Every chunk of a key head at once, its value heads in order. The gradients of q and k are computed transposed (rows:
+// head_dim, columns: tokens), so that a lane's accumulators are neighbours of an output row; U, Y, S and dS lie in
+// LDS transposed too (rows: columns of V, as the workspace holds them). A head goes by in stages: V, 32 columns at a time,
+// then q and k. Four wavefronts bring a stage's operands, cut into pieces, from memory to LDS while eight work on the stage before:
+// 16 tokens by a share of head_dim each.
+constexpr int kGradThreads = 768;
+
 template <typename T, int C, int KP> struct GradLds {
-    static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NM = NI == 1 ? 2 : 3;
-    union {
+    static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NM = NI == 1 ? 2 : 3, KG = 8 / (C / 16);
+    union Stage {
         struct {
             unsigned char go[NI][TB][kBlk], U[3][TB][kBlk], Y[3][TB][kBlk], S[3][KB][kBlk], dS[3][KB][kBlk];
         };
         struct {
             unsigned char k[NI][TB][KB][kBlk], q[NI][TB][KB][kBlk];
             unsigned char Mq[NM][kTri<C>][kBlk], Ma[NM][kTri<C>][kBlk];   // scale D dP and D dA, rows: token i
-            float M[C * (C + 1)];                                        // dP P + dA A below the diagonal
         };
     };
-    float ai[2][C], bj[2][C], ub[2][C];   // a_i, b_j, Y . U, in two parts
-    double row[C], colm[C], G[C];
-    double cs[4];
-    Gates<C> g;
+    struct Small {
+        float ai[KG][C], bj[KG][C], ub[2][C];   // a_i, b_j, Y . U, in parts
+        double row[TB][C], col[2 * TB][C];      // sums of M = dP P + dA A below the diagonal, by blocks of columns and tiles of rows
+        double G[C];
+        double cs[4];
+        Gates<C> g;
+    };
+    static constexpr int kBufs = 2 * sizeof(Stage) + sizeof(Small) <= kDeltaMaxLds ? 2 : 1;
+    Stage stage[kBufs];
+    Small small;
 };
 
-template <typename T, int C, int KP>
-__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
+// The wavefronts that bring the operands.
+template <typename T, int C, int KP> struct GradBring {
     using Lds = GradLds<T, C, KP>;
-    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NT = C / 16, NM = Lds::NM;
-    constexpr int KG = 4 / NT, KW = KB / KG;        // wavefronts on the same tokens, their share of head_dim's blocks
-    constexpr int NJ = (kTri<C> * 2 + 3) / 4;       // tiles of pairs per wavefront
-    constexpr int kStride = TB * KB * kBlk;
-    extern __shared__ __align__(16) unsigned char raw[];
-    Lds &s = *reinterpret_cast<Lds *>(raw);
-    const int group = a.Hv / a.Hk, VG = (a.V + 15) / 16;
-    const int c = int(blockIdx.x % ws.Nt), ph = int(blockIdx.x / ws.Nt), hk = ph % a.Hk, p = ph / a.Hk;
-    const int t0 = c * C, live = max(0, min(C, delta_valid(a, p) - t0));
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, lc = lane & 15, lg = lane >> 4;
-    const int tb = wv % NT / 2, ta = wv % 2, kb0 = wv / NT * KW;     // this wavefront's tokens and blocks of dq, dk
-    const int tok = tb * 32 + block_row(lc, ta);                    // the lane's token
-    const Rows &gr = d.go;
-    dt4 aq[KW][2] = {}, ak[KW][2] = {};
-    for (int hh = 0; live > 0 && hh < group; ++hh) {
-        const int h = hk * group + hh;
-        const int64_t nc = (int64_t(p) * a.Hv + h) * ws.Nt + c;
-        const T *go = static_cast<const T *>(gr.data) + p * gr.sp + t0 * gr.st + h * gr.sh;
-        const ChunkMem<C, 3> *mats = reinterpret_cast<const ChunkMem<C, 3> *>(ws.mats) + nc;
-        if (tid < int(sizeof(Gates<C>) / 4)) reinterpret_cast<float *>(&s.g)[tid] = reinterpret_cast<const float *>(&mats->g)[tid];
-        if (wv == 3) {
-            const double G = chunk_G<C>(a, p, h, t0, live);
-            if (lane < C) s.G[lane] = G;
-        }
-        // over V: dP, dA (transposed: columns i, rows j), S do^T, S Y^T, dS U^T
-        dt4 dP[NJ][2] = {}, dA[NJ][2] = {}, oS[KW][2] = {}, yS[KW][2] = {}, uS[KW][2] = {};
-        double cc = 0.0;
-        float ub[8] = {};
-        for (int vg = 0; vg < VG; vg += 2) {
-            for (int i = tid; i < C * 4; i += 256) {      // eights of do
-                const int t = i / 4, e = vg * 16 + i % 4 * 8;
-                Frag<NI> f = load_pieces(go + min(t, live - 1) * gr.st + min(e, gr.width - 8));
-                if (t >= live || e >= gr.width) clear(f);
+    using Stage = typename Lds::Stage;
+    static constexpr int NI = Lds::NI, KB = Lds::KB, TB = Lds::TB, kBufs = Lds::kBufs;
+    static constexpr int OS = (C * 4 + 255) / 256, US = (TB * 128 + 255) / 256, SS = KB * 128 / 256, QS = C * KP / 8 / 256;
+    const DeltaArgs &a;
+    const DeltaWs &ws;
+    const Rows &gr;
+    int p, hk, c, group, live, t0, VG, nb;      // nb: stages of V
+    Frag<NI> o[OS], k[QS], q[QS];
+    dt4 u[US][2], y[US][2], x[SS][2], z[SS][2];
+    float ub[8];
+    double cc;
+
+    __device__ GradBring(const DeltaArgs &a, const DeltaWs &ws, const Rows &gr, int p, int hk, int c, int live)
+        : a(a), ws(ws), gr(gr), p(p), hk(hk), c(c), group(a.Hv / a.Hk), live(live), t0(c * C), VG((a.V + 15) / 16), nb((VG + 1) / 2) {}
+
+    __device__ __forceinline__ int64_t chunk_of(int hh) const { return (int64_t(p) * a.Hv + hk * group + hh) * ws.Nt + c; }
+    // Stage i of group * (nb + 1).
+    __device__ __forceinline__ void load(int i) {
+        const int tid = threadIdx.x & 255, lane = tid & 63, hh = i / (nb + 1), vb = i % (nb + 1);
+        if (vb < nb) {
+            const int vg = vb * 2;
+            const int64_t nc = chunk_of(hh);
+            const T *go = static_cast<const T *>(gr.data) + p * gr.sp + t0 * gr.st + (hk * group + hh) * gr.sh;
 #pragma unroll
-                for (int n = 0; n < NI; ++n) *reinterpret_cast<db8 *>(s.go[n][t / 32] + block_at(t % 32, i % 4)) = f.p[n];
+            for (int j = 0; j < OS; ++j) {
+                const int s = tid + 256 * j, t = s / 4, e = vg * 16 + s % 4 * 8;
+                o[j] = load_pieces(go + (min(t, live - 1) * int(gr.st) + min(e, gr.width - 8)));
+                if (t >= live || e >= gr.width) clear(o[j]);
             }
-            for (int i = tid; i < TB * 128; i += 256) {   // eights of tokens of U and Y: one per thread
-                const int cg = i / (TB * 64), b = i / 64 % TB, row = cg * 16 + lc;
-                dt4 u[2] = {}, y[2] = {};
-                if (vg + cg < VG) {
-                    const int64_t at = (((nc * VG + vg + cg) * TB + b) * 64 + lane) * 8;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        u[e] = *reinterpret_cast<const dt4 *>(ws.U + at + e * 4);
-                        y[e] = *reinterpret_cast<const dt4 *>(ws.Y + at + e * 4);
-                    }
+            for (int j = 0; j < US; ++j) {
+                const int s = tid + 256 * j, cg = s / (TB * 64), b = s / 64 % TB;
+                const bool in = vg + cg < VG && cg < 2;
+                const int64_t at = (((nc * VG + (in ? vg + cg : 0)) * TB + b) * 64 + lane) * 8;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    u[j][e] = *reinterpret_cast<const dt4 *>(ws.U + at + e * 4);
+                    y[j][e] = *reinterpret_cast<const dt4 *>(ws.Y + at + e * 4);
+                    if (!in) u[j][e] = y[j][e] = dt4{};
                 }
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ub[e] = fmaf(u[e / 4][e % 4], y[e / 4][e % 4], ub[e]);
-                const Frag<3> fu = split<3>(u[0], u[1]), fy = split<3>(y[0], y[1]);
+            for (int j = 0; j < SS; ++j) {
+                const int s = tid + 256 * j, cg = s / (KB * 64), b = s / 64 % KB;
+                const bool in = vg + cg < VG;
+                const int64_t at = (((nc * VG + (in ? vg + cg : 0)) * KB + b) * 64 + lane) * 8;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[j][e] = *reinterpret_cast<const dt4 *>(ws.S + at + e * 4);
+                    z[j][e] = *reinterpret_cast<const dt4 *>(ws.dS + at + e * 4);
+                    if (!in) x[j][e] = z[j][e] = dt4{};
+                }
+            }
+        } else {
+            const bf16 *kp = a.kk.data + p * a.kk.sp + hk * a.kk.sh + t0 * a.kk.st;
+            const bf16 *qp = a.qq.data + p * a.qq.sp + hk * a.qq.sh + t0 * a.qq.st;
+#pragma unroll
+            for (int j = 0; j < QS; ++j) {
+                const int s = tid + 256 * j, b = s / 128, t = b / KB * 32 + s % 128 / 4, e = b % KB * 32 + s % 4 * 8;
+                k[j] = load_keys<NI>(kp + (min(t, live - 1) * int(a.kk.st) + e), a.kk.plane);
+                q[j] = load_keys<NI>(qp + (min(t, live - 1) * int(a.qq.st) + e), a.qq.plane);
+                if (t >= live) {
+                    clear(k[j]);
+                    clear(q[j]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(Lds &l, int i) {
+        const int tid = threadIdx.x & 255, lane = tid & 63, lc = lane & 15, lg = lane >> 4, wv = tid >> 6;
+        const int hh = i / (nb + 1), vb = i % (nb + 1);
+        Stage &s = l.stage[i & (kBufs - 1)];
+        if (vb < nb) {
+            if (vb == 0) {
+                cc = 0.0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ub[e] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < OS; ++j) {
+                const int at = tid + 256 * j, t = at / 4;
+                if (C * 4 % 256 && at >= C * 4) break;
+#pragma unroll
+                for (int n = 0; n < NI; ++n) *reinterpret_cast<db8 *>(s.go[n][t / 32] + block_at(t % 32, at % 4)) = o[j].p[n];
+            }
+#pragma unroll
+            for (int j = 0; j < US; ++j) {       // US = 1: a thread keeps its tokens through all stages
+                const int at = tid + 256 * j, cg = at / (TB * 64), b = at / 64 % TB, row = cg * 16 + lc;
+                if (TB * 128 % 256 && at >= TB * 128) break;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ub[e] = fmaf(u[j][e / 4][e % 4], y[j][e / 4][e % 4], ub[e]);
+                const Frag<3> fu = split<3>(u[j][0], u[j][1]), fy = split<3>(y[j][0], y[j][1]);
 #pragma unroll
                 for (int n = 0; n < 3; ++n) {
                     *reinterpret_cast<db8 *>(s.U[n][b] + block_at(row, lg)) = fu.p[n];
                     *reinterpret_cast<db8 *>(s.Y[n][b] + block_at(row, lg)) = fy.p[n];
                 }
             }
-            for (int i = tid; i < KB * 128; i += 256) {   // eights of head_dim of S and dS
-                const int cg = i / (KB * 64), b = i / 64 % KB, row = cg * 16 + lc;
-                dt4 x[2] = {}, y[2] = {};
-                if (vg + cg < VG) {
-                    const int64_t at = (((nc * VG + vg + cg) * KB + b) * 64 + lane) * 8;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[e] = *reinterpret_cast<const dt4 *>(ws.S + at + e * 4);
-                        y[e] = *reinterpret_cast<const dt4 *>(ws.dS + at + e * 4);
-                    }
-                }
+            for (int j = 0; j < SS; ++j) {
+                const int at = tid + 256 * j, cg = at / (KB * 64), b = at / 64 % KB, row = cg * 16 + lc;
                 float m = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaf(x[e / 4][e % 4], y[e / 4][e % 4], m);
+                for (int e = 0; e < 8; ++e) m = fmaf(x[j][e / 4][e % 4], z[j][e / 4][e % 4], m);
                 cc += double(m);
-                const Frag<3> fx = split<3>(x[0], x[1]), fy = split<3>(y[0], y[1]);
+                const Frag<3> fx = split<3>(x[j][0], x[j][1]), fz = split<3>(z[j][0], z[j][1]);
 #pragma unroll
                 for (int n = 0; n < 3; ++n) {
                     *reinterpret_cast<db8 *>(s.S[n][b] + block_at(row, lg)) = fx.p[n];
-                    *reinterpret_cast<db8 *>(s.dS[n][b] + block_at(row, lg)) = fy.p[n];
+                    *reinterpret_cast<db8 *>(s.dS[n][b] + block_at(row, lg)) = fz.p[n];
                 }
             }
-            lds_barrier();
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {    // tile e of the columns i, both tiles of the rows j
-                const int m = wv + 4 * j, b = m / 2, e = m & 1, bi = b > 0, bj = b == 2;
-                if (b >= kTri<C>) break;
-                const Frag<NI> fo = read_rows<NI>(s.go[0][bi], TB * kBlk, e);
-                const Frag<3> fy = read_cols<3>(s.Y[0][bi], TB * kBlk, e);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const Frag<3> fu = read_cols<3>(s.U[0][bj], TB * kBlk, x);
-                    dP[j][x] = mma<3>(fu, fo, dP[j][x]);
-                    dA[j][x] = mma<3>(fu, fy, dA[j][x]);
-                }
-            }
-            const Frag<NI> fo = read_rows<NI>(s.go[0][tb], TB * kBlk, ta);
-            const Frag<3> fu = read_cols<3>(s.U[0][tb], TB * kBlk, ta), fy = read_cols<3>(s.Y[0][tb], TB * kBlk, ta);
-#pragma unroll
-            for (int b = 0; b < KW; ++b)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const Frag<3> fs = read_cols<3>(s.S[0][kb0 + b], KB * kBlk, e);
-                    oS[b][e] = mma<3>(fs, fo, oS[b][e]);
-                    yS[b][e] = mma<3>(fs, fy, yS[b][e]);
-                    uS[b][e] = mma<3>(read_cols<3>(s.dS[0][kb0 + b], KB * kBlk, e), fu, uS[b][e]);
-                }
-            lds_barrier();
+            return;
         }
-        // Y . U of each token: over the 16 columns of a lane group, then the two column groups
+#pragma unroll
+        for (int j = 0; j < QS; ++j) {
+            const int at = tid + 256 * j, to = at / 128 * kBlk + block_at(at % 128 / 4, at % 4);
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                *reinterpret_cast<db8 *>(&s.k[n][0][0][0] + to) = k[j].p[n];
+                *reinterpret_cast<db8 *>(&s.q[n][0][0][0] + to) = q[j].p[n];
+            }
+        }
+        // Y . U of each token: over the 16 columns of a lane group, in two column groups; S . dS
         if (tid < TB * 128) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
 #pragma unroll
                 for (int m = 8; m > 0; m >>= 1) ub[e] += __shfl_xor(ub[e], m, 64);
-                if (lc == 0) s.ub[tid / (TB * 64)][tid / 64 % TB * 32 + lg * 8 + e] = ub[e];
+                if (lc == 0) l.small.ub[tid / (TB * 64)][tid / 64 % TB * 32 + lg * 8 + e] = ub[e];
             }
         }
 #pragma unroll
         for (int m = 32; m > 0; m >>= 1) cc += __shfl_xor(cc, m, 64);
-        if (lane == 0) s.cs[wv] = cc;
-        {
-            const bf16 *kp = a.kk.data + p * a.kk.sp + hk * a.kk.sh + t0 * a.kk.st;
-            const bf16 *qp = a.qq.data + p * a.qq.sp + hk * a.qq.sh + t0 * a.qq.st;
-#pragma unroll
-            for (int i = tid; i < C * KP / 8; i += 256) {
-                const int b = i / 128, r = i % 128 / 4, t = b / KB * 32 + r, e = b % KB * 32 + i % 4 * 8, at = b * kBlk + block_at(r, i % 4);
-                Frag<NI> fk = load_keys<NI>(kp + (min(t, live - 1) * int(a.kk.st) + e), a.kk.plane);
-                Frag<NI> fq = load_keys<NI>(qp + (min(t, live - 1) * int(a.qq.st) + e), a.qq.plane);
-                if (t >= live) {
-                    clear(fk);
-                    clear(fq);
-                }
-#pragma unroll
-                for (int n = 0; n < NI; ++n) {
-                    *reinterpret_cast<db8 *>(&s.k[n][0][0][0] + at) = fk.p[n];
-                    *reinterpret_cast<db8 *>(&s.q[n][0][0][0] + at) = fq.p[n];
-                }
+        if (lane == 0) l.small.cs[wv] = cc;
+        if (wv == 0) {
+            const double G = chunk_G<C>(a, p, hk * group + hh, t0, live);
+            if (lane < C) l.small.G[lane] = G;
+        }
+        if (wv == 1) {
+            const ChunkMem<C, 3> *mem = reinterpret_cast<const ChunkMem<C, 3> *>(ws.mats) + chunk_of(hh);
+            reinterpret_cast<du4 *>(&l.small.g)[lane] = reinterpret_cast<const du4 *>(&mem->g)[lane];
+        }
+    }
+    __device__ __forceinline__ void run(Lds &l) {
+        const int count = group * (nb + 1);
+        load(0);
+        store(l, 0);
+        if (count > 1) load(1);
+        lds_barrier();
+        for (int i = 0; i < count; ++i) {
+            if constexpr (kBufs == 2) {
+                if (i + 1 < count) store(l, i + 1);
+                if (i + 2 < count) load(i + 2);
+            }
+            if (i % (nb + 1) == nb) lds_barrier();    // the working wavefronts' own
+            lds_barrier();
+            if constexpr (kBufs == 1) {
+                if (i + 1 < count) store(l, i + 1);
+                if (i + 2 < count) load(i + 2);
+                lds_barrier();
             }
         }
+    }
+};
+
+template <typename T, int C, int KP>
+__global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
+    using Lds = GradLds<T, C, KP>;
+    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NT = C / 16, NM = Lds::NM;
+    constexpr int KG = Lds::KG, KW = KB * 2 / KG;   // wavefronts on the same tokens, their share of head_dim in 16-row tiles
+    constexpr int kStride = TB * KB * kBlk;
+    extern __shared__ __align__(16) unsigned char raw[];
+    Lds &l = *reinterpret_cast<Lds *>(raw);
+    typename Lds::Small &sm = l.small;
+    const int group = a.Hv / a.Hk, VG = (a.V + 15) / 16, nb = (VG + 1) / 2;
+    const int c = int(blockIdx.x % ws.Nt), ph = int(blockIdx.x / ws.Nt), hk = ph % a.Hk, p = ph / a.Hk;
+    const int t0 = c * C, live = max(0, min(C, delta_valid(a, p) - t0)), rows = min(C, a.T - t0);
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), lc = lane & 15, lg = lane >> 4;
+    if (wv >= 8) {
+        if (live > 0) {
+            GradBring<T, C, KP> bring(a, ws, d.go, p, hk, c, live);
+            bring.run(l);
+        }
+        return;
+    }
+    const int tile = wv % NT, tb = tile / 2, ta = tile % 2, part = wv / NT, kt0 = part * KW;   // this wavefront's tokens and tiles of dq, dk
+    const int tok = tb * 32 + block_row(lc, ta);                                              // the lane's token
+    dt4 aq[KW] = {}, ak[KW] = {};
+    int stage = 0;
+    auto turn = [&]() {
         lds_barrier();
-        // D, P and A again, and the weights of k and q in the gradients (accumulators: rows j, columns i)
+        if constexpr (Lds::kBufs == 1) lds_barrier();
+        ++stage;
+    };
+    if (live > 0) lds_barrier();
+    for (int hh = 0; live > 0 && hh < group; ++hh) {
+        const int h = hk * group + hh;
+        // dP and dA (transposed: columns i, rows j): tile pe of the columns of row block bi, both row tiles of column block bj
+        const int pb = wv / 2, pe = wv & 1, bi = pb > 0, bj = pb == 2;
+        const bool pairs = pb < kTri<C>;
+        dt4 dP[2] = {}, dA[2] = {}, oS[KW] = {}, yS[KW] = {}, uS[KW] = {};
+        for (int vb = 0; vb < nb; ++vb) {
+            const typename Lds::Stage &s = l.stage[stage & (Lds::kBufs - 1)];
+            Frag<3> fs[2], fd[2];
+            auto tile_of = [&](int j, int t) {
+                fs[j] = read_cols<3>(s.S[0][t / 2], KB * kBlk, t & 1);
+                fd[j] = read_cols<3>(s.dS[0][t / 2], KB * kBlk, t & 1);
+            };
+            const Frag<NI> fo = read_rows<NI>(s.go[0][tb], TB * kBlk, ta);
+            const Frag<3> fu = read_cols<3>(s.U[0][tb], TB * kBlk, ta), fy = read_cols<3>(s.Y[0][tb], TB * kBlk, ta);
+            tile_of(0, kt0);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int m = wv + 4 * j, b = m / 2, e = m & 1, bi = b > 0, bj = b == 2;
-            if (b >= kTri<C>) break;
+            for (int j = 0; j < KW; ++j) {
+                if (j + 1 < KW) tile_of((j + 1) & 1, kt0 + j + 1);
+                lds_point();
+                oS[j] = mma<3>(fs[j & 1], fo, oS[j]);
+                yS[j] = mma<3>(fs[j & 1], fy, yS[j]);
+                uS[j] = mma<3>(fd[j & 1], fu, uS[j]);
+                lds_point();
+            }
+            if (pairs) {
+                const Frag<NI> po = read_rows<NI>(s.go[0][bi], TB * kBlk, pe);
+                const Frag<3> py = read_cols<3>(s.Y[0][bi], TB * kBlk, pe);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const Frag<3> pu = read_cols<3>(s.U[0][bj], TB * kBlk, x);
+                    dP[x] = mma<3>(pu, po, dP[x]);
+                    dA[x] = mma<3>(pu, py, dA[x]);
+                }
+            }
+            turn();
+        }
+        typename Lds::Stage &s = l.stage[stage & (Lds::kBufs - 1)];
+        // D, P and A again, and the weights of k and q in the gradients (accumulators: rows j, columns i)
+        if (pairs) {
             dt4 kk[2] = {}, qk[2] = {};
 #pragma unroll
             for (int x = 0; x < KB; ++x) {
-                const Frag<NI> fk = read_rows<NI>(s.k[0][bi][x], kStride, e), fq = read_rows<NI>(s.q[0][bi][x], kStride, e);
+                const Frag<NI> fk = read_rows<NI>(s.k[0][bi][x], kStride, pe), fq = read_rows<NI>(s.q[0][bi][x], kStride, pe);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const Frag<NI> f = read_rows<NI>(s.k[0][bj][x], kStride, y);
@@ -377,65 +479,78 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
                     qk[y] = mma<3>(f, fq, qk[y]);
                 }
             }
-            const int i = bi * 32 + block_row(lc, e);
-            const double Gi = s.G[i];
-            const float beta = s.g.beta[i];
+            const int i = bi * 32 + block_row(lc, pe);
+            const double Gi = sm.G[i];
+            const float beta = sm.g.beta[i];
             dt4 wq[2], wa[2];
+            double row = 0.0, cols[8];
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int jj = bj * 32 + lg * 8 + y * 4 + r;
-                    const float D = i >= jj ? exp2_of(Gi - s.G[jj]) : 0.0f;
-                    wq[y][r] = i >= jj ? a.scale * (D * dP[j][y][r]) : 0.0f;
-                    wa[y][r] = i > jj ? -beta * (D * dA[j][y][r]) : 0.0f;
-                    s.M[i * (C + 1) + jj] = i > jj ? fmaf(wq[y][r], qk[y][r], wa[y][r] * kk[y][r]) : 0.0f;
+                    const float D = i >= jj ? exp2_of(Gi - sm.G[jj]) : 0.0f;
+                    wq[y][r] = i >= jj ? a.scale * (D * dP[y][r]) : 0.0f;
+                    wa[y][r] = i > jj ? -beta * (D * dA[y][r]) : 0.0f;
+                    const double m = i > jj ? double(fmaf(wq[y][r], qk[y][r], wa[y][r] * kk[y][r])) : 0.0;
+                    row += m;
+                    cols[y * 4 + r] = m;
                 }
+            row += __shfl_xor(row, 16, 64);
+            row += __shfl_xor(row, 32, 64);
+            if (lg == 0) sm.row[bj][i] = row;
+#pragma unroll
+            for (int m = 1; m < 16; m <<= 1)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) cols[r] += __shfl_xor(cols[r], m, 64);
+            if (lc == 0) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) sm.col[bi * 2 + pe][bj * 32 + lg * 8 + r] = cols[r];
+            }
             // a lane holds eight neighbours j of row i
             const Frag<NM> fq = split<NM>(wq[0], wq[1]), fa = split<NM>(wa[0], wa[1]);
 #pragma unroll
             for (int n = 0; n < NM; ++n) {
-                *reinterpret_cast<db8 *>(s.Mq[n][b] + block_at(block_row(lc, e), lg)) = fq.p[n];
-                *reinterpret_cast<db8 *>(s.Ma[n][b] + block_at(block_row(lc, e), lg)) = fa.p[n];
+                *reinterpret_cast<db8 *>(s.Mq[n][pb] + block_at(block_row(lc, pe), lg)) = fq.p[n];
+                *reinterpret_cast<db8 *>(s.Ma[n][pb] + block_at(block_row(lc, pe), lg)) = fa.p[n];
             }
         }
         // the states' part of dq and dk, and its products with q and k
         {
-            const float eG = s.g.eG[tok], eL = s.g.eL[tok], xo = a.scale * eG, xy = -(s.g.beta[tok] * eG);
-            float ai = 0.0f, bj = 0.0f;
+            const float eG = sm.g.eG[tok], eL = sm.g.eL[tok], xo = a.scale * eG, xy = -(sm.g.beta[tok] * eG);
+            float ai = 0.0f, bj_ = 0.0f;
 #pragma unroll
-            for (int b = 0; b < KW; ++b) {
-                dt4 k[2] = {}, q[2] = {};
+            for (int j = 0; j < KW; ++j) {
+                const int t = kt0 + j;
+                dt4 k{}, q{};
 #pragma unroll
                 for (int n = NI - 1; n >= 0; --n) {
-                    const int at = n * kStride + (tb * KB + kb0 + b) * kBlk + block_at(tok % 32, lg);
-                    const du4 kw = *reinterpret_cast<const du4 *>(&s.k[0][0][0][0] + at);
-                    const du4 qw = *reinterpret_cast<const du4 *>(&s.q[0][0][0][0] + at);
+                    const int at = n * kStride + (tb * KB + t / 2) * kBlk + block_at(tok % 32, lg) + (t & 1) * 8;
+                    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+                    const u2 kw = *reinterpret_cast<const u2 *>(&s.k[0][0][0][0] + at), qw = *reinterpret_cast<const u2 *>(&s.q[0][0][0][0] + at);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const int sh = e & 1 ? 0 : 16;
-                        k[e / 4][e % 4] += __uint_as_float((kw[e / 2] << sh) & 0xFFFF0000u);
-                        q[e / 4][e % 4] += __uint_as_float((qw[e / 2] << sh) & 0xFFFF0000u);
+                        k[e] += __uint_as_float((kw[e / 2] << sh) & 0xFFFF0000u);
+                        q[e] += __uint_as_float((qw[e / 2] << sh) & 0xFFFF0000u);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = xo * oS[b][e][r], y = xy * yS[b][e][r], z = eL * uS[b][e][r];
-                        ai += fmaf(x, q[e][r], y * k[e][r]);
-                        bj = fmaf(z, k[e][r], bj);
-                        aq[b][e][r] += x;
-                        ak[b][e][r] += y + z;
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    const float x = xo * oS[j][r], y = xy * yS[j][r], z = eL * uS[j][r];
+                    ai += fmaf(x, q[r], y * k[r]);
+                    bj_ = fmaf(z, k[r], bj_);
+                    aq[j][r] += x;
+                    ak[j][r] += y + z;
+                }
             }
             ai += __shfl_xor(ai, 16, 64);
-            bj += __shfl_xor(bj, 16, 64);
+            bj_ += __shfl_xor(bj_, 16, 64);
             ai += __shfl_xor(ai, 32, 64);
-            bj += __shfl_xor(bj, 32, 64);
+            bj_ += __shfl_xor(bj_, 32, 64);
             if (lg == 0) {
-                s.ai[wv / NT][tok] = ai;
-                s.bj[wv / NT][tok] = bj;
+                sm.ai[part][tok] = ai;
+                sm.bj[part][tok] = bj_;
             }
         }
         lds_barrier();
@@ -445,64 +560,68 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a, DeltaWs ws
             if (x <= tb) {
                 const Frag<NM> mq = read_rows<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta), ma = read_rows<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta);
 #pragma unroll
-                for (int b = 0; b < KW; ++b)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const Frag<NI> k = read_cols<NI>(s.k[0][x][kb0 + b], kStride, e);
-                        aq[b][e] = mma<NM>(k, mq, aq[b][e]);
-                        ak[b][e] = mma<NM>(k, ma, ak[b][e]);
-                    }
+                for (int j = 0; j < KW; ++j) {
+                    const int t = kt0 + j;
+                    const Frag<NI> k = read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1);
+                    aq[j] = mma<NM>(k, mq, aq[j]);
+                    ak[j] = mma<NM>(k, ma, ak[j]);
+                }
             }
             if (x >= tb) {
                 const Frag<NM> mq = read_cols<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta), ma = read_cols<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta);
 #pragma unroll
-                for (int b = 0; b < KW; ++b)
+                for (int j = 0; j < KW; ++j) {
+                    const int t = kt0 + j;
+                    ak[j] = mma<NM>(read_cols<NI>(s.q[0][x][t / 2], kStride, t & 1), mq, ak[j]);
+                    ak[j] = mma<NM>(read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1), ma, ak[j]);
+                }
+            }
+        }
+        // dg: suffix sums of a_i, prefix sums of b_j and of the pairs begun less those ended, a token per lane
+        if (wv == 0) {
+            double suf = 0.0, pre = 0.0;
+            if (lane < C) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        ak[b][e] = mma<NM>(read_cols<NI>(s.q[0][x][kb0 + b], kStride, e), mq, ak[b][e]);
-                        ak[b][e] = mma<NM>(read_cols<NI>(s.k[0][x][kb0 + b], kStride, e), ma, ak[b][e]);
-                    }
+                for (int n = 0; n < KG; ++n) {
+                    suf += double(sm.ai[n][lane]);
+                    pre += double(sm.bj[n][lane]);
+                }
+#pragma unroll
+                for (int n = 0; n < TB; ++n)
+                    if (n <= lane / 32) pre -= sm.row[n][lane];
+#pragma unroll
+                for (int n = 0; n < 2 * TB; ++n)
+                    if (n / 2 >= lane / 32) pre += sm.col[n][lane];
+            }
+            const double own = pre;
+#pragma unroll
+            for (int m = 1; m < C; m <<= 1) {
+                const double x = __shfl_down(suf, m, 64), y = __shfl_up(pre, m, 64);
+                if (lane + m < C) suf += x;
+                if (lane >= m) pre += y;
+            }
+            if (lane < live) {
+                const double x = double(sm.g.last) * (sm.cs[0] + sm.cs[1] + sm.cs[2] + sm.cs[3]) + suf + (pre - own);
+                const int64_t at = (int64_t(p) * a.T + t0 + lane) * a.Hv + h;
+                d.g[at] = float(x);
+                d.beta[at] = (sm.ub[0][lane] + sm.ub[1][lane]) / delta_beta_safe(sm.g.beta[lane]);
             }
         }
-        if (tid < C) {
-            double x = 0.0;
-            for (int j = 0; j < tid; ++j) x += double(s.M[tid * (C + 1) + j]);
-            s.row[tid] = x;
-        } else if (tid >= 128 && tid < 128 + C) {
-            const int j = tid - 128;
-            double x = 0.0;
-            for (int i = j + 1; i < C; ++i) x += double(s.M[i * (C + 1) + j]);
-            s.colm[j] = x;
-        }
-        lds_barrier();
-        if (tid < live) {
-            const int m = tid;
-            double x = double(s.g.last) * (s.cs[0] + s.cs[1] + s.cs[2] + s.cs[3]);
-            for (int i = 0; i < C; ++i) {
-                float y = i >= m ? s.ai[0][i] : s.bj[0][i];
-                if constexpr (KG > 1) y += i >= m ? s.ai[1][i] : s.bj[1][i];
-                x += double(y);
-            }
-            for (int i = 0; i < m; ++i) x += s.colm[i] - s.row[i];   // pairs i >= m > j: those begun and not ended
-            const int64_t at = (int64_t(p) * a.T + t0 + m) * a.Hv + h;
-            d.g[at] = float(x);
-            d.beta[at] = (s.ub[0][m] + s.ub[1][m]) / delta_beta_safe(s.g.beta[m]);
-        }
-        lds_barrier();
+        turn();
     }
-    const int rows = min(C, a.T - t0);
-    for (int i = tid; i < rows * group; i += 256) {
+    for (int i = tid; i < rows * group; i += 512) {
         const int t = i / group, h = hk * group + i % group;
         const int64_t at = (int64_t(p) * a.T + t0 + t) * a.Hv + h;
         if (t >= live) d.g[at] = d.beta[at] = 0.0f;
     }
     if (tok >= rows) return;
 #pragma unroll
-    for (int b = 0; b < KW; ++b) {
-        const int e0 = (kb0 + b) * 32 + lg * 8;
+    for (int j = 0; j < KW; ++j) {
+        const int t = kt0 + j, e0 = t / 2 * 32 + lg * 8 + (t & 1) * 4;
+        if (e0 >= a.K) continue;
         const int64_t at = ((int64_t(p) * a.T + t0 + tok) * a.Hk + hk) * a.K + e0;
-        put_eight(static_cast<T *>(d.q) + at, a.K - e0, aq[b][0], aq[b][1]);
-        put_eight(static_cast<T *>(d.k) + at, a.K - e0, ak[b][0], ak[b][1]);
+        put_four(static_cast<T *>(d.q) + at, a.K - e0, aq[j]);
+        put_four(static_cast<T *>(d.k) + at, a.K - e0, ak[j]);
     }
 }
 
@@ -512,7 +631,7 @@ hipError_t bwd_go(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, hi
                        (Walk<T, C, KP, 3, true>::kLds), st, a, ws, d);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || ws.Nt == 0) return e;
-    hipLaunchKernelGGL((delta_grad_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hk * ws.Nt)), dim3(256),
+    hipLaunchKernelGGL((delta_grad_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hk * ws.Nt)), dim3(kGradThreads),
                        sizeof(GradLds<T, C, KP>), st, a, ws, d);
     return hipGetLastError();
 }
