@@ -6,9 +6,9 @@
 //
 // Bound by memory: a state is 4 K V bytes read and written once per call, against 2 (2 K + 2 V)
 // of bfloat16 rows. A wavefront owns CW columns of one state and keeps them in registers
-// through all tokens: CW / VW lanes side by side hold VW columns each of RG = 64 VW / CW rows
-// at a time, so a load instruction fetches RG row pieces of CW columns, and the reduction over
-// the rows is RG-way across lanes. Wavefronts share nothing.
+// through all tokens: CW / VW lanes side by side hold VW columns each of a row, and
+// RG = 64 VW / CW such groups of lanes a share of the rows each, so a load instruction fetches RG row pieces of CW columns
+// and the reduction over the rows is RG-way across lanes. Wavefronts share nothing.
 #include "delta.h"
 
 namespace sdm {
@@ -44,9 +44,40 @@ __device__ __forceinline__ void cols_store(float *p, int cols, const float (&o)[
     }
 }
 
+// N neighbours of a row of q or k of which `left` are there, zeros after them: 16 bytes (four elements: 8 or 16) per load at any
+// element address.
+__device__ __forceinline__ void row_load(const float *p, float (&o)[4]) {
+    const f4u x = *reinterpret_cast<const f4u *>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = x[j];
+}
+template <int N> __device__ __forceinline__ void row_load(const bf16 *p, float (&o)[N]) {
+    typedef uint32_t raw __attribute__((ext_vector_type(N / 2), aligned(2)));
+    const raw x = *reinterpret_cast<const raw *>(p);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+        o[2 * j] = __uint_as_float(x[j] << 16);
+        o[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+    }
+}
+template <typename T, int N> __device__ __forceinline__ void rows_load(const T *p, int left, float (&o)[N]) {
+    constexpr int S = sizeof(T) == 4 || N < 8 ? 4 : 8;
+#pragma unroll
+    for (int i = 0; i < N; i += S) {
+        float x[S];
+        if (left >= i + S) row_load(p + i, x);
+        else {
+#pragma unroll
+            for (int j = 0; j < S; ++j) x[j] = i + j < left ? to_f32(p[i + j]) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < S; ++j) o[i + j] = x[j];
+    }
+}
+
 template <typename T, int CW, int RPL>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
-    constexpr int LPR = CW / VW, RG = 64 / LPR;      // lanes per row piece, rows at a time
+    constexpr int LPR = CW / VW;                     // lanes per row piece
     const int lane = threadIdx.x & 63;
     const int slices = (a.V + CW - 1) / CW;
     const int64_t wave = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -74,9 +105,10 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
 
     const int64_t s0 = (slot * a.Hv + h) * a.K * a.V + c0;
     float S[RPL][VW];
+    const int row0 = rg * RPL;                       // a lane's rows are neighbours: so are its elements of q and k
 #pragma unroll
     for (int i = 0; i < RPL; ++i) {
-        const int row = i * RG + rg;
+        const int row = row0 + i;
 #pragma unroll
         for (int j = 0; j < VW; ++j) S[i][j] = 0.0f;
         if (row < a.K) cols_load(a.state + s0 + int64_t(row) * a.V, cols, S[i]);
@@ -86,21 +118,20 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     const T *vp = static_cast<const T *>(a.v.data) + p * a.v.sp + h * a.v.sh + c0;
     const float *bp = a.beta + int64_t(p) * a.T * a.Hv + h, *gp = a.g + int64_t(p) * a.T * a.Hv + h;
     for (int t = 0; t < n; ++t) {
-        float kk[RPL], r[VW] = {}, s[VW] = {}, c = 0.0f, v[VW] = {};
+        float kk[RPL], qq[RPL], r[VW] = {}, s[VW] = {}, c = 0.0f, v[VW] = {};
+        rows_load(kp + t * a.k.st + row0, a.K - row0, kk);
+        rows_load(qp + t * a.q.st + row0, a.K - row0, qq);
         const float beta = bp[int64_t(t) * a.Hv], decay = expf(gp[int64_t(t) * a.Hv]);
 #pragma unroll
         for (int j = 0; j < VW; ++j)
             if (j < cols) v[j] = to_f32(vp[t * a.v.st + j]);
 #pragma unroll
         for (int i = 0; i < RPL; ++i) {
-            const int row = i * RG + rg;
-            kk[i] = row < a.K ? to_f32(kp[t * a.k.st + row]) : 0.0f;
-            const float qq = row < a.K ? to_f32(qp[t * a.q.st + row]) : 0.0f;
-            c = fmaf(qq, kk[i], c);
+            c = fmaf(qq[i], kk[i], c);
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
                 r[j] = fmaf(kk[i], S[i][j], r[j]);
-                s[j] = fmaf(qq, S[i][j], s[j]);
+                s[j] = fmaf(qq[i], S[i][j], s[j]);
             }
         }
         c = rows_sum<LPR>(c);
@@ -120,7 +151,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < RPL; ++i) {
-        const int row = i * RG + rg;
+        const int row = row0 + i;
         if (row < a.K) cols_store(a.state_out + s0 + int64_t(row) * a.V, cols, S[i]);
     }
 }

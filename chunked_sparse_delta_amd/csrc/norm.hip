@@ -7,9 +7,9 @@
 //
 // Both passes are bound by memory: each row is read once into registers (16 bytes per lane
 // and load) and its sums run there in float32, so the variance is that of the differences
-// from the mean. A row belongs to W wavefronts of a workgroup (W = 1, 4 or 16, the fewest
-// whose lanes can hold it, norm_max_items); rows of more columns are walked in
-// memory by 16 wavefronts. Rows need no alignment beyond their element's: a vector load or store
+// from the mean. A row belongs to L lanes (8 to 1024, the fewest that can hold it,
+// norm_max_items), several rows to a wavefront where they are short; rows of more columns than 1024 lanes hold are walked
+// in memory. Rows need no alignment beyond their element's: a vector load or store
 // takes any element address, and the columns left over after the whole vectors go one by one.
 //
 // The backward's sums over rows have a fixed order: workgroup g of G takes the row groups g, g + G, ...,
@@ -22,10 +22,11 @@ namespace sdm {
 
 namespace {
 
-// Vectors of a row that a lane of W wavefronts may hold: as many as the registers take (the
-// backward holds five arrays of that size, and 16 wavefronts leave a lane 128 registers).
-constexpr int norm_max_items(int W, int V, bool bwd) {
-    const int elems = W == 1 ? 16 : W == 4 ? (bwd ? 32 : 64) : (bwd ? 16 : 32);
+// Vectors of a row that one of its L lanes may hold: as many as the registers take without costing the wavefronts that
+// hide each other's loads (the backward holds seven arrays of that size: 8192 bfloat16 columns took 130 us
+// with four vectors in 256 lanes and 85 us with one in 1024, 8192 rows). Fewer than 64 lanes hold one each.
+constexpr int norm_max_items(int L, int V, bool bwd) {
+    const int elems = L < 64 ? V : bwd || L == 64 ? 16 : L == 256 ? 64 : 32;
     return elems / V < 8 ? elems / V : 8;
 }
 
@@ -33,11 +34,17 @@ template <typename T> struct NormVec;
 template <> struct NormVec<float> {
     static constexpr int V = 4;
     typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
-    static __device__ __forceinline__ void load(const float *p, float (&o)[4]) {
-        const raw x = *reinterpret_cast<const raw *>(p);
+    static __device__ __forceinline__ void unpack(const raw &x, float (&o)[4]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = x[j];
     }
+    static __device__ __forceinline__ raw part(const float *p, int n) {   // the first n elements, zeros after them
+        raw x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = j < n ? p[j] : 0.0f;
+        return x;
+    }
+    static __device__ __forceinline__ void load(const float *p, float (&o)[4]) { unpack(*reinterpret_cast<const raw *>(p), o); }
     static __device__ __forceinline__ void store(float *p, const float (&o)[4]) {
         *reinterpret_cast<raw *>(p) = raw{o[0], o[1], o[2], o[3]};
     }
@@ -45,14 +52,21 @@ template <> struct NormVec<float> {
 template <> struct NormVec<bf16> {
     static constexpr int V = 8;
     typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
-    static __device__ __forceinline__ void load(const bf16 *p, float (&o)[8]) {
-        const raw x = *reinterpret_cast<const raw *>(p);
+    static __device__ __forceinline__ void unpack(const raw &x, float (&o)[8]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             o[2 * j] = __uint_as_float(x[j] << 16);
             o[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
         }
     }
+    static __device__ __forceinline__ raw part(const bf16 *p, int n) {   // the first n elements, zeros after them
+        raw x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[j] = (2 * j < n ? uint32_t(p[2 * j].bits) : 0u) | (2 * j + 1 < n ? uint32_t(p[2 * j + 1].bits) << 16 : 0u);
+        return x;
+    }
+    static __device__ __forceinline__ void load(const bf16 *p, float (&o)[8]) { unpack(*reinterpret_cast<const raw *>(p), o); }
     static __device__ __forceinline__ void store(bf16 *p, const float (&o)[8]) {
         raw x;
 #pragma unroll
@@ -96,27 +110,27 @@ template <typename T, int V> __device__ __forceinline__ void norm_put(T *p, int 
     }
 }
 
-__device__ __forceinline__ float wave_sum(float x) {
+// Sums of a and b over the row's L lanes (each gets them). `buf` holds two floats per wavefront of a row of more than one
+// and is used by one sum at a time: two buffers taken in turn need one barrier each.
+template <int L> __device__ __forceinline__ float2 row_sum(float a, float b, float *buf) {
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) x += __shfl_xor(x, m, 64);
-    return x;
-}
-
-// Sums of a and b over the row's W wavefronts (every lane gets them). `buf` holds 2 W
-// floats and is used by one sum at a time: two buffers taken in turn need one barrier each.
-template <int W> __device__ __forceinline__ float2 row_sum(float a, float b, float *buf) {
-    a = wave_sum(a);
-    b = wave_sum(b);
-    if constexpr (W > 1) {
+    for (int m = (L < 64 ? L : 64) / 2; m > 0; m >>= 1) {
+        a += __shfl_xor(a, m, 64);
+        b += __shfl_xor(b, m, 64);
+    }
+    if constexpr (L > 64) {
         const int w = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) {
             buf[2 * w] = a;
             buf[2 * w + 1] = b;
         }
-        __syncthreads();
+        // orders LDS only: the next row's loads stay on their way
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
         a = b = 0.0f;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
+        for (int i = 0; i < L / 64; ++i) {
             a += buf[2 * i];
             b += buf[2 * i + 1];
         }
@@ -134,16 +148,16 @@ struct NormArgs {
     float eps;
 };
 
-// Workgroups of max(4, W) wavefronts, 4 rows each where W = 1. ITEMS = 0: the row stays in memory.
-template <int W> constexpr int norm_block = W == 1 ? 256 : 64 * W;
+// Threads of a workgroup: 256 / L rows at a time, or one. ITEMS = 0: the row stays in memory.
+template <int L> constexpr int norm_block = L < 256 ? 256 : L;
 
-template <typename T, typename TW, int W, int ITEMS>
-__global__ __launch_bounds__(norm_block<W>) void norm_fwd_kernel(NormArgs a) {
+template <typename T, typename TW, int L, int ITEMS>
+__global__ __launch_bounds__(norm_block<L>) void norm_fwd_kernel(NormArgs a) {
     constexpr int V = NormVec<T>::V;
-    __shared__ float buf[2][2 * W];
-    const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x, n = a.cols;
-    const int64_t row = W == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
-    if (row >= a.rows) return;   // whole wavefronts; W > 1 has one row per workgroup
+    __shared__ float buf[2][2 * (L > 64 ? L / 64 : 1)];
+    const int t = threadIdx.x % L, n = a.cols;
+    const int64_t row = int64_t(blockIdx.x) * (norm_block<L> / L) + threadIdx.x / L;
+    if (row >= a.rows) return;   // all lanes of a row; rows of more than a wavefront have the workgroup to themselves
     const T *x = static_cast<const T *>(a.x) + row * n;
     T *y = static_cast<T *>(a.y) + row * n;
     const TW *w = static_cast<const TW *>(a.weight), *b = static_cast<const TW *>(a.bias);
@@ -157,14 +171,14 @@ __global__ __launch_bounds__(norm_block<W>) void norm_fwd_kernel(NormArgs a) {
         for (int i = 0; i < R; ++i) {
 #pragma unroll
             for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
-            if (t + i * 64 * W < nv) norm_get<T, V>(x, t + i * 64 * W, n, 0.0f, v[i]);
+            if (t + i * L < nv) norm_get<T, V>(x, t + i * L, n, 0.0f, v[i]);
         }
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) s += v[i][j];
     } else {
-        for (int i = t; i < nv; i += 64 * W) {
+        for (int i = t; i < nv; i += L) {
             norm_get<T, V>(x, i, n, 0.0f, v[0]);
 #pragma unroll
             for (int j = 0; j < V; ++j) s += v[0][j];
@@ -172,7 +186,7 @@ __global__ __launch_bounds__(norm_block<W>) void norm_fwd_kernel(NormArgs a) {
     }
     // The sum's rounding grows with the mean's size: the differences from it are summed again
     // beside their squares, and what is left of them is the mean's correction.
-    const float m0 = row_sum<W>(s, 0.0f, buf[0]).x * inv_n;
+    const float m0 = row_sum<L>(s, 0.0f, buf[0]).x * inv_n;
     float q = 0.0f, e = 0.0f;
     auto add_squares = [&](int i, const float (&o)[V]) {
 #pragma unroll
@@ -184,14 +198,14 @@ __global__ __launch_bounds__(norm_block<W>) void norm_fwd_kernel(NormArgs a) {
     };
     if constexpr (ITEMS > 0) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) add_squares(t + i * 64 * W, v[i]);
+        for (int i = 0; i < R; ++i) add_squares(t + i * L, v[i]);
     } else {
-        for (int i = t; i < nv; i += 64 * W) {
+        for (int i = t; i < nv; i += L) {
             norm_get<T, V>(x, i, n, 0.0f, v[0]);
             add_squares(i, v[0]);
         }
     }
-    const float2 sums = row_sum<W>(q, e, buf[1]);
+    const float2 sums = row_sum<L>(q, e, buf[1]);
     const float off = sums.y * inv_n;
     const float v2 = fmaf(-off, off, sums.x * inv_n), var = v2 < 0.0f ? 0.0f : v2;   // a NaN stays one
     const float rstd = 1.0f / sqrtf(var + a.eps);
@@ -209,9 +223,9 @@ __global__ __launch_bounds__(norm_block<W>) void norm_fwd_kernel(NormArgs a) {
     if constexpr (ITEMS > 0) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            if (t + i * 64 * W < nv) emit(t + i * 64 * W, v[i]);
+            if (t + i * L < nv) emit(t + i * L, v[i]);
     } else {
-        for (int i = t; i < nv; i += 64 * W) {
+        for (int i = t; i < nv; i += L) {
             norm_get<T, V>(x, i, n, 0.0f, v[0]);
             emit(i, v[0]);
         }
@@ -224,14 +238,13 @@ __global__ __launch_bounds__(norm_block<W>) void norm_fwd_kernel(NormArgs a) {
 
 // dx of every row, and each workgroup's sums of dy xh and dy over its rows: in registers, or
 // (ITEMS = 0) in its own rows of the workspace, each column in one thread's care.
-template <typename T, typename TW, int W, int ITEMS>
-__global__ __launch_bounds__(norm_block<W>) void norm_bwd_kernel(NormArgs a) {
+template <typename T, typename TW, int L, int ITEMS>
+__global__ __launch_bounds__(norm_block<L>) void norm_bwd_kernel(NormArgs a) {
     constexpr int V = NormVec<T>::V;
-    constexpr int RPG = W == 1 ? 4 : 1;          // rows of a workgroup at a time
+    constexpr int RPG = norm_block<L> / L;       // rows of a workgroup at a time
     constexpr int R = ITEMS > 0 ? ITEMS : 1;
-    __shared__ float buf[2][2 * W];
-    const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x, n = a.cols;
-    const int wv = W == 1 ? threadIdx.x >> 6 : 0;
+    __shared__ float buf[2][2 * (L > 64 ? L / 64 : 1)];
+    const int t = threadIdx.x % L, n = a.cols, mine = threadIdx.x / L;
     const TW *w = static_cast<const TW *>(a.weight);
     const float inv_n = 1.0f / float(n);
     const int nv = (n + V - 1) / V;
@@ -247,20 +260,43 @@ __global__ __launch_bounds__(norm_block<W>) void norm_bwd_kernel(NormArgs a) {
             g[i][j] = 1.0f;
         }
         if constexpr (ITEMS > 0)
-            if (w && t + i * 64 * W < nv) norm_get<TW, V>(w, t + i * 64 * W, n, 0.0f, g[i]);
+            if (w && t + i * L < nv) norm_get<TW, V>(w, t + i * L, n, 0.0f, g[i]);
     }
     if constexpr (ITEMS == 0) {
         if (a.part)
-            for (int i = t; i < nv; i += 64 * W)
+            for (int i = t; i < nv; i += L)
                 for (int c = i * V; c < min(n, i * V + V); ++c) pw[c] = pb[c] = 0.0f;
     }
     int turn = 0;
+    // the next row is on its way while this one's sums are made
+    typename NormVec<T>::raw xr[R], dr[R];
+    float mean_r = 0.0f, rstd_r = 0.0f;
+    auto bring = [&](int64_t row) {
+        if (row >= a.rows) return;
+        const T *x = static_cast<const T *>(a.x) + row * n, *dy = static_cast<const T *>(a.dy) + row * n;
+        mean_r = a.mean_in[row];
+        rstd_r = a.rstd_in[row];
+        if constexpr (ITEMS > 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int c = (t + i * L) * V;
+                if (c + V <= n) {
+                    xr[i] = *reinterpret_cast<const typename NormVec<T>::raw *>(x + c);
+                    dr[i] = *reinterpret_cast<const typename NormVec<T>::raw *>(dy + c);
+                } else if (c < n) {
+                    xr[i] = NormVec<T>::part(x + c, n - c);
+                    dr[i] = NormVec<T>::part(dy + c, n - c);
+                }
+            }
+        }
+    };
+    bring(int64_t(blockIdx.x) * RPG + mine);
     for (int64_t r0 = int64_t(blockIdx.x) * RPG; r0 < a.rows; r0 += G * RPG) {
-        const int64_t row = r0 + wv;
-        if (W == 1 && row >= a.rows) break;   // a wavefront of its own: nothing waits for it here
+        const int64_t row = r0 + mine;
+        if (RPG > 1 && row >= a.rows) break;   // nothing waits for a row's lanes here
         const T *x = static_cast<const T *>(a.x) + row * n, *dy = static_cast<const T *>(a.dy) + row * n;
         T *dx = a.dx ? static_cast<T *>(a.dx) + row * n : nullptr;
-        const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+        const float mean = mean_r, rstd = rstd_r;
         float xv[R][V], dv[R][V];
         float c1 = 0.0f, c2 = 0.0f;
         auto fetch = [&](int i, float (&xo)[V], float (&d)[V]) {   // xh and dy of vector i, zeros past the row
@@ -284,18 +320,28 @@ __global__ __launch_bounds__(norm_block<W>) void norm_bwd_kernel(NormArgs a) {
                     xv[i][j] = mean;
                     dv[i][j] = 0.0f;
                 }
-                if (t + i * 64 * W < nv) fetch(t + i * 64 * W, xv[i], dv[i]);
+                if (t + i * L < nv) {
+                    NormVec<T>::unpack(xr[i], xv[i]);
+                    NormVec<T>::unpack(dr[i], dv[i]);
+                    if ((t + i * L) * V + V > n) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j)
+                            if ((t + i * L) * V + j >= n) xv[i][j] = mean;
+                    }
+                }
             }
+            bring(row + G * RPG);
 #pragma unroll
             for (int i = 0; i < R; ++i) sums(xv[i], dv[i], g[i]);
         } else {
-            for (int i = t; i < nv; i += 64 * W) {
+            for (int i = t; i < nv; i += L) {
                 fetch(i, xv[0], dv[0]);
                 if (w) norm_get<TW, V>(w, i, n, 0.0f, g[0]);
                 sums(xv[0], dv[0], g[0]);
             }
+            bring(row + G * RPG);
         }
-        const float2 c = row_sum<W>(c1, c2, buf[turn]);
+        const float2 c = row_sum<L>(c1, c2, buf[turn]);
         turn ^= 1;
         const float m1 = c.x * inv_n, m2 = c.y * inv_n;
         auto emit = [&](int i, const float (&xh)[V], const float (&d)[V], const float (&gw)[V], float (&aw)[V],
@@ -312,9 +358,9 @@ __global__ __launch_bounds__(norm_block<W>) void norm_bwd_kernel(NormArgs a) {
         if constexpr (ITEMS > 0) {
 #pragma unroll
             for (int i = 0; i < R; ++i)
-                if (t + i * 64 * W < nv) emit(t + i * 64 * W, xv[i], dv[i], g[i], sw[i], sb[i]);
+                if (t + i * L < nv) emit(t + i * L, xv[i], dv[i], g[i], sw[i], sb[i]);
         } else {
-            for (int i = t; i < nv; i += 64 * W) {
+            for (int i = t; i < nv; i += L) {
                 fetch(i, xv[0], dv[0]);
                 if (w) norm_get<TW, V>(w, i, n, 0.0f, g[0]);
 #pragma unroll
@@ -336,36 +382,35 @@ __global__ __launch_bounds__(norm_block<W>) void norm_bwd_kernel(NormArgs a) {
     }
     if constexpr (ITEMS > 0) {
         if (!a.part) return;
-        if constexpr (W == 1) {   // the four wavefronts' sums, added in order
-            __shared__ float all[3][ITEMS * 64 * V];
+        if constexpr (RPG > 1) {   // the sums of the workgroup's other rows, added in order
+            __shared__ float all[RPG - 1][ITEMS * L * V];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float(&s)[R][V] = k ? sb : sw;
                 if (k) __syncthreads();
-                if (wv > 0) {
+                if (mine > 0) {
 #pragma unroll
                     for (int i = 0; i < R; ++i)
 #pragma unroll
-                        for (int j = 0; j < V; ++j) all[wv - 1][(i * V + j) * 64 + t] = s[i][j];
+                        for (int j = 0; j < V; ++j) all[mine - 1][(i * V + j) * L + t] = s[i][j];
                 }
                 __syncthreads();
-                if (wv == 0) {
+                if (mine == 0) {
+                    for (int m = 0; m < RPG - 1; ++m)
 #pragma unroll
-                    for (int i = 0; i < R; ++i)
+                        for (int i = 0; i < R; ++i)
 #pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            s[i][j] = ((s[i][j] + all[0][(i * V + j) * 64 + t]) + all[1][(i * V + j) * 64 + t]) +
-                                      all[2][(i * V + j) * 64 + t];
+                            for (int j = 0; j < V; ++j) s[i][j] += all[m][(i * V + j) * L + t];
                 }
             }
-            if (wv > 0) return;
+            if (mine > 0) return;
         }
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            if (t + i * 64 * W < nv) {
+            if (t + i * L < nv) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const int c = (t + i * 64 * W) * V + j;
+                    const int c = (t + i * L) * V + j;
                     if (c < n) {
                         pw[c] = sw[i][j];
                         pb[c] = sb[i][j];
@@ -401,43 +446,49 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *part, in
 }
 
 struct NormPlan {
-    int W, items;
+    int L, items;
 };
 NormPlan norm_plan(int32_t cols, int V, bool bwd) {
     const int64_t nv = (int64_t(cols) + V - 1) / V;
-    for (int W : {1, 4, 16}) {
-        const int64_t items = (nv + 64 * W - 1) / (64 * W);
-        if (items <= norm_max_items(W, V, bwd)) return {W, items <= 1 ? 1 : items <= 2 ? 2 : items <= 4 ? 4 : 8};
+    for (int L : {8, 16, 32, 64, 256, 1024}) {
+        const int64_t items = (nv + L - 1) / L;
+        if (items <= norm_max_items(L, V, bwd)) return {L, items <= 1 ? 1 : items <= 2 ? 2 : items <= 4 ? 4 : 8};
     }
-    return {16, 0};
+    return {1024, 0};
 }
 
-template <bool BWD, typename T, typename TW, int W, int ITEMS>
+template <bool BWD, typename T, typename TW, int L, int ITEMS>
 hipError_t norm_go(const NormArgs &a, unsigned grid, hipStream_t st) {
-    if constexpr (ITEMS <= norm_max_items(W, NormVec<T>::V, BWD)) {
+    if constexpr (ITEMS <= norm_max_items(L, NormVec<T>::V, BWD) && (ITEMS > 0 || L == 1024)) {
         if constexpr (BWD)
-            hipLaunchKernelGGL((norm_bwd_kernel<T, TW, W, ITEMS>), dim3(grid), dim3(norm_block<W>), 0, st, a);
+            hipLaunchKernelGGL((norm_bwd_kernel<T, TW, L, ITEMS>), dim3(grid), dim3(norm_block<L>), 0, st, a);
         else
-            hipLaunchKernelGGL((norm_fwd_kernel<T, TW, W, ITEMS>), dim3(grid), dim3(norm_block<W>), 0, st, a);
+            hipLaunchKernelGGL((norm_fwd_kernel<T, TW, L, ITEMS>), dim3(grid), dim3(norm_block<L>), 0, st, a);
         return hipGetLastError();
     } else {
         return hipErrorInvalidValue;   // norm_plan gives no such plan
     }
 }
-template <bool BWD, typename T, typename TW, int W>
+template <bool BWD, typename T, typename TW, int L>
 hipError_t norm_items(const NormArgs &a, const NormPlan &p, unsigned grid, hipStream_t st) {
     switch (p.items) {
-        case 0: return norm_go<BWD, T, TW, W, 0>(a, grid, st);
-        case 1: return norm_go<BWD, T, TW, W, 1>(a, grid, st);
-        case 2: return norm_go<BWD, T, TW, W, 2>(a, grid, st);
-        case 4: return norm_go<BWD, T, TW, W, 4>(a, grid, st);
-        default: return norm_go<BWD, T, TW, W, 8>(a, grid, st);
+        case 0: return norm_go<BWD, T, TW, L, 0>(a, grid, st);
+        case 1: return norm_go<BWD, T, TW, L, 1>(a, grid, st);
+        case 2: return norm_go<BWD, T, TW, L, 2>(a, grid, st);
+        case 4: return norm_go<BWD, T, TW, L, 4>(a, grid, st);
+        default: return norm_go<BWD, T, TW, L, 8>(a, grid, st);
     }
 }
 template <bool BWD, typename T, typename TW>
 hipError_t norm_pick(const NormArgs &a, const NormPlan &p, unsigned grid, hipStream_t st) {
-    return p.W == 1 ? norm_items<BWD, T, TW, 1>(a, p, grid, st)
-         : p.W == 4 ? norm_items<BWD, T, TW, 4>(a, p, grid, st) : norm_items<BWD, T, TW, 16>(a, p, grid, st);
+    switch (p.L) {
+        case 8: return norm_items<BWD, T, TW, 8>(a, p, grid, st);
+        case 16: return norm_items<BWD, T, TW, 16>(a, p, grid, st);
+        case 32: return norm_items<BWD, T, TW, 32>(a, p, grid, st);
+        case 64: return norm_items<BWD, T, TW, 64>(a, p, grid, st);
+        case 256: return norm_items<BWD, T, TW, 256>(a, p, grid, st);
+        default: return norm_items<BWD, T, TW, 1024>(a, p, grid, st);
+    }
 }
 template <bool BWD>
 hipError_t norm_launch(const NormArgs &a, int32_t dtype, int32_t wdtype, const NormPlan &p, unsigned grid,
@@ -447,10 +498,10 @@ hipError_t norm_launch(const NormArgs &a, int32_t dtype, int32_t wdtype, const N
     return norm_pick<BWD, bf16, bf16>(a, p, grid, st);
 }
 
-// Workgroups of the backward.
+// Workgroups of the backward: as many as keep the device full, each with enough rows that its sums cost little.
 int norm_groups(int64_t rows, const NormPlan &p) {
-    const int64_t want = p.W == 16 ? 256 : 512;
-    const int64_t most = p.W == 1 ? (rows + 3) / 4 : rows;
+    const int64_t want = p.L == 1024 ? 256 : 512, at_once = p.L < 256 ? 256 / p.L : 1;
+    const int64_t most = (rows + at_once - 1) / at_once;
     return int(most < want ? (most < 1 ? 1 : most) : want);
 }
 
@@ -497,7 +548,8 @@ int sdm_layer_norm_fwd(int64_t rows, int32_t cols, const void *x, int32_t dtype,
     a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd;
     a.rows = rows; a.cols = cols; a.eps = eps;
     const NormPlan p = norm_plan(cols, dtype == SDM_BF16 ? 8 : 4, false);
-    const unsigned grid = unsigned(p.W == 1 ? (rows + 3) / 4 : rows);
+    const int64_t at_once = p.L < 256 ? 256 / p.L : 1;
+    const unsigned grid = unsigned((rows + at_once - 1) / at_once);
     const hipError_t e = norm_launch<false>(a, dtype, weight_dtype, p, grid, static_cast<hipStream_t>(exec->stream));
     return e == hipSuccess ? SDM_OK : hip_fail(e, "layer norm launch");
 }
