@@ -11,6 +11,7 @@ struct Rows {
     int64_t sp, st, sh;
     int32_t width;
 };
+constexpr int64_t kCus = 256;                  // MI355X
 constexpr int64_t kDeltaMaxStride = 1 << 24;   // of tokens: a chunk's offsets fit 32 bits
 
 // q or k as the chunked kernels take them: rows of the padded head_dim in bfloat16, `plane` elements

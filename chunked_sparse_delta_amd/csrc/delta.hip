@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
     }
     if (wv == (NT == 4 ? 0 : 3)) {      // the wavefront with the fewest products
         const bool in = lane < C && lane < live;
-        const double G = chunk_G<C>(a, p, h, t0, live), GL = __shfl(G, C - 1, 64);
+        const double G = chunk_G<C>(in ? a.g[(int64_t(p) * a.T + t0 + lane) * a.Hv + h] : 0.0f), GL = __shfl(G, C - 1, 64);
         if (lane < C) {
             s.G[lane] = G;
             s.g.beta[lane] = in ? a.beta[(int64_t(p) * a.T + t0 + lane) * a.Hv + h] : 0.0f;
@@ -577,7 +577,6 @@ hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool
 // most of the device idle. Walking segments at once costs the readings' walk again, once for the columns of the state and once
 // for those of the map, a third cheaper (no readings), and a join of about a chunk's time per segment.
 int delta_segments(int64_t heads, int slices, int K, int Nt) {
-    constexpr int64_t kCus = 256;
     const int64_t wgs = heads * slices, maps = heads * (slices + delta_kp(K) / 64);
     int best = 1;
     double least = double(Nt);

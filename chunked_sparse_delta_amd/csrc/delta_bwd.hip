@@ -18,6 +18,8 @@
 //
 // U / beta is the write error; where beta is (nearly) 0 the backward's own X and U are computed
 // with beta 1e-20 instead, which changes no other result, so that it still is.
+#include <type_traits>
+
 #include "delta_walk.h"
 
 namespace sdm {
@@ -56,24 +58,25 @@ __global__ __launch_bounds__(kWalkThreads) void delta_back_kernel(DeltaArgs a, D
         const int64_t nc = int64_t(ph) * ws.Nt + c;
         save_blocks<KB>(ws.dS, nc, VG, cg, S);
         const Gates<C> &g = s.m.g;
+        const int ln = fresh_lane();
         // The products in this order, each group's operands read ahead of the group before it: P^T do, k dS, half of
         // q^T do, X^T dU, the other half, k^T Y; the halves stand where dU and Y are being put together.
         Frag<3> ft[2][2];            // a block of P^T or X^T
         auto tri_of = [&](Frag<3>(&f)[2], const unsigned char *m) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) f[e] = read_cols<3>(m, NTR * kBlk, e);
+            for (int e = 0; e < 2; ++e) f[e] = read_cols<3>(m, NTR * kBlk, e, ln);
         };
         Frag<NI> A[2][TB][2];        // a column block of k
         auto rows_of = [&](Frag<NI>(&f)[TB][2], const unsigned char *m) {
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) f[tb][e] = read_rows<NI>(m + tb * KB * kBlk, W::kStride, e);
+                for (int e = 0; e < 2; ++e) f[tb][e] = read_rows<NI>(m + tb * KB * kBlk, W::kStride, e, ln);
         };
         Frag<NI> fk[2][KB];          // half of a row block of k^T or q^T
         auto cols_of = [&](Frag<NI>(&f)[KB], const unsigned char *m, int i) {
 #pragma unroll
-            for (int x = 0; x < KB; ++x) f[x] = read_cols<NI>(m + (i / 2 * KB + i % 2 * (KB / 2) + x / 2) * kBlk, W::kStride, x & 1);
+            for (int x = 0; x < KB; ++x) f[x] = read_cols<NI>(m + (i / 2 * KB + i % 2 * (KB / 2) + x / 2) * kBlk, W::kStride, x & 1, ln);
         };
         tri_of(ft[0], s.m.P[0][0]);
         dt4 o[TB][2], b[TB][2], eG[TB][2], eL[TB][2];
@@ -229,60 +232,86 @@ template <typename T, int C, int KP> struct GradLds {
     Small small;
 };
 
+// A workgroup's way through its chunks of key heads: stage vb of value head hh of chunk `task`, vb = nb for q and k. Chunks
+// without a valid token have no stages.
+template <int C> struct GradAt {
+    const DeltaArgs &a;
+    int Nt, group, nb, tasks, task, p, hk, c, live, hh, vb;
+    __device__ __forceinline__ GradAt(const DeltaArgs &a, const DeltaWs &ws)
+        : a(a), Nt(ws.Nt), group(a.Hv / a.Hk), nb(((a.V + 15) / 16 + 1) / 2), tasks(a.P * a.Hk * ws.Nt) {
+        enter(blockIdx.x);
+    }
+    __device__ __forceinline__ void enter(int t) {
+        hh = vb = 0;
+        for (task = t; task < tasks; task += gridDim.x) {
+            const int ph = task / Nt;
+            c = task % Nt, hk = ph % a.Hk, p = ph / a.Hk;
+            live = min(C, delta_valid(a, p) - c * C);
+            if (live > 0) break;
+        }
+    }
+    __device__ __forceinline__ bool more() const { return task < tasks; }
+    __device__ __forceinline__ bool keys() const { return vb == nb; }
+    __device__ __forceinline__ void next() {
+        if (++vb <= nb) return;
+        vb = 0;
+        if (++hh == group) enter(task + gridDim.x);
+    }
+};
+
 // The wavefronts that bring the operands.
 template <typename T, int C, int KP> struct GradBring {
     using Lds = GradLds<T, C, KP>;
     using Stage = typename Lds::Stage;
+    using At = GradAt<C>;
     static constexpr int NI = Lds::NI, KB = Lds::KB, TB = Lds::TB, kBufs = Lds::kBufs;
     static constexpr int OS = (C * 4 + 255) / 256, US = (TB * 128 + 255) / 256, SS = KB * 128 / 256, QS = C * KP / 8 / 256;
     const DeltaArgs &a;
     const DeltaWs &ws;
     const Rows &gr;
-    int p, hk, c, group, live, t0, VG, nb;      // nb: stages of V
-    Frag<NI> o[OS], k[QS], q[QS];
-    dt4 u[US][2], y[US][2], x[SS][2], z[SS][2];
-    float ub[8];
+    int VG;
+    // A stage on its way, as it was loaded: do, U, Y, S and dS, or k and q.
+    static constexpr int OW = NI == 1 ? 1 : 2, U0 = OS * OW, Y0 = U0 + 2 * US, X0 = Y0 + 2 * US, Z0 = X0 + 2 * SS, RV = Z0 + 2 * SS;
+    static constexpr int Q0 = QS * NI, RK = 2 * Q0;
+    du4 r[RV > RK ? RV : RK];
+    du4 gates;
+    float g, ub[8];
     double cc;
 
-    __device__ GradBring(const DeltaArgs &a, const DeltaWs &ws, const Rows &gr, int p, int hk, int c, int live)
-        : a(a), ws(ws), gr(gr), p(p), hk(hk), c(c), group(a.Hv / a.Hk), live(live), t0(c * C), VG((a.V + 15) / 16), nb((VG + 1) / 2) {}
+    __device__ GradBring(const DeltaArgs &a, const DeltaWs &ws, const Rows &gr) : a(a), ws(ws), gr(gr), VG((a.V + 15) / 16) {}
 
-    __device__ __forceinline__ int64_t chunk_of(int hh) const { return (int64_t(p) * a.Hv + hk * group + hh) * ws.Nt + c; }
-    // Stage i of group * (nb + 1).
-    __device__ __forceinline__ void load(int i) {
-        const int tid = threadIdx.x & 255, lane = tid & 63, hh = i / (nb + 1), vb = i % (nb + 1);
-        if (vb < nb) {
-            const int vg = vb * 2;
-            const int64_t nc = chunk_of(hh);
-            const T *go = static_cast<const T *>(gr.data) + p * gr.sp + t0 * gr.st + (hk * group + hh) * gr.sh;
+    __device__ __forceinline__ void load(const At &w) {
+        const int tid = threadIdx.x & 255, lane = tid & 63, p = w.p, hk = w.hk, h = hk * w.group + w.hh, live = w.live;
+        const int64_t t0 = int64_t(w.c) * C, nc = (int64_t(p) * a.Hv + h) * ws.Nt + w.c;
+        if (!w.keys()) {
+            const int vg = w.vb * 2;
+            const T *go = static_cast<const T *>(gr.data) + p * gr.sp + t0 * gr.st + h * gr.sh;
+            // columns past V's end are read from its last ones, rows past the last valid token from that one: store clears them
 #pragma unroll
             for (int j = 0; j < OS; ++j) {
-                const int s = tid + 256 * j, t = s / 4, e = vg * 16 + s % 4 * 8;
-                o[j] = load_pieces(go + (min(t, live - 1) * int(gr.st) + min(e, gr.width - 8)));
-                if (t >= live || e >= gr.width) clear(o[j]);
+                const int s = tid + 256 * j, e = vg * 16 + s % 4 * 8;
+                const du4 *from = reinterpret_cast<const du4 *>(go + (min(s / 4, live - 1) * int(gr.st) + min(e, gr.width - 8)));
+#pragma unroll
+                for (int n = 0; n < OW; ++n) r[j * OW + n] = from[n];
             }
 #pragma unroll
             for (int j = 0; j < US; ++j) {
-                const int s = tid + 256 * j, cg = s / (TB * 64), b = s / 64 % TB;
-                const bool in = vg + cg < VG && cg < 2;
-                const int64_t at = (((nc * VG + (in ? vg + cg : 0)) * TB + b) * 64 + lane) * 8;
+                const int s = tid + 256 * j, cg = min(vg + s / (TB * 64), VG - 1), b = s / 64 % TB;
+                const int64_t from = (((nc * VG + cg) * TB + b) * 64 + lane) * 8;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    u[j][e] = *reinterpret_cast<const dt4 *>(ws.U + at + e * 4);
-                    y[j][e] = *reinterpret_cast<const dt4 *>(ws.Y + at + e * 4);
-                    if (!in) u[j][e] = y[j][e] = dt4{};
+                    r[U0 + j * 2 + e] = *reinterpret_cast<const du4 *>(ws.U + from + e * 4);
+                    r[Y0 + j * 2 + e] = *reinterpret_cast<const du4 *>(ws.Y + from + e * 4);
                 }
             }
 #pragma unroll
             for (int j = 0; j < SS; ++j) {
-                const int s = tid + 256 * j, cg = s / (KB * 64), b = s / 64 % KB;
-                const bool in = vg + cg < VG;
-                const int64_t at = (((nc * VG + (in ? vg + cg : 0)) * KB + b) * 64 + lane) * 8;
+                const int s = tid + 256 * j, cg = min(vg + s / (KB * 64), VG - 1), b = s / 64 % KB;
+                const int64_t from = (((nc * VG + cg) * KB + b) * 64 + lane) * 8;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[j][e] = *reinterpret_cast<const dt4 *>(ws.S + at + e * 4);
-                    z[j][e] = *reinterpret_cast<const dt4 *>(ws.dS + at + e * 4);
-                    if (!in) x[j][e] = z[j][e] = dt4{};
+                    r[X0 + j * 2 + e] = *reinterpret_cast<const du4 *>(ws.S + from + e * 4);
+                    r[Z0 + j * 2 + e] = *reinterpret_cast<const du4 *>(ws.dS + from + e * 4);
                 }
             }
         } else {
@@ -290,40 +319,48 @@ template <typename T, int C, int KP> struct GradBring {
             const bf16 *qp = a.qq.data + p * a.qq.sp + hk * a.qq.sh + t0 * a.qq.st;
 #pragma unroll
             for (int j = 0; j < QS; ++j) {
-                const int s = tid + 256 * j, b = s / 128, t = b / KB * 32 + s % 128 / 4, e = b % KB * 32 + s % 4 * 8;
-                k[j] = load_keys<NI>(kp + (min(t, live - 1) * int(a.kk.st) + e), a.kk.plane);
-                q[j] = load_keys<NI>(qp + (min(t, live - 1) * int(a.qq.st) + e), a.qq.plane);
-                if (t >= live) {
-                    clear(k[j]);
-                    clear(q[j]);
+                const int s = tid + 256 * j, b = s / 128, t = min(b / KB * 32 + s % 128 / 4, live - 1), e = b % KB * 32 + s % 4 * 8;
+#pragma unroll
+                for (int n = 0; n < NI; ++n) {
+                    r[j * NI + n] = *reinterpret_cast<const du4 *>(kp + n * a.kk.plane + (t * int(a.kk.st) + e));
+                    r[Q0 + j * NI + n] = *reinterpret_cast<const du4 *>(qp + n * a.qq.plane + (t * int(a.qq.st) + e));
                 }
             }
+            g = lane < live && lane < C ? a.g[(p * int64_t(a.T) + t0 + lane) * a.Hv + h] : 0.0f;
+            gates = reinterpret_cast<const du4 *>(&(reinterpret_cast<const ChunkMem<C, 3> *>(ws.mats) + nc)->g)[lane];
         }
     }
-    __device__ __forceinline__ void store(Lds &l, int i) {
+    static __device__ __forceinline__ dt4 kept(du4 x, bool in) { return in ? __builtin_bit_cast(dt4, x) : dt4{}; }
+    __device__ __forceinline__ void store(Lds &l, const At &w, int i) {
         const int tid = threadIdx.x & 255, lane = tid & 63, lc = lane & 15, lg = lane >> 4, wv = tid >> 6;
-        const int hh = i / (nb + 1), vb = i % (nb + 1);
         Stage &s = l.stage[i & (kBufs - 1)];
-        if (vb < nb) {
-            if (vb == 0) {
+        if (!w.keys()) {
+            if (w.vb == 0) {
                 cc = 0.0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ub[e] = 0.0f;
             }
+            const int vg = w.vb * 2;
 #pragma unroll
             for (int j = 0; j < OS; ++j) {
-                const int at = tid + 256 * j, t = at / 4;
+                const int at = tid + 256 * j, t = at / 4, e = vg * 16 + at % 4 * 8;
                 if (C * 4 % 256 && at >= C * 4) break;
+                Frag<NI> f;
+                if constexpr (NI == 1) f.p[0] = __builtin_bit_cast(db8, r[j]);
+                else f = split<NI>(__builtin_bit_cast(dt4, r[j * 2]), __builtin_bit_cast(dt4, r[j * 2 + 1]));
+                if (t >= w.live || e >= gr.width) clear(f);
 #pragma unroll
-                for (int n = 0; n < NI; ++n) *reinterpret_cast<db8 *>(s.go[n][t / 32] + block_at(t % 32, at % 4)) = o[j].p[n];
+                for (int n = 0; n < NI; ++n) *reinterpret_cast<db8 *>(s.go[n][t / 32] + block_at(t % 32, at % 4)) = f.p[n];
             }
 #pragma unroll
             for (int j = 0; j < US; ++j) {       // US = 1: a thread keeps its tokens through all stages
                 const int at = tid + 256 * j, cg = at / (TB * 64), b = at / 64 % TB, row = cg * 16 + lc;
                 if (TB * 128 % 256 && at >= TB * 128) break;
+                const bool in = vg + cg < VG;
+                const dt4 u[2] = {kept(r[U0 + j * 2], in), kept(r[U0 + j * 2 + 1], in)}, y[2] = {kept(r[Y0 + j * 2], in), kept(r[Y0 + j * 2 + 1], in)};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ub[e] = fmaf(u[j][e / 4][e % 4], y[j][e / 4][e % 4], ub[e]);
-                const Frag<3> fu = split<3>(u[j][0], u[j][1]), fy = split<3>(y[j][0], y[j][1]);
+                for (int e = 0; e < 8; ++e) ub[e] = fmaf(u[e / 4][e % 4], y[e / 4][e % 4], ub[e]);
+                const Frag<3> fu = split<3>(u[0], u[1]), fy = split<3>(y[0], y[1]);
 #pragma unroll
                 for (int n = 0; n < 3; ++n) {
                     *reinterpret_cast<db8 *>(s.U[n][b] + block_at(row, lg)) = fu.p[n];
@@ -333,11 +370,13 @@ template <typename T, int C, int KP> struct GradBring {
 #pragma unroll
             for (int j = 0; j < SS; ++j) {
                 const int at = tid + 256 * j, cg = at / (KB * 64), b = at / 64 % KB, row = cg * 16 + lc;
+                const bool in = vg + cg < VG;
+                const dt4 x[2] = {kept(r[X0 + j * 2], in), kept(r[X0 + j * 2 + 1], in)}, z[2] = {kept(r[Z0 + j * 2], in), kept(r[Z0 + j * 2 + 1], in)};
                 float m = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaf(x[j][e / 4][e % 4], z[j][e / 4][e % 4], m);
+                for (int e = 0; e < 8; ++e) m = fmaf(x[e / 4][e % 4], z[e / 4][e % 4], m);
                 cc += double(m);
-                const Frag<3> fx = split<3>(x[j][0], x[j][1]), fz = split<3>(z[j][0], z[j][1]);
+                const Frag<3> fx = split<3>(x[0], x[1]), fz = split<3>(z[0], z[1]);
 #pragma unroll
                 for (int n = 0; n < 3; ++n) {
                     *reinterpret_cast<db8 *>(s.S[n][b] + block_at(row, lg)) = fx.p[n];
@@ -349,10 +388,11 @@ template <typename T, int C, int KP> struct GradBring {
 #pragma unroll
         for (int j = 0; j < QS; ++j) {
             const int at = tid + 256 * j, to = at / 128 * kBlk + block_at(at % 128 / 4, at % 4);
+            const bool in = at / 128 / KB * 32 + at % 128 / 4 < w.live;
 #pragma unroll
             for (int n = 0; n < NI; ++n) {
-                *reinterpret_cast<db8 *>(&s.k[n][0][0][0] + to) = k[j].p[n];
-                *reinterpret_cast<db8 *>(&s.q[n][0][0][0] + to) = q[j].p[n];
+                *reinterpret_cast<du4 *>(&s.k[n][0][0][0] + to) = in ? r[j * NI + n] : du4{};
+                *reinterpret_cast<du4 *>(&s.q[n][0][0][0] + to) = in ? r[Q0 + j * NI + n] : du4{};
             }
         }
         // Y . U of each token: over the 16 columns of a lane group, in two column groups; S . dS
@@ -368,35 +408,59 @@ template <typename T, int C, int KP> struct GradBring {
         for (int m = 32; m > 0; m >>= 1) cc += __shfl_xor(cc, m, 64);
         if (lane == 0) l.small.cs[wv] = cc;
         if (wv == 0) {
-            const double G = chunk_G<C>(a, p, hk * group + hh, t0, live);
+            const double G = chunk_G<C>(g);
             if (lane < C) l.small.G[lane] = G;
         }
-        if (wv == 1) {
-            const ChunkMem<C, 3> *mem = reinterpret_cast<const ChunkMem<C, 3> *>(ws.mats) + chunk_of(hh);
-            reinterpret_cast<du4 *>(&l.small.g)[lane] = reinterpret_cast<const du4 *>(&mem->g)[lane];
-        }
+        if (wv == 1) reinterpret_cast<du4 *>(&l.small.g)[lane] = gates;
     }
     __device__ __forceinline__ void run(Lds &l) {
-        const int count = group * (nb + 1);
-        load(0);
-        store(l, 0);
-        if (count > 1) load(1);
+        At at(a, ws), sent = at, put = at;      // the stage being worked on, and the next to load and to store
+        if (!at.more()) return;
+        load(sent);
+        sent.next();
+        store(l, put, 0);
+        put.next();
+        if (sent.more()) {
+            load(sent);
+            sent.next();
+        }
         lds_barrier();
-        for (int i = 0; i < count; ++i) {
-            if constexpr (kBufs == 2) {
-                if (i + 1 < count) store(l, i + 1);
-                if (i + 2 < count) load(i + 2);
+        auto ahead = [&](int i) {
+            if (put.more()) {
+                store(l, put, i + 1);
+                put.next();
             }
-            if (i % (nb + 1) == nb) lds_barrier();    // the working wavefronts' own
+            if (sent.more()) {
+                load(sent);
+                sent.next();
+            }
+        };
+        for (int i = 0; at.more(); ++i, at.next()) {
+            if constexpr (kBufs == 2) ahead(i);
+            if (at.keys()) lds_barrier();    // the working wavefronts' own
             lds_barrier();
             if constexpr (kBufs == 1) {
-                if (i + 1 < count) store(l, i + 1);
-                if (i + 2 < count) load(i + 2);
+                ahead(i);
                 lds_barrier();
             }
         }
     }
 };
+
+// Sum over the 16 lanes of a row, by moves within the row.
+__device__ __forceinline__ double lanes16(double x) {
+    auto add = [&](auto ctrl) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0u, uint32_t(u), decltype(ctrl)::value, 0xF, 0xF, false);
+        const uint32_t hi = __builtin_amdgcn_update_dpp(0u, uint32_t(u >> 32), decltype(ctrl)::value, 0xF, 0xF, false);
+        x += __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+    };
+    add(std::integral_constant<int, 0xB1>{});    // quad_perm 1, 0, 3, 2
+    add(std::integral_constant<int, 0x4E>{});    // quad_perm 2, 3, 0, 1
+    add(std::integral_constant<int, 0x141>{});   // row_half_mirror
+    add(std::integral_constant<int, 0x140>{});   // row_mirror
+    return x;
+}
 
 template <typename T, int C, int KP>
 __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
@@ -407,19 +471,13 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
     extern __shared__ __align__(16) unsigned char raw[];
     Lds &l = *reinterpret_cast<Lds *>(raw);
     typename Lds::Small &sm = l.small;
-    const int group = a.Hv / a.Hk, VG = (a.V + 15) / 16, nb = (VG + 1) / 2;
-    const int c = int(blockIdx.x % ws.Nt), ph = int(blockIdx.x / ws.Nt), hk = ph % a.Hk, p = ph / a.Hk;
-    const int t0 = c * C, live = max(0, min(C, delta_valid(a, p) - t0)), rows = min(C, a.T - t0);
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), lc = lane & 15, lg = lane >> 4;
     if (wv >= 8) {
-        if (live > 0) {
-            GradBring<T, C, KP> bring(a, ws, d.go, p, hk, c, live);
-            bring.run(l);
-        }
+        GradBring<T, C, KP> bring(a, ws, d.go);
+        bring.run(l);
         return;
     }
     const int tile = wv % NT, tb = tile / 2, ta = tile % 2, part = wv / NT, kt0 = part * KW;   // this wavefront's tokens and tiles of dq, dk
-    const int tok = tb * 32 + block_row(lc, ta);                                              // the lane's token
     dt4 aq[KW] = {}, ak[KW] = {};
     int stage = 0;
     auto turn = [&]() {
@@ -427,38 +485,42 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
         if constexpr (Lds::kBufs == 1) lds_barrier();
         ++stage;
     };
-    if (live > 0) lds_barrier();
-    for (int hh = 0; live > 0 && hh < group; ++hh) {
-        const int h = hk * group + hh;
+    GradAt<C> at(a, ws);
+    if (at.more()) lds_barrier();
+    const int nb = at.nb;
+    while (at.more()) {
+        const int ln = fresh_lane();
+        const int p = at.p, hk = at.hk, t0 = at.c * C, live = at.live, h = hk * at.group + at.hh;
         // dP and dA (transposed: columns i, rows j): tile pe of the columns of row block bi, both row tiles of column block bj
         const int pb = wv / 2, pe = wv & 1, bi = pb > 0, bj = pb == 2;
         const bool pairs = pb < kTri<C>;
         dt4 dP[2] = {}, dA[2] = {}, oS[KW] = {}, yS[KW] = {}, uS[KW] = {};
         for (int vb = 0; vb < nb; ++vb) {
             const typename Lds::Stage &s = l.stage[stage & (Lds::kBufs - 1)];
-            Frag<3> fs[2], fd[2];
-            auto tile_of = [&](int j, int t) {
-                fs[j] = read_cols<3>(s.S[0][t / 2], KB * kBlk, t & 1);
-                fd[j] = read_cols<3>(s.dS[0][t / 2], KB * kBlk, t & 1);
-            };
-            const Frag<NI> fo = read_rows<NI>(s.go[0][tb], TB * kBlk, ta);
-            const Frag<3> fu = read_cols<3>(s.U[0][tb], TB * kBlk, ta), fy = read_cols<3>(s.Y[0][tb], TB * kBlk, ta);
-            tile_of(0, kt0);
+            Frag<3> fs, fd;     // a tile of S, a tile of dS: one is read while the other's products run
+            const Frag<NI> fo = read_rows<NI>(s.go[0][tb], TB * kBlk, ta, ln);
+            const Frag<3> fy = read_cols<3>(s.Y[0][tb], TB * kBlk, ta, ln);
+            fs = read_cols<3>(s.S[0][kt0 / 2], KB * kBlk, kt0 & 1, ln);
+            const Frag<3> fu = read_cols<3>(s.U[0][tb], TB * kBlk, ta, ln);
 #pragma unroll
             for (int j = 0; j < KW; ++j) {
-                if (j + 1 < KW) tile_of((j + 1) & 1, kt0 + j + 1);
+                const int t = kt0 + j;
+                fd = read_cols<3>(s.dS[0][t / 2], KB * kBlk, t & 1, ln);
                 lds_point();
-                oS[j] = mma<3>(fs[j & 1], fo, oS[j]);
-                yS[j] = mma<3>(fs[j & 1], fy, yS[j]);
-                uS[j] = mma<3>(fd[j & 1], fu, uS[j]);
+                oS[j] = mma<3>(fs, fo, oS[j]);
+                yS[j] = mma<3>(fs, fy, yS[j]);
+                lds_point();
+                if (j + 1 < KW) fs = read_cols<3>(s.S[0][(t + 1) / 2], KB * kBlk, (t + 1) & 1, ln);
+                lds_point();
+                uS[j] = mma<3>(fd, fu, uS[j]);
                 lds_point();
             }
             if (pairs) {
-                const Frag<NI> po = read_rows<NI>(s.go[0][bi], TB * kBlk, pe);
-                const Frag<3> py = read_cols<3>(s.Y[0][bi], TB * kBlk, pe);
+                const Frag<NI> po = read_rows<NI>(s.go[0][bi], TB * kBlk, pe, ln);
+                const Frag<3> py = read_cols<3>(s.Y[0][bi], TB * kBlk, pe, ln);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const Frag<3> pu = read_cols<3>(s.U[0][bj], TB * kBlk, x);
+                    const Frag<3> pu = read_cols<3>(s.U[0][bj], TB * kBlk, x, ln);
                     dP[x] = mma<3>(pu, po, dP[x]);
                     dA[x] = mma<3>(pu, py, dA[x]);
                 }
@@ -466,15 +528,16 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
             turn();
         }
         typename Lds::Stage &s = l.stage[stage & (Lds::kBufs - 1)];
+        const int lp = fresh_lane(), lc = lp & 15, lg = lp >> 4, tok = tb * 32 + block_row(lc, ta);    // the lane's token
         // D, P and A again, and the weights of k and q in the gradients (accumulators: rows j, columns i)
         if (pairs) {
             dt4 kk[2] = {}, qk[2] = {};
 #pragma unroll
             for (int x = 0; x < KB; ++x) {
-                const Frag<NI> fk = read_rows<NI>(s.k[0][bi][x], kStride, pe), fq = read_rows<NI>(s.q[0][bi][x], kStride, pe);
+                const Frag<NI> fk = read_rows<NI>(s.k[0][bi][x], kStride, pe, lp), fq = read_rows<NI>(s.q[0][bi][x], kStride, pe, lp);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const Frag<NI> f = read_rows<NI>(s.k[0][bj][x], kStride, y);
+                    const Frag<NI> f = read_rows<NI>(s.k[0][bj][x], kStride, y, lp);
                     kk[y] = mma<3>(f, fk, kk[y]);
                     qk[y] = mma<3>(f, fq, qk[y]);
                 }
@@ -500,9 +563,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
             row += __shfl_xor(row, 32, 64);
             if (lg == 0) sm.row[bj][i] = row;
 #pragma unroll
-            for (int m = 1; m < 16; m <<= 1)
-#pragma unroll
-                for (int r = 0; r < 8; ++r) cols[r] += __shfl_xor(cols[r], m, 64);
+            for (int r = 0; r < 8; ++r) cols[r] = lanes16(cols[r]);
             if (lc == 0) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) sm.col[bi * 2 + pe][bj * 32 + lg * 8 + r] = cols[r];
@@ -558,22 +619,22 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
 #pragma unroll
         for (int x = 0; x < TB; ++x) {
             if (x <= tb) {
-                const Frag<NM> mq = read_rows<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta), ma = read_rows<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta);
+                const Frag<NM> mq = read_rows<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta, lp), ma = read_rows<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta, lp);
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     const int t = kt0 + j;
-                    const Frag<NI> k = read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1);
+                    const Frag<NI> k = read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1, lp);
                     aq[j] = mma<NM>(k, mq, aq[j]);
                     ak[j] = mma<NM>(k, ma, ak[j]);
                 }
             }
             if (x >= tb) {
-                const Frag<NM> mq = read_cols<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta), ma = read_cols<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta);
+                const Frag<NM> mq = read_cols<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta, lp), ma = read_cols<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta, lp);
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     const int t = kt0 + j;
-                    ak[j] = mma<NM>(read_cols<NI>(s.q[0][x][t / 2], kStride, t & 1), mq, ak[j]);
-                    ak[j] = mma<NM>(read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1), ma, ak[j]);
+                    ak[j] = mma<NM>(read_cols<NI>(s.q[0][x][t / 2], kStride, t & 1, lp), mq, ak[j]);
+                    ak[j] = mma<NM>(read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1, lp), ma, ak[j]);
                 }
             }
         }
@@ -607,21 +668,38 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
                 d.beta[at] = (sm.ub[0][lane] + sm.ub[1][lane]) / delta_beta_safe(sm.g.beta[lane]);
             }
         }
+        const bool last = at.hh + 1 == at.group;
+        at.vb = nb;
+        at.next();
+        if (last) {
+            if (tok < live) {
+#pragma unroll
+                for (int j = 0; j < KW; ++j) {
+                    const int t = kt0 + j, e0 = t / 2 * 32 + lg * 8 + (t & 1) * 4;
+                    if (e0 >= a.K) continue;
+                    const int64_t to = ((int64_t(p) * a.T + t0 + tok) * a.Hk + hk) * a.K + e0;
+                    put_four(static_cast<T *>(d.q) + to, a.K - e0, aq[j]);
+                    put_four(static_cast<T *>(d.k) + to, a.K - e0, ak[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KW; ++j) aq[j] = ak[j] = dt4{};
+        }
         turn();
     }
-    for (int i = tid; i < rows * group; i += 512) {
-        const int t = i / group, h = hk * group + i % group;
-        const int64_t at = (int64_t(p) * a.T + t0 + t) * a.Hv + h;
-        if (t >= live) d.g[at] = d.beta[at] = 0.0f;
-    }
-    if (tok >= rows) return;
-#pragma unroll
-    for (int j = 0; j < KW; ++j) {
-        const int t = kt0 + j, e0 = t / 2 * 32 + lg * 8 + (t & 1) * 4;
-        if (e0 >= a.K) continue;
-        const int64_t at = ((int64_t(p) * a.T + t0 + tok) * a.Hk + hk) * a.K + e0;
-        put_four(static_cast<T *>(d.q) + at, a.K - e0, aq[j]);
-        put_four(static_cast<T *>(d.k) + at, a.K - e0, ak[j]);
+    // padding tokens have gradients of 0
+    const int tasks = a.P * a.Hk * ws.Nt, group = a.Hv / a.Hk;
+    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const int ph = task / ws.Nt, t0 = task % ws.Nt * C, hk = ph % a.Hk, p = ph / a.Hk;
+        const int from = max(0, min(C, delta_valid(a, p) - t0)), rows = min(C, a.T - t0);
+        for (int i = from * group + tid; i < rows * group; i += 512) {
+            const int64_t to = (int64_t(p) * a.T + t0 + i / group) * a.Hv + hk * group + i % group;
+            d.g[to] = d.beta[to] = 0.0f;
+        }
+        for (int i = from * a.K + tid; i < rows * a.K; i += 512) {
+            const int64_t to = ((int64_t(p) * a.T + t0 + i / a.K) * a.Hk + hk) * a.K + i % a.K;
+            static_cast<T *>(d.q)[to] = static_cast<T *>(d.k)[to] = from_f32<T>(0.0f);
+        }
     }
 }
 
@@ -631,7 +709,8 @@ hipError_t bwd_go(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, hi
                        (Walk<T, C, KP, 3, true>::kLds), st, a, ws, d);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || ws.Nt == 0) return e;
-    hipLaunchKernelGGL((delta_grad_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hk * ws.Nt)), dim3(kGradThreads),
+    const int64_t tasks = int64_t(a.P) * a.Hk * ws.Nt;   // a compute unit holds one workgroup: more would start cold
+    hipLaunchKernelGGL((delta_grad_kernel<T, C, KP>), dim3(unsigned(tasks < kCus ? tasks : kCus)), dim3(kGradThreads),
                        sizeof(GradLds<T, C, KP>), st, a, ws, d);
     return hipGetLastError();
 }

@@ -108,9 +108,17 @@ template <int ORD, int NA, int NB, typename F> __device__ __forceinline__ void e
             if (i + j < ORD) f(i, j);
 }
 
+// The lane's number, as a value of its own: addresses made from it stay in the part of the program that makes it. (Where a loop
+// reads many blocks, all their addresses are worth keeping to the compiler, in registers that it then spills.)
+__device__ __forceinline__ int fresh_lane() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // A operand: the rows of tile a of the block at `blk`; N pieces `stride` bytes apart.
-template <int N> __device__ __forceinline__ Frag<N> read_rows(const unsigned char *blk, int stride, int a) {
-    const int lane = threadIdx.x & 63, at = block_at(block_row(lane & 15, a), lane >> 4);
+template <int N> __device__ __forceinline__ Frag<N> read_rows(const unsigned char *blk, int stride, int a, int lane = threadIdx.x & 63) {
+    const int at = block_at(block_row(lane & 15, a), lane >> 4);
     Frag<N> f;
 #pragma unroll
     for (int i = 0; i < N; ++i) f.p[i] = *reinterpret_cast<const db8 *>(blk + i * stride + at);
@@ -118,8 +126,8 @@ template <int N> __device__ __forceinline__ Frag<N> read_rows(const unsigned cha
 }
 // A operand of the block's transpose: columns block_row(., a) as rows, its rows as depth. Each 16 lanes
 // read 4 rows x 16 columns of 16-bit elements, transposed on the way.
-template <int N> __device__ __forceinline__ Frag<N> read_cols(const unsigned char *blk, int stride, int a) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
+template <int N> __device__ __forceinline__ Frag<N> read_cols(const unsigned char *blk, int stride, int a, int lane = threadIdx.x & 63) {
+    const int g = lane >> 4, i = lane & 15;
     Frag<N> f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
@@ -183,11 +191,10 @@ template <typename T> constexpr int kChunk = sizeof(T) == 2 ? 64 : 32;
 __device__ __forceinline__ float delta_beta_safe(float b) { return fabsf(b) < 1e-20f ? 1e-20f : b; }
 
 // The running sum of a chunk's log-decays, over log 2 (so that exp2_of of a difference is the decay between two tokens), by one
-// wavefront: a token per lane. In 64 bits: differences are as exact as the log-decays themselves however large the sum
+// wavefront: a token per lane (g: its log-decay, 0 for padding). In 64 bits: differences are as exact as the log-decays themselves however large the sum
 // grew. A log-decay below -1e4 (-inf among them: it clears the state) counts as -1e4, whose exponential is 0 too.
-template <int C> __device__ __forceinline__ double chunk_G(const DeltaArgs &a, int p, int h, int t0, int live) {
+template <int C> __device__ __forceinline__ double chunk_G(float g) {
     const int lane = threadIdx.x & 63;
-    float g = lane < C && lane < live ? a.g[(int64_t(p) * a.T + t0 + lane) * a.Hv + h] : 0.0f;
     if (g < -1e4f) g = -1e4f;
     double G = double(g) * 1.4426950408889634;
 #pragma unroll
