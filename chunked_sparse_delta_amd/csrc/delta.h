@@ -43,7 +43,7 @@ __device__ __forceinline__ int delta_valid(const DeltaArgs &a, int p) {
 // The chunked kernels' workspace: chunk n = (stream * Hv + head) * Nt + chunk. U, Y, S and dS are
 // kept as the accumulators hold them: [n][16-column group of V][32-row block][lane][8 rows].
 struct DeltaWs {
-    unsigned char *mats;   // [n] ChunkMats
+    unsigned char *mats;   // [n] ChunkMem
     float *U, *Y;          // rows: the chunk's tokens (backward)
     float *S, *dS;         // rows: the padded head_dim; start states, gradients of the end states (backward)
     // A sequence may be walked in `segs` segments of seg_chunks chunks at once (delta_segments): their start states [seg]
@@ -73,10 +73,11 @@ hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16,
 // Whether the chunked kernels can take the rows as they are, and the copies where they cannot (at `to`).
 bool delta_regular_keys(const Rows &r, bool is_bf16);
 bool delta_regular_values(const Rows &r, bool is_bf16);
-hipError_t launch_delta_copy_keys(const Rows &r, KeyRows *k, void *to, int P, int T, int H, bool is_bf16, hipStream_t st);
-hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool is_bf16, hipStream_t st);
-size_t delta_mats_bytes(int K, bool is_bf16, bool backward);   // of a chunk
-hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &g, bool is_bf16, hipStream_t st);
+// (`there`: they are at `to` already.)
+hipError_t launch_delta_copy_keys(const Rows &r, KeyRows *k, void *to, int P, int T, int H, bool is_bf16, bool there, hipStream_t st);
+hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool is_bf16, bool there, hipStream_t st);
+size_t delta_mats_bytes(int K, bool is_bf16);   // of a chunk
+hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &g, bool is_bf16, bool kept, hipStream_t st);
 hipError_t launch_delta_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st);
 
 }  // namespace sdm

@@ -30,22 +30,16 @@ __device__ __forceinline__ dt4 f32_mma(const float *A, const float *B, int ld, d
     return acc;
 }
 
-// The lower 32 x 32 blocks of the row-major m, in float32 or (N = 1) bfloat16.
-template <int C, int N> __device__ __forceinline__ void put_blocks(const float *m, void *out) {
+// The lower 32 x 32 blocks of the row-major m.
+template <int C> __device__ __forceinline__ void put_blocks(const float *m, float (*out)[32][32]) {
     constexpr int LC = PrepLds<C>::LC;
-    for (int i = threadIdx.x; i < kTri<C> * 128; i += 256) {
-        const int b = i / 128, r = i % 128 / 4, c = i % 4, br = b > 0, bc = b == 2;
-        const float *src = m + (br * 32 + r) * LC + bc * 32 + c * 8;
-        const dt4 x = *reinterpret_cast<const dt4 *>(src), y = *reinterpret_cast<const dt4 *>(src + 4);
-        if constexpr (N == 1) static_cast<db8 *>(out)[i] = split<1>(x, y).p[0];
-        else {
-            static_cast<dt4 *>(out)[2 * i] = x;
-            static_cast<dt4 *>(out)[2 * i + 1] = y;
-        }
+    for (int i = threadIdx.x; i < kTri<C> * 256; i += 256) {
+        const int b = i / 256, r = i % 256 / 8, c = i % 8, br = b > 0, bc = b == 2;
+        reinterpret_cast<dt4 *>(out)[i] = *reinterpret_cast<const dt4 *>(m + (br * 32 + r) * LC + bc * 32 + c * 4);
     }
 }
 
-template <typename T, int C, int KP, int NP>
+template <typename T, int C, int KP>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws) {
     constexpr int LC = PrepLds<C>::LC, NT = C / 16, NI = kPieces<T>;
     __shared__ PrepLds<C> s;
@@ -131,8 +125,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
         }
     }
     lds_barrier();
-    ChunkMem<C, NP> *out = reinterpret_cast<ChunkMem<C, NP> *>(ws.mats) + n;
-    put_blocks<C, NP>(s.X, out->P);
+    ChunkMem<C> *out = reinterpret_cast<ChunkMem<C> *>(ws.mats) + n;
+    put_blocks<C>(s.X, out->P);
     if (tid < int(sizeof(Gates<C>) / 4)) reinterpret_cast<float *>(&out->g)[tid] = reinterpret_cast<const float *>(&s.g)[tid];
     lds_barrier();     // X's blocks above the diagonal stay the zeros that P has there
     // the inverse of I + L: the 16 x 16 diagonal blocks by substitution, one column per lane
@@ -176,21 +170,21 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws
         put(s.X + (32 + r0) * LC + c0, -1.0f, x);
         lds_barrier();
     }
-    put_blocks<C, 3>(s.X, out->X);
+    put_blocks<C>(s.X, out->X);
 }
 
 // Every column of the state evolves on its own: a wavefront keeps 16 columns of S in
 // accumulators through the whole sequence, and the four wavefronts of a workgroup share the
 // chunk's k, q, X and P in LDS. One wavefront per SIMD has nothing beside it to hide its waits: the
 // operands of each group of products are read from LDS before the group ahead of it.
-// kRead gives the readings. kSave keeps U and each chunk's start state for the backward instead. kMap, for sequences
+// kRead gives the readings. kSave keeps U and each chunk's start state for the backward instead, kBoth does both. kMap, for sequences
 // walked in segments at once: the segment's end state from a start state of zeros (the first's: from the caller's) and, in
 // workgroups of their own, what it makes of the columns of the identity, with v = 0: the two give a segment's end state from any
 // start state (delta_join_kernel).
-enum { kRead, kSave, kMap };
+enum { kRead, kSave, kBoth, kMap };
 template <typename T, int C, int KP, int MODE>
 __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, DeltaWs ws) {
-    constexpr bool SAVE = MODE == kSave, READ = MODE == kRead;
+    constexpr bool SAVE = MODE == kSave || MODE == kBoth, READ = MODE == kRead || MODE == kBoth;
     constexpr int NI = kPieces<T>, NP = kPPieces<T>(SAVE), KB = KP / 32, TB = C / 32, NTR = kTri<C>;
     constexpr int NS = NI == 1 ? 2 : 3;    // pieces of S and U that reach the readings only
     using W = Walk<T, C, KP, NP, READ>;
@@ -273,7 +267,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
             for (int e = 0; e < 2; ++e) {
                 const int t = tb * 32 + lg * 8 + e * 4;
                 v[tb][e] = W::value(s, tb, e);
-                if (!READ && !in) v[tb][e] = dt4{};
+                if (MODE != kRead && !in) v[tb][e] = dt4{};
                 b[tb][e] = *reinterpret_cast<const dt4 *>(g.beta + t);
                 eG[tb][e] = *reinterpret_cast<const dt4 *>(g.eG + t);
                 et[tb][e] = g.eG[tb * 32 + block_row(lc, e)];
@@ -372,7 +366,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
                 if (i + 1 < NTR) p_of(fp[(i + 1) & 1], i + 1);
                 else kt_of(fk[0], 0);
                 lds_point();
-                each_product<(NP == 1 ? 2 : 3), NP, NS>([&](int m, int l) {
+                each_product<NS, NP, NS>([&](int m, int l) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) y[i > 0][e] = mma1(fv[i == 2].p[l], fp[i & 1][e].p[m], y[i > 0][e]);
                 });
@@ -487,14 +481,16 @@ template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const
     const dim3 chunks(unsigned(int64_t(a.P) * a.Hv * ws.Nt));
     constexpr int N0 = kPPieces<T>(false), N1 = kPPieces<T>(true);
     if (ws.Nt > 0) {
-        if (ws.backward) hipLaunchKernelGGL((delta_prep_kernel<T, C, KP, N1>), chunks, dim3(256), 0, st, a, ws);
-        else hipLaunchKernelGGL((delta_prep_kernel<T, C, KP, N0>), chunks, dim3(256), 0, st, a, ws);
+        hipLaunchKernelGGL((delta_prep_kernel<T, C, KP>), chunks, dim3(256), 0, st, a, ws);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const unsigned heads = unsigned(a.P) * unsigned(a.Hv), slices = unsigned(a.V + 63) / 64;
     if (ws.backward) {
-        hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kSave>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
+        if (a.out)
+            hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kBoth>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, N1, true>::kLds), st, a, ws);
+        else
+            hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kSave>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
         return hipGetLastError();
     }
     if (ws.segs > 1) {
@@ -517,13 +513,14 @@ template <typename T> hipError_t fwd_pick(const DeltaArgs &a, const DeltaWs &ws,
 
 template <typename T, int C, int KP> hipError_t fwd_attr() {
     constexpr int N0 = kPPieces<T>(false), N1 = kPPieces<T>(true);
-    constexpr size_t l0 = Walk<T, C, KP, N0, true>::kLds, l1 = Walk<T, C, KP, N1, false>::kLds;
-    static_assert(l0 <= kDeltaMaxLds && l1 <= kDeltaMaxLds, "LDS of a workgroup");
+    constexpr size_t l0 = Walk<T, C, KP, N0, true>::kLds, l1 = Walk<T, C, KP, N1, false>::kLds, l2 = Walk<T, C, KP, N1, true>::kLds;
+    static_assert(l0 <= kDeltaMaxLds && l1 <= kDeltaMaxLds && l2 <= kDeltaMaxLds, "LDS of a workgroup");
     auto set = [](auto kernel, size_t bytes) {
         return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     };
     hipError_t e = set(&delta_state_kernel<T, C, KP, kRead>, l0);
     if (e == hipSuccess) e = set(&delta_state_kernel<T, C, KP, kSave>, l1);
+    if (e == hipSuccess) e = set(&delta_state_kernel<T, C, KP, kBoth>, l2);
     return e == hipSuccess ? set(&delta_state_kernel<T, C, KP, kMap>, Walk<T, C, KP, N0, false>::kLds) : e;
 }
 template <typename T> hipError_t fwd_attrs() {
@@ -552,24 +549,27 @@ bool delta_regular_values(const Rows &r, bool is_bf16) { return r.width % 8 == 0
 
 static unsigned copy_grid(int64_t threads) { return unsigned(threads / 256 + 1 < 8192 ? threads / 256 + 1 : 8192); }
 
-hipError_t launch_delta_copy_keys(const Rows &r, KeyRows *k, void *to, int P, int T, int H, bool is_bf16, hipStream_t st) {
+hipError_t launch_delta_copy_keys(const Rows &r, KeyRows *k, void *to, int P, int T, int H, bool is_bf16, bool there, hipStream_t st) {
     const int KP = delta_kp(r.width);
     const int64_t rows = int64_t(P) * T * H;
     bf16 *out = static_cast<bf16 *>(to);
     const dim3 grid(copy_grid(rows * (KP / 8)));
+    *k = {out, rows * KP, int64_t(T) * H * KP, int64_t(H) * KP, KP};
+    if (there) return hipSuccess;
     if (is_bf16) hipLaunchKernelGGL(delta_copy_keys_kernel<bf16>, grid, dim3(256), 0, st, r, out, rows, T, H, KP);
     else hipLaunchKernelGGL(delta_copy_keys_kernel<float>, grid, dim3(256), 0, st, r, out, rows, T, H, KP);
-    *k = {out, rows * KP, int64_t(T) * H * KP, int64_t(H) * KP, KP};
     return hipGetLastError();
 }
 
-hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool is_bf16, hipStream_t st) {
+hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool is_bf16, bool there, hipStream_t st) {
     const int VP = (r->width + 7) / 8 * 8;
     const int64_t rows = int64_t(P) * T * H;
     const dim3 grid(copy_grid(rows * VP));
-    if (is_bf16) hipLaunchKernelGGL(delta_copy_values_kernel<bf16>, grid, dim3(256), 0, st, *r, static_cast<bf16 *>(to), rows, T, H, VP);
-    else hipLaunchKernelGGL(delta_copy_values_kernel<float>, grid, dim3(256), 0, st, *r, static_cast<float *>(to), rows, T, H, VP);
+    const Rows from = *r;
     *r = {to, int64_t(T) * H * VP, int64_t(H) * VP, VP, VP};
+    if (there) return hipSuccess;
+    if (is_bf16) hipLaunchKernelGGL(delta_copy_values_kernel<bf16>, grid, dim3(256), 0, st, from, static_cast<bf16 *>(to), rows, T, H, VP);
+    else hipLaunchKernelGGL(delta_copy_values_kernel<float>, grid, dim3(256), 0, st, from, static_cast<float *>(to), rows, T, H, VP);
     return hipGetLastError();
 }
 
@@ -593,10 +593,6 @@ int delta_segments(int64_t heads, int slices, int K, int Nt) {
     return best;
 }
 
-size_t delta_mats_bytes(int K, bool is_bf16, bool backward) {
-    const bool three = backward || !is_bf16;
-    if (delta_chunk(K, is_bf16) == 64) return three ? sizeof(ChunkMem<64, 3>) : sizeof(ChunkMem<64, 1>);
-    return three ? sizeof(ChunkMem<32, 3>) : sizeof(ChunkMem<32, 1>);
-}
+size_t delta_mats_bytes(int K, bool is_bf16) { return delta_chunk(K, is_bf16) == 64 ? sizeof(ChunkMem<64>) : sizeof(ChunkMem<32>); }
 
 }  // namespace sdm

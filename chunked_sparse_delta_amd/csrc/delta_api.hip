@@ -85,7 +85,7 @@ Layout layout(const sdm_delta_shape *s, bool backward, void *base) {
     Layout l{};
     l.ws.Nt = int32_t(Nt);
     l.ws.backward = backward;
-    l.ws.mats = reinterpret_cast<unsigned char *>(take(n * delta_mats_bytes(s->head_dim, b16, backward)));
+    l.ws.mats = reinterpret_cast<unsigned char *>(take(n * delta_mats_bytes(s->head_dim, b16)));
     if (backward) {
         l.ws.U = floats(n * C * VP);
         l.ws.Y = floats(n * C * VP);
@@ -109,9 +109,9 @@ Layout layout(const sdm_delta_shape *s, bool backward, void *base) {
     return l;
 }
 
-// Checks the workspace and makes the rows regular (go: NULL in the forward).
-int take_workspace(const sdm_delta_shape *s, DeltaArgs *a, Rows *go, const sdm_exec *exec, DeltaWs *ws) {
-    const size_t need = layout(s, go != nullptr, nullptr).bytes;
+// Checks the workspace and makes the rows regular (go: NULL in the forward; kept: the copies of q, k and v are there).
+int take_workspace(const sdm_delta_shape *s, bool backward, DeltaArgs *a, Rows *go, bool kept, const sdm_exec *exec, DeltaWs *ws) {
+    const size_t need = layout(s, backward, nullptr).bytes;
     if (!exec->workspace || exec->workspace_bytes < need)
         return fail(SDM_ERR_WORKSPACE, "workspace of %zu bytes is below the %zu bytes needed",
                     exec->workspace ? exec->workspace_bytes : size_t(0), need);
@@ -119,23 +119,23 @@ int take_workspace(const sdm_delta_shape *s, DeltaArgs *a, Rows *go, const sdm_e
     int cus = 0;
     const int rc = device_cus(&cus);
     if (rc) return rc;
-    const Layout l = layout(s, go != nullptr, exec->workspace);
+    const Layout l = layout(s, backward, exec->workspace);
     *ws = l.ws;
     if (a->T == 0) return SDM_OK;
     const bool b16 = s->dtype == SDM_BF16;
     const hipStream_t st = static_cast<hipStream_t>(exec->stream);
     auto keys = [&](const Rows &r, KeyRows *k, void *to) {
-        if (!delta_regular_keys(r, b16)) return launch_delta_copy_keys(r, k, to, a->P, a->T, a->Hk, b16, st);
+        if (!delta_regular_keys(r, b16)) return launch_delta_copy_keys(r, k, to, a->P, a->T, a->Hk, b16, kept, st);
         *k = {static_cast<const bf16 *>(r.data), 0, r.sp, r.st, r.sh};
         return hipSuccess;
     };
-    auto values = [&](Rows *r, void *to) {
-        return delta_regular_values(*r, b16) ? hipSuccess : launch_delta_copy_values(r, to, a->P, a->T, a->Hv, b16, st);
+    auto values = [&](Rows *r, void *to, bool there) {
+        return delta_regular_values(*r, b16) ? hipSuccess : launch_delta_copy_values(r, to, a->P, a->T, a->Hv, b16, there, st);
     };
     hipError_t e = keys(a->q, &a->qq, l.q);
     if (e == hipSuccess) e = keys(a->k, &a->kk, l.k);
-    if (e == hipSuccess) e = values(&a->v, l.v);
-    if (e == hipSuccess && go) e = values(go, l.go);
+    if (e == hipSuccess) e = values(&a->v, l.v, kept);
+    if (e == hipSuccess && go) e = values(go, l.go, false);
     return e == hipSuccess ? SDM_OK : hip_fail(e, "gated delta copy launch");
 }
 
@@ -148,7 +148,7 @@ size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *s, int32_t backwar
     return layout(s, backward != 0, nullptr).bytes;
 }
 
-int sdm_gated_delta_fwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
+static int delta_fwd(bool keep, const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
                         const float *log_decay, const float *state, float *state_out, const int32_t *valid, void *out,
                         const sdm_exec *exec) {
     g_err[0] = 0;
@@ -162,11 +162,23 @@ int sdm_gated_delta_fwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_r
     if (state && state_out && state != state_out && overlap(state, state_out, bytes))
         return fail(SDM_ERR_SHAPE, "state_out overlaps state without being it");
     DeltaWs ws{};
-    if ((rc = take_workspace(s, &a, nullptr, exec, &ws))) return rc;
+    if ((rc = take_workspace(s, keep, &a, nullptr, false, exec, &ws))) return rc;
     a.state_out = state_out;
     a.out = out;
     const hipError_t e = launch_delta_fwd(a, ws, s->dtype == SDM_BF16, static_cast<hipStream_t>(exec->stream));
     return e == hipSuccess ? SDM_OK : hip_fail(e, "gated delta launch");
+}
+
+int sdm_gated_delta_fwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
+                        const float *log_decay, const float *state, float *state_out, const int32_t *valid, void *out,
+                        const sdm_exec *exec) {
+    return delta_fwd(false, s, q, k, v, beta, log_decay, state, state_out, valid, out, exec);
+}
+
+int sdm_gated_delta_fwd_keep(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
+                             const float *log_decay, const float *state, float *state_out, const int32_t *valid, void *out,
+                             const sdm_exec *exec) {
+    return delta_fwd(true, s, q, k, v, beta, log_decay, state, state_out, valid, out, exec);
 }
 
 int sdm_gated_delta_step(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
@@ -195,7 +207,7 @@ int sdm_gated_delta_step(const sdm_delta_shape *s, const sdm_rows *q, const sdm_
     return e == hipSuccess ? SDM_OK : hip_fail(e, "gated delta step launch");
 }
 
-int sdm_gated_delta_bwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
+static int delta_bwd(bool kept, const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
                         const float *log_decay, const float *state, const int32_t *valid, const void *grad_out,
                         const float *grad_state_out, const sdm_delta_grads *grads, const sdm_exec *exec) {
     g_err[0] = 0;
@@ -218,10 +230,22 @@ int sdm_gated_delta_bwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_r
         return fail(SDM_ERR_SHAPE, "the state's gradient overlaps an input");
     DeltaWs ws{};
     Rows go{grad_out, int64_t(a.T) * a.Hv * a.V, int64_t(a.Hv) * a.V, a.V, a.V};
-    if ((rc = take_workspace(s, &a, &go, exec, &ws))) return rc;
+    if ((rc = take_workspace(s, true, &a, &go, kept, exec, &ws))) return rc;
     const DeltaGrads g{go, grad_state_out, grads->q, grads->k, grads->v, grads->beta, grads->log_decay, grads->state};
-    const hipError_t e = launch_delta_bwd(a, ws, g, s->dtype == SDM_BF16, static_cast<hipStream_t>(exec->stream));
+    const hipError_t e = launch_delta_bwd(a, ws, g, s->dtype == SDM_BF16, kept, static_cast<hipStream_t>(exec->stream));
     return e == hipSuccess ? SDM_OK : hip_fail(e, "gated delta backward launch");
+}
+
+int sdm_gated_delta_bwd(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
+                        const float *log_decay, const float *state, const int32_t *valid, const void *grad_out,
+                        const float *grad_state_out, const sdm_delta_grads *grads, const sdm_exec *exec) {
+    return delta_bwd(false, s, q, k, v, beta, log_decay, state, valid, grad_out, grad_state_out, grads, exec);
+}
+
+int sdm_gated_delta_bwd_kept(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
+                             const float *log_decay, const float *state, const int32_t *valid, const void *grad_out,
+                             const float *grad_state_out, const sdm_delta_grads *grads, const sdm_exec *exec) {
+    return delta_bwd(true, s, q, k, v, beta, log_decay, state, valid, grad_out, grad_state_out, grads, exec);
 }
 
 }  // extern "C"

@@ -1,7 +1,7 @@
 // The chunked gated delta rule, backward.
 //
-// The forward's chunk quantities are computed again (delta.hip keeps U and every chunk's start
-// state S0). With dS1 the gradient of a chunk's end state:
+// The forward's chunk quantities are computed again, or were kept (delta.hip: X, P, U and every chunk's
+// start state S0). With dS1 the gradient of a chunk's end state:
 //     dU = P^T do + e^{G_C - G} k dS1,   Y = X^T dU
 //     dv = beta Y,   dbeta = Y . U / beta,   dA = -(beta Y) U^T,   dP = do U^T
 //     dS0 = e^{G_C} dS1 + (scale e^G q)^T do - (e^G k)^T (beta Y)
@@ -327,7 +327,7 @@ template <typename T, int C, int KP> struct GradBring {
                 }
             }
             g = lane < live && lane < C ? a.g[(p * int64_t(a.T) + t0 + lane) * a.Hv + h] : 0.0f;
-            gates = reinterpret_cast<const du4 *>(&(reinterpret_cast<const ChunkMem<C, 3> *>(ws.mats) + nc)->g)[lane];
+            gates = reinterpret_cast<const du4 *>(&(reinterpret_cast<const ChunkMem<C> *>(ws.mats) + nc)->g)[lane];
         }
     }
     static __device__ __forceinline__ dt4 kept(du4 x, bool in) { return in ? __builtin_bit_cast(dt4, x) : dt4{}; }
@@ -471,7 +471,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
     extern __shared__ __align__(16) unsigned char raw[];
     Lds &l = *reinterpret_cast<Lds *>(raw);
     typename Lds::Small &sm = l.small;
-    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), lc = lane & 15, lg = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     if (wv >= 8) {
         GradBring<T, C, KP> bring(a, ws, d.go);
         bring.run(l);
@@ -744,9 +744,11 @@ hipError_t delta_bwd_prepare() {
     return e == hipSuccess ? bwd_attrs<bf16>() : e;
 }
 
-hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, bool is_bf16, hipStream_t st) {
-    const hipError_t e = launch_delta_fwd(a, ws, is_bf16, st);
-    if (e != hipSuccess) return e;
+hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, bool is_bf16, bool kept, hipStream_t st) {
+    if (!kept) {
+        const hipError_t e = launch_delta_fwd(a, ws, is_bf16, st);
+        if (e != hipSuccess) return e;
+    }
     return is_bf16 ? bwd_pick<bf16>(a, ws, d, st) : bwd_pick<float>(a, ws, d, st);
 }
 

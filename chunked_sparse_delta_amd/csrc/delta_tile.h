@@ -142,12 +142,7 @@ template <int N> __device__ __forceinline__ Frag<N> read_cols(const unsigned cha
     return f;
 }
 
-// Eight elements as pieces.
-__device__ __forceinline__ Frag<1> load_pieces(const bf16 *p) { return {{*reinterpret_cast<const db8 *>(p)}}; }
-__device__ __forceinline__ Frag<3> load_pieces(const float *p) {
-    return split<3>(*reinterpret_cast<const dt4 *>(p), *reinterpret_cast<const dt4 *>(p + 4));
-}
-// ... and those of a row of q or k.
+// Eight elements of a row of q or k.
 template <int N> __device__ __forceinline__ Frag<N> load_keys(const bf16 *p, int64_t plane) {
     Frag<N> f;
 #pragma unroll
@@ -159,29 +154,6 @@ template <int N> __device__ __forceinline__ void clear(Frag<N> &f) {
     for (int i = 0; i < N; ++i) f.p[i] = __builtin_bit_cast(db8, du4{0, 0, 0, 0});
 }
 
-// Eight neighbours of an output row of which `left` are inside it: one 16-byte store (two for float32) at any element
-// address where all are.
-__device__ __forceinline__ void put_eight(bf16 *p, int left, dt4 a, dt4 b) {
-    typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
-    const raw x = {f32x2_to_bf16x2(a[0], a[1]), f32x2_to_bf16x2(a[2], a[3]), f32x2_to_bf16x2(b[0], b[1]), f32x2_to_bf16x2(b[2], b[3])};
-    if (left >= 8) *reinterpret_cast<raw *>(p) = x;
-    else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < left) p[j].bits = uint16_t(x[j / 2] >> (j & 1 ? 16 : 0));
-    }
-}
-__device__ __forceinline__ void put_eight(float *p, int left, dt4 a, dt4 b) {
-    typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
-    if (left >= 8) {
-        *reinterpret_cast<raw *>(p) = raw{a[0], a[1], a[2], a[3]};
-        *reinterpret_cast<raw *>(p + 4) = raw{b[0], b[1], b[2], b[3]};
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < left) p[j] = j < 4 ? a[j] : b[j - 4];
-    }
-}
 // Pieces of an input element.
 template <typename T> constexpr int kPieces = sizeof(T) == 2 ? 1 : 3;
 // Tokens of a chunk where head_dim is at most 128 (32 above it): two chunks' operands in LDS at once.
@@ -224,12 +196,11 @@ struct BlockAt {
     }
 };
 
-// What the prep kernel leaves of a chunk for the kernels that walk it: the lower 32 x 32 blocks of X in float32, those of P
-// in float32 or, where one piece is wanted (NP = 1), in bfloat16, rows of 32; and the gates.
+// What the prep kernel leaves of a chunk for the kernels that walk it: the lower 32 x 32 blocks of X and P, rows of 32, and the
+// gates.
 template <int C> constexpr int kTri = C == 64 ? 3 : 1;     // blocks (0, 0), (1, 0), (1, 1)
-template <int C, int NP> struct ChunkMem {
-    float X[kTri<C>][32][32];
-    unsigned char P[kTri<C>][NP == 1 ? 2048 : 4096];
+template <int C> struct ChunkMem {
+    float X[kTri<C>][32][32], P[kTri<C>][32][32];
     Gates<C> g;
 };
 // ... and as these have it in LDS: blocks in pieces.
@@ -238,8 +209,8 @@ template <int C, int NP> struct ChunkMats {
     unsigned char P[NP][kTri<C>][kBlk];
     Gates<C> g;
 };
-// Pieces of P. The forward's readings are all that P goes into there: in bfloat16 they are rounded anyway, and P with them (the
-// error against 64 bits grows from 1.66e-3 to at most 1.41 times that). The backward's P reaches float32 gradients.
-template <typename T> constexpr int kPPieces(bool backward) { return backward || sizeof(T) == 4 ? 3 : 1; }
+// Pieces of P. The readings are all that P goes into in the forward: rounded to bfloat16, they take two (one piece would make
+// their error against 64 bits half as large again). The backward's P reaches float32 gradients.
+template <typename T> constexpr int kPPieces(bool backward) { return backward || sizeof(T) == 4 ? 3 : 2; }
 
 }  // namespace sdm

@@ -23,13 +23,11 @@ constexpr int kWalkThreads = 512;
 
 // T: the inputs' type; NP: pieces of P; Q: q and P are wanted too.
 template <typename T, int C, int KP, int NP, bool Q> struct Walk {
-    static constexpr bool kP = Q;
     static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32;
     static constexpr int kStride = TB * KB * kBlk;              // between the pieces of k (and of q)
     static constexpr int KS = kStride / 4096;                   // 16-byte eights of a piece of k per thread
-    using Mem = ChunkMem<C, NP>;
+    using Mem = ChunkMem<C>;
     static constexpr int NE = kTri<C> * 128, ES = (NE + 255) / 256;   // eights of X (and of P), and those of a thread
-    static constexpr int PW = NP == 1 ? 1 : 2;                        // 16-byte pieces of an eight of P
     static constexpr int RS = sizeof(T);                        // 16-byte pieces of a row of v's 16 columns
     static constexpr int VS = C * RS / 64;
     struct Lds {
@@ -55,7 +53,7 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
         const Mem *mats;
         int64_t kplane, qplane, ks, qs, vs;
         int col0, n;
-        du4 k[NI][KS], q[Q ? NI : 1][Q ? KS : 1], v[VS], x[ES][2], pp[ES][PW], g;
+        du4 k[NI][KS], q[Q ? NI : 1][Q ? KS : 1], v[VS], x[ES][2], pp[Q ? ES : 1][2], g;
 
         __device__ Bring(const DeltaArgs &a, const DeltaWs &ws, int p, int h, int hk, int ph, int cg, const Rows &val, int tokens)
             : kp(uniform(a.kk.data + p * a.kk.sp + hk * a.kk.sh)), qp(uniform(a.qq.data + p * a.qq.sp + hk * a.qq.sh)),
@@ -88,12 +86,11 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
 #pragma unroll
             for (int i = 0; i < ES; ++i) {
                 const int e = min(tid + 256 * i, NE - 1);
-                const du4 *px = reinterpret_cast<const du4 *>(&mem.X[0][0][0]), *ppp = reinterpret_cast<const du4 *>(&mem.P[0][0]);
+                const du4 *px = reinterpret_cast<const du4 *>(&mem.X[0][0][0]), *from = reinterpret_cast<const du4 *>(&mem.P[0][0][0]);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) x[i][w] = px[e * 2 + w];
-                if constexpr (kP) {
-#pragma unroll
-                    for (int w = 0; w < PW; ++w) pp[i][w] = ppp[e * PW + w];
+                for (int w = 0; w < 2; ++w) {
+                    x[i][w] = px[e * 2 + w];
+                    if constexpr (Q) pp[i][w] = from[e * 2 + w];
                 }
             }
             g = reinterpret_cast<const du4 *>(&mem.g)[lane];
@@ -116,14 +113,14 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
                 const int e = tid + 256 * i;
                 if (NE % 256 && e >= NE) break;
                 const int at = block_at(e % 128 / 4, e % 4);
-                auto put = [&](unsigned char *blk, const Frag<3> &f) {
+                const Frag<3> fx = split<3>(__builtin_bit_cast(dt4, x[i][0]), __builtin_bit_cast(dt4, x[i][1]));
 #pragma unroll
-                    for (int n = 0; n < 3; ++n) *reinterpret_cast<db8 *>(blk + n * kTri<C> * kBlk + at) = f.p[n];
-                };
-                put(s.m.X[0][e / 128], split<3>(__builtin_bit_cast(dt4, x[i][0]), __builtin_bit_cast(dt4, x[i][1])));
-                if constexpr (kP && NP == 1) *reinterpret_cast<du4 *>(s.m.P[0][e / 128] + at) = pp[i][0];
-                if constexpr (kP && NP == 3)
-                    put(s.m.P[0][e / 128], split<3>(__builtin_bit_cast(dt4, pp[i][0]), __builtin_bit_cast(dt4, pp[i][PW - 1])));
+                for (int n = 0; n < 3; ++n) *reinterpret_cast<db8 *>(s.m.X[n][e / 128] + at) = fx.p[n];
+                if constexpr (Q) {
+                    const Frag<NP> fp = split<NP>(__builtin_bit_cast(dt4, pp[i][0]), __builtin_bit_cast(dt4, pp[i][1]));
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) *reinterpret_cast<db8 *>(s.m.P[n][e / 128] + at) = fp.p[n];
+                }
             }
             if (wv == 0) reinterpret_cast<du4 *>(&s.m.g)[lane] = g;
         }

@@ -44,12 +44,14 @@ def bind(lib) -> None:
     lib.sdm_gated_delta_fwd.argtypes = [p] * 11
     lib.sdm_gated_delta_step.argtypes = [p] * 9 + [i64, p, p, p]
     lib.sdm_gated_delta_bwd.argtypes = [p] * 12
+    lib.sdm_gated_delta_fwd_keep.argtypes = [p] * 11
+    lib.sdm_gated_delta_bwd_kept.argtypes = [p] * 12
     lib.sdm_layer_norm_fwd.argtypes = [i64, i32, p, i32, p, p, i32, f32, p, p, p, p]
     lib.sdm_layer_norm_bwd_workspace_bytes.argtypes = [i64, i32, i32]
     lib.sdm_layer_norm_bwd_workspace_bytes.restype = sz
     lib.sdm_layer_norm_bwd.argtypes = [i64, i32, p, p, i32, p, i32, p, p, p, p, p, p]
-    for fn in (lib.sdm_gated_delta_fwd, lib.sdm_gated_delta_step, lib.sdm_gated_delta_bwd, lib.sdm_layer_norm_fwd,
-               lib.sdm_layer_norm_bwd):
+    for fn in (lib.sdm_gated_delta_fwd, lib.sdm_gated_delta_step, lib.sdm_gated_delta_bwd, lib.sdm_gated_delta_fwd_keep,
+               lib.sdm_gated_delta_bwd_kept, lib.sdm_layer_norm_fwd, lib.sdm_layer_norm_bwd):
         fn.restype = ctypes.c_int
 
 
@@ -161,12 +163,15 @@ def _scratch(lib, shape, backward, dev, stream):
 def gated_delta_fwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, log_decay: torch.Tensor,
                     q: torch.Tensor, *, scale: float | None = None, valid_tokens: torch.Tensor | None = None,
                     state_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                    workspace: torch.Tensor | None = None, keep: bool = False, stream=None) -> torch.Tensor:
     """The rule over whole sequences; returns the readings [P, T, Hv, V]. ``state`` is advanced in place, or left as it
     is where ``state_out`` is given, which then gets the final state. ``state=None`` starts from zeros (the final state
-    goes to ``state_out`` if given). ``workspace`` (uint8, GPU, gated_delta_workspace_bytes) is allocated if omitted."""
+    goes to ``state_out`` if given). ``workspace`` (uint8, GPU, gated_delta_workspace_bytes) is allocated if omitted. ``keep``: the given workspace, of the backward's size,
+    keeps what gated_delta_bwd(kept=workspace) then does not compute again."""
     lib = _load()
     full, shape, qr, kr, vr, dev, index = _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens)
+    if keep and workspace is None:
+        raise ValueError("keep needs a workspace (gated_delta_workspace_bytes(..., backward=True))")
     if state is not None:
         _need(state, "state", full, torch.float32, dev)
     if state_out is None:
@@ -176,8 +181,9 @@ def gated_delta_fwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
     out = _out(out, v, stream)
     if workspace is None:
         workspace = _scratch(lib, shape, 0, dev, stream)
-    rc = lib.sdm_gated_delta_fwd(shape, qr, kr, vr, beta.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(state_out),
-                                 _ptr(valid_tokens), out.data_ptr(), _exec(stream, index, workspace))
+    call = lib.sdm_gated_delta_fwd_keep if keep else lib.sdm_gated_delta_fwd
+    rc = call(shape, qr, kr, vr, beta.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(state_out), _ptr(valid_tokens),
+              out.data_ptr(), _exec(stream, index, workspace))
     if rc:
         _check_rc(lib, rc)
     return out
@@ -217,10 +223,11 @@ def gated_delta_step(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta
 def gated_delta_bwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, log_decay: torch.Tensor,
                     q: torch.Tensor, grad_out: torch.Tensor, *, grad_state: torch.Tensor | None = None,
                     scale: float | None = None, valid_tokens: torch.Tensor | None = None,
-                    workspace: torch.Tensor | None = None, stream=None) -> dict:
+                    workspace: torch.Tensor | None = None, kept: torch.Tensor | None = None, stream=None) -> dict:
     """Backward of gated_delta_fwd from the ``state`` it STARTED from (None: zeros). ``grad_out`` [P, T, Hv, V] is the
     gradient of the readings, ``grad_state`` (float32, optional) that of the final state. Returns dict(state, k, v, beta,
-    log_decay, q): k, v and q in the inputs' dtype (sums over sharing heads in float32), the others float32."""
+    log_decay, q): k, v and q in the inputs' dtype (sums over sharing heads in float32), the others float32. ``kept``: the workspace of a
+    gated_delta_fwd(keep=True) with the same inputs, in place of ``workspace``; without it the forward is computed again."""
     lib = _load()
     full, shape, qr, kr, vr, dev, index = _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens)
     _need(grad_out, "grad_out", v.shape, v.dtype, dev)
@@ -233,12 +240,14 @@ def gated_delta_bwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
              log_decay=torch.empty_like(log_decay), q=torch.empty(q.shape, dtype=q.dtype, device=dev))
     if stream is not None:
         _used_on(stream, *g.values())
-    if workspace is None:
+    if kept is not None:
+        workspace = kept
+    elif workspace is None:
         workspace = _scratch(lib, shape, 1, dev, stream)
-    rc = lib.sdm_gated_delta_bwd(shape, qr, kr, vr, beta.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(valid_tokens),
-                                 grad_out.data_ptr(), _ptr(grad_state),
-                                 _GRADS(*(g[n].data_ptr() for n in ("q", "k", "v", "beta", "log_decay", "state"))),
-                                 _exec(stream, index, workspace))
+    call = lib.sdm_gated_delta_bwd if kept is None else lib.sdm_gated_delta_bwd_kept
+    rc = call(shape, qr, kr, vr, beta.data_ptr(), log_decay.data_ptr(), _ptr(state), _ptr(valid_tokens), grad_out.data_ptr(),
+              _ptr(grad_state), _GRADS(*(g[n].data_ptr() for n in ("q", "k", "v", "beta", "log_decay", "state"))),
+              _exec(stream, index, workspace))
     if rc:
         _check_rc(lib, rc)
     return g
@@ -246,32 +255,41 @@ def gated_delta_bwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
 
 class _GatedDeltaRule(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, state, k, v, beta, log_decay, q, scale, valid_tokens):
-        P, _, Hv, V = v.shape
-        final = torch.empty((P, Hv, k.shape[3], V), dtype=torch.float32, device=v.device)
-        out = gated_delta_fwd(state, k, v, beta, log_decay, q, scale=scale, valid_tokens=valid_tokens, state_out=final)
-        ctx.save_for_backward(state, k, v, beta, log_decay, q, valid_tokens)
+    def forward(ctx, state, k, v, beta, log_decay, q, scale, valid_tokens, recompute):
+        P, T, Hv, V = v.shape
+        Hk, K = k.shape[2:]
+        final = torch.empty((P, Hv, K, V), dtype=torch.float32, device=v.device)
+        kept = None
+        if not recompute and any(ctx.needs_input_grad):
+            n = gated_delta_workspace_bytes(P, T, Hk, Hv, K, V, v.dtype, True)
+            kept = torch.empty(max(n, 256), dtype=torch.uint8, device=v.device)     # 0: the call itself reports why
+        out = gated_delta_fwd(state, k, v, beta, log_decay, q, scale=scale, valid_tokens=valid_tokens, state_out=final,
+                              workspace=kept, keep=kept is not None)
+        ctx.save_for_backward(state, k, v, beta, log_decay, q, valid_tokens, kept)
         ctx.scale = scale
         ctx.set_materialize_grads(False)
         return out, final
 
     @staticmethod
     def backward(ctx, grad_out, grad_state):
-        state, k, v, beta, log_decay, q, valid = ctx.saved_tensors
+        state, k, v, beta, log_decay, q, valid, kept = ctx.saved_tensors
         if grad_out is None and grad_state is None:
-            return (None,) * 8
+            return (None,) * 9
         go = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if grad_out is None else grad_out.contiguous()
         gs = None if grad_state is None else grad_state.contiguous()
-        g = gated_delta_bwd(state, k, v, beta, log_decay, q, go, grad_state=gs, scale=ctx.scale, valid_tokens=valid)
+        g = gated_delta_bwd(state, k, v, beta, log_decay, q, go, grad_state=gs, scale=ctx.scale, valid_tokens=valid, kept=kept)
         names = ("state", "k", "v", "beta", "log_decay", "q")
-        return (*(g[n] if need else None for n, need in zip(names, ctx.needs_input_grad)), None, None)
+        return (*(g[n] if need else None for n, need in zip(names, ctx.needs_input_grad)), None, None, None)
 
 
 def gated_delta_rule(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, log_decay: torch.Tensor,
-                     q: torch.Tensor, *, scale: float | None = None, valid_tokens: torch.Tensor | None = None):
+                     q: torch.Tensor, *, scale: float | None = None, valid_tokens: torch.Tensor | None = None,
+                     recompute: bool = False):
     """The rule for autograd: returns (readings, final state); ``state`` (None: zeros) is not changed. Gradients reach
-    the state, k, v, beta, log_decay and q through gated_delta_bwd, which computes the forward again from its inputs."""
-    return _GatedDeltaRule.apply(state, k, v, beta, log_decay, q, scale, valid_tokens)
+    the state, k, v, beta, log_decay and q through gated_delta_bwd. Until the backward the forward keeps what it computed
+    per chunk (gated_delta_workspace_bytes(..., backward=True)); ``recompute=True`` keeps the inputs alone and computes the
+    forward again, for less memory and about a quarter more time."""
+    return _GatedDeltaRule.apply(state, k, v, beta, log_decay, q, scale, valid_tokens, recompute)
 
 
 # ---- layer norm ------------------------------------------------------------------------------------------------------

@@ -70,8 +70,8 @@ int sdm_gated_delta_step(const sdm_delta_shape *shape, const sdm_rows *q, const 
                          const int32_t *state_ids, int64_t slots, const int32_t *valid_tokens, void *out,
                          const sdm_exec *exec);
 
-/* Workspace bytes of sdm_gated_delta_fwd (backward = 0) or sdm_gated_delta_bwd (1); 0 for
- * shapes they reject. */
+/* Workspace bytes of sdm_gated_delta_fwd (backward = 0) or of the backward and of
+ * sdm_gated_delta_fwd_keep (1); 0 for shapes they reject. */
 size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *shape, int32_t backward);
 
 /*
@@ -100,6 +100,20 @@ int sdm_gated_delta_bwd(const sdm_delta_shape *shape, const sdm_rows *q, const s
                         const float *beta, const float *log_decay, const float *state, const int32_t *valid_tokens,
                         const void *grad_out, const float *grad_state_out, const sdm_delta_grads *grads,
                         const sdm_exec *exec);
+
+/*
+ * The pair for training that computes the forward once: sdm_gated_delta_fwd_keep is
+ * sdm_gated_delta_fwd on a workspace of the backward's size, in which it leaves what
+ * sdm_gated_delta_bwd_kept, with the same inputs and that workspace unchanged, then does not
+ * compute again. A token whose |beta| is below 1e-20 counts as one of 1e-20 in both.
+ */
+int sdm_gated_delta_fwd_keep(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
+                             const float *beta, const float *log_decay, const float *state, float *state_out,
+                             const int32_t *valid_tokens, void *out, const sdm_exec *exec);
+int sdm_gated_delta_bwd_kept(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
+                             const float *beta, const float *log_decay, const float *state, const int32_t *valid_tokens,
+                             const void *grad_out, const float *grad_state_out, const sdm_delta_grads *grads,
+                             const sdm_exec *exec);
 
 /*
  * Layer norm over the last axis of a dense device [rows, cols] array in dtype:

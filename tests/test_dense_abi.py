@@ -26,7 +26,8 @@ def lib():
 def test_exports(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(sdm_\w+)\s*\(", text)))
-    assert names == ["sdm_gated_delta_bwd", "sdm_gated_delta_fwd", "sdm_gated_delta_step", "sdm_gated_delta_workspace_bytes",
+    assert names == ["sdm_gated_delta_bwd", "sdm_gated_delta_bwd_kept", "sdm_gated_delta_fwd", "sdm_gated_delta_fwd_keep",
+                     "sdm_gated_delta_step", "sdm_gated_delta_workspace_bytes",
                      "sdm_layer_norm_bwd", "sdm_layer_norm_bwd_workspace_bytes", "sdm_layer_norm_fwd"]
     assert all(hasattr(lib, n) for n in names)
 

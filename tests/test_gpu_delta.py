@@ -111,6 +111,26 @@ def test_backward_matches_oracle(gpu, P, T, Hk, Hv, K, V, dtype, valid):
         assert torch.equal(got[n], again[n]), n
 
 
+@pytest.mark.parametrize("P,T,Hk,Hv,K,V,dtype,valid", CASES, ids=IDS)
+def test_kept_forward(gpu, P, T, Hk, Hv, K, V, dtype, valid):
+    """A forward that keeps what it computed gives the readings to the bar and the backward's own gradients, twice over."""
+    import chunked_sparse_delta_amd as sdm
+    g = gpu_of(make(P, T, Hk, Hv, K, V, DT[dtype], seed=6), gpu)
+    go = torch.randn((P, T, Hv, V), generator=torch.Generator().manual_seed(5)).to(DT[dtype]).to(gpu)
+    vt = None if valid is None else torch.tensor(valid, dtype=torch.int32, device=gpu)
+    ws = torch.full((sdm.gated_delta_workspace_bytes(P, T, Hk, Hv, K, V, DT[dtype], True),), 0xFF, dtype=torch.uint8, device=gpu)
+    a, b = torch.empty_like(g["state"]), torch.empty_like(g["state"])
+    out = sdm.gated_delta_fwd(*(g[n] for n in NAMES), valid_tokens=vt, state_out=a, workspace=ws, keep=True)
+    plain = sdm.gated_delta_fwd(*(g[n] for n in NAMES), valid_tokens=vt, state_out=b)
+    close(out, plain.double().cpu(), "readings", DT[dtype])
+    close(a, b.double().cpu(), "state")
+    want = sdm.gated_delta_bwd(*(g[n] for n in NAMES), go, valid_tokens=vt)
+    for _ in range(2):
+        got = sdm.gated_delta_bwd(*(g[n] for n in NAMES), go, valid_tokens=vt, kept=ws)
+        for n in NAMES:
+            assert torch.equal(got[n], want[n]), n
+
+
 def test_no_state_and_no_tokens(gpu):
     """state=None starts from zeros; T = 0 copies the state and gives an empty result; gradients of no tokens."""
     import chunked_sparse_delta_amd as sdm
@@ -266,13 +286,16 @@ def test_autograd(gpu):
     g = gpu_of(make(2, 50, 1, 2, 32, 24, torch.float32), gpu)
     for t in g.values():
         t.requires_grad_()
-    out, state = sdm.gated_delta_rule(*(g[n] for n in NAMES))
-    loss = (out.transpose(1, 2) ** 2).sum() + state.sum()
-    grads = torch.autograd.grad(loss, [g[n] for n in NAMES])
-    with torch.no_grad():
-        want = sdm.gated_delta_bwd(*(g[n] for n in NAMES), 2 * out, grad_state=torch.ones_like(state))
-    for n, t in zip(NAMES, grads):
-        assert torch.equal(t, want[n]), n
+    for recompute in (False, True):
+        out, state = sdm.gated_delta_rule(*(g[n] for n in NAMES), recompute=recompute)
+        loss = (out.transpose(1, 2) ** 2).sum() + state.sum()
+        grads = torch.autograd.grad(loss, [g[n] for n in NAMES])
+        with torch.no_grad():
+            end = torch.empty_like(state)
+            assert torch.equal(out, sdm.gated_delta_fwd(*(g[n] for n in NAMES), state_out=end)) and torch.equal(state, end)
+            want = sdm.gated_delta_bwd(*(g[n] for n in NAMES), 2 * out, grad_state=torch.ones_like(state))
+        for n, t in zip(NAMES, grads):
+            assert torch.equal(t, want[n]), n
     out, _ = sdm.gated_delta_rule(None, *(g[n].detach() for n in NAMES[1:5]), g["q"])
     out.sum().backward()
     assert g["q"].grad is not None and g["k"].grad is None
