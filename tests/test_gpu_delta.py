@@ -131,6 +131,124 @@ def test_kept_forward(gpu, P, T, Hk, Hv, K, V, dtype, valid):
             assert torch.equal(got[n], want[n]), n
 
 
+# Few states and many chunks: the forward walks segments of such sequences at once and joins them. A segment's start state is
+# one more sum of head_dim products of float32 quantities: within the float32 bar's derivation.
+LONG = [
+    (1, 1500, 1, 1, 64, 64, "f32", None), (1, 2111, 1, 2, 40, 20, "bf16", None), (2, 1100, 1, 1, 200, 33, "bf16", (1100, 517)),
+    (3, 1024, 1, 1, 128, 64, "bf16", (0, 70, 1024)), (2, 700, 1, 1, 128, 128, "f32", (33, 699)),
+]
+
+
+@pytest.mark.parametrize("decay", [0.3, 0.0])
+@pytest.mark.parametrize("state", [True, False])
+@pytest.mark.parametrize("P,T,Hk,Hv,K,V,dtype,valid", LONG)
+def test_long_sequences_of_few_states(gpu, P, T, Hk, Hv, K, V, dtype, valid, state, decay):
+    import chunked_sparse_delta_amd as sdm
+    x = make(P, T, Hk, Hv, K, V, DT[dtype], seed=9, state=state, decay=decay)
+    y, g = f64_of(x), gpu_of(x, gpu)
+    start = y["state"] if state else torch.zeros((P, Hv, K, V), dtype=torch.float64)
+    want, final = oracle.gated_delta(start, *(y[n] for n in NAMES[1:]), K ** -0.5, valid)
+    vt = None if valid is None else torch.tensor(valid, dtype=torch.int32, device=gpu)
+    end = torch.full((P, Hv, K, V), float("nan"), device=gpu)
+    out = sdm.gated_delta_fwd(*(g[n] for n in NAMES), valid_tokens=vt, state_out=end)
+    close(out, want, "readings", DT[dtype])
+    close(end, final, "state")
+    for p in range(P):
+        if valid is not None:
+            assert (out[p, valid[p]:] == 0).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(gpu, seed):
+    """Every entry point on drawn sizes, types, valid counts, and rows at odd element offsets."""
+    import random
+    import chunked_sparse_delta_amd as sdm
+    rng = random.Random(seed)
+    Hk, dt = rng.randint(1, 4), rng.choice([torch.float32, torch.bfloat16])
+    P, T, Hv, K, V = rng.randint(1, 4), rng.randint(1, 200), Hk * rng.randint(1, 3), rng.randint(1, 256), rng.randint(1, 150)
+    valid = [rng.randint(0, T) for _ in range(P)] if rng.random() < 0.5 else None
+    x = make(P, T, Hk, Hv, K, V, dt, seed=seed)
+    go = torch.randn((P, T, Hv, V), generator=torch.Generator().manual_seed(seed)).to(dt)
+    y, g = f64_of(x, grad=True), gpu_of(x, gpu)
+    if rng.random() < 0.5:
+        for n in "kvq":     # one element past an aligned address, a token stride that no vector divides
+            t = g[n]
+            flat = torch.full((t.shape[0], t.shape[1], t[0, 0].numel() + 3), float("nan"), dtype=dt, device=gpu)
+            g[n] = flat[..., 1:1 + t[0, 0].numel()].unflatten(2, t.shape[2:]).copy_(t)
+    vt = None if valid is None else torch.tensor(valid, dtype=torch.int32, device=gpu)
+    out, final = oracle.gated_delta(*(y[n] for n in NAMES), K ** -0.5, valid)
+    for call in (sdm.gated_delta_fwd, sdm.gated_delta_step):
+        end = torch.empty_like(g["state"])
+        close(call(*(g[n] for n in NAMES), valid_tokens=vt, state_out=end), out, "readings", dt)
+        close(end, final, "state")
+    (out * go.double()).sum().backward()
+    got = sdm.gated_delta_bwd(*(g[n] for n in NAMES), go.to(gpu), valid_tokens=vt)
+    for n in NAMES:
+        close(got[n], y[n].grad, n, got[n].dtype)
+
+
+def test_rows_past_32_bits(gpu):
+    """Streams and heads of q, k and v, and slots of a state pool, further apart than 2^32 elements."""
+    import chunked_sparse_delta_amd as sdm
+    P, T, H, K, V = 2, 70, 2, 64, 64
+    x = make(P, T, H, H, K, V, torch.bfloat16)
+    g = gpu_of(x, gpu)
+    far = 2 ** 32 + 8
+    room = torch.empty(far + 2 ** 21, dtype=torch.bfloat16, device=gpu)
+    for n, at, stride in (("q", 0, (far, 2 * K, K)), ("k", 2 ** 19, (2 ** 20, K, far)), ("v", 3 * 2 ** 18, (far, V, 2 ** 16))):
+        g[n + "far"] = room.as_strided((P, T, H, K), (*stride, 1), at).copy_(g[n])
+    for call in (sdm.gated_delta_fwd, sdm.gated_delta_step):
+        a, b = torch.empty_like(g["state"]), torch.empty_like(g["state"])
+        one = call(g["state"], g["k"], g["v"], g["beta"], g["log_decay"], g["q"], state_out=a)
+        two = call(g["state"], g["kfar"], g["vfar"], g["beta"], g["log_decay"], g["qfar"], state_out=b)
+        assert torch.equal(one, two) and torch.equal(a, b)
+    del room, g["qfar"], g["kfar"], g["vfar"]
+    slots = 2 ** 32 // (H * K * V) + 2
+    pool = torch.empty((slots, H, K, V), device=gpu)
+    ids = torch.tensor([slots - 1, 0], dtype=torch.int32, device=gpu)
+    pool[slots - 1], pool[0] = g["state"][0], g["state"][1]
+    start = g["state"].clone()
+    out = sdm.gated_delta_step(pool, *(g[n] for n in NAMES[1:]), state_ids=ids)
+    want = sdm.gated_delta_step(start, *(g[n] for n in NAMES[1:]))
+    assert torch.equal(out, want) and torch.equal(pool[slots - 1], start[0]) and torch.equal(pool[0], start[1])
+
+
+def test_graph(gpu):
+    """Captured calls replay with the eager calls' bits, other work in between."""
+    import chunked_sparse_delta_amd as sdm
+    for P, T, K, V, dt in ((1, 600, 64, 64, torch.float32), (2, 130, 40, 24, torch.bfloat16)):
+        g = gpu_of(make(P, T, 1, 2, K, V, dt), gpu)
+        go = torch.randn((P, T, 2, V), device=gpu).to(dt)
+        x = torch.randn((T, 2 * V), device=gpu).to(dt)
+        w = torch.randn(2 * V, device=gpu).to(dt)
+
+        def work():
+            end = torch.empty_like(g["state"])
+            y, mean, rstd = sdm.layer_norm_fwd(x, w)
+            return [sdm.gated_delta_fwd(*(g[n] for n in NAMES), state_out=end), end, y,
+                    *sdm.layer_norm_bwd(y, x, mean, rstd, w).values(),
+                    sdm.gated_delta_step(*(g[n] for n in NAMES), state_out=torch.empty_like(end)),
+                    *sdm.gated_delta_bwd(*(g[n] for n in NAMES), go).values()]
+
+        work()
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            work()
+        torch.cuda.current_stream().wait_stream(side)
+        with torch.cuda.graph(graph):
+            got = work()
+        for seed in range(3):
+            torch.cuda.synchronize()
+            new = gpu_of(make(P, T, 1, 2, K, V, dt, seed=seed), gpu)
+            for n in NAMES:
+                g[n].copy_(new[n])
+            want = work()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_no_state_and_no_tokens(gpu):
     """state=None starts from zeros; T = 0 copies the state and gives an empty result; gradients of no tokens."""
     import chunked_sparse_delta_amd as sdm
