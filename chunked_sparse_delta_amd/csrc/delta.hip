@@ -325,12 +325,12 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
 #pragma unroll
             for (int e = 0; e < 2; ++e) f[e] = read_rows<NP>(s.m.P[0][i], NTR * kBlk, e);
         };
-        Frag<NI> fk[2][KB];          // blocks of k^T, half of a row block of them at a time
+        Frag<NI> fk[2][KB];          // blocks of k^T, half of a row block of them at a time (the halves of all row blocks in turn)
         auto kt_of = [&](Frag<NI>(&f)[KB], int i) {
 #pragma unroll
             for (int m = 0; m < KB; ++m) {
-                const int kb = i % 2 * (KB / 2) + m / 2;
-                f[m] = read_cols<NI>(s.k[0][i / 2][kb], W::kStride, m & 1);
+                const int kb = i / TB * (KB / 2) + m / 2;
+                f[m] = read_cols<NI>(s.k[0][i % TB][kb], W::kStride, m & 1);
             }
         };
 #pragma unroll
@@ -391,14 +391,16 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
             each_product<3, NI, 3>([&](int x, int l) {
 #pragma unroll
                 for (int m = 0; m < KB; ++m) {
-                    const int kb = i % 2 * (KB / 2) + m / 2;
-                    S[kb][m & 1] = mma1(fk[i & 1][m].p[x], fu[i / 2].p[l], S[kb][m & 1]);
+                    const int kb = i / TB * (KB / 2) + m / 2;
+                    S[kb][m & 1] = mma1(fk[i & 1][m].p[x], fu[i % TB].p[l], S[kb][m & 1]);
                 }
             });
             lds_point();
-        }
+            if (i % TB == TB - 1) {      // half of the rows are there
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
+                for (int kb = i / TB * (KB / 2); kb < (i / TB + 1) * (KB / 2); ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
+            }
+        }
         W::turn();
     }
     if constexpr (READ) {
@@ -416,38 +418,62 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
 }
 
 // The segments' start states from their maps M and their end states from zeros N, in order: S_{i + 1} = M_i S_i + N_i. A
-// wavefront takes 16 columns; the next rows of M are on their way under the products.
+// workgroup takes 16 columns, its four wavefronts a quarter of the rows each, which meet in LDS between the steps; the next step's
+// M is on its way under the products. (A wavefront for all the rows of 16 columns, splitting all of M by itself, took
+// 38 us for three steps of 16 heads of 128 x 128; this takes 13.5.)
 template <int KP> __global__ __launch_bounds__(256, 1) void delta_join_kernel(DeltaWs ws, int heads, int VP) {
-    constexpr int KB = KP / 32;
-    const int slices = (VP + 63) / 64, slice = blockIdx.x % slices, ph = blockIdx.x / slices;
-    const int lane = threadIdx.x & 63, lc = lane & 15, lg = lane >> 4, col = (slice * 4 + int(threadIdx.x >> 6)) * 16 + lc;
-    dt4 S[KB][2], N[KB][2];
-    load_state<KB>(S, ws.seg_state + int64_t(heads) * KP * VP, ph, KP, VP, col);
-    for (int i = 1; i + 1 < ws.segs; ++i) {
-        float *next = ws.seg_state + int64_t(i + 1) * heads * KP * VP;
-        load_state<KB>(N, next, ph, KP, VP, col);
-        Frag<3> fs[KB];
+    constexpr int KB = KP / 32, TILES = KB / 2, BUF = KP <= 128 ? 2 : 1;     // TILES of a wavefront, 16 rows each
+    __shared__ dt4 shared[2][2 * KB][64];
+    const int VG = VP / 16, ph = blockIdx.x / VG, lane = threadIdx.x & 63, lc = lane & 15, lg = lane >> 4;
+    const int col = int(blockIdx.x) % VG * 16 + lc, t0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * TILES;
+    auto at = [&](int i, int t) { return (int64_t(i) * heads + ph) * KP * VP + int64_t(t / 2 * 32 + lg * 8 + t % 2 * 4) * VP + col; };
+    auto tile_of = [&](int i, int t) {
+        dt4 x;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(S[kb][0], S[kb][1]);
+        for (int r = 0; r < 4; ++r) x[r] = ws.seg_state[at(i, t) + r * VP];
+        return x;
+    };
+    struct Next {
+        dt4 m[TILES][KB][2], n[TILES];
+    } next[BUF];
+    auto load = [&](Next &x, int i) {
         const float *M = ws.seg_map + (int64_t(i) * heads + ph) * KP * KP + lg * 8;
-        dt4 m[2][KB][2];
-        auto load = [&](dt4(&x)[KB][2], int t) {     // row tile t of M
-            const float *row = M + (t / 2 * 32 + block_row(lc, t & 1)) * KP;
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+            const float *row = M + ((t0 + j) / 2 * 32 + block_row(lc, (t0 + j) & 1)) * KP;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) x[kb][e] = *reinterpret_cast<const dt4 *>(row + kb * 32 + e * 4);
-        };
-        load(m[0], 0);
-#pragma unroll
-        for (int t = 0; t < 2 * KB; ++t) {
-            if (t + 1 < 2 * KB) load(m[(t + 1) & 1], t + 1);
-            dt4 x[2] = {N[t / 2][t & 1], dt4{}};
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) x[kb & 1] = mma<3>(split<3>(m[t & 1][kb][0], m[t & 1][kb][1]), fs[kb], x[kb & 1]);
-            S[t / 2][t & 1] = x[0] + x[1];
+                for (int e = 0; e < 2; ++e) x.m[j][kb][e] = *reinterpret_cast<const dt4 *>(row + kb * 32 + e * 4);
+            x.n[j] = tile_of(i + 1, t0 + j);
         }
-        store_state<KB>(S, next, ph, KP, VP, col);
+    };
+    const int last = ws.segs - 2;
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) shared[1][t0 + j][lane] = tile_of(1, t0 + j);
+    if (last > 0) load(next[0], 1);
+    lds_barrier();
+    auto step = [&](int i, Next &now, Next &then) {
+        Frag<3> fs[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) fs[kb] = split<3>(shared[i & 1][2 * kb][lane], shared[i & 1][2 * kb + 1][lane]);
+        if (BUF == 2 && i < last) load(then, i + 1);
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+            dt4 x[2] = {now.n[j], dt4{}};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) x[kb & 1] = mma<3>(split<3>(now.m[j][kb][0], now.m[j][kb][1]), fs[kb], x[kb & 1]);
+            x[0] += x[1];
+            shared[~i & 1][t0 + j][lane] = x[0];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ws.seg_state[at(i + 1, t0 + j) + r * VP] = x[0][r];
+        }
+        if (BUF == 1 && i < last) load(then, i + 1);
+        lds_barrier();
+    };
+    for (int i = 1; i <= last; i += 2) {
+        step(i, next[0], next[BUF - 1]);
+        if (i < last) step(i + 1, next[BUF - 1], next[0]);
     }
 }
 
@@ -496,7 +522,7 @@ template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const
     if (ws.segs > 1) {
         hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kMap>), dim3(heads * (slices + KP / 64) * unsigned(ws.segs - 1)), dim3(kWalkThreads),
                            (Walk<T, C, KP, N0, false>::kLds), st, a, ws);
-        hipLaunchKernelGGL(delta_join_kernel<KP>, dim3(heads * slices), dim3(256), 0, st, ws, int(heads), (a.V + 15) / 16 * 16);
+        hipLaunchKernelGGL(delta_join_kernel<KP>, dim3(heads * (unsigned(a.V + 15) / 16)), dim3(256), 0, st, ws, int(heads), (a.V + 15) / 16 * 16);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -575,7 +601,7 @@ hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool
 
 // A workgroup walks a sequence's chunks one after the other, at a pace that hardly depends on the others: few states leave
 // most of the device idle. Walking segments at once costs the readings' walk again, once for the columns of the state and once
-// for those of the map, a third cheaper (no readings), and a join of about a chunk's time per segment.
+// for those of the map, a third cheaper (no readings), and a join of about a chunk's time per segment (4 us of 3.4).
 int delta_segments(int64_t heads, int slices, int K, int Nt) {
     const int64_t wgs = heads * slices, maps = heads * (slices + delta_kp(K) / 64);
     int best = 1;
@@ -584,7 +610,7 @@ int delta_segments(int64_t heads, int slices, int K, int Nt) {
     for (int g = 3; g <= 32 && Nt / g >= 4; ++g) {
         const int64_t len = (Nt + g - 1) / g;
         const int64_t a = (wgs + (g - 2) * maps + kCus - 1) / kCus, b = (wgs * g + kCus - 1) / kCus;
-        const double t = double(len) * (0.7 * double(a) + double(b)) + 1.2 * double(g) + 6.0;
+        const double t = double(len) * (0.7 * double(a) + double(b)) + 1.0 * double(g) + 6.0;
         if (t < 0.9 * least) {
             least = t / 0.9 < least ? t : least;
             best = g;
