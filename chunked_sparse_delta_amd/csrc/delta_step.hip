@@ -9,6 +9,8 @@
 // through all tokens: CW / VW lanes side by side hold VW columns each of a row, and
 // RG = 64 VW / CW such groups of lanes a share of the rows each, so a load instruction fetches RG row pieces of CW columns
 // and the reduction over the rows is RG-way across lanes. Wavefronts share nothing.
+// Measured: 64 streams x 32 heads of 128 x 128: 56 us, 4.8 TB/s (a large copy: 5.1); one stream of 16 heads: 7.4 us, the way to
+// memory and back twice after a launch; 7 x 10 heads of 72 x 200, three tokens, float32: 11.6 us.
 #include "delta.h"
 
 namespace sdm {

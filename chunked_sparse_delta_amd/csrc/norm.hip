@@ -15,6 +15,10 @@
 // The backward's sums over rows have a fixed order: workgroup g of G takes the row groups g, g + G, ...,
 // keeps its columns' sums in registers and writes them once; a second kernel adds the G
 // partial rows in order.
+//
+// Measured, 16384 rows of 4096 bfloat16 columns: forward 47 us (5.7 TB/s; 59 in the middle of a training step), backward 82 to 91
+// us (402 MB, 4.4 to 4.9 TB/s) and 4 for the sums over workgroups; a large copy: 5.1 TB/s. 64 rows: 5 us, a launch and two ways
+// to memory. 1001 rows of 1537 float32 columns: 7.8 and 10.7 + 4.3 us.
 #include "common.h"
 #include "host.h"
 

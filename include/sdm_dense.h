@@ -51,6 +51,9 @@ typedef struct {
  *   exec->workspace: sdm_gated_delta_workspace_bytes(shape, 0) bytes, 256-byte aligned.
  * Arithmetic: products of the inputs and of float32 quantities accumulate in float32; the
  * state stays float32 throughout; out is rounded once. Bitwise reproducible.
+ * Chunks of tokens are computed as one: an infinity or NaN in a live token's inputs may reach
+ * readings of earlier tokens of its chunk (up to 63 before it), never other heads or streams.
+ * Padding tokens may hold anything.
  */
 int sdm_gated_delta_fwd(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
                         const float *beta, const float *log_decay, const float *state, float *state_out,
