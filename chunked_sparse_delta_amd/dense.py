@@ -23,6 +23,7 @@ import ctypes
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _DTYPES, _check_rc, _expect, _load, _stream_ptr
 
@@ -69,11 +70,16 @@ def _on(device: torch.device) -> int:
     return index
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tensors made here (on the current stream's pool) but used on the caller's stream stay whole until that work ends."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+def _new(shape, dtype, dev, stream):
+    """A new tensor for work on ``stream``, in that stream's memory: whatever used the memory before did so in that stream's
+    order. The caller may use it on the current stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(here)
+    return t
 
 
 def _exec(stream, index, workspace=None) -> bytes:
@@ -139,9 +145,7 @@ def _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens):
 
 def _out(out, v, stream):
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)   # dense whatever v's strides are
-        if stream is not None:
-            _used_on(stream, out)
+        out = _new(v.shape, v.dtype, v.device, stream)   # dense whatever v's strides are
     else:
         _need(out, "out", v.shape, v.dtype, v.device)
     return out
@@ -154,10 +158,7 @@ def gated_delta_workspace_bytes(P: int, T: int, Hk: int, Hv: int, K: int, V: int
 
 
 def _scratch(lib, shape, backward, dev, stream):
-    ws = torch.empty(max(lib.sdm_gated_delta_workspace_bytes(shape, backward), 256), dtype=torch.uint8, device=dev)
-    if stream is not None:
-        _used_on(stream, ws)
-    return ws
+    return _new((max(lib.sdm_gated_delta_workspace_bytes(shape, backward), 256),), torch.uint8, dev, stream)
 
 
 def gated_delta_fwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, log_decay: torch.Tensor,
@@ -226,20 +227,19 @@ def gated_delta_bwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
                     workspace: torch.Tensor | None = None, kept: torch.Tensor | None = None, stream=None) -> dict:
     """Backward of gated_delta_fwd from the ``state`` it STARTED from (None: zeros). ``grad_out`` [P, T, Hv, V] is the
     gradient of the readings, ``grad_state`` (float32, optional) that of the final state. Returns dict(state, k, v, beta,
-    log_decay, q): k, v and q in the inputs' dtype (sums over sharing heads in float32), the others float32. ``kept``: the workspace of a
-    gated_delta_fwd(keep=True) with the same inputs, in place of ``workspace``; without it the forward is computed again."""
+    log_decay, q): k, v and q in the inputs' dtype (sums over sharing heads in float32), the others float32. ``kept``: the
+    workspace of a gated_delta_fwd(keep=True) with the same inputs, in place of ``workspace``; without it the forward is
+    computed again."""
     lib = _load()
     full, shape, qr, kr, vr, dev, index = _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens)
     _need(grad_out, "grad_out", v.shape, v.dtype, dev)
     for t, n in ((state, "state"), (grad_state, "grad_state")):
         if t is not None:
             _need(t, n, full, torch.float32, dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    g = dict(state=torch.empty(full, **f32), k=torch.empty(k.shape, dtype=k.dtype, device=dev),
-             v=torch.empty(v.shape, dtype=v.dtype, device=dev), beta=torch.empty_like(beta),
-             log_decay=torch.empty_like(log_decay), q=torch.empty(q.shape, dtype=q.dtype, device=dev))
-    if stream is not None:
-        _used_on(stream, *g.values())
+    f32 = torch.float32
+    g = {n: _new(size, dtype, dev, stream) for n, size, dtype in (
+        ("state", full, f32), ("k", k.shape, k.dtype), ("v", v.shape, v.dtype), ("beta", beta.shape, f32),
+        ("log_decay", beta.shape, f32), ("q", q.shape, q.dtype))}
     if kept is not None:
         workspace = kept
     elif workspace is None:
@@ -271,6 +271,7 @@ class _GatedDeltaRule(torch.autograd.Function):
         return out, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out, grad_state):
         state, k, v, beta, log_decay, q, valid, kept = ctx.saved_tensors
         if grad_out is None and grad_state is None:
@@ -325,15 +326,14 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     lib = _load()
     rows, N, code, wdtype, index = _norm_inputs(x, weight, bias)
     if out is None:
-        out = torch.empty_like(x)
-        if stream is not None:
-            _used_on(stream, out)
+        out = torch.empty_like(x) if stream is None else _new(x.shape, x.dtype, x.device, stream)
     else:
         _need(out, "out", x.shape, x.dtype, x.device)
-    mean = x.new_empty((rows,), dtype=torch.float32)
-    rstd = torch.empty_like(mean)
-    if stream is not None:
-        _used_on(stream, mean, rstd)
+    if stream is None:
+        mean = x.new_empty((rows,), dtype=torch.float32)
+        rstd = torch.empty_like(mean)
+    else:
+        mean, rstd = _new((rows,), torch.float32, x.device, stream), _new((rows,), torch.float32, x.device, stream)
     rc = lib.sdm_layer_norm_fwd(rows, N, x.data_ptr(), code, _ptr(weight), _ptr(bias), code if wdtype is None else _DTYPES[wdtype],
                                 eps, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _exec(stream, index))
     if rc:
@@ -358,17 +358,13 @@ def layer_norm_bwd(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, 
     g = {}
     for n in need:
         if n == "x":
-            g[n] = torch.empty_like(x)
+            g[n] = torch.empty_like(x) if stream is None else _new(x.shape, x.dtype, dev, stream)
         elif n in ("weight", "bias"):
-            g[n] = torch.empty((N,), dtype=wdtype, device=dev)
+            g[n] = _new((N,), wdtype, dev, stream)
         else:
             raise ValueError(f"need names x, weight and bias, got {need}")
     if workspace is None and ("weight" in g or "bias" in g):
-        workspace = torch.empty(lib.sdm_layer_norm_bwd_workspace_bytes(rows, N, code), dtype=torch.uint8, device=dev)
-        if stream is not None:
-            _used_on(stream, workspace)
-    if stream is not None:
-        _used_on(stream, *g.values())
+        workspace = _new((lib.sdm_layer_norm_bwd_workspace_bytes(rows, N, code),), torch.uint8, dev, stream)
     rc = lib.sdm_layer_norm_bwd(rows, N, grad_out.data_ptr(), x.data_ptr(), code, _ptr(weight), _DTYPES[wdtype],
                                 mean.data_ptr(), rstd.data_ptr(), _ptr(g.get("x")), _ptr(g.get("weight")), _ptr(g.get("bias")),
                                 _exec(stream, index, workspace))
@@ -386,6 +382,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         x, weight, mean, rstd = ctx.saved_tensors
         need = tuple(n for n, on in zip(("x", "weight", "bias"), ctx.needs_input_grad) if on)

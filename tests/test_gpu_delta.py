@@ -435,6 +435,62 @@ def test_streams(gpu):
     assert torch.equal(base, g["state"])
 
 
+@pytest.mark.parametrize("call", ["fwd", "step", "bwd", "norm_fwd", "norm_bwd"])
+def test_memory_of_another_stream(gpu, call):
+    """A call on a stream of its own does not get, for its outputs or its workspace, memory that the current stream's work
+    still writes."""
+    import chunked_sparse_delta_amd as sdm
+    P, T, K, V = 2, 150, 64, 64
+    g = gpu_of(make(P, T, 1, 2, K, V, torch.float32), gpu)
+    x, w = torch.randn(300, 640, device=gpu), torch.randn(640, device=gpu)
+    _, mean, rstd = sdm.layer_norm_fwd(x, w)
+    side = torch.cuda.Stream()
+
+    def run(**kw):
+        args = [g[n] for n in NAMES]
+        if call == "norm_fwd":
+            return list(sdm.layer_norm_fwd(x, w, **kw))
+        if call == "norm_bwd":
+            return list(sdm.layer_norm_bwd(x, x, mean, rstd, w, **kw).values())
+        if call == "bwd":
+            return list(sdm.gated_delta_bwd(*args, g["v"], **kw).values())
+        end = torch.zeros_like(g["state"])
+        torch.cuda.synchronize()
+        return [(sdm.gated_delta_fwd if call == "fwd" else sdm.gated_delta_step)(*args, state_out=end, **kw), end]
+
+    want = run()
+    torch.cuda.synchronize()
+    sizes = [4096, 2 ** 15, 2 ** 17, 2 ** 18, 2 ** 19, 2 ** 20, 2 ** 22]
+    old = [torch.empty(n // 4, device=gpu) for n in sizes for _ in range(6)]
+    end = torch.zeros_like(g["state"])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    for t in old:
+        t.fill_(7.0)
+    del old, t
+    if call in ("fwd", "step"):
+        got = [(sdm.gated_delta_fwd if call == "fwd" else sdm.gated_delta_step)(*(g[n] for n in NAMES), state_out=end,
+                                                                                stream=side), end]
+    else:
+        got = run(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_no_second_gradient(gpu):
+    """Gradients of the gradients are refused, not silently left out."""
+    import chunked_sparse_delta_amd as sdm
+    g = gpu_of(make(1, 5, 1, 1, 8, 8, torch.float32), gpu)
+    for t in g.values():
+        t.requires_grad_()
+    out, _ = sdm.gated_delta_rule(*(g[n] for n in NAMES))
+    y = sdm.layer_norm(g["v"].detach().requires_grad_())
+    for z, t in ((out, g["k"]), (y, y.grad_fn.next_functions[0][0].variable)):
+        (first,) = torch.autograd.grad((z ** 2).sum(), t, create_graph=True)
+        with pytest.raises(RuntimeError):
+            first.sum().backward()
+
+
 def test_split_sequences(gpu):
     """A sequence cut anywhere, its state handed on, and single tokens after a prompt: the whole sequence's results."""
     import chunked_sparse_delta_amd as sdm
