@@ -41,11 +41,11 @@ template <int C> __device__ __forceinline__ void put_blocks(const float *m, floa
 
 // X, P and the gates of one chunk per workgroup. A wavefront takes 16 rows of both products, with all its operands on their way
 // before the first one; the inverse is substitution within blocks of 16 and products between them, in float32.
-// Measured: 61 us for the 4096 chunks of 16 heads of 16384 tokens (head_dim 128, bfloat16), 15 ns a chunk with four workgroups
-// to a compute unit; 170 MB in and out are 33 us at a copy's 5.1 TB/s. The rest is its chain of phases: the operands' way
-// from memory, 16 dependent steps of substitution, the two joins.
+// Measured: 56 us for the 4096 chunks of 16 heads of 16384 tokens (head_dim 128, bfloat16), four workgroups on a compute unit (61
+// with three, whose registers the compiler takes if it may); 170 MB in and out are 33 us at a copy's 5.1 TB/s. The rest is
+// its chain of phases: the operands' way from memory, 16 dependent steps of substitution, the two joins.
 template <typename T, int C, int KP>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, DeltaWs ws) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 1) void delta_prep_kernel(DeltaArgs a, DeltaWs ws) {
     constexpr int LC = PrepLds<C>::LC, NT = C / 16, NI = kPieces<T>;
     __shared__ PrepLds<C> s;
     const int64_t n = blockIdx.x;
