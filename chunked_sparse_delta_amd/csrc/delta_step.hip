@@ -9,19 +9,30 @@
 // through all tokens: CW / VW lanes side by side hold VW columns each of a row, and
 // RG = 64 VW / CW such groups of lanes a share of the rows each, so a load instruction fetches RG row pieces of CW columns
 // and the reduction over the rows is RG-way across lanes. Wavefronts share nothing.
-// Measured: 64 streams x 32 heads of 128 x 128: 56 us, 4.8 TB/s (a large copy: 5.1); one stream of 16 heads: 7.4 us, the way to
-// memory and back twice after a launch; 7 x 10 heads of 72 x 200, three tokens, float32: 11.6 us.
+// Measured: 64 streams x 32 heads of 128 x 128: 46 us, 5.8 TB/s (a large copy: 5.1); one stream of 16 heads: 5.7 us, a launch
+// and the way to memory and back; 7 x 10 heads of 72 x 200, float32: 6.2 us, three tokens 8.6. Every load of a row is one
+// instruction in the lanes that have it whole, and one branch in the others: with a branch per element the first figure was 56.
+#include <type_traits>
+
 #include "delta.h"
 
 namespace sdm {
 
 namespace {
 
-// Sum over the lanes whose index differs in the bits from `low` up.
+// Sum over the lanes whose index differs in the bits from LOW (4 or 8) up, the same bits in all of them: rotations within rows of
+// 16 lanes, then the halves of pairs of rows and of the wavefront, swapped. (With four shuffles through LDS a further token of 128 x
+// 128 took 1.1 us, this way 0.87.)
 template <int LOW> __device__ __forceinline__ float rows_sum(float x) {
-#pragma unroll
-    for (int m = LOW; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
-    return x;
+    auto rotated = [](float y, auto ctrl) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(y), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    x += rotated(x, std::integral_constant<int, 0x128>{});                            // by 8
+    if constexpr (LOW == 4) x += rotated(x, std::integral_constant<int, 0x124>{});    // by 4
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(h[0]) + __uint_as_float(h[1]);
 }
 
 // The lane's VW columns of a state row of which `cols` are left: one load or store at any element address where all are.
@@ -34,7 +45,12 @@ __device__ __forceinline__ void cols_load(const float *p, int cols, float (&o)[V
         for (int j = 0; j < VW; ++j) o[j] = x[j];
     } else {
 #pragma unroll
-        for (int j = 0; j < VW; ++j) o[j] = j < cols ? p[j] : 0.0f;
+        for (int j = 0; j < VW; ++j) o[j] = 0.0f;
+        if (cols > 0) {     // one branch for the lanes past the end
+#pragma unroll
+            for (int j = 0; j < VW; ++j)
+                if (j < cols) o[j] = p[j];
+        }
     }
 }
 __device__ __forceinline__ void cols_store(float *p, int cols, const float (&o)[VW]) {
@@ -70,10 +86,26 @@ template <typename T, int N> __device__ __forceinline__ void rows_load(const T *
         if (left >= i + S) row_load(p + i, x);
         else {
 #pragma unroll
-            for (int j = 0; j < S; ++j) x[j] = i + j < left ? to_f32(p[i + j]) : 0.0f;
+            for (int j = 0; j < S; ++j) x[j] = 0.0f;
+            if (left > i) {     // one branch for the lanes past the end
+#pragma unroll
+                for (int j = 0; j < S; ++j)
+                    if (i + j < left) x[j] = to_f32(p[i + j]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < S; ++j) o[i + j] = x[j];
+    }
+}
+
+__device__ __forceinline__ void out_store(float *p, int cols, const float (&o)[VW]) { cols_store(p, cols, o); }
+__device__ __forceinline__ void out_store(bf16 *p, int cols, const float (&o)[VW]) {
+    typedef uint32_t raw __attribute__((ext_vector_type(2), aligned(2)));
+    if (cols >= VW) *reinterpret_cast<raw *>(p) = raw{f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3])};
+    else {
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+            if (j < cols) p[j] = from_f32<bf16>(o[j]);
     }
 }
 
@@ -95,11 +127,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     const bool idle = slot < 0 || slot >= a.slots;
     const int n = idle ? 0 : delta_valid(a, p);
     auto put = [&](int t, const float (&o)[VW]) {
-        if (rg == 0) {
-#pragma unroll
-            for (int j = 0; j < VW; ++j)
-                if (j < cols) out[t * so + j] = from_f32<T>(o[j]);
-        }
+        if (rg == 0) out_store(out + t * so, cols, o);
     };
     const float zero[VW] = {};
     for (int t = n; t < a.T; ++t) put(t, zero);
@@ -120,13 +148,11 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     const T *vp = static_cast<const T *>(a.v.data) + p * a.v.sp + h * a.v.sh + c0;
     const float *bp = a.beta + int64_t(p) * a.T * a.Hv + h, *gp = a.g + int64_t(p) * a.T * a.Hv + h;
     for (int t = 0; t < n; ++t) {
-        float kk[RPL], qq[RPL], r[VW] = {}, s[VW] = {}, c = 0.0f, v[VW] = {};
+        float kk[RPL], qq[RPL], r[VW] = {}, s[VW] = {}, c = 0.0f, v[VW];
         rows_load(kp + t * a.k.st + row0, a.K - row0, kk);
         rows_load(qp + t * a.q.st + row0, a.K - row0, qq);
+        rows_load(vp + t * a.v.st, cols, v);
         const float beta = bp[int64_t(t) * a.Hv], decay = expf(gp[int64_t(t) * a.Hv]);
-#pragma unroll
-        for (int j = 0; j < VW; ++j)
-            if (j < cols) v[j] = to_f32(vp[t * a.v.st + j]);
 #pragma unroll
         for (int i = 0; i < RPL; ++i) {
             c = fmaf(qq[i], kk[i], c);
