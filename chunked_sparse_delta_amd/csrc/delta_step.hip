@@ -200,9 +200,9 @@ template <typename T, int CW> hipError_t step_rows(const DeltaArgs &a, hipStream
     return hipErrorInvalidValue;   // step_pick takes wide slices for K <= 64 only
 }
 template <typename T> hipError_t step_pick(const DeltaArgs &a, int cus, hipStream_t st) {
-    // Eight rows of four columns per lane keep enough loads on their way: 16 columns and K = 128 took 55 us where 32 took 60
-    // (64 streams x 32 heads x 128 x 128); with K = 64, 32 columns took 14.9 us where 16 took 18.0 (128 x 16 x 64 x 64). Few
-    // states take the narrow slices for the wavefronts they give.
+    // Eight rows of four columns per lane keep enough loads on their way: with K = 128, 16 columns took 55 us where 32 (sixteen
+    // rows) took 60 (64 streams x 32 heads x 128 x 128; 46 since); with K = 64, 32 columns take 15.7 us where 16 take 18.6 (128 x
+    // 16 x 64 x 64). Few states take the narrow slices for the wavefronts they give.
     if (a.K <= 64 && int64_t(a.P) * a.Hv * ((a.V + 31) / 32) >= 8 * cus) return step_rows<T, 32>(a, st);
     return step_rows<T, 16>(a, st);
 }
