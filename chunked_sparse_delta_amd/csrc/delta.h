@@ -46,8 +46,8 @@ struct DeltaWs {
     unsigned char *mats;   // [n] ChunkMem
     float *U, *Y;          // rows: the chunk's tokens (backward)
     float *S, *dS;         // rows: the padded head_dim; start states, gradients of the end states (backward)
-    // A sequence may be walked in `segs` segments of seg_chunks chunks at once (delta_segments): their start states [seg]
-    // [stream * Hv + head][KP][VP] and the maps from a segment's start state to its end state [seg][..][KP][KP].
+    // A sequence may be walked in `segs` segments of seg_chunks chunks at once (delta_segments): their start states (the first's
+    // too) [seg][stream * Hv + head][KP][VP] and the maps from a segment's start state to its end state [seg][..][KP][KP].
     float *seg_state, *seg_map;
     int32_t Nt, segs, seg_chunks;
     bool backward;         // X is computed for the backward (delta_beta_safe)

@@ -221,8 +221,10 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
     T *out = static_cast<T *>(a.out) + (int64_t(p) * a.T * a.Hv + h) * a.V;
     const int os = a.Hv * a.V;
     dt4 S[KB][2];
-    if (seg == 0) load_state<KB>(S, a.state, ph, a.K, a.V, col);
-    else if (READ) load_state<KB>(S, seg_state, ph, KP, VP, col);
+    // Walked in segments, the readings' launch writes the final state in one workgroup while others begin: it reads start states from
+    // the workspace alone, the first segment's too, since the caller's state may be advanced in place.
+    if (MODE == kRead && ws.segs > 1) load_state<KB>(S, seg_state, ph, KP, VP, col);
+    else if (seg == 0) load_state<KB>(S, a.state, ph, a.K, a.V, col);
     else {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
@@ -231,6 +233,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) S[kb][e][r] = map && kb * 32 + lg * 8 + e * 4 + r == col ? 1.0f : 0.0f;
     }
+    if (MODE == kMap && seg == 0) store_state<KB>(S, seg_state, ph, KP, VP, col);
     W::begin();
     dt4 y[TB][2] = {};
     const int left = a.V - oc;
