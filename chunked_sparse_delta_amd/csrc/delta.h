@@ -69,7 +69,8 @@ inline int delta_chunk(int K, bool is_bf16) { return is_bf16 && K <= 128 ? 64 : 
 
 hipError_t delta_prepare();
 hipError_t delta_bwd_prepare();
-hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16, hipStream_t st);
+// `results`: the readings and the final state are wanted (else, with ws.backward, only what the backward takes).
+hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16, bool results, hipStream_t st);
 // Whether the chunked kernels can take the rows as they are, and the copies where they cannot (at `to`).
 bool delta_regular_keys(const Rows &r, bool is_bf16);
 bool delta_regular_values(const Rows &r, bool is_bf16);

@@ -519,7 +519,7 @@ template <typename T> __global__ __launch_bounds__(256) void delta_copy_values_k
     }
 }
 
-template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const DeltaWs &ws, hipStream_t st) {
+template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const DeltaWs &ws, bool results, hipStream_t st) {
     const dim3 chunks(unsigned(int64_t(a.P) * a.Hv * ws.Nt));
     constexpr int N0 = kPPieces<T>(false), N1 = kPPieces<T>(true);
     if (ws.Nt > 0) {
@@ -529,7 +529,7 @@ template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const
     }
     const unsigned heads = unsigned(a.P) * unsigned(a.Hv), slices = unsigned(a.V + 63) / 64;
     if (ws.backward) {
-        if (a.out)
+        if (results)     // a call without tokens has no `out`, but a final state
             hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kBoth>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, N1, true>::kLds), st, a, ws);
         else
             hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kSave>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
@@ -545,11 +545,11 @@ template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const
     hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kRead>), dim3(heads * slices * unsigned(ws.segs)), dim3(kWalkThreads), (Walk<T, C, KP, N0, true>::kLds), st, a, ws);
     return hipGetLastError();
 }
-template <typename T> hipError_t fwd_pick(const DeltaArgs &a, const DeltaWs &ws, hipStream_t st) {
+template <typename T> hipError_t fwd_pick(const DeltaArgs &a, const DeltaWs &ws, bool results, hipStream_t st) {
     switch (delta_kp(a.K)) {
-        case 64: return fwd_go<T, kChunk<T>, 64>(a, ws, st);
-        case 128: return fwd_go<T, kChunk<T>, 128>(a, ws, st);
-        default: return fwd_go<T, 32, 256>(a, ws, st);
+        case 64: return fwd_go<T, kChunk<T>, 64>(a, ws, results, st);
+        case 128: return fwd_go<T, kChunk<T>, 128>(a, ws, results, st);
+        default: return fwd_go<T, 32, 256>(a, ws, results, st);
     }
 }
 
@@ -579,8 +579,8 @@ hipError_t delta_prepare() {
     return e == hipSuccess ? fwd_attrs<bf16>() : e;
 }
 
-hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16, hipStream_t st) {
-    return is_bf16 ? fwd_pick<bf16>(a, ws, st) : fwd_pick<float>(a, ws, st);
+hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16, bool results, hipStream_t st) {
+    return is_bf16 ? fwd_pick<bf16>(a, ws, results, st) : fwd_pick<float>(a, ws, results, st);
 }
 
 static bool rows_aligned(const Rows &r, int elements) {

@@ -165,7 +165,7 @@ static int delta_fwd(bool keep, const sdm_delta_shape *s, const sdm_rows *q, con
     if ((rc = take_workspace(s, keep, &a, nullptr, false, exec, &ws))) return rc;
     a.state_out = state_out;
     a.out = out;
-    const hipError_t e = launch_delta_fwd(a, ws, s->dtype == SDM_BF16, static_cast<hipStream_t>(exec->stream));
+    const hipError_t e = launch_delta_fwd(a, ws, s->dtype == SDM_BF16, true, static_cast<hipStream_t>(exec->stream));
     return e == hipSuccess ? SDM_OK : hip_fail(e, "gated delta launch");
 }
 

@@ -753,7 +753,7 @@ hipError_t delta_bwd_prepare() {
 
 hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, bool is_bf16, bool kept, hipStream_t st) {
     if (!kept) {
-        const hipError_t e = launch_delta_fwd(a, ws, is_bf16, st);
+        const hipError_t e = launch_delta_fwd(a, ws, is_bf16, false, st);
         if (e != hipSuccess) return e;
     }
     return is_bf16 ? bwd_pick<bf16>(a, ws, d, st) : bwd_pick<float>(a, ws, d, st);
