@@ -552,10 +552,20 @@ int sdm_layer_norm_fwd(int64_t rows, int32_t cols, const void *x, int32_t dtype,
     a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd;
     a.rows = rows; a.cols = cols; a.eps = eps;
     const NormPlan p = norm_plan(cols, dtype == SDM_BF16 ? 8 : 4, false);
-    const int64_t at_once = p.L < 256 ? 256 / p.L : 1;
-    const unsigned grid = unsigned((rows + at_once - 1) / at_once);
-    const hipError_t e = norm_launch<false>(a, dtype, weight_dtype, p, grid, static_cast<hipStream_t>(exec->stream));
-    return e == hipSuccess ? SDM_OK : hip_fail(e, "layer norm launch");
+    // A launch holds less than 2^32 threads, L to a row: more rows go in several.
+    const int64_t at_once = p.L < 256 ? 256 / p.L : 1, most = int64_t(1) << 31;
+    const size_t row_bytes = size_t(cols) * (dtype == SDM_BF16 ? 2 : 4);
+    for (int64_t left = rows; left > 0; left -= a.rows) {
+        a.rows = left < most / p.L ? left : most / p.L;
+        const unsigned grid = unsigned((a.rows + at_once - 1) / at_once);
+        const hipError_t e = norm_launch<false>(a, dtype, weight_dtype, p, grid, static_cast<hipStream_t>(exec->stream));
+        if (e != hipSuccess) return hip_fail(e, "layer norm launch");
+        a.x = static_cast<const char *>(a.x) + size_t(a.rows) * row_bytes;
+        a.y = static_cast<char *>(a.y) + size_t(a.rows) * row_bytes;
+        a.mean += a.rows;
+        a.rstd += a.rows;
+    }
+    return SDM_OK;
 }
 
 size_t sdm_layer_norm_bwd_workspace_bytes(int64_t rows, int32_t cols, int32_t dtype) {
