@@ -6,8 +6,8 @@ using namespace sdm;
 
 namespace {
 
-// Everything but the pointers.
-int check_delta(const sdm_delta_shape *s) {
+// Everything but the pointers; `chunks`: for the kernels that take sequences chunk by chunk.
+int check_delta(const sdm_delta_shape *s, bool chunks) {
     if (!s) return fail(SDM_ERR_NULL, "shape must not be NULL");
     if (s->dtype != SDM_F32 && s->dtype != SDM_BF16) return fail(SDM_ERR_DTYPE, "dtype must be SDM_F32 or SDM_BF16, got %d", s->dtype);
     if (s->streams < 1 || s->tokens < 0 || s->key_heads < 1 || s->value_heads < 1 || s->head_dim < 1 || s->value_dim < 1)
@@ -25,6 +25,13 @@ int check_delta(const sdm_delta_shape *s) {
     if (s->tokens > (1 << 30) || heads * (int64_t(s->tokens) / 16 + 1) >= int64_t(0x7fffffff) ||
         heads * ((s->value_dim + 15) / 16) >= int64_t(0x7fffffff))
         return fail(SDM_ERR_RANGE, "%d tokens of %lld heads are too many", s->tokens, (long long)heads);
+    if (!chunks) return SDM_OK;
+    // 32-bit offsets in a chunk, from its first token to the end of its last one's row, of copies with padded widths too
+    const int C = delta_chunk(s->head_dim, s->dtype == SDM_BF16), last = (s->tokens < C ? s->tokens : C) - 1;
+    const int64_t keys = int64_t(s->key_heads) * delta_kp(s->head_dim), values = int64_t(s->value_heads) * ((s->value_dim + 7) / 8 * 8);
+    if (last > 0 && last * (keys > values ? keys : values) > (int64_t(1) << 31) - 65536)
+        return fail(SDM_ERR_RANGE, "%d tokens of %lld (keys) or %lld (values) padded elements pass 32-bit offsets", last + 1,
+                    (long long)keys, (long long)values);
     return SDM_OK;
 }
 
@@ -33,9 +40,9 @@ bool overlap(const void *a, const void *b, size_t n) {
     return x < y + n && y < x + n;
 }
 
-int check_delta_inputs(const sdm_delta_shape *s, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
+int check_delta_inputs(const sdm_delta_shape *s, bool chunks, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v, const float *beta,
                        const float *log_decay, const float *state, const int32_t *valid, const sdm_exec *exec, DeltaArgs *a) {
-    const int rc = check_delta(s);
+    const int rc = check_delta(s, chunks);
     if (rc) return rc;
     if (!q || !k || !v || !exec) return fail(SDM_ERR_NULL, "q, k, v and exec must not be NULL");
     const size_t es = s->dtype == SDM_BF16 ? 2 : 4;
@@ -144,7 +151,7 @@ int take_workspace(const sdm_delta_shape *s, bool backward, DeltaArgs *a, Rows *
 extern "C" {
 
 size_t sdm_gated_delta_workspace_bytes(const sdm_delta_shape *s, int32_t backward) {
-    if (check_delta(s) != SDM_OK) return 0;
+    if (check_delta(s, true) != SDM_OK) return 0;
     return layout(s, backward != 0, nullptr).bytes;
 }
 
@@ -153,7 +160,7 @@ static int delta_fwd(bool keep, const sdm_delta_shape *s, const sdm_rows *q, con
                         const sdm_exec *exec) {
     g_err[0] = 0;
     DeltaArgs a{};
-    int rc = check_delta_inputs(s, q, k, v, beta, log_decay, state, valid, exec, &a);
+    int rc = check_delta_inputs(s, true, q, k, v, beta, log_decay, state, valid, exec, &a);
     if (rc) return rc;
     if (s->tokens > 0 && !out) return fail(SDM_ERR_NULL, "out must not be NULL");
     if (!aligned(out, s->dtype == SDM_BF16 ? 2 : 4)) return fail(SDM_ERR_ALIGN, "out must be aligned to its element size");
@@ -186,7 +193,7 @@ int sdm_gated_delta_step(const sdm_delta_shape *s, const sdm_rows *q, const sdm_
                          int64_t slots, const int32_t *valid, void *out, const sdm_exec *exec) {
     g_err[0] = 0;
     DeltaArgs a{};
-    int rc = check_delta_inputs(s, q, k, v, beta, log_decay, state, valid, exec, &a);
+    int rc = check_delta_inputs(s, false, q, k, v, beta, log_decay, state, valid, exec, &a);
     if (rc) return rc;
     if (slots < (state_ids ? 0 : s->streams))
         return fail(SDM_ERR_SHAPE, "%lld states for %d streams", (long long)slots, s->streams);
@@ -212,7 +219,7 @@ static int delta_bwd(bool kept, const sdm_delta_shape *s, const sdm_rows *q, con
                         const float *grad_state_out, const sdm_delta_grads *grads, const sdm_exec *exec) {
     g_err[0] = 0;
     DeltaArgs a{};
-    int rc = check_delta_inputs(s, q, k, v, beta, log_decay, state, valid, exec, &a);
+    int rc = check_delta_inputs(s, true, q, k, v, beta, log_decay, state, valid, exec, &a);
     if (rc) return rc;
     if (!grads) return fail(SDM_ERR_NULL, "grads must not be NULL");
     if (s->tokens > 0 && (!grad_out || !grads->q || !grads->k || !grads->v || !grads->beta || !grads->log_decay))

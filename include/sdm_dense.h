@@ -29,6 +29,9 @@ typedef struct {
     int32_t dtype;        /* sdm_dtype of q, k, v, out and their gradients */
     float scale;
 } sdm_delta_shape;
+/* Sequences (all but sdm_gated_delta_step) go by chunks of C = 64 tokens (bfloat16 with K <= 128)
+ * or 32, with K padded to 64, 128 or 256 and V to a multiple of 8: (min(C, T) - 1) * Hk * K and
+ * (min(C, T) - 1) * Hv * V, padded, are at most 2^31 - 2^16. SDM_ERR_RANGE past these limits. */
 
 /* A device [P, T, heads, width] array whose rows of `width` elements are dense; strides in
  * elements, >= 0, the token's below 2^24 (slices of one fused projection need no copy). Rows

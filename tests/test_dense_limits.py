@@ -1,0 +1,37 @@
+"""Shapes that the dense operators' kernels could not address or launch are refused on the host (no GPU needed)."""
+
+import pytest
+
+from tests.test_dense_abi import NULL, RANGE, Delta, lib  # noqa: F401
+
+
+def code_of(lib, form, **shape):
+    """The call's code; q is NULL, so that nothing runs: a shape that is accepted gives NULL."""
+    c = Delta(lib)
+    c.shape |= shape
+    c.ptr["q"] = None
+    return c.run(form)[0]
+
+
+def size(lib, backward, **shape):
+    c = Delta(lib)
+    return lib.sdm_gated_delta_workspace_bytes(c.dense._SHAPE(*(c.shape | shape).values()), backward)
+
+
+# Rows that the kernels cannot load as they are come as copies with padded widths: the offsets in a chunk of those have
+# to fit 32 bits.
+KEYS = dict(streams=1, tokens=64, key_heads=540000, value_heads=540000, head_dim=31, value_dim=1, dtype=1)     # 63 x 540000 x 64
+VALUES = dict(streams=1, tokens=64, key_heads=1, value_heads=5000000, head_dim=1, value_dim=1, dtype=1)        # 63 x 5000000 x 8
+
+
+@pytest.mark.parametrize("shape", [KEYS, VALUES])
+def test_offsets_of_padded_rows(lib, shape):
+    for form in ("fwd", "bwd"):
+        assert code_of(lib, form, **shape) == RANGE
+        assert code_of(lib, form, **shape | dict(tokens=63)) == (RANGE if shape is VALUES else NULL)
+        assert code_of(lib, form, **shape | dict(tokens=1)) == NULL
+    assert code_of(lib, "step", **shape) == NULL
+    for backward in (0, 1):
+        assert size(lib, backward, **shape) == 0 and size(lib, backward, **shape | dict(tokens=1)) > 0
+    # float32: chunks of 32 tokens
+    assert code_of(lib, "fwd", **KEYS | dict(dtype=0)) == NULL
