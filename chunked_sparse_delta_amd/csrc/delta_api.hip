@@ -25,13 +25,22 @@ int check_delta(const sdm_delta_shape *s, bool chunks) {
     if (s->tokens > (1 << 30) || heads * (int64_t(s->tokens) / 16 + 1) >= int64_t(0x7fffffff) ||
         heads * ((s->value_dim + 15) / 16) >= int64_t(0x7fffffff))
         return fail(SDM_ERR_RANGE, "%d tokens of %lld heads are too many", s->tokens, (long long)heads);
-    if (!chunks) return SDM_OK;
+    // A launch of 2^32 threads or more would run a part of its workgroups, without an error.
+    const int64_t threads = int64_t(1) << 32;
+    if (!chunks) {
+        if (heads * ((s->value_dim + 15) / 16) * 64 >= threads)
+            return fail(SDM_ERR_RANGE, "%lld heads of value_dim %d are too many for a launch", (long long)heads, s->value_dim);
+        return SDM_OK;
+    }
     // 32-bit offsets in a chunk, from its first token to the end of its last one's row, of copies with padded widths too
     const int C = delta_chunk(s->head_dim, s->dtype == SDM_BF16), last = (s->tokens < C ? s->tokens : C) - 1;
     const int64_t keys = int64_t(s->key_heads) * delta_kp(s->head_dim), values = int64_t(s->value_heads) * ((s->value_dim + 7) / 8 * 8);
     if (last > 0 && last * (keys > values ? keys : values) > (int64_t(1) << 31) - 65536)
         return fail(SDM_ERR_RANGE, "%d tokens of %lld (keys) or %lld (values) padded elements pass 32-bit offsets", last + 1,
                     (long long)keys, (long long)values);
+    if (heads * ((s->value_dim + 63) / 64) * 512 >= threads || heads * ((int64_t(s->tokens) + C - 1) / C) * 256 >= threads)
+        return fail(SDM_ERR_RANGE, "%lld heads of value_dim %d and %d tokens are too many for a launch", (long long)heads, s->value_dim,
+                    s->tokens);
     return SDM_OK;
 }
 

@@ -31,7 +31,9 @@ typedef struct {
 } sdm_delta_shape;
 /* Sequences (all but sdm_gated_delta_step) go by chunks of C = 64 tokens (bfloat16 with K <= 128)
  * or 32, with K padded to 64, 128 or 256 and V to a multiple of 8: (min(C, T) - 1) * Hk * K and
- * (min(C, T) - 1) * Hv * V, padded, are at most 2^31 - 2^16. SDM_ERR_RANGE past these limits. */
+ * (min(C, T) - 1) * Hv * V, padded, are at most 2^31 - 2^16; P * Hv * ceil(V / 64) is below 2^23
+ * and P * Hv * ceil(T / C) below 2^24. In sdm_gated_delta_step P * Hv * ceil(V / 16) is below 2^26.
+ * SDM_ERR_RANGE past these limits. */
 
 /* A device [P, T, heads, width] array whose rows of `width` elements are dense; strides in
  * elements, >= 0, the token's below 2^24 (slices of one fused projection need no copy). Rows

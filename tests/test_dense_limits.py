@@ -35,3 +35,19 @@ def test_offsets_of_padded_rows(lib, shape):
         assert size(lib, backward, **shape) == 0 and size(lib, backward, **shape | dict(tokens=1)) > 0
     # float32: chunks of 32 tokens
     assert code_of(lib, "fwd", **KEYS | dict(dtype=0)) == NULL
+
+
+# A launch holds less than 2^32 threads: 512 for 64 columns of a state, 256 for a chunk of a head, 64 for 16 columns of a state
+# in a call on single tokens.
+def test_launches(lib):
+    one = dict(streams=1 << 20, tokens=1, key_heads=1, value_heads=8, head_dim=1, value_dim=64, dtype=0)
+    for form in ("fwd", "bwd"):
+        assert code_of(lib, form, **one) == RANGE
+        assert code_of(lib, form, **one | dict(streams=(1 << 20) - 1)) == NULL
+        assert code_of(lib, form, **one | dict(streams=1 << 19, value_dim=65)) == RANGE
+        assert code_of(lib, form, **one | dict(streams=1 << 19, tokens=129)) == RANGE      # chunks of 32 tokens
+        assert code_of(lib, form, **one | dict(streams=1 << 19, tokens=96)) == NULL
+    assert size(lib, 0, **one) == size(lib, 1, **one) == 0
+    assert code_of(lib, "step", **one) == NULL
+    assert code_of(lib, "step", **one | dict(value_dim=129)) == RANGE
+    assert code_of(lib, "step", **one | dict(value_dim=112)) == NULL
