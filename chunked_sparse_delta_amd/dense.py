@@ -89,8 +89,8 @@ def _exec(stream, index, workspace=None) -> bytes:
         s = stream.cuda_stream
     if workspace is None:
         return _EXEC(s, 0, 0, 0, 0, 0, 0)
-    if workspace.device.type != "cuda" or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
+    if workspace.device.type != "cuda" or workspace.device.index != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
     return _EXEC(s, workspace.data_ptr(), workspace.numel() * workspace.element_size(), 0, 0, 0, 0)
 
 

@@ -51,3 +51,32 @@ def test_launches(lib):
     assert code_of(lib, "step", **one) == NULL
     assert code_of(lib, "step", **one | dict(value_dim=129)) == RANGE
     assert code_of(lib, "step", **one | dict(value_dim=112)) == NULL
+
+
+def test_workspace_of_another_device():
+    """A workspace on another GPU than the call's is refused: the kernels would reach for memory that is not theirs."""
+    import torch
+    from chunked_sparse_delta_amd import dense
+
+    class On:      # as much of a tensor, and of a stream, as the check reads
+        cuda_stream = 0
+
+        def __init__(self, device):
+            self.device = torch.device(device)
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 256
+
+        def numel(self):
+            return 512
+
+        def element_size(self):
+            return 1
+
+    assert len(dense._exec(On("cuda:1"), 1, On("cuda:1"))) == len(dense._exec(On("cuda:1"), 1))
+    for device in ("cuda:1", "cpu"):
+        with pytest.raises(ValueError):
+            dense._exec(On("cuda:0"), 0, On(device))
