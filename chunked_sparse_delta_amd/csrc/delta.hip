@@ -182,23 +182,23 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 1) void delta_prep_kernel
 // accumulators through the whole sequence, and the four wavefronts of a workgroup share the
 // chunk's k, q, X and P in LDS. One wavefront per SIMD has nothing beside it to hide its waits: the
 // operands of each group of products are read from LDS before the group ahead of it.
-// Precision: S and U are three bfloat16 pieces each where they reach the state (products to 2^-23), two where they reach
-// readings that are rounded to bfloat16.
-// Bound by that one wavefront's chain: a chunk of 64 tokens of 128 x 128 (bfloat16) takes 3.4 us with half of the compute units
-// at work, 4.0 with all (the clock falls from 2.38 to 2.17 GHz): 8400 cycles, of them 2912 in 182 matrix instructions and, by
-// count, about 1600 in splits and gates, the rest the way from one group of products through LDS or a split to the next.
-// kRead gives the readings (4 x 16 heads of up to 4096 tokens: 212 us). kSave keeps U and each chunk's start state for the
-// backward instead, kBoth does both (4 x 16 heads of 2048 tokens: 145 us). kMap, for sequences walked in segments at once: the
+// Precision: S, U, X and P are three bfloat16 pieces each wherever they go, so that products keep float32's bits (2^-23); the readings
+// are rounded once. (Two pieces of S, U and P where they reach bfloat16 readings took 222 us where this takes 249 for 4 x 16 heads of
+// 4096 tokens of 128 x 128, but terms of a reading that cancel then had 16 bits.)
+// Bound by that one wavefront's chain: a chunk of 64 tokens of 128 x 128 (bfloat16) takes 3.9 us with half of the compute units
+// at work, 5.0 with all: of the 8700 cycles of the first, 3456 in 216 matrix instructions (by counters), the rest splits,
+// gates and the way from one group of products through LDS or a split to the next.
+// kRead gives the readings (4 x 16 heads of up to 4096 tokens: 235 us). kSave keeps U and each chunk's start state for the
+// backward instead, kBoth does both (4 x 16 heads of 2048 tokens: 160 us). kMap, for sequences walked in segments at once: the
 // segment's end state from a start state of zeros (the first's: from the caller's) and, in workgroups of their own, what it
 // makes of the columns of the identity, with v = 0: the two give a segment's end state from any start state
-// (delta_join_kernel); 2.5 us a chunk.
+// (delta_join_kernel); 2.6 us a chunk.
 enum { kRead, kSave, kBoth, kMap };
 template <typename T, int C, int KP, int MODE>
 __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, DeltaWs ws) {
     constexpr bool SAVE = MODE == kSave || MODE == kBoth, READ = MODE == kRead || MODE == kBoth;
-    constexpr int NI = kPieces<T>, NP = kPPieces<T>(SAVE), KB = KP / 32, TB = C / 32, NTR = kTri<C>;
-    constexpr int NS = NI == 1 ? 2 : 3;    // pieces of S and U that reach the readings only
-    using W = Walk<T, C, KP, NP, READ>;
+    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NTR = kTri<C>;
+    using W = Walk<T, C, KP, READ>;
     extern __shared__ __align__(16) unsigned char raw[];
     typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int vslices = (a.V + 63) / 64, VG = (a.V + 15) / 16, VP = VG * 16, heads = a.P * a.Hv;
@@ -263,6 +263,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
     for (int c = c0; c < c1; ++c) {
         const typename W::Lds &s = bufs[(c - c0) & (W::kBufs - 1)];
         const Gates<C> &g = s.m.g;
+        const int ln = NI == 1 ? fresh_lane() : lane;     // float32 inputs spill more with addresses of each chunk's own
         if (READ && c > c0) put(c - 1);
         // k S and q S
         Frag<NI> A[2][TB][2];
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) f[tb][e] = read_rows<NI>(m + tb * KB * kBlk, W::kStride, e);
+                for (int e = 0; e < 2; ++e) f[tb][e] = read_rows<NI>(m + tb * KB * kBlk, W::kStride, e, ln);
         };
         rows_of(A[0], s.k[0][0][0]);
         dt4 v[TB][2], b[TB][2], eG[TB][2];
@@ -295,7 +296,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
         Frag<3> fx[2][2], fr[TB];    // X's blocks, a step ahead
         auto x_of = [&](Frag<3>(&f)[2], int i) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) f[e] = read_rows<3>(s.m.X[0][i], NTR * kBlk, e);
+            for (int e = 0; e < 2; ++e) f[e] = read_rows<3>(s.m.X[0][i], NTR * kBlk, e, ln);
         };
 #pragma unroll
         for (int i = 0; i < KQ; ++i) {
@@ -311,7 +312,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
                         for (int e = 0; e < 2; ++e) x[tb][e] = mma1(A[i & 1][tb][e].p[m], fs[i % KB].p[l], x[tb][e]);
                 });
             } else {
-                each_product<NS, NI, NS>([&](int m, int l) {
+                each_product<3, NI, 3>([&](int m, int l) {
 #pragma unroll
                     for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
@@ -334,17 +335,17 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
         }
         // U = X r, then P U; block i of the lower triangle is row block i > 0, column block i == 2
         dt4 U[TB][2] = {};
-        Frag<NP> fp[2][2];
-        auto p_of = [&](Frag<NP>(&f)[2], int i) {
+        Frag<3> fp[2][2];
+        auto p_of = [&](Frag<3>(&f)[2], int i) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) f[e] = read_rows<NP>(s.m.P[0][i], NTR * kBlk, e);
+            for (int e = 0; e < 2; ++e) f[e] = read_rows<3>(s.m.P[0][i], NTR * kBlk, e, ln);
         };
         Frag<NI> fk[2][KB];          // blocks of k^T, half of a row block of them at a time (the halves of all row blocks in turn)
         auto kt_of = [&](Frag<NI>(&f)[KB], int i) {
 #pragma unroll
             for (int m = 0; m < KB; ++m) {
                 const int kb = i / TB * (KB / 2) + m / 2;
-                f[m] = read_cols<NI>(s.k[0][i % TB][kb], W::kStride, m & 1);
+                f[m] = read_cols<NI>(s.k[0][i % TB][kb], W::kStride, m & 1, ln);
             }
         };
 #pragma unroll
@@ -368,10 +369,10 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
         const float last = g.last;
         if constexpr (SAVE) save_blocks<TB>(ws.U, nc, VG, cg, U);
         if constexpr (READ) {
-            Frag<NS> fv[TB];
+            Frag<3> fv[TB];
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
-                fv[tb] = split<NS>(U[tb][0], U[tb][1]);
+                fv[tb] = split<3>(U[tb][0], U[tb][1]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) y[tb][e] *= a.scale * et[tb][e];
             }
@@ -380,7 +381,7 @@ __global__ __launch_bounds__(kWalkThreads) void delta_state_kernel(DeltaArgs a, 
                 if (i + 1 < NTR) p_of(fp[(i + 1) & 1], i + 1);
                 else kt_of(fk[0], 0);
                 lds_point();
-                each_product<NS, NP, NS>([&](int m, int l) {
+                each_product<3, 3, 3>([&](int m, int l) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) y[i > 0][e] = mma1(fv[i == 2].p[l], fp[i & 1][e].p[m], y[i > 0][e]);
                 });
@@ -521,7 +522,6 @@ template <typename T> __global__ __launch_bounds__(256) void delta_copy_values_k
 
 template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const DeltaWs &ws, bool results, hipStream_t st) {
     const dim3 chunks(unsigned(int64_t(a.P) * a.Hv * ws.Nt));
-    constexpr int N0 = kPPieces<T>(false), N1 = kPPieces<T>(true);
     if (ws.Nt > 0) {
         hipLaunchKernelGGL((delta_prep_kernel<T, C, KP>), chunks, dim3(256), 0, st, a, ws);
         const hipError_t e = hipGetLastError();
@@ -530,19 +530,19 @@ template <typename T, int C, int KP> hipError_t fwd_go(const DeltaArgs &a, const
     const unsigned heads = unsigned(a.P) * unsigned(a.Hv), slices = unsigned(a.V + 63) / 64;
     if (ws.backward) {
         if (results)     // a call without tokens has no `out`, but a final state
-            hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kBoth>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, N1, true>::kLds), st, a, ws);
+            hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kBoth>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, true>::kLds), st, a, ws);
         else
-            hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kSave>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, N1, false>::kLds), st, a, ws);
+            hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kSave>), dim3(heads * slices), dim3(kWalkThreads), (Walk<T, C, KP, false>::kLds), st, a, ws);
         return hipGetLastError();
     }
     if (ws.segs > 1) {
         hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kMap>), dim3(heads * (slices + KP / 64) * unsigned(ws.segs - 1)), dim3(kWalkThreads),
-                           (Walk<T, C, KP, N0, false>::kLds), st, a, ws);
+                           (Walk<T, C, KP, false>::kLds), st, a, ws);
         hipLaunchKernelGGL(delta_join_kernel<KP>, dim3(heads * (unsigned(a.V + 15) / 16)), dim3(256), 0, st, ws, int(heads), (a.V + 15) / 16 * 16);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kRead>), dim3(heads * slices * unsigned(ws.segs)), dim3(kWalkThreads), (Walk<T, C, KP, N0, true>::kLds), st, a, ws);
+    hipLaunchKernelGGL((delta_state_kernel<T, C, KP, kRead>), dim3(heads * slices * unsigned(ws.segs)), dim3(kWalkThreads), (Walk<T, C, KP, true>::kLds), st, a, ws);
     return hipGetLastError();
 }
 template <typename T> hipError_t fwd_pick(const DeltaArgs &a, const DeltaWs &ws, bool results, hipStream_t st) {
@@ -554,16 +554,15 @@ template <typename T> hipError_t fwd_pick(const DeltaArgs &a, const DeltaWs &ws,
 }
 
 template <typename T, int C, int KP> hipError_t fwd_attr() {
-    constexpr int N0 = kPPieces<T>(false), N1 = kPPieces<T>(true);
-    constexpr size_t l0 = Walk<T, C, KP, N0, true>::kLds, l1 = Walk<T, C, KP, N1, false>::kLds, l2 = Walk<T, C, KP, N1, true>::kLds;
-    static_assert(l0 <= kDeltaMaxLds && l1 <= kDeltaMaxLds && l2 <= kDeltaMaxLds, "LDS of a workgroup");
+    constexpr size_t l0 = Walk<T, C, KP, true>::kLds, l1 = Walk<T, C, KP, false>::kLds;
+    static_assert(l0 <= kDeltaMaxLds && l1 <= kDeltaMaxLds, "LDS of a workgroup");
     auto set = [](auto kernel, size_t bytes) {
         return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     };
     hipError_t e = set(&delta_state_kernel<T, C, KP, kRead>, l0);
     if (e == hipSuccess) e = set(&delta_state_kernel<T, C, KP, kSave>, l1);
-    if (e == hipSuccess) e = set(&delta_state_kernel<T, C, KP, kBoth>, l2);
-    return e == hipSuccess ? set(&delta_state_kernel<T, C, KP, kMap>, Walk<T, C, KP, N0, false>::kLds) : e;
+    if (e == hipSuccess) e = set(&delta_state_kernel<T, C, KP, kBoth>, l0);
+    return e == hipSuccess ? set(&delta_state_kernel<T, C, KP, kMap>, l1) : e;
 }
 template <typename T> hipError_t fwd_attrs() {
     hipError_t e = fwd_attr<T, kChunk<T>, 64>();
@@ -618,7 +617,7 @@ hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool
 // A workgroup walks a sequence's chunks one after the other, at a pace that hardly depends on the others: few states leave
 // most of the device idle (16 heads of 16384 tokens of 128 x 128, two workgroups each: the whole call fell from 0.79 to 0.43 ms
 // with five segments at once). Walking segments at once costs the readings' walk again, once for the columns of the state and once
-// for those of the map, a third cheaper (no readings), and a join of about a chunk's time per segment (4 us of 3.4).
+// for those of the map, a third cheaper (no readings), and a join of about a chunk's time per segment.
 int delta_segments(int64_t heads, int slices, int K, int Nt) {
     const int64_t wgs = heads * slices, maps = heads * (slices + delta_kp(K) / 64);
     int best = 1;

@@ -27,12 +27,13 @@ namespace sdm {
 namespace {
 
 // dS from the last chunk to the first, as delta_state_kernel walks S. Bound like it by the one computing wavefront of a SIMD: 198
-// matrix instructions (1.3 us) of a chunk's 5.3 (64 tokens of 128 x 128, bfloat16; 4 x 16 heads of 2048 tokens: 168 us); beside
-// the walk's chain it writes dS1, Y and dv, 56 KB a chunk.
+// matrix instructions (1.3 us) of a chunk's 5.3 (64 tokens of 128 x 128, bfloat16; 4 x 16 heads of 2048 tokens: 173 us); beside
+// the walk's chain it writes dS1, Y and dv, 56 KB a chunk. Its 256 registers do not hold it all: 15 vector registers of that variant
+// are spilled, 71 of float32's with head_dim above 128 (2 x 8 heads of 1024 tokens of 200 x 200: 299 us).
 template <typename T, int C, int KP>
 __global__ __launch_bounds__(kWalkThreads) void delta_back_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
     constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NTR = kTri<C>;
-    using W = Walk<T, C, KP, 3, true>;
+    using W = Walk<T, C, KP, true>;
     extern __shared__ __align__(16) unsigned char raw[];
     typename W::Lds *bufs = reinterpret_cast<typename W::Lds *>(raw);
     const int slices = (a.V + 63) / 64, VG = (a.V + 15) / 16;
@@ -213,14 +214,14 @@ __global__ __launch_bounds__(kWalkThreads) void delta_back_kernel(DeltaArgs a, D
 constexpr int kGradThreads = 768;
 
 template <typename T, int C, int KP> struct GradLds {
-    static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NM = NI == 1 ? 2 : 3, KG = 8 / (C / 16);
+    static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, KG = 8 / (C / 16);
     union Stage {
         struct {
             unsigned char go[NI][TB][kBlk], U[3][TB][kBlk], Y[3][TB][kBlk], S[3][KB][kBlk], dS[3][KB][kBlk];
         };
         struct {
             unsigned char k[NI][TB][KB][kBlk], q[NI][TB][KB][kBlk];
-            unsigned char Mq[NM][kTri<C>][kBlk], Ma[NM][kTri<C>][kBlk];   // scale D dP and D dA, rows: token i
+            unsigned char Mq[3][kTri<C>][kBlk], Ma[3][kTri<C>][kBlk];   // scale D dP and D dA, rows: token i
         };
     };
     struct Small {
@@ -466,13 +467,13 @@ __device__ __forceinline__ double lanes16(double x) {
 }
 
 // The value heads' shares of dq and dk meet in accumulators: no atomics, one rounding. One workgroup per compute unit walks its
-// share of the chunks. Bound by the memory it reads, S0, dS1, U and Y in float32: 470 MB of 4 x 16 heads of 2048 tokens of 128 x 128
-// in 205 us, 2.3 TB/s on the whole: near the copy's rate while a chunk's states come in, well under it through the
-// products with q and k between them.
+// share of the chunks. Bound by the memory it reads, S0, dS1, U and Y in float32: 0.51 GB in and 0.06 out (by counters) for 4 x 16
+// heads of 2048 tokens of 128 x 128 in 215 us, 2.7 TB/s on the whole: near the copy's rate while a chunk's states come in, well under
+// it through the products with q and k between them.
 template <typename T, int C, int KP>
 __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, DeltaWs ws, DeltaGrads d) {
     using Lds = GradLds<T, C, KP>;
-    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NT = C / 16, NM = Lds::NM;
+    constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32, NT = C / 16;
     constexpr int KG = Lds::KG, KW = KB * 2 / KG;   // wavefronts on the same tokens, their share of head_dim in 16-row tiles
     constexpr int kStride = TB * KB * kBlk;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -576,9 +577,9 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
                 for (int r = 0; r < 8; ++r) sm.col[bi * 2 + pe][bj * 32 + lg * 8 + r] = cols[r];
             }
             // a lane holds eight neighbours j of row i
-            const Frag<NM> fq = split<NM>(wq[0], wq[1]), fa = split<NM>(wa[0], wa[1]);
+            const Frag<3> fq = split<3>(wq[0], wq[1]), fa = split<3>(wa[0], wa[1]);
 #pragma unroll
-            for (int n = 0; n < NM; ++n) {
+            for (int n = 0; n < 3; ++n) {
                 *reinterpret_cast<db8 *>(s.Mq[n][pb] + block_at(block_row(lc, pe), lg)) = fq.p[n];
                 *reinterpret_cast<db8 *>(s.Ma[n][pb] + block_at(block_row(lc, pe), lg)) = fa.p[n];
             }
@@ -626,22 +627,22 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
 #pragma unroll
         for (int x = 0; x < TB; ++x) {
             if (x <= tb) {
-                const Frag<NM> mq = read_rows<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta, lp), ma = read_rows<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta, lp);
+                const Frag<3> mq = read_rows<3>(s.Mq[0][tb + x], kTri<C> * kBlk, ta, lp), ma = read_rows<3>(s.Ma[0][tb + x], kTri<C> * kBlk, ta, lp);
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     const int t = kt0 + j;
                     const Frag<NI> k = read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1, lp);
-                    aq[j] = mma<NM>(k, mq, aq[j]);
-                    ak[j] = mma<NM>(k, ma, ak[j]);
+                    aq[j] = mma<3>(k, mq, aq[j]);
+                    ak[j] = mma<3>(k, ma, ak[j]);
                 }
             }
             if (x >= tb) {
-                const Frag<NM> mq = read_cols<NM>(s.Mq[0][tb + x], kTri<C> * kBlk, ta, lp), ma = read_cols<NM>(s.Ma[0][tb + x], kTri<C> * kBlk, ta, lp);
+                const Frag<3> mq = read_cols<3>(s.Mq[0][tb + x], kTri<C> * kBlk, ta, lp), ma = read_cols<3>(s.Ma[0][tb + x], kTri<C> * kBlk, ta, lp);
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     const int t = kt0 + j;
-                    ak[j] = mma<NM>(read_cols<NI>(s.q[0][x][t / 2], kStride, t & 1, lp), mq, ak[j]);
-                    ak[j] = mma<NM>(read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1, lp), ma, ak[j]);
+                    ak[j] = mma<3>(read_cols<NI>(s.q[0][x][t / 2], kStride, t & 1, lp), mq, ak[j]);
+                    ak[j] = mma<3>(read_cols<NI>(s.k[0][x][t / 2], kStride, t & 1, lp), ma, ak[j]);
                 }
             }
         }
@@ -713,7 +714,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaArgs a, D
 template <typename T, int C, int KP>
 hipError_t bwd_go(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, hipStream_t st) {
     hipLaunchKernelGGL((delta_back_kernel<T, C, KP>), dim3(unsigned(int64_t(a.P) * a.Hv * ((a.V + 63) / 64))), dim3(kWalkThreads),
-                       (Walk<T, C, KP, 3, true>::kLds), st, a, ws, d);
+                       (Walk<T, C, KP, true>::kLds), st, a, ws, d);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || ws.Nt == 0) return e;
     const int64_t tasks = int64_t(a.P) * a.Hk * ws.Nt;   // a compute unit holds one workgroup: more would start cold
@@ -730,7 +731,7 @@ hipError_t bwd_pick(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &d, 
     }
 }
 template <typename T, int C, int KP> hipError_t bwd_attr() {
-    constexpr size_t lw = Walk<T, C, KP, 3, true>::kLds, lg = sizeof(GradLds<T, C, KP>);
+    constexpr size_t lw = Walk<T, C, KP, true>::kLds, lg = sizeof(GradLds<T, C, KP>);
     static_assert(lw <= kDeltaMaxLds && lg <= kDeltaMaxLds, "LDS of a workgroup");
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_back_kernel<T, C, KP>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lw);

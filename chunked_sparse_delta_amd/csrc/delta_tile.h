@@ -204,13 +204,9 @@ template <int C> struct ChunkMem {
     Gates<C> g;
 };
 // ... and as these have it in LDS: blocks in pieces.
-template <int C, int NP> struct ChunkMats {
+template <int C> struct ChunkMats {
     unsigned char X[3][kTri<C>][kBlk];
-    unsigned char P[NP][kTri<C>][kBlk];
+    unsigned char P[3][kTri<C>][kBlk];
     Gates<C> g;
 };
-// Pieces of P. The readings are all that P goes into in the forward: rounded to bfloat16, they take two (one piece would make
-// their error against 64 bits half as large again). The backward's P reaches float32 gradients.
-template <typename T> constexpr int kPPieces(bool backward) { return backward || sizeof(T) == 4 ? 3 : 2; }
-
 }  // namespace sdm

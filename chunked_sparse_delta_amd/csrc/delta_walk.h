@@ -21,8 +21,8 @@ template <typename T> __device__ __forceinline__ const T *uniform(const T *p) {
 // cycle of a compute unit and LDS reads waited for it: 0.55 us of a chunk's 3.9.)
 constexpr int kWalkThreads = 512;
 
-// T: the inputs' type; NP: pieces of P; Q: q and P are wanted too.
-template <typename T, int C, int KP, int NP, bool Q> struct Walk {
+// T: the inputs' type; Q: q and P are wanted too.
+template <typename T, int C, int KP, bool Q> struct Walk {
     static constexpr int NI = kPieces<T>, KB = KP / 32, TB = C / 32;
     static constexpr int kStride = TB * KB * kBlk;              // between the pieces of k (and of q)
     static constexpr int KS = kStride / 4096;                   // 16-byte eights of a piece of k per thread
@@ -33,7 +33,7 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
     struct Lds {
         unsigned char k[NI][TB][KB][kBlk];
         unsigned char q[Q ? NI : 0][TB][KB][kBlk];
-        ChunkMats<C, NP> m;
+        ChunkMats<C> m;
         T v[4][C][16];
     };
     static constexpr int kBufs = 2 * sizeof(Lds) <= kDeltaMaxLds ? 2 : 1;
@@ -117,9 +117,9 @@ template <typename T, int C, int KP, int NP, bool Q> struct Walk {
 #pragma unroll
                 for (int n = 0; n < 3; ++n) *reinterpret_cast<db8 *>(s.m.X[n][e / 128] + at) = fx.p[n];
                 if constexpr (Q) {
-                    const Frag<NP> fp = split<NP>(__builtin_bit_cast(dt4, pp[i][0]), __builtin_bit_cast(dt4, pp[i][1]));
+                    const Frag<3> fp = split<3>(__builtin_bit_cast(dt4, pp[i][0]), __builtin_bit_cast(dt4, pp[i][1]));
 #pragma unroll
-                    for (int n = 0; n < NP; ++n) *reinterpret_cast<db8 *>(s.m.P[n][e / 128] + at) = fp.p[n];
+                    for (int n = 0; n < 3; ++n) *reinterpret_cast<db8 *>(s.m.P[n][e / 128] + at) = fp.p[n];
                 }
             }
             if (wv == 0) reinterpret_cast<du4 *>(&s.m.g)[lane] = g;
