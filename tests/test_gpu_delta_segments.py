@@ -7,7 +7,8 @@ start state [KP, VP] and map [KP, KP] in float32. Every test asks for it, so tha
 import pytest
 import torch
 
-from tests.test_gpu_delta import NAMES, gpu_of, make
+from oracle import dense as oracle
+from tests.test_gpu_delta import NAMES, close, f64_of, gpu_of, make
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,52 @@ def test_state_advanced_in_place(gpu, P, T, Hk, Hv, K, V, dtype, valid, busy):
         out = sdm.gated_delta_fwd(state, *(g[n] for n in NAMES[1:]), valid_tokens=vt)
         assert torch.equal(out, want) and torch.equal(state, end)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("decay", [0.3, 0.0])
+@pytest.mark.parametrize("P,T,Hk,Hv,K,V,dtype,valid", [
+    (3, 2112, 1, 1, 128, 64, "bf16", (449, 0, 2112)), (2, 700, 1, 1, 128, 128, "f32", (161, 0)),
+    (4, 1400, 1, 2, 72, 24, "bf16", (0, 1, 0, 321)), (2, 1600, 2, 2, 33, 70, "f32", (1600, 0)),
+])
+def test_streams_of_few_or_no_tokens(gpu, P, T, Hk, Hv, K, V, dtype, valid, decay):
+    """Streams that end in the first segment, at a segment's first token, or before their first token, beside whole ones, against the
+    token loop in 64 bits."""
+    import chunked_sparse_delta_amd as sdm
+    assert segments(P, T, Hk, Hv, K, V, DT[dtype])[0] > 2
+    x = make(P, T, Hk, Hv, K, V, DT[dtype], seed=12, decay=decay)
+    y, g = f64_of(x), gpu_of(x, gpu)
+    want, final = oracle.gated_delta(*(y[n] for n in NAMES), K ** -0.5, valid)
+    end = torch.full((P, Hv, K, V), float("nan"), device=gpu)
+    out = sdm.gated_delta_fwd(*(g[n] for n in NAMES), valid_tokens=torch.tensor(valid, dtype=torch.int32, device=gpu), state_out=end)
+    close(out, want, "readings", DT[dtype])
+    close(end, final, "state")
+    for p in range(P):
+        assert (out[p, valid[p]:] == 0).all()
+        assert valid[p] > 0 or torch.equal(end[p], g["state"][p])
+
+
+@pytest.mark.parametrize("P,T,Hv,K,V,dtype", [(1, 1500, 2, 64, 64, "f32"), (2, 1500, 2, 128, 40, "bf16")])
+def test_graph(gpu, P, T, Hv, K, V, dtype):
+    """A captured call in segments replays with the eager call's bits, other work in between; the state advances with every replay."""
+    import chunked_sparse_delta_amd as sdm
+    assert segments(P, T, 1, Hv, K, V, DT[dtype])[0] > 2
+    g = gpu_of(make(P, T, 1, Hv, K, V, DT[dtype], seed=13), gpu)
+    state, rest = g["state"].clone(), [g[n] for n in NAMES[1:]]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        sdm.gated_delta_fwd(state, *rest)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        got = sdm.gated_delta_fwd(state, *rest)
+    state.copy_(g["state"])
+    mine = g["state"].clone()
+    for seed in range(4):
+        torch.cuda.synchronize()
+        new = gpu_of(make(P, T, 1, Hv, K, V, DT[dtype], seed=seed), gpu)
+        for n in NAMES[1:]:
+            g[n].copy_(new[n])
+        want = sdm.gated_delta_fwd(mine, *rest)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(state, mine)
