@@ -54,10 +54,11 @@ typedef struct {
  *     place), but must not overlap it otherwise.
  *   valid_tokens, out [P, T, Hv, V]: as for sdm_fwd.
  *   exec->workspace: sdm_gated_delta_workspace_bytes(shape, 0) bytes, 256-byte aligned.
- * Arithmetic: products of the inputs and of float32 quantities accumulate in float32; the
- * state stays float32 throughout; out is rounded once. Bitwise reproducible.
+ * Arithmetic: products of the inputs and of float32 quantities (24 bits, to 2^-23) accumulate in
+ * float32; the state stays float32 throughout; out is rounded once. Bitwise reproducible.
  * Chunks of tokens are computed as one: an infinity or NaN in a live token's inputs may reach
- * readings of earlier tokens of its chunk (up to 63 before it), never other heads or streams.
+ * readings of earlier tokens of its chunk (up to 63 before it), never other streams or heads that
+ * do not read it, nor, from v or a state, other columns; what an infinity reaches may be NaN.
  * Padding tokens may hold anything.
  */
 int sdm_gated_delta_fwd(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
