@@ -12,7 +12,8 @@ struct Rows {
     int32_t width;
 };
 constexpr int64_t kCus = 256;                  // MI355X
-constexpr int64_t kDeltaMaxStride = 1 << 24;   // of the caller's tokens: a chunk's offsets fit 32 bits (of copies: check_delta)
+// Of tokens that the chunked kernels take as they are: a chunk's offsets fit 32 bits (those of copies: check_delta).
+constexpr int64_t kDeltaMaxStride = 1 << 24;
 
 // q or k as the chunked kernels take them: rows of the padded head_dim in bfloat16, `plane` elements
 // between the pieces of a float32 input (see delta_tile.h), every row 16-byte aligned. They are

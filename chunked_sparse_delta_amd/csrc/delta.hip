@@ -583,7 +583,8 @@ hipError_t launch_delta_fwd(const DeltaArgs &a, const DeltaWs &ws, bool is_bf16,
 }
 
 static bool rows_aligned(const Rows &r, int elements) {
-    return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.sp % elements == 0 && r.st % elements == 0 && r.sh % elements == 0;
+    return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.sp % elements == 0 && r.st % elements == 0 && r.sh % elements == 0 &&
+           r.st < kDeltaMaxStride;
 }
 bool delta_regular_keys(const Rows &r, bool is_bf16) { return is_bf16 && r.width == delta_kp(r.width) && rows_aligned(r, 8); }
 bool delta_regular_values(const Rows &r, bool is_bf16) { return r.width % 8 == 0 && rows_aligned(r, is_bf16 ? 8 : 4); }

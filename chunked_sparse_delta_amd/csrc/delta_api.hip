@@ -62,7 +62,6 @@ int check_delta_inputs(const sdm_delta_shape *s, bool chunks, const sdm_rows *q,
         if (!aligned(rows[i]->data, es)) return fail(SDM_ERR_ALIGN, "%s must be aligned to its element size", names[i]);
         if (rows[i]->stream < 0 || rows[i]->token < 0 || rows[i]->head < 0)
             return fail(SDM_ERR_SHAPE, "%s: strides must be >= 0", names[i]);
-        if (rows[i]->token >= kDeltaMaxStride) return fail(SDM_ERR_RANGE, "%s: the token stride must be below 2^24", names[i]);
     }
     if (s->tokens > 0 && (!beta || !log_decay)) return fail(SDM_ERR_NULL, "beta and log_decay must not be NULL");
     const void *f[] = {beta, log_decay, state, valid};

@@ -36,8 +36,8 @@ typedef struct {
  * SDM_ERR_RANGE past these limits. */
 
 /* A device [P, T, heads, width] array whose rows of `width` elements are dense; strides in
- * elements, >= 0, the token's below 2^24 (slices of one fused projection need no copy). Rows
- * need their element's alignment only. */
+ * elements, >= 0 (slices of one fused projection need no copy). Rows need their element's
+ * alignment only. */
 typedef struct {
     const void *data;
     int64_t stream;

@@ -133,3 +133,26 @@ def test_operands_have_float32s_bits(gpu, K, dtype, kind):
     for one in got:
         err = (one[0, :, 0].double().cpu()[live] - want).norm()
         assert err <= CANCEL * terms.norm() + 2.0 ** -8 * want.norm(), (err / terms.norm()).item()
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_tokens_far_apart(gpu, T):
+    """Rows of tokens 2^24 elements and more apart (a time-major array of a large batch), and one token with any stride: the bits of
+    dense rows."""
+    import chunked_sparse_delta_amd as sdm
+    P, H, K, V = 2, 2, 64, 64
+    g = gpu_of(make(P, T, H, H, K, V, torch.bfloat16), gpu)
+    far = 2 ** 24 + 64
+    room = torch.empty(70 * far, dtype=torch.bfloat16, device=gpu)
+    f = dict(g)
+    for i, n in enumerate("qkv"):
+        f[n] = room.as_strided((P, T, H, K), (2 ** 20, far if T > 1 else 2 ** 40, K, 1), i * 2 ** 22).copy_(g[n])
+    go = torch.randn((P, T, H, V), device=gpu).bfloat16()
+    res = []
+    for x in (g, f):
+        one = []
+        for call in (sdm.gated_delta_fwd, sdm.gated_delta_step):
+            end = torch.empty_like(g["state"])
+            one += [call(*(x[n] for n in NAMES), state_out=end), end]
+        res.append(one + list(sdm.gated_delta_bwd(*(x[n] for n in NAMES), go).values()))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
