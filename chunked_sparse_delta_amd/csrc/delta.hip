@@ -616,9 +616,13 @@ hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool
 }
 
 // A workgroup walks a sequence's chunks one after the other, at a pace that hardly depends on the others: few states leave
-// most of the device idle (16 heads of 16384 tokens of 128 x 128, two workgroups each: the whole call fell from 0.79 to 0.43 ms
-// with five segments at once). Walking segments at once costs the readings' walk again, once for the columns of the state and once
-// for those of the map, a third cheaper (no readings), and a join of about a chunk's time per segment.
+// most of the device idle. Walking segments at once costs the readings' walk again, once for the columns of the state and once
+// for those of the map, a third cheaper (no readings), and a join of about a chunk's time per segment; a launch's workgroups beyond
+// a compute unit each come in turns. Times below are in chunks of the readings' walk, and segments have to gain a tenth.
+// Measured, whole call, one walk / the segments taken (us): bfloat16, 16 heads of 16384 tokens of 128 x 128 872 / 357 (5; with 8 335, with
+// 3 527); 8 of 8192 of 200 x 200 773 / 343 (5); 64 of 2048 of 64 x 64 121 / 93 (3; with 8 115); float32, 16 of 4096 of 128 x 128 405 / 200
+// (5; with 6 226); 8 of 16384 of 64 x 64 1011 / 205 (15); 4 of 4096 of 256 x 256 1007 / 315 (8). Four heads of 1344 tokens of 72 x 40,
+// bfloat16, stay at one walk (89) where five segments would take 66.
 int delta_segments(int64_t heads, int slices, int K, int Nt) {
     const int64_t wgs = heads * slices, maps = heads * (slices + delta_kp(K) / 64);
     int best = 1;
@@ -629,7 +633,7 @@ int delta_segments(int64_t heads, int slices, int K, int Nt) {
         const int64_t a = (wgs + (g - 2) * maps + kCus - 1) / kCus, b = (wgs * g + kCus - 1) / kCus;
         const double t = double(len) * (0.7 * double(a) + double(b)) + 1.0 * double(g) + 6.0;
         if (t < 0.9 * least) {
-            least = t / 0.9 < least ? t : least;
+            least = t;
             best = g;
         }
     }

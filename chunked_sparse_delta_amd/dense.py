@@ -167,8 +167,9 @@ def gated_delta_fwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
                     workspace: torch.Tensor | None = None, keep: bool = False, stream=None) -> torch.Tensor:
     """The rule over whole sequences; returns the readings [P, T, Hv, V]. ``state`` is advanced in place, or left as it
     is where ``state_out`` is given, which then gets the final state. ``state=None`` starts from zeros (the final state
-    goes to ``state_out`` if given). ``workspace`` (uint8, GPU, gated_delta_workspace_bytes) is allocated if omitted. ``keep``: the given workspace, of the backward's size,
-    keeps what gated_delta_bwd(kept=workspace) then does not compute again."""
+    goes to ``state_out`` if given). ``workspace`` (uint8, GPU, gated_delta_workspace_bytes) is allocated if omitted.
+    ``keep``: the given workspace, of the backward's size, keeps what gated_delta_bwd(kept=workspace) then does not compute
+    again."""
     lib = _load()
     full, shape, qr, kr, vr, dev, index = _rule_inputs(k, v, beta, log_decay, q, scale, valid_tokens)
     if keep and workspace is None:
@@ -289,7 +290,7 @@ def gated_delta_rule(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor
     """The rule for autograd: returns (readings, final state); ``state`` (None: zeros) is not changed. Gradients reach
     the state, k, v, beta, log_decay and q through gated_delta_bwd. Until the backward the forward keeps what it computed
     per chunk (gated_delta_workspace_bytes(..., backward=True)); ``recompute=True`` keeps the inputs alone and computes the
-    forward again, for less memory and about a quarter more time."""
+    forward again, for less memory and about a sixth more time."""
     return _GatedDeltaRule.apply(state, k, v, beta, log_decay, q, scale, valid_tokens, recompute)
 
 
