@@ -32,6 +32,7 @@ struct DeltaArgs {
     const int32_t *valid;        // [P] or null
     const int32_t *ids;          // [P] or null (step)
     int64_t slots;               // states (step)
+    int64_t g_stream, g_token;   // g's strides (linear attention's step)
     void *out;                   // [P, T, Hv, V]
     int32_t P, T, Hk, Hv, K, V;
     float scale;
@@ -81,5 +82,6 @@ hipError_t launch_delta_copy_values(Rows *r, void *to, int P, int T, int H, bool
 size_t delta_mats_bytes(int K, bool is_bf16);   // of a chunk
 hipError_t launch_delta_bwd(const DeltaArgs &a, const DeltaWs &ws, const DeltaGrads &g, bool is_bf16, bool kept, hipStream_t st);
 hipError_t launch_delta_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st);
+hipError_t launch_linear_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st);   // without beta
 
 }  // namespace sdm

@@ -2,7 +2,8 @@
 //
 // With r = k S and s = q S of the state before the token, a = exp(g) and c = q k:
 //     u = beta (v - a r),   out = scale (a s + c u),   S = a S + k u
-// so both products and c need the old state only and share one reduction.
+// so both products and c need the old state only and share one reduction. Linear attention (DELTA false) is the same with
+// u = v and without r; its decay may be one of each head's.
 //
 // Bound by memory: a state is 4 K V bytes read and written once per call, against 2 (2 K + 2 V)
 // of bfloat16 rows. A wavefront owns CW columns of one state and keeps them in registers
@@ -109,7 +110,7 @@ __device__ __forceinline__ void out_store(bf16 *p, int cols, const float (&o)[VW
     }
 }
 
-template <typename T, int CW, int RPL>
+template <typename T, int CW, int RPL, bool DELTA>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     constexpr int LPR = CW / VW;                     // lanes per row piece
     const int lane = threadIdx.x & 63;
@@ -146,19 +147,20 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     const T *kp = static_cast<const T *>(a.k.data) + p * a.k.sp + hk * a.k.sh;
     const T *qp = static_cast<const T *>(a.q.data) + p * a.q.sp + hk * a.q.sh;
     const T *vp = static_cast<const T *>(a.v.data) + p * a.v.sp + h * a.v.sh + c0;
-    const float *bp = a.beta + int64_t(p) * a.T * a.Hv + h, *gp = a.g + int64_t(p) * a.T * a.Hv + h;
+    const float *bp = DELTA ? a.beta + int64_t(p) * a.T * a.Hv + h : nullptr;
+    const float *gp = DELTA ? a.g + int64_t(p) * a.T * a.Hv + h : a.g + p * a.g_stream + h;
     for (int t = 0; t < n; ++t) {
         float kk[RPL], qq[RPL], r[VW] = {}, s[VW] = {}, c = 0.0f, v[VW];
         rows_load(kp + t * a.k.st + row0, a.K - row0, kk);
         rows_load(qp + t * a.q.st + row0, a.K - row0, qq);
         rows_load(vp + t * a.v.st, cols, v);
-        const float beta = bp[int64_t(t) * a.Hv], decay = expf(gp[int64_t(t) * a.Hv]);
+        const float beta = DELTA ? bp[int64_t(t) * a.Hv] : 0.0f, decay = expf(gp[DELTA ? int64_t(t) * a.Hv : t * a.g_token]);
 #pragma unroll
         for (int i = 0; i < RPL; ++i) {
             c = fmaf(qq[i], kk[i], c);
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
-                r[j] = fmaf(kk[i], S[i][j], r[j]);
+                if (DELTA) r[j] = fmaf(kk[i], S[i][j], r[j]);
                 s[j] = fmaf(qq[i], S[i][j], s[j]);
             }
         }
@@ -166,9 +168,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
         float u[VW], o[VW];
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
-            r[j] = rows_sum<LPR>(r[j]);
+            if (DELTA) r[j] = rows_sum<LPR>(r[j]);
             s[j] = rows_sum<LPR>(s[j]);
-            u[j] = beta * (v[j] - decay * r[j]);
+            u[j] = DELTA ? beta * (v[j] - decay * r[j]) : v[j];
             o[j] = a.scale * fmaf(c, u[j], decay * s[j]);
         }
         put(t, o);
@@ -184,33 +186,36 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     }
 }
 
-template <typename T, int CW, int RPL> hipError_t step_go(const DeltaArgs &a, hipStream_t st) {
+template <typename T, int CW, int RPL, bool DELTA> hipError_t step_go(const DeltaArgs &a, hipStream_t st) {
     const int64_t waves = int64_t(a.P) * a.Hv * ((a.V + CW - 1) / CW);
-    hipLaunchKernelGGL((delta_step_kernel<T, CW, RPL>), dim3(unsigned((waves + 3) / 4)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((delta_step_kernel<T, CW, RPL, DELTA>), dim3(unsigned((waves + 3) / 4)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 // The fewest rows per lane that hold K.
-template <typename T, int CW> hipError_t step_rows(const DeltaArgs &a, hipStream_t st) {
+template <typename T, int CW, bool DELTA> hipError_t step_rows(const DeltaArgs &a, hipStream_t st) {
     constexpr int RG = 64 * VW / CW;
-    if (a.K <= 64) return step_go<T, CW, 64 / RG>(a, st);
+    if (a.K <= 64) return step_go<T, CW, 64 / RG, DELTA>(a, st);
     if constexpr (CW == 16) {
-        if (a.K <= 128) return step_go<T, CW, 128 / RG>(a, st);
-        return step_go<T, CW, 256 / RG>(a, st);
+        if (a.K <= 128) return step_go<T, CW, 128 / RG, DELTA>(a, st);
+        return step_go<T, CW, 256 / RG, DELTA>(a, st);
     }
     return hipErrorInvalidValue;   // step_pick takes wide slices for K <= 64 only
 }
-template <typename T> hipError_t step_pick(const DeltaArgs &a, int cus, hipStream_t st) {
+template <typename T, bool DELTA> hipError_t step_pick(const DeltaArgs &a, int cus, hipStream_t st) {
     // Eight rows of four columns per lane keep enough loads on their way: with K = 128, 16 columns took 55 us where 32 (sixteen
     // rows) took 60 (64 streams x 32 heads x 128 x 128; 46 since); with K = 64, 32 columns take 15.7 us where 16 take 18.6 (128 x
     // 16 x 64 x 64). Few states take the narrow slices for the wavefronts they give.
-    if (a.K <= 64 && int64_t(a.P) * a.Hv * ((a.V + 31) / 32) >= 8 * cus) return step_rows<T, 32>(a, st);
-    return step_rows<T, 16>(a, st);
+    if (a.K <= 64 && int64_t(a.P) * a.Hv * ((a.V + 31) / 32) >= 8 * cus) return step_rows<T, 32, DELTA>(a, st);
+    return step_rows<T, 16, DELTA>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_delta_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st) {
-    return is_bf16 ? step_pick<bf16>(a, cus, st) : step_pick<float>(a, cus, st);
+    return is_bf16 ? step_pick<bf16, true>(a, cus, st) : step_pick<float, true>(a, cus, st);
+}
+hipError_t launch_linear_step(const DeltaArgs &a, bool is_bf16, int cus, hipStream_t st) {
+    return is_bf16 ? step_pick<bf16, false>(a, cus, st) : step_pick<float, false>(a, cus, st);
 }
 
 }  // namespace sdm

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "sdm_dense.h"
+#include "sdm_linear.h"
 
 namespace sdm {
 

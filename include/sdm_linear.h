@@ -1,0 +1,89 @@
+/*
+ * sdm_linear.h - C ABI of linear attention with a decay for each head and of group norm with
+ * an activation. Conventions, error codes, sdm_exec and sdm_last_error() are sdm.h's;
+ * sdm_delta_shape and sdm_rows are sdm_dense.h's.
+ */
+#ifndef SDM_LINEAR_H
+#define SDM_LINEAR_H
+
+#include "sdm_dense.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Linear attention with a decay: stream p and value head h own a float32 state S of
+ * [head_dim, value_dim]; token t does
+ *     S = exp(g) S + k v,  out = scale q S
+ * (the gated delta rule without its correction). Value head h reads key head
+ * h / (value_heads / key_heads). head_dim and value_dim are at most 256, tokens at
+ * most 2^30, P * Hv * ceil(K * V / 256) and P * Hv * (T / 64 + 1) * ceil(max(K, V) / 64) below
+ * 2^24; SDM_ERR_RANGE past these limits (sdm_linear_attention_step: head_dim at most 256 and
+ * value_dim 65536 as in sdm_gated_delta_step, with that function's limits).
+ *
+ * log_decay: device float32 [Hv], a decay for each head (decay_per_token 0), or [P, T, Hv],
+ * one for each token (1). A decay: <= 0, -inf to clear the state. Larger ones are taken too
+ * while the sums over up to 256 neighbouring tokens stay within 80 of zero.
+ *
+ * Over whole sequences and, from a start state, the state after them.
+ *   q, k: [P, T, Hk, K]; v: [P, T, Hv, V] (strided rows, element alignment).
+ *   state: device float32 [P, Hv, K, V], or NULL for zeros. state_out: the same shape, or
+ *     NULL (not wanted); it may be `state` itself (advanced in place), but must not overlap
+ *     it otherwise.
+ *   valid_tokens, out [P, T, Hv, V]: as for sdm_fwd.
+ *   kept: NULL, or a device buffer of sdm_linear_attention_kept_bytes(shape) bytes, 256-byte
+ *     aligned, in which the call leaves what sdm_linear_attention_bwd then does not compute again.
+ *   exec->workspace: sdm_linear_attention_workspace_bytes(shape, SDM_LINEAR_FORWARD) bytes,
+ *     256-byte aligned (not used where `kept` is given).
+ * Arithmetic: products of the inputs and of float32 quantities (24 bits, to 2^-23) accumulate
+ * in float32; the state stays float32; out is rounded once. Bitwise reproducible.
+ * Tokens are taken 32 at once: an infinity or NaN in a live token's k or v may reach readings
+ * of up to 31 tokens before it, of the heads that read it; what an infinity reaches may be
+ * NaN. Padding tokens may hold anything.
+ */
+enum { SDM_LINEAR_FORWARD = 0, SDM_LINEAR_BACKWARD = 1, SDM_LINEAR_BACKWARD_KEPT = 2 };
+
+/* 0 for shapes they reject. */
+size_t sdm_linear_attention_workspace_bytes(const sdm_delta_shape *shape, int32_t what);
+size_t sdm_linear_attention_kept_bytes(const sdm_delta_shape *shape);
+
+int sdm_linear_attention_fwd(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
+                             const float *log_decay, int32_t decay_per_token, const float *state, float *state_out,
+                             const int32_t *valid_tokens, void *out, void *kept, const sdm_exec *exec);
+
+/*
+ * The same token by token, for single tokens and a few at once: each state is read and
+ * written once, whatever T. State, state_out, state_ids, slots: as for sdm_gated_delta_step.
+ * No workspace.
+ */
+int sdm_linear_attention_step(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
+                              const float *log_decay, int32_t decay_per_token, const float *state, float *state_out,
+                              const int32_t *state_ids, int64_t slots, const int32_t *valid_tokens, void *out,
+                              const sdm_exec *exec);
+
+/*
+ * The backward of sdm_linear_attention_fwd: for J = sum(grad_out * out) + sum(grad_state_out *
+ * final state) the gradient of every input.
+ *   state: the state the forward STARTED from (not read where `kept` is given).
+ *   grad_out: device [P, T, Hv, V] in dtype, dense. grad_state_out: device float32
+ *     [P, Hv, K, V], or NULL for zeros.
+ *   kept: NULL (the forward's states are computed again), or what a forward with the same inputs left.
+ *   grads (sdm_delta_grads, beta not used): dense, every element written (padding tokens:
+ *     zeros): q, k and v in dtype, each sum over the sharing value heads in float32 and rounded
+ *     once; log_decay float32 in log_decay's shape, or NULL; state float32, or NULL. None may
+ *     overlap an input, except that grads->state may be grad_state_out.
+ *   exec->workspace: sdm_linear_attention_workspace_bytes(shape, SDM_LINEAR_BACKWARD, or
+ *     SDM_LINEAR_BACKWARD_KEPT with `kept`) bytes, 256-byte aligned.
+ * The log-decays' gradient gathers differences over up to 256 tokens, in 64 bits.
+ */
+int sdm_linear_attention_bwd(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
+                             const float *log_decay, int32_t decay_per_token, const float *state,
+                             const int32_t *valid_tokens, const void *grad_out, const float *grad_state_out,
+                             const void *kept, const sdm_delta_grads *grads, const sdm_exec *exec);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SDM_LINEAR_H */
