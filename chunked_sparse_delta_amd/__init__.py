@@ -35,7 +35,8 @@ __all__ = ["SdmError", "sdm_fwd", "sdm_fwd_noalloc", "sdm_fwd_phase1", "sdm_fwd_
            "SDM_ERRORS", "gated_delta_fwd", "gated_delta_step", "gated_delta_bwd", "gated_delta_rule",
            "gated_delta_workspace_bytes", "layer_norm_fwd", "layer_norm_bwd", "layer_norm",
            "linear_attention_fwd", "linear_attention_step", "linear_attention_bwd", "linear_attention",
-           "linear_attention_workspace_bytes", "linear_attention_kept_bytes"]
+           "linear_attention_workspace_bytes", "linear_attention_kept_bytes",
+           "group_norm_fwd", "group_norm_bwd", "group_norm", "group_norm_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.environ.get("SDM_LIBRARY", os.path.join(_HERE, "libsdm.so"))
@@ -124,6 +125,7 @@ def _load():
             lib.sdm_bwd.restype = ctypes.c_int
             dense.bind(lib)
             linear.bind(lib)
+            group.bind(lib)
             lib.sdm_error_string.argtypes = [ctypes.c_int]
             lib.sdm_error_string.restype = ctypes.c_char_p
             lib.sdm_last_error.argtypes = []
@@ -595,8 +597,9 @@ def product_key_topk_backward(lin: torch.Tensor, grad_val: torch.Tensor, factors
     return graw
 
 
-from . import dense, linear  # noqa: E402  (they take their helpers from above)
+from . import dense, group, linear  # noqa: E402  (they take their helpers from above)
 from .dense import (gated_delta_bwd, gated_delta_fwd, gated_delta_rule, gated_delta_step,  # noqa: E402
                     gated_delta_workspace_bytes, layer_norm, layer_norm_bwd, layer_norm_fwd)
+from .group import group_norm, group_norm_bwd, group_norm_fwd, group_norm_workspace_bytes  # noqa: E402
 from .linear import (linear_attention, linear_attention_bwd, linear_attention_fwd,  # noqa: E402
                      linear_attention_kept_bytes, linear_attention_step, linear_attention_workspace_bytes)

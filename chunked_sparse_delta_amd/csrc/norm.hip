@@ -19,7 +19,7 @@
 // Measured, 16384 rows of 4096 bfloat16 columns: forward 47 us (5.7 TB/s; 59 in the middle of a training step), backward 82 to 91
 // us (402 MB, 4.4 to 4.9 TB/s) and 4 for the sums over workgroups; a large copy: 5.1 TB/s. 64 rows: 5 us, a launch and two ways
 // to memory. 1001 rows of 1537 float32 columns: 7.8 and 10.7 + 4.3 us.
-#include "common.h"
+#include "norm_vec.h"
 #include "host.h"
 
 namespace sdm {
@@ -32,86 +32,6 @@ namespace {
 constexpr int norm_max_items(int L, int V, bool bwd) {
     const int elems = L < 64 ? V : bwd || L == 64 ? 16 : L == 256 ? 64 : 32;
     return elems / V < 8 ? elems / V : 8;
-}
-
-template <typename T> struct NormVec;
-template <> struct NormVec<float> {
-    static constexpr int V = 4;
-    typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
-    static __device__ __forceinline__ void unpack(const raw &x, float (&o)[4]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = x[j];
-    }
-    static __device__ __forceinline__ raw part(const float *p, int n) {   // the first n elements, zeros after them
-        raw x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = j < n ? p[j] : 0.0f;
-        return x;
-    }
-    static __device__ __forceinline__ void load(const float *p, float (&o)[4]) { unpack(*reinterpret_cast<const raw *>(p), o); }
-    static __device__ __forceinline__ void store(float *p, const float (&o)[4]) {
-        *reinterpret_cast<raw *>(p) = raw{o[0], o[1], o[2], o[3]};
-    }
-};
-template <> struct NormVec<bf16> {
-    static constexpr int V = 8;
-    typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
-    static __device__ __forceinline__ void unpack(const raw &x, float (&o)[8]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            o[2 * j] = __uint_as_float(x[j] << 16);
-            o[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
-        }
-    }
-    static __device__ __forceinline__ raw part(const bf16 *p, int n) {   // the first n elements, zeros after them
-        raw x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            x[j] = (2 * j < n ? uint32_t(p[2 * j].bits) : 0u) | (2 * j + 1 < n ? uint32_t(p[2 * j + 1].bits) << 16 : 0u);
-        return x;
-    }
-    static __device__ __forceinline__ void load(const bf16 *p, float (&o)[8]) { unpack(*reinterpret_cast<const raw *>(p), o); }
-    static __device__ __forceinline__ void store(bf16 *p, const float (&o)[8]) {
-        raw x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = f32x2_to_bf16x2(o[2 * j], o[2 * j + 1]);
-        *reinterpret_cast<raw *>(p) = x;
-    }
-};
-
-// V elements of type T at any element address.
-template <typename T, int V> __device__ __forceinline__ void norm_load(const T *p, float (&o)[V]) {
-    if constexpr (V == NormVec<T>::V) NormVec<T>::load(p, o);
-    else {   // float32 parameters beside bfloat16 rows
-        float a[4], b[4];
-        NormVec<T>::load(p, a);
-        NormVec<T>::load(p + 4, b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            o[j] = a[j];
-            o[4 + j] = b[j];
-        }
-    }
-}
-
-// Vector i of a row of n columns at p: `fill` past its end.
-template <typename T, int V>
-__device__ __forceinline__ void norm_get(const T *p, int i, int n, float fill, float (&o)[V]) {
-    const int c = i * V;
-    if (c + V <= n) norm_load<T, V>(p + c, o);
-    else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = c + j < n ? to_f32(p[c + j]) : fill;
-    }
-}
-template <typename T, int V> __device__ __forceinline__ void norm_put(T *p, int i, int n, const float (&o)[V]) {
-    const int c = i * V;
-    if (c + V <= n) NormVec<T>::store(p + c, o);
-    else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (c + j < n) p[c + j] = from_f32<T>(o[j]);
-    }
 }
 
 // Sums of a and b over the row's L lanes (each gets them). `buf` holds two floats per wavefront of a row of more than one

@@ -82,6 +82,51 @@ int sdm_linear_attention_bwd(const sdm_delta_shape *shape, const sdm_rows *q, co
                              const int32_t *valid_tokens, const void *grad_out, const float *grad_state_out,
                              const void *kept, const sdm_delta_grads *grads, const sdm_exec *exec);
 
+/*
+ * Group norm with an activation over channels-last x [samples, rows, channels] in dtype, the
+ * channels in `groups` groups of neighbours. Per sample and group, over its valid rows:
+ *   y = act((x - mean) rstd weight + bias), rstd = 1 / sqrt(var + eps)
+ *   act(z) = z, z sigmoid(z) or z Phi(z); float32 arithmetic, y rounded once.
+ *   x: rows of `channels` dense elements, x_row elements apart, a sample's x_sample apart (a
+ *     slice of a wider array needs no copy; element alignment).
+ *   weight, bias: device [channels] in weight_dtype, or NULL (1 and 0). float32 rows take
+ *     float32 parameters, bfloat16 rows either type.
+ *   valid_rows: device int32 [samples], or NULL: rows at and past it are padding, which may hold
+ *     anything; they do not count and give +0. A sample without a valid row has mean 0 and var 0.
+ *   y: dense [samples, rows, channels]; mean, rstd: device float32 [samples, groups], written.
+ *   exec->workspace: sdm_group_norm_workspace_bytes(shape, 0) bytes, 256-byte aligned (where that is
+ *     0, none).
+ * At most 2^31 - 1 samples and rows of 2^20 channels. Bitwise reproducible.
+ */
+enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1, SDM_ACT_GELU = 2 };
+typedef struct {
+    int64_t samples;
+    int64_t rows;
+    int32_t channels;
+    int32_t groups;
+    int32_t dtype;
+    int32_t weight_dtype;
+    int32_t activation;   /* SDM_ACT_* */
+    float eps;
+} sdm_group_shape;
+
+/* Workspace bytes of the forward (backward = 0) or the backward (1). */
+size_t sdm_group_norm_workspace_bytes(const sdm_group_shape *shape, int32_t backward);
+
+int sdm_group_norm_fwd(const sdm_group_shape *shape, const void *x, int64_t x_sample, int64_t x_row, const void *weight,
+                       const void *bias, const int32_t *valid_rows, void *y, float *mean, float *rstd,
+                       const sdm_exec *exec);
+
+/*
+ * Its backward, from the mean and rstd that the forward wrote. grad_out, grad_x: dense
+ * [samples, rows, channels] in dtype (padding rows of grad_x: zeros); grad_weight, grad_bias:
+ * [channels] in weight_dtype; each gradient may be NULL (not wanted). Sums run in float32 in a
+ * fixed order.
+ */
+int sdm_group_norm_bwd(const sdm_group_shape *shape, const void *grad_out, const void *x, int64_t x_sample, int64_t x_row,
+                       const void *weight, const void *bias, const int32_t *valid_rows, const float *mean,
+                       const float *rstd, void *grad_x, void *grad_weight, void *grad_bias, const sdm_exec *exec);
+
 #ifdef __cplusplus
 }
 #endif

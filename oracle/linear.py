@@ -29,3 +29,29 @@ def linear_attention(state, k, v, log_decay, q, scale, valid=None):
         outs.append(torch.stack(rows) if T else torch.zeros(0, Hv, V, dtype=torch.float64))
         finals.append(S)
     return torch.stack(outs), torch.stack(finals)
+
+
+def group_norm(x, groups, weight=None, bias=None, activation=None, eps=1e-5, valid=None):
+    """(y, mean, rstd) of a float64 x [N, L, C]; rows at and past valid[n] do not count and give 0."""
+    N, L, C = x.shape
+    D = C // groups
+    ys, means, rstds = [], [], []
+    for n in range(N):
+        rows = L if valid is None else max(0, min(int(valid[n]), L))
+        live = x[n, :rows].reshape(rows, groups, D)
+        m = live.sum((0, 2)) / max(1, rows * D)
+        d = live - m[:, None]
+        r = 1.0 / torch.sqrt((d * d).sum((0, 2)) / max(1, rows * D) + eps)
+        z = (d * r[:, None]).reshape(rows, C)
+        if weight is not None:
+            z = z * weight
+        if bias is not None:
+            z = z + bias
+        if activation == "silu":
+            z = z / (1.0 + torch.exp(-z))
+        elif activation == "gelu":
+            z = 0.5 * z * torch.erfc(-z * 0.5 ** 0.5)
+        ys.append(torch.cat([z, torch.zeros(L - rows, C, dtype=torch.float64)]))
+        means.append(m)
+        rstds.append(r)
+    return torch.stack(ys), torch.stack(means), torch.stack(rstds)
