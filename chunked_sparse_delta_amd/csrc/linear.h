@@ -15,6 +15,14 @@ struct LinGates {
     int64_t sp, st;
 };
 
+// Tokens of a segment of a sequence of T. Longer ones have fewer states to write and read, shorter ones fewer pairs of tokens: of
+// bfloat16 rows 256 took 170 us where 128 took 185 (4 x 16 heads of up to 4096 tokens of 128 x 128), of float32 rows, whose products cost
+// twice as much, 128 took 78 us where 256 took 101 and 64, with twice the states, 75 (2 x 10 heads of 1500 tokens of 72 x 200).
+inline int lin_seg_tokens(bool is_bf16, int T) {
+    const int most = is_bf16 ? kLinSegMax : 128;
+    return T >= most ? most : T > 128 ? (T + 127) / 128 * 128 : 128;
+}
+
 struct LinArgs {
     Rows q, k, v;
     LinGates gates;
@@ -33,6 +41,7 @@ struct LinWs {
     float *dS;         // [ph][segs][K][V]: the same for the state's gradient: a segment's end (backward)
     float *dots;       // [ph][segs][lin_dot_parts]: <end state, its gradient> by wavefronts (backward)
     float *rows, *cols;  // [slices][ph][T]: the gates' shares through dq and dk, a slice of K each (backward)
+    float *rest;       // dq's and dk's sums between the value heads that share a key head, lin_rest_floats each (backward)
     double *sums;      // [ph][segs]: a segment's sum of log-decay gradients (backward, a decay for each head)
     int32_t segs, tokens;
 };
@@ -48,6 +57,11 @@ struct LinGrads {
 inline int lin_width(int n) { return n <= 64 ? 64 : n <= 128 ? 128 : 256; }   // padded depth of scores
 inline int lin_slice(int n) { return n <= 64 ? 64 : 128; }                    // columns of a workgroup
 inline int lin_slices(int n) { return (n + lin_slice(n) - 1) / lin_slice(n); }
+// Over how many XCDs units of workgroups that share their operands are dealt; the grid is padded to as many.
+__host__ __device__ inline int lin_xcds(int64_t units) { return units % kXcds == 0 || units >= 8 * kXcds ? kXcds : 1; }
+inline size_t lin_rest_floats(int P, int Hk, int K, int segs, int seg_tokens) {
+    return size_t(P) * size_t(segs) * size_t(Hk) * size_t(seg_tokens) * size_t(lin_slices(K) * lin_slice(K));
+}
 int lin_dot_parts(int K, int V);
 
 hipError_t linear_prepare();

@@ -29,18 +29,18 @@ struct StateArgs {
     bool back, final;        // back: weights scale e^{G_t}; final: the one segment's end state, from base
 };
 
-template <typename T, int KP, int ZW> struct StateCfg {
+template <typename T, int KP, int ZW, bool EVEN> struct StateCfg {
     static constexpr int NI = kPieces<T>, KT = NI == 1 && KP <= 128 ? 64 : 32;
-    using Y = Tile<T, KT, KP>;
-    using Z = Tile<T, KT, ZW>;
+    using Y = Tile<T, KT, KP, EVEN>;
+    using Z = Tile<T, KT, ZW, EVEN>;
     static constexpr size_t kTiles = size_t(NI) * Y::kPlane + 3 * size_t(Z::kPlane);
     static constexpr size_t kLds = kTiles + kLinSegMax * sizeof(float) + (kLinSegMax + 4) * sizeof(double);
 };
 
 // sum_t w_t y_t z_t over one segment: all of y's columns and ZW of z's. A wavefront takes ZW / 4 columns; z is weighted and cut into
 // pieces on its way to LDS.
-template <typename T, int KP, int ZW> __global__ __launch_bounds__(256, 2) void lin_state_kernel(StateArgs a) {
-    using C = StateCfg<T, KP, ZW>;
+template <typename T, int KP, int ZW, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_state_kernel(StateArgs a) {
+    using C = StateCfg<T, KP, ZW, EVEN>;
     constexpr int NI = C::NI, KT = C::KT, KB = KP / 32, ZB = ZW / 32, TB = KT / 32, NC = ZW / 64;
     using Y = typename C::Y;
     using Z = typename C::Z;
@@ -58,8 +58,8 @@ template <typename T, int KP, int ZW> __global__ __launch_bounds__(256, 2) void 
     Y ty;
     Z tz;
     auto bring = [&](int t0) {
-        ty.load(yr + t0 * a.y.st, a.y.st, live - t0, 0, a.K);
-        tz.load(zr + t0 * a.z.st, a.z.st, live - t0, z0, a.V);
+        ty.load(yr + t0 * a.y.st, a.y.st, live - t0, 0, a.K, threadIdx.x);
+        tz.load(zr + t0 * a.z.st, a.z.st, live - t0, z0, a.V, threadIdx.x);
     };
     if (live > 0) bring(0);
     segment_gates(a.gates, p, h, s0, live, G, total_of);
@@ -76,8 +76,8 @@ template <typename T, int KP, int ZW> __global__ __launch_bounds__(256, 2) void 
             for (int c = 0; c < NC; ++c) acc[kb][e][c] = dt4{};
     for (int t0 = 0; t0 < live; t0 += KT) {
         lds_barrier();
-        ty.store(ly);
-        tz.store_weighted(lz, w + t0);
+        ty.store(ly, threadIdx.x);
+        tz.store_weighted(lz, w + t0, threadIdx.x);
         lds_barrier();
         if (t0 + KT < live) bring(t0 + KT);
 #pragma unroll
@@ -250,13 +250,17 @@ __global__ __launch_bounds__(64) void lin_gate_sum_kernel(const double *sums, fl
     if (threadIdx.x == 0) g[h] = float(s);
 }
 
-template <typename T, int KP, int ZW> hipError_t state_go(const StateArgs &a, hipStream_t st) {
+template <typename T, int KP, int ZW, bool EVEN> hipError_t state_go(const StateArgs &a, hipStream_t st) {
     const int64_t slices = (a.V + ZW - 1) / ZW;
-    hipLaunchKernelGGL((lin_state_kernel<T, KP, ZW>), dim3(unsigned(slices * a.segs * a.P * a.Hv)), dim3(256), (StateCfg<T, KP, ZW>::kLds), st, a);
+    hipLaunchKernelGGL((lin_state_kernel<T, KP, ZW, EVEN>), dim3(unsigned(slices * a.segs * a.P * a.Hv)), dim3(256), (StateCfg<T, KP, ZW, EVEN>::kLds), st, a);
     return hipGetLastError();
 }
+template <typename T, int KP, int ZW> hipError_t state_even(const StateArgs &a, hipStream_t st) {
+    constexpr int vec = 16 / sizeof(T);
+    return a.K % vec == 0 && a.V % vec == 0 ? state_go<T, KP, ZW, true>(a, st) : state_go<T, KP, ZW, false>(a, st);
+}
 template <typename T, int KP> hipError_t state_slices(const StateArgs &a, hipStream_t st) {
-    return lin_slice(a.V) == 64 ? state_go<T, KP, 64>(a, st) : state_go<T, KP, 128>(a, st);
+    return lin_slice(a.V) == 64 ? state_even<T, KP, 64>(a, st) : state_even<T, KP, 128>(a, st);
 }
 template <typename T> hipError_t state_pick(const StateArgs &a, hipStream_t st) {
     switch (lin_width(a.K)) {
@@ -276,9 +280,11 @@ template <bool BACK> hipError_t launch_scan(const ScanArgs &a, int heads, hipStr
 }
 
 template <typename T, int KP, int ZW> hipError_t state_attr() {
-    static_assert(StateCfg<T, KP, ZW>::kLds <= 80 * 1024, "two workgroups to a compute unit");
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_state_kernel<T, KP, ZW>), hipFuncAttributeMaxDynamicSharedMemorySize,
-                               int(StateCfg<T, KP, ZW>::kLds));
+    constexpr size_t bytes = StateCfg<T, KP, ZW, true>::kLds;
+    static_assert(bytes <= 80 * 1024, "two workgroups to a compute unit");
+    auto set = [](auto kernel) { return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes)); };
+    const hipError_t e = set(&lin_state_kernel<T, KP, ZW, true>);
+    return e == hipSuccess ? set(&lin_state_kernel<T, KP, ZW, false>) : e;
 }
 template <typename T> hipError_t state_prepare() {
     hipError_t e = state_attr<T, 64, 64>();
@@ -304,6 +310,7 @@ AttendArgs attend_args(const LinArgs &a, const LinWs &ws) {
     t.gates = a.gates;
     t.valid = a.valid;
     t.P = a.P; t.T = a.T; t.Hk = a.Hk; t.Hv = a.Hv; t.K = a.K; t.V = a.V;
+    t.segs = ws.segs;
     t.seg_tokens = ws.tokens;
     return t;
 }
@@ -384,10 +391,12 @@ hipError_t launch_linear_bwd(const LinArgs &a, const LinWs &ws, const LinGrads &
         q.M = ws.S; q.M_head = (ws.segs + 1) * KV; q.M_seg = KV;
         q.out = g.q; q.dot = g.g ? ws.rows : nullptr;
         q.a0 = q.a1 = a.scale;
+        q.rest = ws.rest;
         k.x = a.v; k.y = g.go; k.z = a.q; k.own = a.k;
         k.M = ws.dS; k.M_head = ws.segs * KV; k.M_seg = KV;
         k.out = g.k; k.dot = g.g ? ws.cols : nullptr;
         k.a0 = 1.0f; k.a1 = a.scale; k.back = true;
+        k.rest = ws.rest + lin_rest_floats(a.P, a.Hk, a.K, ws.segs, ws.tokens);
         if ((e = is_bf16 ? attend_keys_bf16(t, st) : attend_keys_f32(t, st)) != hipSuccess) return e;
         AttendSide v = k;
         v.x = a.k; v.y = a.q; v.z = g.go;

@@ -30,7 +30,7 @@ int check_shape(const sdm_delta_shape *s, bool step) {
         return SDM_OK;
     }
     const int widest = s->head_dim > s->value_dim ? s->head_dim : s->value_dim;
-    if (heads * ((s->head_dim * s->value_dim + 255) / 256) >= groups || heads * (s->tokens / 64 + 1) * ((widest + 63) / 64) >= groups)
+    if (heads * ((s->head_dim * s->value_dim + 255) / 256) >= groups || heads * (s->tokens / 64 + 4) * ((widest + 63) / 64) >= groups / 2)
         return fail(SDM_ERR_RANGE, "%lld states of %d x %d and %d tokens are too many for a launch", (long long)heads, s->head_dim,
                     s->value_dim, s->tokens);
     return SDM_OK;
@@ -93,7 +93,7 @@ void take_states(const sdm_delta_shape *s, LinWs *ws, Taker &t) {
 }
 LinWs segments(const sdm_delta_shape *s) {
     LinWs ws{};
-    ws.tokens = kLinSegMax;
+    ws.tokens = lin_seg_tokens(s->dtype == SDM_BF16, s->tokens);
     ws.segs = s->tokens > ws.tokens ? (s->tokens + ws.tokens - 1) / ws.tokens : 1;
     return ws;
 }
@@ -109,6 +109,7 @@ size_t layout(const sdm_delta_shape *s, int what, LinWs *ws, void *base) {
         ws->rows = t.take<float>(gates);
         ws->cols = t.take<float>(gates);
         ws->sums = t.take<double>(heads * segs);
+        ws->rest = t.take<float>(s->value_heads > s->key_heads ? 2 * lin_rest_floats(s->streams, s->key_heads, s->head_dim, ws->segs, ws->tokens) : 0);
     }
     return t.bytes();
 }

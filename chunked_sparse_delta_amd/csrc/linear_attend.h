@@ -25,6 +25,7 @@ struct AttendSide {
     int64_t M_head, M_seg;
     void *out;               // dense [P, T, heads, width of z]
     float *dot;              // KEYS: [slices][ph][T], or null
+    float *rest;             // KEYS with shared key heads: lin_rest_floats
     float a0, a1;
     bool back;               // b at or after a
 };
@@ -32,45 +33,59 @@ struct AttendArgs {
     AttendSide side[2];      // blockIdx.y
     LinGates gates;
     const int32_t *valid;
-    int32_t P, T, Hk, Hv, K, V, seg_tokens;
+    int32_t P, T, Hk, Hv, K, V, segs, seg_tokens;
 };
 
-template <typename T, int XP, int ZW, bool KEYS> struct AttendCfg {
+template <typename T, int XP, int ZW, bool KEYS, bool EVEN> struct AttendCfg {
     static constexpr int NI = kPieces<T>;
     // Tokens of a wavefront in sixteens: two share every operand read from LDS, where the registers hold them.
     static constexpr int NQ = NI == 1 && XP <= 128 ? 2 : 1;
     static constexpr int QT = 64 * NQ, KT = NI == 1 && XP <= 128 ? 64 : 32;
-    using Y = Tile<T, KT, XP>;
-    using Z = Tile<T, KT, ZW>;
-    using S = Tile<float, KEYS ? ZW : 32, KEYS ? 32 : ZW>;
+    using Y = Tile<T, KT, XP, EVEN>;
+    using Z = Tile<T, KT, ZW, EVEN>;
+    using S = Tile<float, KEYS ? ZW : 32, KEYS ? 32 : ZW, EVEN>;
     static constexpr size_t kTiles = size_t(NI) * (Y::kPlane + Z::kPlane), kState = 3 * size_t(S::kPlane);
-    static constexpr size_t kLds = (kTiles > kState ? kTiles : kState) + (kLinSegMax + 4) * sizeof(double);
+    static constexpr size_t kGates = (kLinSegMax + 4) * sizeof(double) + kLinSegMax * sizeof(float);
+    // Two workgroups share a compute unit: two buffers of tiles where that leaves 80 KB to each; SR blocks of M at a time of SD on their way.
+    static constexpr int kBufs = 2 * kTiles + kGates <= 80 * 1024 ? 2 : 1;
+    static constexpr int SR = KEYS ? 1 : 2, SD = SR;
+    static constexpr int DY = NI == 1 ? 2 : 1;     // blocks of scores' depth whose operands are read at once
+    static constexpr bool kEarly = !KEYS && NI == 1;      // the first tile too is loaded ahead of everything
+    static constexpr int FB = KEYS ? 1 : 2;               // buffers of operands read from LDS
+    static constexpr size_t kLds = (kBufs * kTiles > SR * kState ? kBufs * kTiles : SR * kState) + kGates;
     static_assert(kLinSegMax % QT == 0, "a query tile lies in one segment");
 };
 
-template <typename T, int XP, int ZW, bool KEYS>
+template <typename T, int XP, int ZW, bool KEYS, bool EVEN>
 __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
-    using C = AttendCfg<T, XP, ZW, KEYS>;
+    using C = AttendCfg<T, XP, ZW, KEYS, EVEN>;
     constexpr int NI = C::NI, NQ = C::NQ, QT = C::QT, KT = C::KT, XB = XP / 32, ZB = ZW / 32, TB = KT / 32;
     using Y = typename C::Y;
     using Z = typename C::Z;
     extern __shared__ __align__(16) unsigned char lds[];
     unsigned char *ly = lds, *lz = lds + NI * Y::kPlane;
-    double *G = reinterpret_cast<double *>(lds + C::kLds) - (kLinSegMax + 4), *total_of = G + kLinSegMax;
-    const AttendSide &s = a.side[blockIdx.y];
+    double *total_of = reinterpret_cast<double *>(lds + C::kLds) - 4, *G = total_of - kLinSegMax;
+    float *local = reinterpret_cast<float *>(G) - kLinSegMax;     // a token's decay to the edge of its 32 on the side of the a
+    const AttendSide &s = a.side[KEYS ? blockIdx.y : 0];
     const bool back = s.back;
     const int heads = KEYS ? a.Hk : a.Hv, group = a.Hv / a.Hk, X = s.x.width, Zw = s.z.width;
-    const int slices = (Zw + ZW - 1) / ZW, tiles = (a.T + QT - 1) / QT;
-    const int slice = blockIdx.x % slices, tile = blockIdx.x / slices % tiles;
-    const int oh = blockIdx.x / slices / tiles % heads, p = blockIdx.x / slices / tiles / heads;
-    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lc = lane & 15, lg = lane >> 4;
-    const int z0 = slice * ZW, q0 = tile * QT, n = lin_valid(a.valid, p, a.T);
-    const int seg = q0 / a.seg_tokens, s0 = seg * a.seg_tokens, s1 = min(s0 + a.seg_tokens, n);
+    const int slices = (Zw + ZW - 1) / ZW, seg_tiles = a.seg_tokens / QT;
+    // What reads the same keys, values and states goes to one XCD (blocks are dealt to the eight in turn), where there is enough for
+    // all of them: the tiles and slices of a segment, of the value heads that share a key head.
+    const int unit = slices * seg_tiles * (KEYS ? 1 : group), units = a.P * a.Hk * a.segs, xcds = lin_xcds(units);
+    const int at_xcd = blockIdx.x / xcds, u = at_xcd / unit * xcds + int(blockIdx.x) % xcds, in_unit = at_xcd % unit;
+    if (u >= units) return;
+    const int seg = u % a.segs, khead = u / a.segs % a.Hk, p = u / a.segs / a.Hk;
+    const int slice = in_unit % slices, oh = KEYS ? khead : khead * group + in_unit / slices / seg_tiles;
+    const int lc = threadIdx.x & 15, lg = threadIdx.x >> 4 & 3, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int s0 = seg * a.seg_tokens, tile = in_unit / slices % seg_tiles, q0 = s0 + (back ? tile : seg_tiles - 1 - tile) * QT, n = lin_valid(a.valid, p, a.T), s1 = min(s0 + a.seg_tokens, n);
+    const int z0 = slice * ZW;
+    if (q0 >= a.T) return;      // (the tiles that see most of their segment come first)
     const int qw = q0 + wv * 16 * NQ, diag = qw & ~31;     // the wavefront's first token; the 32 tokens that it lies in
     T *out = static_cast<T *>(s.out) + (int64_t(p) * a.T * heads + oh) * Zw + z0;
     const int64_t os = int64_t(heads) * Zw;
     auto put = [&](int t, int zb, dt4 lo, dt4 hi) {
-        if (t < a.T) eight_store(out + t * os + zb * 32 + lg * 8, Zw - z0 - zb * 32 - lg * 8, lo, hi);
+        if (t < a.T) eight_store<EVEN>(out + t * os + zb * 32 + lg * 8, Zw - z0 - zb * 32 - lg * 8, lo, hi);
     };
     if (q0 >= n) {
 #pragma unroll
@@ -79,73 +94,109 @@ __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
             for (int zb = 0; zb < ZB; ++zb) put(qw + nq * 16 + lc, zb, dt4{}, dt4{});
         return;
     }
-    dt4 sum[KEYS ? ZB : 1][2][NQ];
-    if constexpr (KEYS) {
-#pragma unroll
-        for (int zb = 0; zb < ZB; ++zb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int nq = 0; nq < NQ; ++nq) sum[zb][e][nq] = dt4{};
-    }
+    const bool x_whole = qw + 16 * NQ <= n && XP <= X;
     dt4 acc[ZB][2][NQ];
     auto rows = [&](const Rows &r, int head) { return static_cast<const T *>(r.data) + p * r.sp + head * r.sh; };
     const int first = KEYS ? oh * group : oh, count = KEYS ? group : 1;
     for (int h = first; h < first + count; ++h) {
         const int hk = h / group;
+        // The thread's number as a value of its own: addresses made from it stay in this turn of the loop, where the compiler
+        // would keep them all in registers through it.
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, lc = lane & 15, lg = lane >> 4;
         // x and y are of one kind (keys or values), z of the other
         const T *xr = rows(s.x, KEYS ? h : hk), *yr = rows(s.y, KEYS ? h : hk), *zr = rows(s.z, KEYS ? hk : h);
+        // everything that is read first is on its way before the gates' sums are waited for (KEYS: where registers allow)
+        Eight<T> ex[NQ][XB];
+        auto bring_x = [&]() {
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+                const T *row = xr + int64_t(min(qw + nq * 16 + lc, n - 1)) * s.x.st;
+#pragma unroll
+                for (int d = 0; d < XB; ++d) ex[nq][d] = eight_load<EVEN>(row, d * 32 + lg * 8, X);
+            }
+        };
+        if (!KEYS) bring_x();
+        const float *M = s.M ? s.M + (int64_t(p) * a.Hv + h) * s.M_head + seg * s.M_seg : nullptr;
+        typename C::S tm[C::SD];
+        auto bring_state = [&](int d) {
+            const int V = a.V;
+            if constexpr (KEYS) tm[d % C::SD].load(M + int64_t(z0) * V, V, Zw - z0, d * 32, V, tid);
+            else tm[d % C::SD].load(M + int64_t(min(d * 32, X - 1)) * V, V, max(X - d * 32, 1), z0, V, tid);     // no rows left: x is 0 there
+        };
+        if (M) {
+#pragma unroll
+            for (int d = 0; d < C::SD; ++d) bring_state(d);
+        }
+        // tiles of the segment, from its far end to the wavefront's own tokens
+        const int k0 = back ? (s1 - 1 - s0) / KT : 0, k1 = back ? (q0 - s0) / KT : (min(q0 + QT, s1) - 1 - s0) / KT, step = back ? -1 : 1;
+        Y ty;
+        Z tz;
+        auto bring = [&](int kt) {
+            const int t0 = s0 + kt * KT;
+            ty.load(yr + int64_t(t0) * s.y.st, s.y.st, s1 - t0, 0, X, tid);
+            tz.load(zr + int64_t(t0) * s.z.st, s.z.st, s1 - t0, z0, Zw, tid);
+        };
+        if (C::kEarly) bring(k0);
         segment_gates(a.gates, p, h, s0, s1 - s0, G, total_of);
+        if (KEYS) bring_x();
         Frag<NI> fx[NQ][XB];
 #pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-            const int t = qw + nq * 16 + lc;
-            const T *row = xr + int64_t(t) * s.x.st;
+        for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-            for (int d = 0; d < XB; ++d) fx[nq][d] = pieces(eight(row + d * 32 + lg * 8, t < n ? X - d * 32 - lg * 8 : 0));
-        }
+            for (int d = 0; d < XB; ++d) {
+                if (!x_whole) eight_mask(ex[nq][d], d * 32 + lg * 8, X, qw + nq * 16 + lc < n);
+                fx[nq][d] = pieces(ex[nq][d]);
+            }
 #pragma unroll
         for (int zb = 0; zb < ZB; ++zb)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = dt4{};
-        // the product with the state
-        if (s.M) {
-            const float *M = s.M + (int64_t(p) * a.Hv + h) * s.M_head + seg * s.M_seg;
-            const int V = a.V;
-            typename C::S t;
-            auto bring = [&](int d) {
-                if constexpr (KEYS) t.load(M + int64_t(z0) * V, V, Zw - z0, d * 32, V);
-                else t.load(M + int64_t(d * 32) * V, V, X - d * 32, z0, V);
-            };
-            bring(0);
+        // the product with the state, 32 SR of its rows (KEYS: columns) at a time
+        if (M) {
 #pragma unroll
-            for (int d = 0; d < XB; ++d) {
+            for (int d0 = 0; d0 < XB; d0 += C::SR) {
                 lds_barrier();
-                t.store(lds);
+#pragma unroll
+                for (int i = 0; i < C::SR; ++i) tm[(d0 + i) % C::SD].store(lds + i * C::kState, tid);
                 lds_barrier();
-                if (d + 1 < XB) bring(d + 1);
 #pragma unroll
-                for (int zb = 0; zb < ZB; ++zb) {
-                    Frag<3> f[2];
+                for (int i = 0; i < C::SR; ++i)
+                    if (d0 + i + C::SD < XB) bring_state(d0 + i + C::SD);
+                // a step's operands are read from LDS ahead of the products of the step before it
+                Frag<3> f[C::FB][2];
+                auto read = [&](int j) {
+                    const unsigned char *blk = lds + j / ZB * C::kState + j % ZB * kBlk;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        f[e] = KEYS ? read_rows<3>(lds + zb * kBlk, C::S::kPlane, e) : read_cols<3>(lds + zb * kBlk, C::S::kPlane, e);
+                    for (int e = 0; e < 2; ++e) f[j % C::FB][e] = KEYS ? read_rows<3>(blk, C::S::kPlane, e, lane) : read_cols<3>(blk, C::S::kPlane, e, lane);
+                };
+                if (C::FB == 2) read(0);
+#pragma unroll
+                for (int j = 0; j < C::SR * ZB; ++j) {
+                    if (C::FB == 1) read(j);
+                    else if (j + 1 < C::SR * ZB) read(j + 1);
+                    if (C::FB == 2) lds_point();
+                    const int zb = j % ZB, d = d0 + j / ZB;
                     each_product<3, 3, NI>([&](int m, int l) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = mma1(f[e].p[m], fx[nq][d].p[l], acc[zb][e][nq]);
+                            for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = mma1(f[j % C::FB][e].p[m], fx[nq][d].p[l], acc[zb][e][nq]);
                     });
+                    if (C::FB == 2) lds_point();
                 }
             }
         } else {
             lds_barrier();
         }
+        const double sign = back ? -1.0 : 1.0;
+        auto edge_of = [&](int b) { return back ? (b > 0 ? G[b - 1] : 0.0) : G[b + 31]; };    // of the 32 tokens from b on
+        local[threadIdx.x] = exp2_of(sign * (edge_of(threadIdx.x & ~31) - G[threadIdx.x]));
         // Decays are taken relative to a border of the wavefront's tokens until the pairs within its 32: e^{ref - H_b} before it
         // and e^{H_a - ref} after, both at most 1 where the log-decays are (H: G, or -G where b follows a).
-        const double sign = back ? -1.0 : 1.0;
         const int border = back ? min(qw + 16 * NQ, s1) - 1 - s0 : qw - 1 - s0;
         const double ref = border >= 0 && border < kLinSegMax ? sign * G[border] : 0.0;
         const float ws = s.a0 * exp2_of(ref + (back ? G[s1 - 1 - s0] : 0.0));
@@ -159,48 +210,62 @@ __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
 #pragma unroll
                 for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] *= ws;
         float self[NQ] = {};     // a1 (x_a . y_a), in the lanes that come upon it
-        // tiles of the segment, from its far end to the wavefront's own tokens
-        const int k0 = back ? (s1 - 1 - s0) / KT : 0, k1 = back ? (q0 - s0) / KT : (min(q0 + QT, s1) - 1 - s0) / KT, step = back ? -1 : 1;
-        Y ty;
-        Z tz;
-        auto bring = [&](int kt) {
-            const int t0 = s0 + kt * KT;
-            ty.load(yr + int64_t(t0) * s.y.st, s.y.st, s1 - t0, 0, X);
-            tz.load(zr + int64_t(t0) * s.z.st, s.z.st, s1 - t0, z0, Zw);
-        };
-        bring(k0);
-        for (int kt = k0;; kt += step) {
+        if (!C::kEarly) bring(k0);
+        lds_barrier();
+        ty.store(ly, tid);
+        tz.store(lz, tid);
+        if (k0 != k1) bring(k0 + step);
+        for (int kt = k0, turn = 0;; kt += step, ++turn) {
+            // the next tile goes to the other buffer, or to this one once it is free
+            unsigned char *cy = ly + (C::kBufs == 2 && (turn & 1) ? C::kTiles : 0), *cz = cy + (lz - ly);
             lds_barrier();
-            ty.store(ly);
-            tz.store(lz);
-            lds_barrier();
-            if (kt != k1) bring(kt + step);
+            if (C::kBufs == 2 && kt != k1) {
+                unsigned char *ny = ly + (turn & 1 ? 0 : C::kTiles);
+                ty.store(ny, tid);
+                tz.store(ny + (lz - ly), tid);
+                if (kt + step != k1) bring(kt + 2 * step);
+            }
             for (int i = 0; i < TB; ++i) {
                 const int tb = back ? TB - 1 - i : i, b0 = s0 + kt * KT + tb * 32;
                 if (qw >= s1 || b0 >= s1 || (back ? b0 < diag : b0 > diag)) continue;
                 dt4 st[2][NQ] = {};
+                Frag<NI> fy[C::FB][C::DY][2], fz[C::FB][2];
+                auto read_y = [&](int j) {
 #pragma unroll
-                for (int d = 0; d < XB; ++d) {
-                    Frag<NI> f[2];
+                    for (int i = 0; i < C::DY; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) f[e] = read_rows<NI>(ly + (tb * XB + d) * kBlk, Y::kPlane, e);
-                    each_product<3, NI, NI>([&](int m, int l) {
+                        for (int e = 0; e < 2; ++e) fy[j % C::FB][i][e] = read_rows<NI>(cy + (tb * XB + j * C::DY + i) * kBlk, Y::kPlane, e, lane);
+                };
+                auto read_z = [&](int zb) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e) fz[zb % C::FB][e] = read_cols<NI>(cz + (tb * ZB + zb) * kBlk, Z::kPlane, e, lane);
+                };
+                if (C::FB == 2) read_y(0);
 #pragma unroll
-                            for (int nq = 0; nq < NQ; ++nq) st[e][nq] = mma1(f[e].p[m], fx[nq][d].p[l], st[e][nq]);
-                    });
+                for (int j = 0; j < XB / C::DY; ++j) {
+                    if (C::FB == 1) read_y(j);
+                    else if (j + 1 < XB / C::DY) read_y(j + 1);
+                    else read_z(0);
+                    if (C::FB == 2) lds_point();
+#pragma unroll
+                    for (int i = 0; i < C::DY; ++i)
+                        each_product<3, NI, NI>([&](int m, int l) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int nq = 0; nq < NQ; ++nq) st[e][nq] = mma1(fy[j % C::FB][i][e].p[m], fx[nq][j * C::DY + i].p[l], st[e][nq]);
+                        });
+                    if (C::FB == 2) lds_point();
                 }
                 const double *Gb = G + (b0 - s0) + lg * 8;
                 if (b0 != diag) {
+                    const float w = s.a1 * exp2_of(ref - sign * edge_of(b0 - s0));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e) {
+                        const dt4 d = w * *reinterpret_cast<const dt4 *>(local + (b0 - s0) + lg * 8 + e * 4);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float w = s.a1 * exp2_of(ref - sign * Gb[e * 4 + r]);
-#pragma unroll
-                            for (int nq = 0; nq < NQ; ++nq) st[e][nq][r] *= w;
-                        }
+                        for (int nq = 0; nq < NQ; ++nq) st[e][nq] *= d;
+                    }
                 } else {
 #pragma unroll
                     for (int nq = 0; nq < NQ; ++nq) {
@@ -227,40 +292,56 @@ __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
                 for (int nq = 0; nq < NQ; ++nq) fp[nq] = split<3>(st[0][nq], st[1][nq]);
 #pragma unroll
                 for (int zb = 0; zb < ZB; ++zb) {
-                    Frag<NI> f[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) f[e] = read_cols<NI>(lz + (tb * ZB + zb) * kBlk, Z::kPlane, e);
+                    if (C::FB == 1) read_z(zb);
+                    else if (zb + 1 < ZB) read_z(zb + 1);
+                    if (C::FB == 2) lds_point();
                     each_product<3, NI, 3>([&](int m, int l) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = mma1(f[e].p[m], fp[nq].p[l], acc[zb][e][nq]);
+                            for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = mma1(fz[zb % C::FB][e].p[m], fp[nq].p[l], acc[zb][e][nq]);
                     });
+                    if (C::FB == 2) lds_point();
                 }
             }
             if (kt == k1) break;
+            if (C::kBufs == 1) {
+                lds_barrier();
+                ty.store(ly, tid);
+                tz.store(lz, tid);
+                if (kt + step != k1) bring(kt + 2 * step);
+            }
         }
         if constexpr (KEYS) {
-            const T *mine = rows(s.own, oh) + z0, *other = zr + z0;
+            // The sum over the value heads that share the key head waits in memory for the next one: registers hold one head's alone.
+            const bool begins = h == first, ends = h + 1 == first + count;
+            dt4 *rest = reinterpret_cast<dt4 *>(s.rest) +
+                        ((((int64_t(p) * a.segs + seg) * a.Hk + oh) * seg_tiles + (q0 - s0) / QT) * slices + slice) * (2 * ZB * NQ * 256) + tid;
+            const T *mine = rows(s.own, oh);
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
-                const int t = qw + nq * 16 + lc, at = (t - diag) & 31;
+                const int t = qw + nq * 16 + lc, at = (t - diag) & 31, row = min(t, n - 1);
                 const float w = __shfl(self[nq], at / 8 * 16 + lc, 64);
                 float dot = 0.0f;
 #pragma unroll
                 for (int zb = 0; zb < ZB; ++zb) {
-                    const int left = t < n ? Zw - z0 - zb * 32 - lg * 8 : 0;
+                    __builtin_amdgcn_sched_barrier(0);      // not all the rows' loads at once: registers
+                    const int c = z0 + zb * 32 + lg * 8;
                     dt4 m[2], o[2];
-                    eight_values(eight(mine + int64_t(t) * s.own.st + zb * 32 + lg * 8, left), m[0], m[1]);
-                    eight_values(eight(other + int64_t(t) * s.z.st + zb * 32 + lg * 8, left), o[0], o[1]);
+                    eight_values(eight<EVEN>(mine + row * s.own.st, c, Zw, t < n), m[0], m[1]);
+                    eight_values(eight<EVEN>(zr + row * s.z.st, c, Zw, t < n), o[0], o[1]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e) {
+                        dt4 &x = acc[zb][e][nq];
+                        dt4 *r = rest + ((zb * 2 + e) * NQ + nq) * 256;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float x = acc[zb][e][nq][r];
-                            dot = fmaf(m[e][r], x, dot);
-                            sum[zb][e][nq][r] += fmaf(w, o[e][r], x);
+                        for (int i = 0; i < 4; ++i) {
+                            dot = fmaf(m[e][i], x[i], dot);
+                            x[i] = fmaf(w, o[e][i], x[i]);
                         }
+                        if (!begins) x += *r;
+                        if (!ends) *r = x;
+                    }
                 }
                 dot += __shfl_xor(dot, 16, 64);
                 dot += __shfl_xor(dot, 32, 64);
@@ -273,24 +354,24 @@ __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
     for (int nq = 0; nq < NQ; ++nq) {
         const int t = qw + nq * 16 + lc;
 #pragma unroll
-        for (int zb = 0; zb < ZB; ++zb) {
-            dt4 o[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) o[e] = t < n ? (KEYS ? sum[KEYS ? zb : 0][e][nq] : acc[zb][e][nq]) : dt4{};
-            put(t, zb, o[0], o[1]);
-        }
+        for (int zb = 0; zb < ZB; ++zb) put(t, zb, t < n ? acc[zb][0][nq] : dt4{}, t < n ? acc[zb][1][nq] : dt4{});
     }
 }
 
-template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_go(const AttendArgs &a, int sides, hipStream_t st) {
-    using C = AttendCfg<T, XP, ZW, KEYS>;
-    const int64_t tiles = (int64_t(a.T) + C::QT - 1) / C::QT, slices = (a.side[0].z.width + ZW - 1) / ZW;
-    hipLaunchKernelGGL((lin_attend_kernel<T, XP, ZW, KEYS>), dim3(unsigned(tiles * slices * a.P * (KEYS ? a.Hk : a.Hv)), unsigned(sides)), dim3(256),
-                       C::kLds, st, a);
+template <typename T, int XP, int ZW, bool KEYS, bool EVEN> hipError_t attend_go(const AttendArgs &a, int sides, hipStream_t st) {
+    using C = AttendCfg<T, XP, ZW, KEYS, EVEN>;
+    const int64_t slices = (a.side[0].z.width + ZW - 1) / ZW, unit = slices * (a.seg_tokens / C::QT) * (KEYS ? 1 : a.Hv / a.Hk);
+    const int64_t units = int64_t(a.P) * a.Hk * a.segs;
+    hipLaunchKernelGGL((lin_attend_kernel<T, XP, ZW, KEYS, EVEN>), dim3(unsigned((units + lin_xcds(units) - 1) / lin_xcds(units) * lin_xcds(units) * unit), unsigned(sides)),
+                       dim3(256), C::kLds, st, a);
     return hipGetLastError();
 }
+template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_even(const AttendArgs &a, int sides, hipStream_t st) {
+    constexpr int vec = 16 / sizeof(T);
+    return a.K % vec == 0 && a.V % vec == 0 ? attend_go<T, XP, ZW, KEYS, true>(a, sides, st) : attend_go<T, XP, ZW, KEYS, false>(a, sides, st);
+}
 template <typename T, int XP, bool KEYS> hipError_t attend_slices(const AttendArgs &a, int sides, hipStream_t st) {
-    return lin_slice(a.side[0].z.width) == 64 ? attend_go<T, XP, 64, KEYS>(a, sides, st) : attend_go<T, XP, 128, KEYS>(a, sides, st);
+    return lin_slice(a.side[0].z.width) == 64 ? attend_even<T, XP, 64, KEYS>(a, sides, st) : attend_even<T, XP, 128, KEYS>(a, sides, st);
 }
 template <typename T, bool KEYS> hipError_t attend(const AttendArgs &a, int sides, hipStream_t st) {
     switch (lin_width(a.side[0].x.width)) {
@@ -300,9 +381,12 @@ template <typename T, bool KEYS> hipError_t attend(const AttendArgs &a, int side
     }
 }
 template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_attr() {
-    static_assert(AttendCfg<T, XP, ZW, KEYS>::kLds <= 80 * 1024, "two workgroups to a compute unit");
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_attend_kernel<T, XP, ZW, KEYS>), hipFuncAttributeMaxDynamicSharedMemorySize,
-                               int(AttendCfg<T, XP, ZW, KEYS>::kLds));
+    static_assert(AttendCfg<T, XP, ZW, KEYS, true>::kLds <= 80 * 1024, "two workgroups to a compute unit");
+    auto set = [](auto kernel) {
+        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(AttendCfg<T, XP, ZW, KEYS, true>::kLds));
+    };
+    const hipError_t e = set(&lin_attend_kernel<T, XP, ZW, KEYS, true>);
+    return e == hipSuccess ? set(&lin_attend_kernel<T, XP, ZW, KEYS, false>) : e;
 }
 template <typename T, bool KEYS> hipError_t attend_prepare() {
     hipError_t e = attend_attr<T, 64, 64, KEYS>();

@@ -15,35 +15,59 @@ template <> struct Eight<bf16> {
 template <> struct Eight<float> {
     dt4 a, b;
 };
-__device__ __forceinline__ void eight_load(const bf16 *p, Eight<bf16> &o) {
+// Eight elements from column c on of a row of `width` at p. Past its end there may be anything, until eight_mask. EVEN: the width is a
+// multiple of 16 bytes, so that every load is one whole vector and none is behind a branch; else the vector across the end goes by elements.
+template <bool EVEN> __device__ __forceinline__ Eight<bf16> eight_load(const bf16 *p, int c, int width) {
     typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
-    o.w = *reinterpret_cast<const raw *>(p);
-}
-__device__ __forceinline__ void eight_load(const float *p, Eight<float> &o) {
-    typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
-    o.a = *reinterpret_cast<const raw *>(p);
-    o.b = *reinterpret_cast<const raw *>(p + 4);
-}
-__device__ __forceinline__ void eight_part(const bf16 *p, int left, Eight<bf16> &o) {
+    Eight<bf16> o;
+    const bool whole = EVEN ? c < width : c + 8 <= width;
+    if (EVEN || width >= 8) o.w = *reinterpret_cast<const raw *>(p + (whole ? c : 0));
+    if (!EVEN && !whole && c < width) {
+        uint32_t h[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        o.w[j] = (2 * j < left ? uint32_t(p[2 * j].bits) : 0u) | (2 * j + 1 < left ? uint32_t(p[2 * j + 1].bits) << 16 : 0u);
+        for (int j = 0; j < 8; ++j) h[j] = p[min(c + j, width - 1)].bits;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.w[j] = (c + 2 * j < width ? h[2 * j] : 0u) | (c + 2 * j + 1 < width ? h[2 * j + 1] << 16 : 0u);
+    }
+    return o;
 }
-__device__ __forceinline__ void eight_part(const float *p, int left, Eight<float> &o) {
+template <bool EVEN> __device__ __forceinline__ Eight<float> eight_load(const float *p, int c, int width) {
+    typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
+    Eight<float> o;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int at = c + 4 * e;
+        const bool whole = EVEN ? at < width : at + 4 <= width;
+        dt4 x = {};
+        if (EVEN || width >= 4) x = *reinterpret_cast<const raw *>(p + (whole ? at : 0));
+        if (!EVEN && !whole && at < width) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float h = p[min(at + j, width - 1)];
+                x[j] = at + j < width ? h : 0.0f;
+            }
+        }
+        (e ? o.b : o.a) = x;
+    }
+    return o;
+}
+// Zeros past the row's end and, where the row is not `live`, in its place. (Apart from the load, since it waits for it.)
+__device__ __forceinline__ void eight_mask(Eight<bf16> &o, int c, int width, bool live) {
+    const bool in = live && c < width;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o.w[j] = in ? o.w[j] : 0u;
+}
+__device__ __forceinline__ void eight_mask(Eight<float> &o, int c, int width, bool live) {
+    const bool in = live && c < width, more = live && c + 4 < width;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        o.a[j] = j < left ? p[j] : 0.0f;
-        o.b[j] = 4 + j < left ? p[4 + j] : 0.0f;
+        o.a[j] = in ? o.a[j] : 0.0f;
+        o.b[j] = more ? o.b[j] : 0.0f;
     }
 }
-__device__ __forceinline__ void eight_clear(Eight<bf16> &o) { o.w = du4{}; }
-__device__ __forceinline__ void eight_clear(Eight<float> &o) { o.a = o.b = dt4{}; }
-// The elements p[0 .. 8) of which `left` are there (zeros after them; <= 0: none, and p is not read).
-template <typename T> __device__ __forceinline__ Eight<T> eight(const T *p, int left) {
-    Eight<T> o;
-    if (left >= 8) eight_load(p, o);
-    else if (left > 0) eight_part(p, left, o);
-    else eight_clear(o);
+template <bool EVEN, typename T> __device__ __forceinline__ Eight<T> eight(const T *p, int c, int width, bool live) {
+    Eight<T> o = eight_load<EVEN>(p, c, width);
+    eight_mask(o, c, width, live);
     return o;
 }
 __device__ __forceinline__ void eight_values(const Eight<bf16> &x, dt4 &a, dt4 &b) {
@@ -62,65 +86,72 @@ __device__ __forceinline__ void eight_values(const Eight<float> &x, dt4 &a, dt4 
 __device__ __forceinline__ Frag<1> pieces(const Eight<bf16> &x) { return {{__builtin_bit_cast(db8, x.w)}}; }
 __device__ __forceinline__ Frag<3> pieces(const Eight<float> &x) { return split<3>(x.a, x.b); }
 
-// a and b, rounded, to p[0 .. 8) of which `left` are there.
-__device__ __forceinline__ void eight_store(bf16 *p, int left, dt4 a, dt4 b) {
+// a and b, rounded, to p[0 .. 8) of which `left` are there (EVEN: all, or none, or for float32 four).
+template <bool EVEN> __device__ __forceinline__ void eight_store(bf16 *p, int left, dt4 a, dt4 b) {
     typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
     const raw w = {f32x2_to_bf16x2(a[0], a[1]), f32x2_to_bf16x2(a[2], a[3]), f32x2_to_bf16x2(b[0], b[1]), f32x2_to_bf16x2(b[2], b[3])};
-    if (left >= 8) *reinterpret_cast<raw *>(p) = w;
-    else {
+    if (EVEN ? left > 0 : left >= 8) *reinterpret_cast<raw *>(p) = w;
+    else if (!EVEN) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (j < left) p[j].bits = uint16_t(w[j / 2] >> (j & 1 ? 16 : 0));
     }
 }
-__device__ __forceinline__ void eight_store(float *p, int left, dt4 a, dt4 b) {
+template <bool EVEN> __device__ __forceinline__ void eight_store(float *p, int left, dt4 a, dt4 b) {
     typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
-    if (left >= 8) {
-        *reinterpret_cast<raw *>(p) = raw{a[0], a[1], a[2], a[3]};
-        *reinterpret_cast<raw *>(p + 4) = raw{b[0], b[1], b[2], b[3]};
-    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < left) p[j] = j < 4 ? a[j & 3] : b[j & 3];
+    for (int e = 0; e < 2; ++e) {
+        const dt4 x = e ? b : a;
+        if (EVEN ? left > 4 * e : left >= 4 * e + 4) *reinterpret_cast<raw *>(p + 4 * e) = raw{x[0], x[1], x[2], x[3]};
+        else if (!EVEN) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (4 * e + j < left) p[4 * e + j] = x[j];
+        }
     }
 }
 
-// A tile of ROWS tokens (a multiple of 32) and W columns from column c0 of `width`, brought by the 256 threads of a workgroup and
-// kept in LDS as [piece][32 rows][32 columns] blocks. Rows outside [0, live) and columns past the width are zeros.
-template <typename T, int ROWS, int W> struct Tile {
+// A tile of ROWS rows (a multiple of 32) and W columns from column c0 of `width`, brought by the 256 threads of a workgroup and
+// (tid: a thread's number) kept in LDS as [piece][32 rows][32 columns] blocks. Rows from `live` >= 1 on and columns past the width are zeros.
+template <typename T, int ROWS, int W, bool EVEN> struct Tile {
     static constexpr int N = ROWS * W / 2048, WB = W / 32, kPlane = ROWS / 32 * WB * kBlk;   // eights of a thread
     static_assert(ROWS * W % 2048 == 0, "whole eights for every thread");
     Eight<T> x[N];
-    // rows: of the tile's first token; st: a token's stride
-    __device__ __forceinline__ void load(const T *rows, int64_t st, int live, int c0, int width) {
+    int live, c0, width;
+    static __device__ __forceinline__ int row_of(int slot) { return slot / 128 / WB * 32 + slot % 128 / 4; }
+    static __device__ __forceinline__ int col_of(int slot) { return slot / 128 % WB * 32 + slot % 4 * 8; }
+    // rows: the tile's first row; st: a row's stride
+    __device__ __forceinline__ void load(const T *rows, int64_t st, int live_, int c0_, int width_, int tid) {
+        live = live_;
+        c0 = c0_;
+        width = width_;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int slot = int(threadIdx.x) + 256 * i, blk = slot / 128, r = blk / WB * 32 + slot % 128 / 4;
-            const int c = c0 + blk % WB * 32 + slot % 4 * 8;
-            x[i] = eight(rows + r * st + c, r < live ? width - c : 0);
+            const int slot = tid + 256 * i;
+            x[i] = eight_load<EVEN>(rows + min(row_of(slot), live - 1) * st, c0 + col_of(slot), width);
         }
     }
-    __device__ __forceinline__ void store(unsigned char *lds) const {
+    template <int NP, typename F> __device__ __forceinline__ void put(unsigned char *lds, int tid, F cut) {
+        const bool whole = live >= ROWS && c0 + W <= width;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int slot = int(threadIdx.x) + 256 * i, at = slot / 128 * kBlk + block_at(slot % 128 / 4, slot % 4);
-            const auto f = pieces(x[i]);
+            const int slot = tid + 256 * i, at = slot / 128 * kBlk + block_at(slot % 128 / 4, slot % 4);
+            if (!whole) eight_mask(x[i], c0 + col_of(slot), width, row_of(slot) < live);
+            const Frag<NP> f = cut(x[i], row_of(slot));
 #pragma unroll
-            for (int n = 0; n < kPieces<T>; ++n) *reinterpret_cast<db8 *>(lds + n * kPlane + at) = f.p[n];
+            for (int n = 0; n < NP; ++n) *reinterpret_cast<db8 *>(lds + n * kPlane + at) = f.p[n];
         }
+    }
+    __device__ __forceinline__ void store(unsigned char *lds, int tid) {
+        put<kPieces<T>>(lds, tid, [](const Eight<T> &e, int) { return pieces(e); });
     }
     // ... each row times its weight, in three pieces.
-    __device__ __forceinline__ void store_weighted(unsigned char *lds, const float *w) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int slot = int(threadIdx.x) + 256 * i, blk = slot / 128, at = blk * kBlk + block_at(slot % 128 / 4, slot % 4);
-            const float f = w[blk / WB * 32 + slot % 128 / 4];
+    __device__ __forceinline__ void store_weighted(unsigned char *lds, const float *w, int tid) {
+        put<3>(lds, tid, [w](const Eight<T> &e, int row) {
             dt4 a, b;
-            eight_values(x[i], a, b);
-            const Frag<3> s = split<3>(a * f, b * f);
-#pragma unroll
-            for (int n = 0; n < 3; ++n) *reinterpret_cast<db8 *>(lds + n * kPlane + at) = s.p[n];
-        }
+            eight_values(e, a, b);
+            return split<3>(a * w[row], b * w[row]);
+        });
     }
 };
 

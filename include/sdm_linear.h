@@ -18,8 +18,8 @@ extern "C" {
  *     S = exp(g) S + k v,  out = scale q S
  * (the gated delta rule without its correction). Value head h reads key head
  * h / (value_heads / key_heads). head_dim and value_dim are at most 256, tokens at
- * most 2^30, P * Hv * ceil(K * V / 256) and P * Hv * (T / 64 + 1) * ceil(max(K, V) / 64) below
- * 2^24; SDM_ERR_RANGE past these limits (sdm_linear_attention_step: head_dim at most 256 and
+ * most 2^30, P * Hv * ceil(K * V / 256) below 2^24 and P * Hv * (T / 64 + 4) * ceil(max(K, V) / 64)
+ * below 2^23; SDM_ERR_RANGE past these limits (sdm_linear_attention_step: head_dim at most 256 and
  * value_dim 65536 as in sdm_gated_delta_step, with that function's limits).
  *
  * log_decay: device float32 [Hv], a decay for each head (decay_per_token 0), or [P, T, Hv],
