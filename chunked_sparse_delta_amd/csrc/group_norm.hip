@@ -13,6 +13,8 @@
 //  - Split: longer samples are cut into blocks of rows; one kernel leaves each block's sums, the next joins them and reads the rows again.
 // Statistics: a thread's mean and sum of squared differences from it, joined with their counts (no difference of large sums).
 // All sums run in float32 in a fixed order: results are the same from run to run.
+#include <type_traits>
+
 #include "host.h"
 #include "norm_vec.h"
 
@@ -67,7 +69,9 @@ template <int V> __device__ __forceinline__ void gn_params(const void *p, bool f
     norm_get<float, V>(static_cast<const float *>(p) + c, 0, left, none, o);
 }
 
-__device__ __forceinline__ float gn_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+// 1 / (1 + 2^(-z / log 2)): the exponent's rounding, 2^-24 of it, is |z| 2^-24 of a value that falls as e^z: at most 2^-24 in z sigmoid(z).
+// (With expf, whose instructions made the forward's time, 8192 x 4096 took 56 us; so 36.)
+__device__ __forceinline__ float gn_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z)); }
 __device__ __forceinline__ float gn_phi(float z) { return 0.5f * erfcf(-0.70710678f * z); }
 
 template <int V> __device__ __forceinline__ void gn_act(int act, float (&z)[V]) {
@@ -135,6 +139,27 @@ struct GnStat {
 };
 __device__ __forceinline__ GnStat gn_shuffle(const GnStat &s, int m) { return {__shfl_xor(s.n, m, 64), __shfl_xor(s.mean, m, 64), __shfl_xor(s.m2, m, 64)}; }
 
+// The sum over `lanes` (a power of two) neighbouring lanes, for each of them: within rows of 16 by register moves, then by
+// swapped halves.
+__device__ __forceinline__ float gn_lanes_sum(float x, int lanes) {
+    auto moved = [](float y, auto ctrl) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(y), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    if (lanes >= 2) x += moved(x, std::integral_constant<int, 0xB1>{});      // lane ^ 1
+    if (lanes >= 4) x += moved(x, std::integral_constant<int, 0x4E>{});      // lane ^ 2
+    if (lanes >= 8) x += moved(x, std::integral_constant<int, 0x141>{});     // the other four of eight
+    if (lanes >= 16) x += moved(x, std::integral_constant<int, 0x140>{});    // the other eight of a row
+    if (lanes >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if (lanes >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return x;
+}
+
 // ---- resident --------------------------------------------------------------------------------------------------------
 
 // LDS of the joins: per thread (kVectors) or per channel and thread row (kChannels), and per group of every sample.
@@ -179,7 +204,10 @@ template <typename T, int NT, int ITEMS, int MODE> __global__ __launch_bounds__(
             for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
                 for (int j = 0; j < V; ++j) s += x[i][j];
-            GnStat t{float(live * V), live > 0 ? s / float(live * V) : 0.0f, 0.0f};
+            // kShuffle: a group's lanes hold equally many rows, so that plain sums over them do
+            const int count = MODE == kShuffle ? live * D : live * V;
+            if (MODE == kShuffle) s = gn_lanes_sum(s, a.p.lanes);
+            GnStat t{float(count), count > 0 ? s / float(count) : 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
@@ -188,7 +216,7 @@ template <typename T, int NT, int ITEMS, int MODE> __global__ __launch_bounds__(
                     if (i < live) t.m2 = fmaf(d, d, t.m2);
                 }
             if constexpr (MODE == kShuffle) {
-                for (int m = a.p.lanes / 2; m > 0; m >>= 1) t.add(gn_shuffle(t, m));
+                t.m2 = gn_lanes_sum(t.m2, a.p.lanes);
             } else {
                 __shared__ GnLds<MODE, NT, V> s;
                 s.a[threadIdx.x] = t.mean;
@@ -375,10 +403,8 @@ template <typename T, int NT, int ITEMS, int MODE> __global__ __launch_bounds__(
                 t2 += c2[j];
             }
             if constexpr (MODE == kShuffle) {
-                for (int m = a.p.lanes / 2; m > 0; m >>= 1) {
-                    t1 += __shfl_xor(t1, m, 64);
-                    t2 += __shfl_xor(t2, m, 64);
-                }
+                t1 = gn_lanes_sum(t1, a.p.lanes);
+                t2 = gn_lanes_sum(t2, a.p.lanes);
             } else {
                 s.a[threadIdx.x] = t1;
                 s.b[threadIdx.x] = t2;
@@ -406,10 +432,8 @@ template <typename T, int NT, int ITEMS, int MODE> __global__ __launch_bounds__(
                     t1 += s.a[from];
                     t2 += s.b[from];
                 }
-                for (int m = a.p.lanes / 2; m > 0; m >>= 1) {
-                    t1 += __shfl_xor(t1, m, 64);
-                    t2 += __shfl_xor(t2, m, 64);
-                }
+                t1 = gn_lanes_sum(t1, a.p.lanes);
+                t2 = gn_lanes_sum(t2, a.p.lanes);
                 if (lane == 0) {
                     s.ga[g] = t1;
                     s.gb[g] = t2;
@@ -637,27 +661,41 @@ template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_bwd_sums_
     }
 }
 
-// A sample's sums of each channel (into its first block's place) and, weighted, of each group: sums[sample][G][2]. A workgroup per group.
+// A sample's sums of each channel (into its first block's place) and, weighted, of each group: sums[sample][G][2]. A workgroup per
+// group: its threads share the group's channels, up to 256 at a time, and the blocks.
 __global__ __launch_bounds__(256) void gn_bwd_join_kernel(GnArgs a, float *sums) {
     __shared__ float s1[256], s2[256];
+    const int at_once = min(a.D, 256), shares = 256 / at_once, mine = int(threadIdx.x) / at_once, i0 = int(threadIdx.x) % at_once;
     for (int64_t to = blockIdx.x; to < a.N * a.G; to += gridDim.x) {
         const int64_t n = to / a.G;
         const int g = int(to % a.G);
         float t1 = 0.0f, t2 = 0.0f;
-        for (int i = threadIdx.x; i < a.D; i += 256) {
-            const int c = g * a.D + i;
+        for (int i = i0; i < a.D + i0; i += at_once) {      // every thread as often
+            const int c = g * a.D + min(i, a.D - 1);
             float *p = a.part + n * a.p.blocks * 2 * a.C + c;
             float u2 = 0.0f, u1 = 0.0f;
-#pragma unroll 8
-            for (int k = 0; k < a.p.blocks; ++k) {
-                u2 += p[int64_t(k) * 2 * a.C];
-                u1 += p[int64_t(k) * 2 * a.C + a.C];
+            if (mine < shares) {
+#pragma unroll 4
+                for (int k = mine; k < a.p.blocks; k += shares) {
+                    u2 += p[int64_t(k) * 2 * a.C];
+                    u1 += p[int64_t(k) * 2 * a.C + a.C];
+                }
             }
-            p[0] = u2;
-            p[a.C] = u1;
-            const float w = !a.weight ? 1.0f : a.w_f32 ? static_cast<const float *>(a.weight)[c] : to_f32(static_cast<const bf16 *>(a.weight)[c]);
-            t1 = fmaf(w, u1, t1);
-            t2 = fmaf(w, u2, t2);
+            __syncthreads();
+            s1[threadIdx.x] = u1;
+            s2[threadIdx.x] = u2;
+            __syncthreads();
+            if (mine == 0 && i < a.D) {
+                for (int m = 1; m < shares; ++m) {
+                    u1 += s1[m * at_once + i0];
+                    u2 += s2[m * at_once + i0];
+                }
+                p[0] = u2;
+                p[a.C] = u1;
+                const float w = !a.weight ? 1.0f : a.w_f32 ? static_cast<const float *>(a.weight)[c] : to_f32(static_cast<const bf16 *>(a.weight)[c]);
+                t1 = fmaf(w, u1, t1);
+                t2 = fmaf(w, u2, t2);
+            }
         }
         __syncthreads();
         s1[threadIdx.x] = t1;
@@ -803,14 +841,15 @@ GnPlan gn_plan(int64_t N, int64_t L, int C, int G, int V, bool bwd) {
     p.blocks = int((L + p.block_rows - 1) / p.block_rows);
     return p;
 }
-// Workgroups of a resident tile: each takes samples in turn.
-unsigned gn_grid(const GnPlan &p, int64_t N) {
-    const int64_t blocks = (N + p.spw - 1) / p.spw, want = (p.threads == 256 ? 2048 : 512) / p.tiles;
+// Workgroups of a resident tile: each takes samples in turn. The backward's, half as many as fill the device, leave a row of
+// sums each (8192 x 4096 bfloat16: 2048 took 57 + 6 us, 1024 52 + 4, 512 61 + 4).
+unsigned gn_grid(const GnPlan &p, int64_t N, bool bwd) {
+    const int64_t blocks = (N + p.spw - 1) / p.spw, want = (p.threads == 256 ? (bwd ? 1024 : 2048) : 512) / p.tiles;
     return unsigned(blocks < want ? blocks : want < 1 ? 1 : want);
 }
 
 template <bool BWD, typename T, int NT, int ITEMS, int MODE> hipError_t gn_go(const GnArgs &a, hipStream_t st) {
-    const dim3 grid(gn_grid(a.p, a.N), unsigned(a.p.tiles));
+    const dim3 grid(gn_grid(a.p, a.N, BWD), unsigned(a.p.tiles));
     if constexpr (BWD) hipLaunchKernelGGL((gn_bwd_kernel<T, NT, ITEMS, MODE>), grid, dim3(NT), 0, st, a);
     else hipLaunchKernelGGL((gn_fwd_kernel<T, NT, ITEMS, MODE>), grid, dim3(NT), 0, st, a);
     return hipGetLastError();
@@ -838,7 +877,7 @@ template <bool BWD, typename T> hipError_t gn_resident(const GnArgs &a, hipStrea
 }
 
 size_t gn_floats(int64_t N, int C, int G, const GnPlan &p, bool bwd) {
-    if (p.items > 0) return bwd ? size_t(gn_grid(p, N)) * size_t(C) * 2 : 0;
+    if (p.items > 0) return bwd ? size_t(gn_grid(p, N, true)) * size_t(C) * 2 : 0;
     if (!bwd) return size_t(N) * size_t(p.blocks) * size_t(p.gt > 0 ? G : p.tiles) * 2;
     return size_t(N) * (size_t(p.blocks) * size_t(C) * 2 + size_t(G) * 2);
 }
@@ -860,7 +899,7 @@ template <typename T> hipError_t gn_bwd(const GnArgs &a, bool sums, void *dw, vo
     if (a.N == 0) {     // no rows: the reductions write zeros
     } else if (a.p.items > 0) {
         if ((e = gn_resident<true, T>(a, st)) != hipSuccess) return e;
-        count = gn_grid(a.p, a.N);
+        count = gn_grid(a.p, a.N, true);
         stride = a.C;
         second = count * a.C;
     } else {

@@ -10,7 +10,8 @@
 // e^{G_end - G_j} of the tokens' part in the end state. With r_i the readings' share of token i but its own pair (i, i), c_j the
 // same of j as a key (both from linear_attend.h), dG_i = r_i - c_i and dG_end has <S1, dS1> besides, so
 //     dg_m = sum_{i >= m} (r_i - c_i) + <S1, dS1>
-// over the segment: the sums that cancel span one segment, in 64 bits, and leave out what any decay leaves alone.
+// over the segment: the sums that cancel span one segment, in 64 bits, and leave out what any decay leaves alone. At the segment's
+// start this has to be <S0, dS0>: what it misses, the roundings of all the shares, is spread over the segment, which halves it.
 #include "linear_attend.h"
 
 namespace sdm {
@@ -130,7 +131,7 @@ struct ScanArgs {
     const float *first;      // [ph][KV]: the state it begins with, or null
     float *last;             // [ph][KV]: the state it ends with, or null
     const float *with;       // backward: the forward's states [ph][segs + 1][KV], or null
-    float *dots;             // backward: [ph][segs][parts]
+    float *dots;             // backward: [ph][segs + 1][parts]
     const int32_t *valid;
     int32_t T, Hv, KV, segs, slots, seg_tokens, parts;
 };
@@ -148,6 +149,18 @@ template <int N, bool BACK> __global__ __launch_bounds__(256) void lin_scan_kern
     float *S = a.S + int64_t(ph) * a.slots * a.KV + i;
     const float *with = BACK && a.with ? a.with + (int64_t(ph) * (a.segs + 1) + 1) * a.KV + i : nullptr;
     const float *decay = a.decay + int64_t(ph) * a.segs;
+    // <x, y> of the wavefront's elements at the start of segment m
+    auto put_dot = [&](int m, raw x, raw y) {
+        float dot = 0.0f;
+        if (in) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) dot = fmaf(x[e], y[e], dot);
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
+        if ((threadIdx.x & 63) == 0)
+            a.dots[(int64_t(ph) * (a.segs + 1) + m) * a.parts + blockIdx.x % blocks * 4 + (threadIdx.x >> 6)] = dot;
+    };
     raw s = {};
     if (in && a.first) s = *reinterpret_cast<const raw *>(a.first + int64_t(ph) * a.KV + i);
     for (int m0 = 0; m0 < live; m0 += AHEAD) {
@@ -164,17 +177,7 @@ template <int N, bool BACK> __global__ __launch_bounds__(256) void lin_scan_kern
         for (int j = 0; j < AHEAD; ++j) {
             const int m = BACK ? live - 1 - m0 - j : m0 + j;
             if (m0 + j >= live) break;
-            if (BACK && with) {
-                float dot = 0.0f;
-                if (in) {
-#pragma unroll
-                    for (int e = 0; e < N; ++e) dot = fmaf(o[j][e], s[e], dot);
-                }
-#pragma unroll
-                for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d, 64);
-                if ((threadIdx.x & 63) == 0)
-                    a.dots[(int64_t(ph) * a.segs + m) * a.parts + blockIdx.x % blocks * 4 + (threadIdx.x >> 6)] = dot;
-            }
+            if (BACK && with) put_dot(m + 1, o[j], s);
             if (in) {
                 *reinterpret_cast<raw *>(S + int64_t(m) * a.KV) = s;
                 const float d = decay[m];
@@ -182,6 +185,11 @@ template <int N, bool BACK> __global__ __launch_bounds__(256) void lin_scan_kern
                 for (int e = 0; e < N; ++e) s[e] = fmaf(d, s[e], u[j][e]);
             }
         }
+    }
+    if (BACK && with && live > 0) {
+        raw x = {};
+        if (in) x = *reinterpret_cast<const raw *>(with - a.KV);
+        put_dot(0, x, s);
     }
     if (!in) return;
     if (!BACK) *reinterpret_cast<raw *>(S + int64_t(live) * a.KV) = s;
@@ -211,14 +219,19 @@ __global__ __launch_bounds__(256) void lin_gate_grad_kernel(GateGradArgs a) {
     __shared__ double buf[4];
     const int seg = blockIdx.x % a.segs, ph = blockIdx.x / a.segs, h = ph % a.Hv, p = ph / a.Hv, tid = threadIdx.x;
     const int s0 = seg * a.seg_tokens, live = min(a.seg_tokens, lin_valid(a.valid, p, a.T) - s0), t = s0 + tid;
-    double tail = 0.0, d = 0.0;
+    double head = 0.0, tail = 0.0, d = 0.0;     // at the segment's start and end
     if (live > 0)
-        for (int i = tid; i < a.parts; i += 256) tail += a.dots[(int64_t(ph) * a.segs + seg) * a.parts + i];
+        for (int i = tid; i < a.parts; i += 256) {
+            const float *at = a.dots + (int64_t(ph) * (a.segs + 1) + seg) * a.parts + i;
+            head += at[0];
+            tail += at[a.parts];
+        }
     if (tid < live)
         for (int s = 0; s < a.slices; ++s) {
             const int64_t at = (int64_t(s) * a.P * a.Hv + ph) * a.T + t;
             d += double(a.rows[at]) - double(a.cols[at]);
         }
+    head = block_sum(head, buf);
     tail = block_sum(tail, buf);
     const double all = block_sum(d, buf);
     double before = d;       // the sum up to this token
@@ -231,7 +244,7 @@ __global__ __launch_bounds__(256) void lin_gate_grad_kernel(GateGradArgs a) {
     if ((tid & 63) == 63) buf[tid >> 6] = before;
     __syncthreads();
     for (int w = 0; w < tid >> 6; ++w) before += buf[w];
-    const double g = tid < live ? tail + (all - before + d) : 0.0;
+    const double g = tid < live ? tail + (all - before + d) + (head - (tail + all)) * double(live - tid) / double(live) : 0.0;
     if (a.g) {
         if (tid < a.seg_tokens && t < a.T) a.g[(int64_t(p) * a.T + t) * a.Hv + h] = float(g);
     } else {

@@ -105,7 +105,7 @@ size_t layout(const sdm_delta_shape *s, int what, LinWs *ws, void *base) {
         const size_t heads = size_t(s->streams) * size_t(s->value_heads), segs = size_t(ws->segs);
         const size_t gates = size_t(lin_slices(s->head_dim)) * heads * size_t(s->tokens);
         ws->dS = t.take<float>(heads * segs * size_t(s->head_dim) * size_t(s->value_dim));
-        ws->dots = t.take<float>(heads * segs * size_t(lin_dot_parts(s->head_dim, s->value_dim)));
+        ws->dots = t.take<float>(heads * (segs + 1) * size_t(lin_dot_parts(s->head_dim, s->value_dim)));
         ws->rows = t.take<float>(gates);
         ws->cols = t.take<float>(gates);
         ws->sums = t.take<double>(heads * segs);

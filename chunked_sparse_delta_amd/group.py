@@ -103,13 +103,20 @@ def group_norm_fwd(x: torch.Tensor, groups: int, weight: torch.Tensor | None = N
                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Group norm and activation. Returns (y, mean, rstd); mean and rstd float32 [N, groups] are what group_norm_bwd needs.
     ``workspace`` (uint8, GPU, group_norm_workspace_bytes) is allocated if omitted and needed."""
+    plan = _inputs(x, groups, weight, bias, activation, eps, valid_rows)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype, plan[3])
+    return _values(plan, x, groups, weight, bias, valid_rows, out, workspace, stream)
+
+
+def _values(plan, x, groups, weight, bias, valid_rows, out=None, workspace=None, stream=None):
+    """group_norm_fwd of checked arguments."""
     lib = _load()
-    shape, rows, _, dev, index = _inputs(x, groups, weight, bias, activation, eps, valid_rows)
+    shape, rows, _, dev, index = plan
     if out is None:
         out = _new(x.shape, x.dtype, dev, stream)     # dense whatever x's strides are
-    else:
-        _need(out, "out", x.shape, x.dtype, dev)
-    mean, rstd = (_new((x.shape[0], groups), torch.float32, dev, stream) for _ in range(2))
+    size = (x.shape[0], groups)
+    mean, rstd = _new(size, torch.float32, dev, stream), _new(size, torch.float32, dev, stream)
     workspace = _scratch(lib, shape, 0, workspace, dev, stream)
     rc = lib.sdm_group_norm_fwd(shape, *rows, _ptr(weight), _ptr(bias), _ptr(valid_rows), out.data_ptr(), mean.data_ptr(),
                                 rstd.data_ptr(), _exec(stream, index, workspace))
@@ -124,19 +131,22 @@ def group_norm_bwd(grad_out: torch.Tensor, x: torch.Tensor, groups: int, mean: t
                    workspace: torch.Tensor | None = None, stream=None) -> dict:
     """Backward of group_norm_fwd: dict(x, weight, bias) of the gradients named in ``need``; the weight's and bias's in
     their dtype (x's where both are None)."""
-    lib = _load()
-    shape, rows, wdtype, dev, index = _inputs(x, groups, weight, bias, activation, eps, valid_rows)
+    plan = _inputs(x, groups, weight, bias, activation, eps, valid_rows)
+    dev = plan[3]
     _need(grad_out, "grad_out", x.shape, x.dtype, dev)
     for t, n in ((mean, "mean"), (rstd, "rstd")):
         _need(t, n, (x.shape[0], groups), torch.float32, dev)
-    g = {}
     for n in need:
-        if n == "x":
-            g[n] = _new(x.shape, x.dtype, dev, stream)
-        elif n in ("weight", "bias"):
-            g[n] = _new((x.shape[-1],), wdtype, dev, stream)
-        else:
+        if n not in ("x", "weight", "bias"):
             raise ValueError(f"need names x, weight and bias, got {need}")
+    return _grads(plan, grad_out, x, mean, rstd, weight, bias, valid_rows, need, workspace, stream)
+
+
+def _grads(plan, grad_out, x, mean, rstd, weight, bias, valid_rows, need, workspace=None, stream=None):
+    """group_norm_bwd of checked arguments."""
+    lib = _load()
+    shape, rows, wdtype, dev, index = plan
+    g = {n: _new(x.shape, x.dtype, dev, stream) if n == "x" else _new(x.shape[-1:], wdtype, dev, stream) for n in need}
     workspace = _scratch(lib, shape, 1, workspace, dev, stream)
     rc = lib.sdm_group_norm_bwd(shape, grad_out.data_ptr(), *rows, _ptr(weight), _ptr(bias), _ptr(valid_rows), mean.data_ptr(),
                                 rstd.data_ptr(), _ptr(g.get("x")), _ptr(g.get("weight")), _ptr(g.get("bias")),
@@ -149,19 +159,18 @@ def group_norm_bwd(grad_out: torch.Tensor, x: torch.Tensor, groups: int, mean: t
 class _GroupNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, groups, weight, bias, activation, eps, valid_rows):
-        y, mean, rstd = group_norm_fwd(x, groups, weight, bias, activation=activation, eps=eps, valid_rows=valid_rows)
+        ctx.plan = plan = _inputs(x, groups, weight, bias, activation, eps, valid_rows)
+        y, mean, rstd = _values(plan, x, groups, weight, bias, valid_rows)
         ctx.save_for_backward(x, weight, bias, valid_rows, mean, rstd)
-        ctx.how = groups, activation, eps
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
         x, weight, bias, valid, mean, rstd = ctx.saved_tensors
-        groups, activation, eps = ctx.how
-        need = tuple(n for n, on in zip(("x", "weight", "bias"), (ctx.needs_input_grad[0], *ctx.needs_input_grad[2:4])) if on)
-        g = group_norm_bwd(grad_out.contiguous(), x, groups, mean, rstd, weight, bias, activation=activation, eps=eps,
-                           valid_rows=valid, need=need)
+        wants = ctx.needs_input_grad
+        need = [n for n, on in (("x", wants[0]), ("weight", wants[2]), ("bias", wants[3])) if on]
+        g = _grads(ctx.plan, grad_out.contiguous(), x, mean, rstd, weight, bias, valid, need)
         return g.get("x"), None, g.get("weight"), g.get("bias"), None, None, None
 
 

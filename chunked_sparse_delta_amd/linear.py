@@ -81,12 +81,11 @@ def linear_attention_kept_bytes(P: int, T: int, Hk: int, Hv: int, K: int, V: int
 
 
 def _buffer(t, name, least, dev):
-    """A caller's buffer for what a forward keeps."""
+    """Checks a caller's buffer for what a forward keeps."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev or not t.is_contiguous() or t.numel() * t.element_size() < least:
         raise ValueError(f"{name} must be a contiguous tensor of {least} bytes on {dev}")
-    return t.data_ptr()
 
 
 def linear_attention_fwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, q: torch.Tensor, *,
@@ -100,7 +99,8 @@ def linear_attention_fwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: tor
     omitted. ``kept`` (uint8, GPU, linear_attention_kept_bytes) gets what linear_attention_bwd(kept=kept) then does not
     compute again."""
     lib = _load()
-    full, head, dev, index = _inputs(k, v, log_decay, q, scale, valid_tokens)
+    plan = _inputs(k, v, log_decay, q, scale, valid_tokens)
+    full, head, dev, _ = plan
     if state is not None:
         _need(state, "state", full, torch.float32, dev)
     if state_out is None:
@@ -108,14 +108,22 @@ def linear_attention_fwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: tor
     else:
         _need(state_out, "state_out", full, torch.float32, dev)
     out = _out(out, v, stream)
-    keep = 0 if kept is None else _buffer(kept, "kept", lib.sdm_linear_attention_kept_bytes(head[0]), dev)
+    if kept is not None:
+        _buffer(kept, "kept", lib.sdm_linear_attention_kept_bytes(head[0]), dev)
+    _values(plan, state, state_out, valid_tokens, out, kept, workspace, stream)
+    return out
+
+
+def _values(plan, state, state_out, valid_tokens, out, kept, workspace=None, stream=None):
+    """linear_attention_fwd of checked arguments."""
+    lib = _load()
+    _, head, dev, index = plan
     if workspace is None and kept is None:
         workspace = _new((max(lib.sdm_linear_attention_workspace_bytes(head[0], 0), 256),), torch.uint8, dev, stream)
-    rc = lib.sdm_linear_attention_fwd(*head, _ptr(state), _ptr(state_out), _ptr(valid_tokens), out.data_ptr(), keep,
+    rc = lib.sdm_linear_attention_fwd(*head, _ptr(state), _ptr(state_out), _ptr(valid_tokens), out.data_ptr(), _ptr(kept),
                                       _exec(stream, index, workspace))
     if rc:
         _check_rc(lib, rc)
-    return out
 
 
 def linear_attention_step(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -157,8 +165,8 @@ def linear_attention_bwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: tor
     log_decay, q): k, v and q (always there) in the inputs' dtype (sums over sharing heads in float32), state and log_decay
     float32, where ``need`` names them. ``kept``: what a linear_attention_fwd(kept=...) with the same inputs left; without
     it the states are computed again."""
-    lib = _load()
-    full, head, dev, index = _inputs(k, v, log_decay, q, scale, valid_tokens)
+    plan = _inputs(k, v, log_decay, q, scale, valid_tokens)
+    full, head, dev, _ = plan
     _need(grad_out, "grad_out", v.shape, v.dtype, dev)
     for t, n in ((state, "state"), (grad_state, "grad_state")):
         if t is not None:
@@ -166,15 +174,25 @@ def linear_attention_bwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: tor
     for n in need:
         if n not in ("state", "k", "v", "log_decay", "q"):
             raise ValueError(f"need names state, k, v, log_decay and q, got {need}")
+    if kept is not None:
+        _buffer(kept, "kept", _load().sdm_linear_attention_kept_bytes(head[0]), dev)
+    return _grads(plan, state, k, v, log_decay, q, grad_out, grad_state, valid_tokens, kept, need, workspace, stream)
+
+
+def _grads(plan, state, k, v, log_decay, q, grad_out, grad_state, valid_tokens, kept, need, workspace=None, stream=None):
+    """linear_attention_bwd of checked arguments."""
+    lib = _load()
+    full, head, dev, index = plan
     f32 = torch.float32
-    g = {n: _new(size, dtype, dev, stream) for n, size, dtype in (
-        ("state", full, f32), ("k", k.shape, k.dtype), ("v", v.shape, v.dtype), ("log_decay", log_decay.shape, f32),
-        ("q", q.shape, q.dtype)) if n in need or n in ("k", "v", "q")}
-    keep = 0 if kept is None else _buffer(kept, "kept", lib.sdm_linear_attention_kept_bytes(head[0]), dev)
+    g = {"k": _new(k.shape, k.dtype, dev, stream), "v": _new(v.shape, v.dtype, dev, stream), "q": _new(q.shape, q.dtype, dev, stream)}
+    if "state" in need:
+        g["state"] = _new(full, f32, dev, stream)
+    if "log_decay" in need:
+        g["log_decay"] = _new(log_decay.shape, f32, dev, stream)
     if workspace is None:
         n = lib.sdm_linear_attention_workspace_bytes(head[0], 1 if kept is None else 2)
         workspace = _new((max(n, 256),), torch.uint8, dev, stream)
-    rc = lib.sdm_linear_attention_bwd(*head, _ptr(state), _ptr(valid_tokens), grad_out.data_ptr(), _ptr(grad_state), keep,
+    rc = lib.sdm_linear_attention_bwd(*head, _ptr(state), _ptr(valid_tokens), grad_out.data_ptr(), _ptr(grad_state), _ptr(kept),
                                       _GRADS(g["q"].data_ptr(), g["k"].data_ptr(), g["v"].data_ptr(), 0,
                                              _ptr(g.get("log_decay")) or 0, _ptr(g.get("state")) or 0),
                                       _exec(stream, index, workspace))
@@ -186,16 +204,18 @@ def linear_attention_bwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: tor
 class _LinearAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, state, k, v, log_decay, q, scale, valid_tokens, recompute):
-        P, T, Hv, V = v.shape
-        Hk, K = k.shape[2:]
-        final = torch.empty((P, Hv, K, V), dtype=torch.float32, device=v.device)
+        ctx.plan = plan = _inputs(k, v, log_decay, q, scale, valid_tokens)
+        full, head, dev, _ = plan
+        if state is not None:
+            _need(state, "state", full, torch.float32, dev)
+        final = torch.empty(full, dtype=torch.float32, device=dev)
         kept = None
         if not recompute and any(ctx.needs_input_grad):
-            n = linear_attention_kept_bytes(P, T, Hk, Hv, K, V, v.dtype)
-            kept = torch.empty(max(n, 256), dtype=torch.uint8, device=v.device)     # 0: the call itself reports why
-        out = linear_attention_fwd(state, k, v, log_decay, q, scale=scale, valid_tokens=valid_tokens, state_out=final, kept=kept)
+            n = _load().sdm_linear_attention_kept_bytes(head[0])
+            kept = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)     # 0: the call itself reports why
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        _values(plan, state, final, valid_tokens, out, kept)
         ctx.save_for_backward(state, k, v, log_decay, q, valid_tokens, kept)
-        ctx.scale = scale
         ctx.set_materialize_grads(False)
         return out, final
 
@@ -207,11 +227,11 @@ class _LinearAttention(torch.autograd.Function):
             return (None,) * 8
         go = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if grad_out is None else grad_out.contiguous()
         gs = None if grad_state is None else grad_state.contiguous()
-        names = ("state", "k", "v", "log_decay", "q")
-        need = tuple(n for n, on in zip(names, ctx.needs_input_grad) if on)
-        g = linear_attention_bwd(state, k, v, log_decay, q, go, grad_state=gs, scale=ctx.scale, valid_tokens=valid, kept=kept,
-                                 need=need)
-        return (*(g[n] if on else None for n, on in zip(names, ctx.needs_input_grad)), None, None, None)
+        wants = ctx.needs_input_grad
+        need = [n for n, on in (("state", wants[0]), ("log_decay", wants[3])) if on]
+        g = _grads(ctx.plan, state, k, v, log_decay, q, go, gs, valid, kept, need)
+        return (g.get("state"), g["k"] if wants[1] else None, g["v"] if wants[2] else None, g.get("log_decay"),
+                g["q"] if wants[4] else None, None, None, None)
 
 
 def linear_attention(state, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, q: torch.Tensor, *,
