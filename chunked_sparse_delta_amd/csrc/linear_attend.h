@@ -15,7 +15,7 @@
 // 32 rows of M, while the next one is on its way through registers.
 #pragma once
 
-#include "linear_tile.h"
+#include "linear_state.h"
 
 namespace sdm {
 
@@ -57,7 +57,7 @@ template <typename T, int XP, int ZW, bool KEYS, bool EVEN> struct AttendCfg {
 };
 
 template <typename T, int XP, int ZW, bool KEYS, bool EVEN>
-__global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
+__device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block) {
     using C = AttendCfg<T, XP, ZW, KEYS, EVEN>;
     constexpr int NI = C::NI, NQ = C::NQ, QT = C::QT, KT = C::KT, XB = XP / 32, ZB = ZW / 32, TB = KT / 32;
     using Y = typename C::Y;
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
     // What reads the same keys, values and states goes to one XCD (blocks are dealt to the eight in turn), where there is enough for
     // all of them: the tiles and slices of a segment, of the value heads that share a key head.
     const int unit = slices * seg_tiles * (KEYS ? 1 : group), units = a.P * a.Hk * a.segs, xcds = lin_xcds(units);
-    const int at_xcd = blockIdx.x / xcds, u = at_xcd / unit * xcds + int(blockIdx.x) % xcds, in_unit = at_xcd % unit;
+    const int at_xcd = block / xcds, u = at_xcd / unit * xcds + int(block) % xcds, in_unit = at_xcd % unit;
     if (u >= units) return;
     const int seg = u % a.segs, khead = u / a.segs % a.Hk, p = u / a.segs / a.Hk;
     const int slice = in_unit % slices, oh = KEYS ? khead : khead * group + in_unit / slices / seg_tiles;
@@ -358,35 +358,59 @@ __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
     }
 }
 
-template <typename T, int XP, int ZW, bool KEYS, bool EVEN> hipError_t attend_go(const AttendArgs &a, int sides, hipStream_t st) {
+template <typename T, int XP, int ZW, bool KEYS, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
+    lin_attend<T, XP, ZW, KEYS, EVEN>(a, blockIdx.x);
+}
+// A sequence of one segment: its readings and, by the workgroups from `attends` on, its end state. (One launch for two: of 200
+// tokens of 4 heads of 64 x 64, 13.6 us and 9 one after the other.)
+template <typename T, int XP, int ZW, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_single_kernel(AttendArgs a, StateArgs s, int attends) {
+    if (int(blockIdx.x) < attends) lin_attend<T, XP, ZW, false, EVEN>(a, blockIdx.x);
+    else lin_state<T, XP, ZW, EVEN>(s, int(blockIdx.x) - attends);
+}
+
+// single: the end states that go with the readings of one segment, or null.
+template <typename T, int XP, int ZW, bool KEYS, bool EVEN> hipError_t attend_go(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
     using C = AttendCfg<T, XP, ZW, KEYS, EVEN>;
     const int64_t slices = (a.side[0].z.width + ZW - 1) / ZW, unit = slices * (a.seg_tokens / C::QT) * (KEYS ? 1 : a.Hv / a.Hk);
-    const int64_t units = int64_t(a.P) * a.Hk * a.segs;
-    hipLaunchKernelGGL((lin_attend_kernel<T, XP, ZW, KEYS, EVEN>), dim3(unsigned((units + lin_xcds(units) - 1) / lin_xcds(units) * lin_xcds(units) * unit), unsigned(sides)),
-                       dim3(256), C::kLds, st, a);
+    const int64_t units = int64_t(a.P) * a.Hk * a.segs, xcds = lin_xcds(units), blocks = (units + xcds - 1) / xcds * xcds * unit;
+    if constexpr (!KEYS) {
+        if (single) {
+            constexpr size_t other = StateCfg<T, XP, ZW, EVEN>::kLds;
+            hipLaunchKernelGGL((lin_single_kernel<T, XP, ZW, EVEN>), dim3(unsigned(blocks + slices * a.P * a.Hv)), dim3(256),
+                               C::kLds > other ? C::kLds : other, st, a, *single, int(blocks));
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((lin_attend_kernel<T, XP, ZW, KEYS, EVEN>), dim3(unsigned(blocks), KEYS ? 2u : 1u), dim3(256), C::kLds, st, a);
     return hipGetLastError();
 }
-template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_even(const AttendArgs &a, int sides, hipStream_t st) {
+template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_even(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
     constexpr int vec = 16 / sizeof(T);
-    return a.K % vec == 0 && a.V % vec == 0 ? attend_go<T, XP, ZW, KEYS, true>(a, sides, st) : attend_go<T, XP, ZW, KEYS, false>(a, sides, st);
+    return a.K % vec == 0 && a.V % vec == 0 ? attend_go<T, XP, ZW, KEYS, true>(a, single, st) : attend_go<T, XP, ZW, KEYS, false>(a, single, st);
 }
-template <typename T, int XP, bool KEYS> hipError_t attend_slices(const AttendArgs &a, int sides, hipStream_t st) {
-    return lin_slice(a.side[0].z.width) == 64 ? attend_even<T, XP, 64, KEYS>(a, sides, st) : attend_even<T, XP, 128, KEYS>(a, sides, st);
+template <typename T, int XP, bool KEYS> hipError_t attend_slices(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
+    return lin_slice(a.side[0].z.width) == 64 ? attend_even<T, XP, 64, KEYS>(a, single, st) : attend_even<T, XP, 128, KEYS>(a, single, st);
 }
-template <typename T, bool KEYS> hipError_t attend(const AttendArgs &a, int sides, hipStream_t st) {
+template <typename T, bool KEYS> hipError_t attend(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
     switch (lin_width(a.side[0].x.width)) {
-        case 64: return attend_slices<T, 64, KEYS>(a, sides, st);
-        case 128: return attend_slices<T, 128, KEYS>(a, sides, st);
-        default: return attend_slices<T, 256, KEYS>(a, sides, st);
+        case 64: return attend_slices<T, 64, KEYS>(a, single, st);
+        case 128: return attend_slices<T, 128, KEYS>(a, single, st);
+        default: return attend_slices<T, 256, KEYS>(a, single, st);
     }
 }
 template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_attr() {
-    static_assert(AttendCfg<T, XP, ZW, KEYS, true>::kLds <= 80 * 1024, "two workgroups to a compute unit");
-    auto set = [](auto kernel) {
-        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(AttendCfg<T, XP, ZW, KEYS, true>::kLds));
+    constexpr size_t bytes = AttendCfg<T, XP, ZW, KEYS, true>::kLds, other = StateCfg<T, XP, ZW, true>::kLds;
+    static_assert(bytes <= 80 * 1024 && other <= 80 * 1024, "two workgroups to a compute unit");
+    auto set = [](auto kernel, size_t n) {
+        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(n));
     };
-    const hipError_t e = set(&lin_attend_kernel<T, XP, ZW, KEYS, true>);
-    return e == hipSuccess ? set(&lin_attend_kernel<T, XP, ZW, KEYS, false>) : e;
+    hipError_t e = set(&lin_attend_kernel<T, XP, ZW, KEYS, true>, bytes);
+    if (e == hipSuccess) e = set(&lin_attend_kernel<T, XP, ZW, KEYS, false>, bytes);
+    if constexpr (!KEYS) {
+        if (e == hipSuccess) e = set(&lin_single_kernel<T, XP, ZW, true>, bytes > other ? bytes : other);
+        if (e == hipSuccess) e = set(&lin_single_kernel<T, XP, ZW, false>, bytes > other ? bytes : other);
+    }
+    return e;
 }
 template <typename T, bool KEYS> hipError_t attend_prepare() {
     hipError_t e = attend_attr<T, 64, 64, KEYS>();
@@ -399,8 +423,8 @@ template <typename T, bool KEYS> hipError_t attend_prepare() {
 }
 
 // One translation unit for each element type and kind (linear_attend_*.hip).
-hipError_t attend_values_bf16(const AttendArgs &a, hipStream_t st);
-hipError_t attend_values_f32(const AttendArgs &a, hipStream_t st);
+hipError_t attend_values_bf16(const AttendArgs &a, const StateArgs *single, hipStream_t st);
+hipError_t attend_values_f32(const AttendArgs &a, const StateArgs *single, hipStream_t st);
 hipError_t attend_keys_bf16(const AttendArgs &a, hipStream_t st);
 hipError_t attend_keys_f32(const AttendArgs &a, hipStream_t st);
 hipError_t attend_prepare_values_bf16();

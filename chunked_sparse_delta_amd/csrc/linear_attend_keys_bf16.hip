@@ -3,7 +3,7 @@
 
 namespace sdm {
 
-hipError_t attend_keys_bf16(const AttendArgs &a, hipStream_t st) { return attend<bf16, true>(a, 2, st); }
+hipError_t attend_keys_bf16(const AttendArgs &a, hipStream_t st) { return attend<bf16, true>(a, nullptr, st); }
 hipError_t attend_prepare_keys_bf16() { return attend_prepare<bf16, true>(); }
 
 }  // namespace sdm

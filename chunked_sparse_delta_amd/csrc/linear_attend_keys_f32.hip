@@ -3,7 +3,7 @@
 
 namespace sdm {
 
-hipError_t attend_keys_f32(const AttendArgs &a, hipStream_t st) { return attend<float, true>(a, 2, st); }
+hipError_t attend_keys_f32(const AttendArgs &a, hipStream_t st) { return attend<float, true>(a, nullptr, st); }
 hipError_t attend_prepare_keys_f32() { return attend_prepare<float, true>(); }
 
 }  // namespace sdm

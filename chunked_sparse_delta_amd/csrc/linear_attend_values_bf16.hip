@@ -3,7 +3,7 @@
 
 namespace sdm {
 
-hipError_t attend_values_bf16(const AttendArgs &a, hipStream_t st) { return attend<bf16, false>(a, 1, st); }
+hipError_t attend_values_bf16(const AttendArgs &a, const StateArgs *single, hipStream_t st) { return attend<bf16, false>(a, single, st); }
 hipError_t attend_prepare_values_bf16() { return attend_prepare<bf16, false>(); }
 
 }  // namespace sdm

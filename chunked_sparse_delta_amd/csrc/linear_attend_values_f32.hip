@@ -3,7 +3,7 @@
 
 namespace sdm {
 
-hipError_t attend_values_f32(const AttendArgs &a, hipStream_t st) { return attend<float, false>(a, 1, st); }
+hipError_t attend_values_f32(const AttendArgs &a, const StateArgs *single, hipStream_t st) { return attend<float, false>(a, single, st); }
 hipError_t attend_prepare_values_f32() { return attend_prepare<float, false>(); }
 
 }  // namespace sdm
