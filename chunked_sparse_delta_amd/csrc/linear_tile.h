@@ -83,8 +83,27 @@ __device__ __forceinline__ void eight_values(const Eight<float> &x, dt4 &a, dt4 
     a = x.a;
     b = x.b;
 }
+// split<3>, each value on its own: there an infinity or NaN would reach the other value of its pair, here another column.
+__device__ __forceinline__ Frag<3> split_apart(dt4 a, dt4 b) {
+    Frag<3> f;
+    float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        du4 w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __builtin_amdgcn_perm(__float_as_uint(x[2 * j + 1]), __float_as_uint(x[2 * j]), 0x07060302);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] -= __uint_as_float(__float_as_uint(x[j]) & 0xFFFF0000u);
+        f.p[i] = __builtin_bit_cast(db8, w);
+    }
+    du4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = f32x2_to_bf16x2(x[2 * j], x[2 * j + 1]);
+    f.p[2] = __builtin_bit_cast(db8, w);
+    return f;
+}
 __device__ __forceinline__ Frag<1> pieces(const Eight<bf16> &x) { return {{__builtin_bit_cast(db8, x.w)}}; }
-__device__ __forceinline__ Frag<3> pieces(const Eight<float> &x) { return split<3>(x.a, x.b); }
+__device__ __forceinline__ Frag<3> pieces(const Eight<float> &x) { return split_apart(x.a, x.b); }
 
 // a and b, rounded, to p[0 .. 8) of which `left` are there (EVEN: all, or none, or for float32 four).
 template <bool EVEN> __device__ __forceinline__ void eight_store(bf16 *p, int left, dt4 a, dt4 b) {
@@ -150,7 +169,7 @@ template <typename T, int ROWS, int W, bool EVEN> struct Tile {
         put<3>(lds, tid, [w](const Eight<T> &e, int row) {
             dt4 a, b;
             eight_values(e, a, b);
-            return split<3>(a * w[row], b * w[row]);
+            return split_apart(a * w[row], b * w[row]);
         });
     }
 };

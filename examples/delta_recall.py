@@ -1,10 +1,12 @@
 """Trains a small model of pre-norm gated delta layers on associative recall, then answers with it token by token.
 
-    python examples/delta_recall.py [--steps 300]
+    python examples/delta_recall.py [--steps 300] [--layer linear]
 
 A sequence is pairs (key, value) and then, again and again, one of the keys, each to be answered with its value. Training
 runs layer_norm and gated_delta_rule with their gradients. Answering runs the pairs through gated_delta_fwd once, which leaves
-each layer's state, and then one token at a time through gated_delta_step on the states in place.
+each layer's state, and then one token at a time through gated_delta_step on the states in place. With --layer linear the
+layers are linear attention with a decay for each head and a norm of each head's readings with an activation: linear_attention and
+group_norm with their gradients, then linear_attention_fwd and linear_attention_step.
 """
 
 import argparse
@@ -52,13 +54,37 @@ class DeltaLayer(nn.Module):
         return x + self.output(out.flatten(-2))
 
 
+class LinearLayer(nn.Module):
+    """x + Wo silu(heads' norm(linear attention(Wi norm(x)))), decays fixed for each head."""
+
+    def __init__(self, width, key_heads=2, value_heads=4, head_dim=32, value_dim=32):
+        super().__init__()
+        self.sizes = [key_heads * head_dim, key_heads * head_dim, value_heads * value_dim]
+        self.heads, self.shape = (key_heads, head_dim), (value_heads, value_dim)
+        self.norm = Norm(width)
+        self.inputs = nn.Linear(width, sum(self.sizes))
+        self.weight, self.bias = nn.Parameter(torch.ones(value_heads * value_dim)), nn.Parameter(torch.zeros(value_heads * value_dim))
+        self.output = nn.Linear(value_heads * value_dim, width)
+        # memories of 8, 32, 128, ... tokens
+        self.register_buffer("log_decay", torch.log1p(-0.125 * 0.25 ** torch.arange(value_heads)))
+
+    state = DeltaLayer.state
+
+    def forward(self, x, state, form):
+        q, k, v = self.inputs(self.norm(x)).split(self.sizes, -1)
+        q, k = (nn.functional.silu(t).unflatten(-1, self.heads) for t in (q, k))
+        out = form(state, k, v.unflatten(-1, self.shape), self.log_decay, q)
+        out = sdm.group_norm(out.flatten(2).flatten(0, 1), self.shape[0], self.weight, self.bias, activation="silu")
+        return x + self.output(out.unflatten(0, x.shape[:2]))
+
+
 class Model(nn.Module):
-    def __init__(self, width=128, layers=2):
+    def __init__(self, width=128, layers=2, layer=DeltaLayer):
         super().__init__()
         self.embed = nn.Embedding(2 * KEYS, width)
         # a value's token also sees the key before it: what a short convolution gives such models
         self.before = nn.Embedding(2 * KEYS, width)
-        self.layers = nn.ModuleList(DeltaLayer(width) for _ in range(layers))
+        self.layers = nn.ModuleList(layer(width) for _ in range(layers))
         self.norm, self.head = Norm(width), nn.Linear(width, KEYS)
 
     def states(self, streams, device):
@@ -75,6 +101,15 @@ def train_form(state, *inputs):
     return sdm.gated_delta_rule(None, *inputs)[0]
 
 
+def linear_train_form(state, *inputs):
+    return sdm.linear_attention(None, *inputs)[0]
+
+
+# a layer's forms: for training, for a prompt and for single tokens
+FORMS = {DeltaLayer: (train_form, sdm.gated_delta_fwd, sdm.gated_delta_step),
+         LinearLayer: (linear_train_form, sdm.linear_attention_fwd, sdm.linear_attention_step)}
+
+
 def batch(streams, pairs, asked, gen):
     """Tokens [streams, 2 pairs + asked], the token before each, and the answers to the last `asked`."""
     keys = torch.rand((streams, KEYS), generator=gen).argsort(1)[:, :pairs]
@@ -85,15 +120,15 @@ def batch(streams, pairs, asked, gen):
     return tokens, before, values.gather(1, which)
 
 
-def train(device, steps, streams=64, pairs=8, asked=15, seed=0):
+def train(device, steps, streams=64, pairs=8, asked=15, seed=0, layer=DeltaLayer):
     torch.manual_seed(seed)
     gen = torch.Generator().manual_seed(seed)
-    model = Model().to(device)
+    model = Model(layer=layer).to(device)
     opt = torch.optim.AdamW(model.parameters(), lr=2e-3)
     losses = []
     for _ in range(steps):
         tokens, before, answers = (t.to(device) for t in batch(streams, pairs, asked, gen))
-        logits = model(tokens, before, model.states(streams, device), train_form)[:, -asked:]
+        logits = model(tokens, before, model.states(streams, device), FORMS[layer][0])[:, -asked:]
         loss = nn.functional.cross_entropy(logits.flatten(0, 1), answers.flatten())
         opt.zero_grad()
         loss.backward()
@@ -107,17 +142,19 @@ def answer(model, tokens, before, asked):
     """Logits of the last `asked` tokens, one step each after one pass over the others; the states advance in place."""
     states = model.states(len(tokens), tokens.device)
     n = tokens.shape[1] - asked
-    model(tokens[:, :n], before[:, :n], states, sdm.gated_delta_fwd)
-    return torch.cat([model(tokens[:, t:t + 1], before[:, t:t + 1], states, sdm.gated_delta_step)
+    _, prompt, step = FORMS[type(model.layers[0])]
+    model(tokens[:, :n], before[:, :n], states, prompt)
+    return torch.cat([model(tokens[:, t:t + 1], before[:, t:t + 1], states, step)
                       for t in range(n, n + asked)], 1)
 
 
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=300)
+    ap.add_argument("--layer", choices=("delta", "linear"), default="delta")
     args = ap.parse_args(argv)
     device = torch.device("cuda:0")
-    model, losses = train(device, args.steps)
+    model, losses = train(device, args.steps, layer=LinearLayer if args.layer == "linear" else DeltaLayer)
     tokens, before, answers = (t.to(device) for t in batch(256, 8, 15, torch.Generator().manual_seed(1)))
     logits = answer(model, tokens, before, 15)
     right = (logits.argmax(-1) == answers).float().mean().item()

@@ -39,8 +39,8 @@ extern "C" {
  * Arithmetic: products of the inputs and of float32 quantities (24 bits, to 2^-23) accumulate
  * in float32; the state stays float32; out is rounded once. Bitwise reproducible.
  * Tokens are taken 32 at once: an infinity or NaN in a live token's k or v may reach readings
- * of up to 31 tokens before it, of the heads that read it; what an infinity reaches may be
- * NaN. Padding tokens may hold anything.
+ * of up to 31 tokens before it, of the heads that read it (from v or a state: its own column
+ * alone); what an infinity reaches may be NaN. Padding tokens may hold anything.
  */
 enum { SDM_LINEAR_FORWARD = 0, SDM_LINEAR_BACKWARD = 1, SDM_LINEAR_BACKWARD_KEPT = 2 };
 

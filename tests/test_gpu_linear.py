@@ -413,3 +413,75 @@ def test_graph(gpu):
         torch.cuda.synchronize()
         eager = [out, final, step_state, s] + list(g.values())
         assert all(torch.equal(a, b) for a, b in zip(got, eager)), i
+
+
+def test_refusals(gpu):
+    """Shapes, types and devices that do not go together are refused before anything runs."""
+    import chunked_sparse_delta_amd as sdm
+    x = on(make(1, 5, 1, 2, 8, 12, torch.float32), gpu)
+    state, k, v, g, q = (x[n] for n in NAMES)
+    bad = [
+        ((state, k, v, g[..., :1], q), ValueError), ((state, k, v, g.double(), q), TypeError), ((state, k, v, g, q[:, :4]), ValueError),
+        ((state, k, v.bfloat16(), g, q), TypeError), ((state[:, :1], k, v, g, q), ValueError), ((state, k.cpu(), v, g, q), ValueError),
+        ((state, k[..., ::2], v, g, q[..., ::2]), ValueError), ((state.bfloat16(), k, v, g, q), TypeError),
+        ((state, k, v[:, :, :1], g, torch.cat([q, q], 2)), ValueError)]
+    for args, error in bad:
+        for call in (sdm.linear_attention_fwd, sdm.linear_attention_step, sdm.linear_attention):
+            with pytest.raises(error):
+                call(*args)
+    with pytest.raises(ValueError):
+        sdm.linear_attention_fwd(state, k, v, g, q, kept=torch.empty(16, dtype=torch.uint8, device=gpu))
+    with pytest.raises(ValueError):
+        sdm.linear_attention_bwd(state, k, v, g, q, v, need=("beta",))
+    with pytest.raises(ValueError):
+        sdm.linear_attention_bwd(state, k, v, g, q, v[:, :4])
+    with pytest.raises(sdm.SdmError):
+        sdm.linear_attention_fwd(state, k, v, g, q, state_out=state, workspace=torch.empty(16, dtype=torch.uint8, device=gpu))
+    with pytest.raises(sdm.SdmError):       # value_dim past 256 for sequences
+        wide = torch.zeros(1, 5, 2, 300, device=gpu)
+        sdm.linear_attention_fwd(None, k, wide, g, q)
+    assert torch.equal(state.cpu(), make(1, 5, 1, 2, 8, 12, torch.float32)["state"])
+
+
+def test_retained_graph(gpu):
+    """The backward may run twice on what the forward kept: it only reads it."""
+    import chunked_sparse_delta_amd as sdm
+    x = {n: None if t is None else t.to(gpu).requires_grad_() for n, t in make(1, 600, 1, 2, 32, 32, torch.float32).items()}
+    out, final = sdm.linear_attention(*(x[n] for n in NAMES))
+    loss = out.square().sum() + final.sum()
+    a, b = (torch.autograd.grad(loss, [x[n] for n in NAMES], retain_graph=True) for _ in range(2))
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_terms_that_cancel(gpu, dtype):
+    """Readings and gradients whose terms cancel keep float32's bits: every sixteenth value, 2^12 times the others, meets its
+    negative one token later with the same key, so that the small ones alone are left."""
+    import chunked_sparse_delta_amd as sdm
+    dt = DT[dtype]
+    x = make(1, 128, 1, 1, 64, 64, dt, seed=21)
+    x["log_decay"] = torch.zeros(1, 128, 1)
+    big = 4096.0 * torch.randn(1, 8, 1, 64, generator=torch.Generator().manual_seed(0))
+    x["v"][:, 0::16], x["v"][:, 1::16] = big.to(dt), -big.to(dt)
+    x["k"][:, 1::16] = x["k"][:, 0::16]
+    out, final = run(gpu, x)
+    (o, s), (ao, as_) = want(x), want(x, absolute=True)
+    close(out, o, ao, dt)
+    close(final, s, as_, torch.float32)
+    # the bar on what is left, where 16 bits of the large terms would not do: 2^-17 of them is past it
+    assert (final.double().cpu() - s).abs().max() <= 2.0 ** -19 * as_.max()
+
+
+def test_reach_of_an_infinity(gpu):
+    """An infinity in a live token's v stays in its column, its stream and its head, and reaches at most the 31 tokens before it
+    and those after."""
+    x = make(2, 300, 2, 2, 32, 40, torch.bfloat16, seed=17)
+    clean, _ = run(gpu, x)
+    x["v"][1, 170, 1, 7] = math.inf
+    out, final = run(gpu, x)
+    same = out == clean
+    hit = ~same
+    assert not hit[0].any() and not hit[1, :, 0].any() and not hit[1, :139].any()
+    hit[1, :, 1, 7] = False
+    assert not hit.any()
+    assert not torch.isfinite(out[1, 170:, 1, 7]).any() and not torch.isfinite(final[1, 1, :, 7]).any()
