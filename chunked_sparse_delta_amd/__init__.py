@@ -597,7 +597,7 @@ def product_key_topk_backward(lin: torch.Tensor, grad_val: torch.Tensor, factors
     return graw
 
 
-from . import dense, group, linear  # noqa: E402  (they take their helpers from above)
+from . import dense, linear, group  # noqa: E402  (they take their helpers from above)
 from .dense import (gated_delta_bwd, gated_delta_fwd, gated_delta_rule, gated_delta_step,  # noqa: E402
                     gated_delta_workspace_bytes, layer_norm, layer_norm_bwd, layer_norm_fwd)
 from .group import group_norm, group_norm_bwd, group_norm_fwd, group_norm_workspace_bytes  # noqa: E402

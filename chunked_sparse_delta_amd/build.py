@@ -1,4 +1,5 @@
-"""Build libsdm.so (the HIP kernels and the C ABI of include/sdm.h) in-tree for gfx950.
+"""Build libsdm.so (the HIP kernels and the C ABI of include/sdm.h) in-tree for gfx950, and _binding.so, the C++ part of the
+binding of linear attention and group norm (host code on torch tensors).
 
     python -m chunked_sparse_delta_amd.build
 """
@@ -14,6 +15,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsdm.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = os.environ.get("SDM_OFFLOAD_ARCH", "gfx950")
 
 # Packed fp32 instructions are disabled for every device pass (hardware notes).
@@ -26,8 +28,31 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(HERE, "csrc", "*.hip")))
 
 
+def build_binding(verbose: bool = False) -> str:
+    """Compile and link _binding.so against the torch that is installed."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(os.environ.get("HIPCC", "/opt/rocm/bin/hipcc"))))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DTORCH_EXTENSION_NAME=_binding", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           *[a for d in include for a in ("-isystem", d)], "-o", tmp, os.path.join(HERE, "csrc", "binding.cpp"),
+           "-L", os.path.join(home, "lib"), "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_hip"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp ({res.returncode}):\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source to an object (in parallel), then link libsdm.so."""
+    """Compile every source to an object (in parallel), then link libsdm.so; _binding.so beside it."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -47,8 +72,10 @@ def build(verbose: bool = False) -> str:
         return obj
 
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(4, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs]
     if verbose:

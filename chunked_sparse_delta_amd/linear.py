@@ -16,12 +16,12 @@ tokens at and past it are padding, they leave the state alone and read 0. ``scal
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
-from torch.autograd.function import once_differentiable
 
-from . import _DTYPES, _check_rc, _load
-from .dense import _GRADS, _SHAPE, _exec, _need, _new, _on, _out, _ptr, _view
+from . import _DTYPES, SdmError, _load
+from .dense import _SHAPE
 
 __all__ = ["linear_attention_fwd", "linear_attention_step", "linear_attention_bwd", "linear_attention",
            "linear_attention_workspace_bytes", "linear_attention_kept_bytes"]
@@ -42,28 +42,39 @@ def bind(lib) -> None:
         fn.restype = ctypes.c_int
 
 
-def _inputs(k, v, log_decay, q, scale, valid_tokens):
-    if not isinstance(v, torch.Tensor) or not isinstance(k, torch.Tensor) or not isinstance(log_decay, torch.Tensor):
-        raise TypeError("k, v and log_decay must be torch tensors")
-    dtype, dev, vs, ks = v.dtype, v.device, v.shape, k.shape
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"v must be float32 or bfloat16, got {dtype}")
-    if len(vs) != 4 or len(ks) != 4:
-        raise ValueError(f"k and v must be [P, T, heads, width], got {tuple(ks)} and {tuple(vs)}")
-    index = _on(dev)
-    P, T, Hv, V = vs
-    Hk, K = ks[2], ks[3]
-    if Hk < 1 or Hv % Hk:
-        raise ValueError(f"the value heads ({Hv}) must be a multiple of the key heads ({Hk})")
-    keys = (P, T, Hk, K)
-    kr, qr, vr = _view(k, "k", keys, dtype, dev), _view(q, "q", keys, dtype, dev), _view(v, "v", vs, dtype, dev)
-    per_token = log_decay.dim() != 1
-    _need(log_decay, "log_decay", (P, T, Hv) if per_token else (Hv,), torch.float32, dev)
-    if valid_tokens is not None:
-        _need(valid_tokens, "valid_tokens", (P,), torch.int32, dev)
-    shape = _SHAPE(P, T, Hk, Hv, K, V, code, K ** -0.5 if scale is None else scale)
-    return (P, Hv, K, V), (shape, qr, kr, vr, log_decay.data_ptr(), 1 if per_token else 0), dev, index
+_lock = threading.Lock()
+_module = None
+
+
+def _binding():
+    """The binding's C++ part (csrc/binding.cpp), with the loaded library's functions."""
+    global _module
+    if _module is None:
+        lib = _load()
+        with _lock:
+            if _module is None:
+                try:
+                    from . import _binding as module
+                except ImportError as e:
+                    raise RuntimeError(f"_binding.so cannot be loaded ({e}): build it first "
+                                       "(python -m chunked_sparse_delta_amd.build)") from e
+                names = ["sdm_linear_attention_fwd", "sdm_linear_attention_step", "sdm_linear_attention_bwd",
+                         "sdm_linear_attention_workspace_bytes", "sdm_linear_attention_kept_bytes", "sdm_group_norm_fwd",
+                         "sdm_group_norm_bwd", "sdm_group_norm_workspace_bytes", "sdm_last_error"]
+                module.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, SdmError)
+                _module = module
+    return _module
+
+
+def _on(stream, call, *args):
+    """``call`` on ``stream``: what it allocates comes from that stream's memory (whatever used it before did so in that
+    stream's order); the caller may use the results on the current stream."""
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        got = call(*args)
+    for t in (got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,)):
+        t.record_stream(here)
+    return got
 
 
 def linear_attention_workspace_bytes(P: int, T: int, Hk: int, Hv: int, K: int, V: int, dtype: torch.dtype,
@@ -80,14 +91,6 @@ def linear_attention_kept_bytes(P: int, T: int, Hk: int, Hv: int, K: int, V: int
     return _load().sdm_linear_attention_kept_bytes(_SHAPE(P, T, Hk, Hv, K, V, _DTYPES.get(dtype, -1), 1.0))
 
 
-def _buffer(t, name, least, dev):
-    """Checks a caller's buffer for what a forward keeps."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev or not t.is_contiguous() or t.numel() * t.element_size() < least:
-        raise ValueError(f"{name} must be a contiguous tensor of {least} bytes on {dev}")
-
-
 def linear_attention_fwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, q: torch.Tensor, *,
                          scale: float | None = None, valid_tokens: torch.Tensor | None = None,
                          state_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -98,32 +101,10 @@ def linear_attention_fwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: tor
     state goes to ``state_out`` if given). ``workspace`` (uint8, GPU, linear_attention_workspace_bytes) is allocated if
     omitted. ``kept`` (uint8, GPU, linear_attention_kept_bytes) gets what linear_attention_bwd(kept=kept) then does not
     compute again."""
-    lib = _load()
-    plan = _inputs(k, v, log_decay, q, scale, valid_tokens)
-    full, head, dev, _ = plan
-    if state is not None:
-        _need(state, "state", full, torch.float32, dev)
-    if state_out is None:
-        state_out = state
-    else:
-        _need(state_out, "state_out", full, torch.float32, dev)
-    out = _out(out, v, stream)
-    if kept is not None:
-        _buffer(kept, "kept", lib.sdm_linear_attention_kept_bytes(head[0]), dev)
-    _values(plan, state, state_out, valid_tokens, out, kept, workspace, stream)
-    return out
-
-
-def _values(plan, state, state_out, valid_tokens, out, kept, workspace=None, stream=None):
-    """linear_attention_fwd of checked arguments."""
-    lib = _load()
-    _, head, dev, index = plan
-    if workspace is None and kept is None:
-        workspace = _new((max(lib.sdm_linear_attention_workspace_bytes(head[0], 0), 256),), torch.uint8, dev, stream)
-    rc = lib.sdm_linear_attention_fwd(*head, _ptr(state), _ptr(state_out), _ptr(valid_tokens), out.data_ptr(), _ptr(kept),
-                                      _exec(stream, index, workspace))
-    if rc:
-        _check_rc(lib, rc)
+    call = _binding().linear_attention_fwd
+    if stream is not None:
+        return _on(stream, call, state, k, v, log_decay, q, scale, valid_tokens, state_out, out, workspace, kept)
+    return call(state, k, v, log_decay, q, scale, valid_tokens, state_out, out, workspace, kept)
 
 
 def linear_attention_step(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
@@ -134,25 +115,10 @@ def linear_attention_step(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     [slots, Hv, K, V] is a pool; ``state_ids`` (int32 [P], distinct) names each stream's slot, an id outside the pool an
     idle stream, which reads 0; without it stream p has slot p. The states are advanced in place, or written to
     ``state_out`` (the same shape; slots that no stream names are left alone there)."""
-    lib = _load()
-    full, head, dev, index = _inputs(k, v, log_decay, q, scale, valid_tokens)
-    if not isinstance(state, torch.Tensor) or state.dim() != 4:
-        raise ValueError("state must be a [slots, Hv, K, V] tensor")
-    slots = state.shape[0]
-    pool = (slots, *full[1:])
-    _need(state, "state", pool, torch.float32, dev)
-    if state_out is None:
-        state_out = state
-    else:
-        _need(state_out, "state_out", pool, torch.float32, dev)
-    if state_ids is not None:
-        _need(state_ids, "state_ids", full[:1], torch.int32, dev)
-    out = _out(out, v, stream)
-    rc = lib.sdm_linear_attention_step(*head, state.data_ptr(), state_out.data_ptr(), _ptr(state_ids), slots,
-                                       _ptr(valid_tokens), out.data_ptr(), _exec(stream, index))
-    if rc:
-        _check_rc(lib, rc)
-    return out
+    call = _binding().linear_attention_step
+    if stream is not None:
+        return _on(stream, call, state, k, v, log_decay, q, state_ids, scale, valid_tokens, state_out, out)
+    return call(state, k, v, log_decay, q, state_ids, scale, valid_tokens, state_out, out)
 
 
 def linear_attention_bwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, q: torch.Tensor,
@@ -165,73 +131,9 @@ def linear_attention_bwd(state, k: torch.Tensor, v: torch.Tensor, log_decay: tor
     log_decay, q): k, v and q (always there) in the inputs' dtype (sums over sharing heads in float32), state and log_decay
     float32, where ``need`` names them. ``kept``: what a linear_attention_fwd(kept=...) with the same inputs left; without
     it the states are computed again."""
-    plan = _inputs(k, v, log_decay, q, scale, valid_tokens)
-    full, head, dev, _ = plan
-    _need(grad_out, "grad_out", v.shape, v.dtype, dev)
-    for t, n in ((state, "state"), (grad_state, "grad_state")):
-        if t is not None:
-            _need(t, n, full, torch.float32, dev)
-    for n in need:
-        if n not in ("state", "k", "v", "log_decay", "q"):
-            raise ValueError(f"need names state, k, v, log_decay and q, got {need}")
-    if kept is not None:
-        _buffer(kept, "kept", _load().sdm_linear_attention_kept_bytes(head[0]), dev)
-    return _grads(plan, state, k, v, log_decay, q, grad_out, grad_state, valid_tokens, kept, need, workspace, stream)
-
-
-def _grads(plan, state, k, v, log_decay, q, grad_out, grad_state, valid_tokens, kept, need, workspace=None, stream=None):
-    """linear_attention_bwd of checked arguments."""
-    lib = _load()
-    full, head, dev, index = plan
-    f32 = torch.float32
-    g = {"k": _new(k.shape, k.dtype, dev, stream), "v": _new(v.shape, v.dtype, dev, stream), "q": _new(q.shape, q.dtype, dev, stream)}
-    if "state" in need:
-        g["state"] = _new(full, f32, dev, stream)
-    if "log_decay" in need:
-        g["log_decay"] = _new(log_decay.shape, f32, dev, stream)
-    if workspace is None:
-        n = lib.sdm_linear_attention_workspace_bytes(head[0], 1 if kept is None else 2)
-        workspace = _new((max(n, 256),), torch.uint8, dev, stream)
-    rc = lib.sdm_linear_attention_bwd(*head, _ptr(state), _ptr(valid_tokens), grad_out.data_ptr(), _ptr(grad_state), _ptr(kept),
-                                      _GRADS(g["q"].data_ptr(), g["k"].data_ptr(), g["v"].data_ptr(), 0,
-                                             _ptr(g.get("log_decay")) or 0, _ptr(g.get("state")) or 0),
-                                      _exec(stream, index, workspace))
-    if rc:
-        _check_rc(lib, rc)
-    return g
-
-
-class _LinearAttention(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, state, k, v, log_decay, q, scale, valid_tokens, recompute):
-        ctx.plan = plan = _inputs(k, v, log_decay, q, scale, valid_tokens)
-        full, head, dev, _ = plan
-        if state is not None:
-            _need(state, "state", full, torch.float32, dev)
-        final = torch.empty(full, dtype=torch.float32, device=dev)
-        kept = None
-        if not recompute and any(ctx.needs_input_grad):
-            n = _load().sdm_linear_attention_kept_bytes(head[0])
-            kept = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)     # 0: the call itself reports why
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-        _values(plan, state, final, valid_tokens, out, kept)
-        ctx.save_for_backward(state, k, v, log_decay, q, valid_tokens, kept)
-        ctx.set_materialize_grads(False)
-        return out, final
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, grad_out, grad_state):
-        state, k, v, log_decay, q, valid, kept = ctx.saved_tensors
-        if grad_out is None and grad_state is None:
-            return (None,) * 8
-        go = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if grad_out is None else grad_out.contiguous()
-        gs = None if grad_state is None else grad_state.contiguous()
-        wants = ctx.needs_input_grad
-        need = [n for n, on in (("state", wants[0]), ("log_decay", wants[3])) if on]
-        g = _grads(ctx.plan, state, k, v, log_decay, q, go, gs, valid, kept, need)
-        return (g.get("state"), g["k"] if wants[1] else None, g["v"] if wants[2] else None, g.get("log_decay"),
-                g["q"] if wants[4] else None, None, None, None)
+    call = _binding().linear_attention_bwd
+    args = (state, k, v, log_decay, q, grad_out, grad_state, scale, valid_tokens, workspace, kept, list(need))
+    return call(*args) if stream is None else _on(stream, call, *args)
 
 
 def linear_attention(state, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, q: torch.Tensor, *,
@@ -239,4 +141,4 @@ def linear_attention(state, k: torch.Tensor, v: torch.Tensor, log_decay: torch.T
     """Linear attention for autograd: returns (readings, final state); ``state`` (None: zeros) is not changed. Gradients
     reach the state, k, v, log_decay and q through linear_attention_bwd. Until the backward the forward keeps the states
     between segments of tokens (linear_attention_kept_bytes); ``recompute=True`` keeps the inputs alone."""
-    return _LinearAttention.apply(state, k, v, log_decay, q, scale, valid_tokens, recompute)
+    return _binding().linear_attention(state, k, v, log_decay, q, scale, valid_tokens, recompute)
