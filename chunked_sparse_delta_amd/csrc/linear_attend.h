@@ -34,6 +34,7 @@ struct AttendArgs {
     LinGates gates;
     const int32_t *valid;
     int32_t P, T, Hk, Hv, K, V, segs, seg_tokens;
+    bool whole;
 };
 
 template <typename T, int XP, int ZW, bool KEYS, bool EVEN> struct AttendCfg {
@@ -46,13 +47,7 @@ template <typename T, int XP, int ZW, bool KEYS, bool EVEN> struct AttendCfg {
     using S = Tile<float, KEYS ? ZW : 32, KEYS ? 32 : ZW, EVEN>;
     static constexpr size_t kTiles = size_t(NI) * (Y::kPlane + Z::kPlane), kState = 3 * size_t(S::kPlane);
     static constexpr size_t kGates = (kLinSegMax + 4) * sizeof(double) + kLinSegMax * sizeof(float);
-    // Two workgroups share a compute unit: two buffers of tiles where that leaves 80 KB to each; SR blocks of M at a time of SD on their way.
-    static constexpr int kBufs = 2 * kTiles + kGates <= 80 * 1024 ? 2 : 1;
-    static constexpr int SR = KEYS ? 1 : 2, SD = SR;
-    static constexpr int DY = NI == 1 ? 2 : 1;     // blocks of scores' depth whose operands are read at once
-    static constexpr bool kEarly = !KEYS && NI == 1;      // the first tile too is loaded ahead of everything
-    static constexpr int FB = KEYS ? 1 : 2;               // buffers of operands read from LDS
-    static constexpr size_t kLds = (kBufs * kTiles > SR * kState ? kBufs * kTiles : SR * kState) + kGates;
+    static constexpr size_t kLds = (kTiles > kState ? kTiles : kState) + kGates;
     static_assert(kLinSegMax % QT == 0, "a query tile lies in one segment");
 };
 
@@ -72,63 +67,54 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
     const int slices = (Zw + ZW - 1) / ZW, seg_tiles = a.seg_tokens / QT;
     // What reads the same keys, values and states goes to one XCD (blocks are dealt to the eight in turn), where there is enough for
     // all of them: the tiles and slices of a segment, of the value heads that share a key head.
-    const int unit = slices * seg_tiles * (KEYS ? 1 : group), units = a.P * a.Hk * a.segs, xcds = lin_xcds(units);
+    // A workgroup takes one tile, or (`whole`, not KEYS) all of a segment's in turn.
+    const int tiles = !KEYS && a.whole ? 1 : seg_tiles;
+    const int unit = slices * tiles * (KEYS ? 1 : group), units = a.P * a.Hk * a.segs, xcds = lin_xcds(units);
     const int at_xcd = block / xcds, u = at_xcd / unit * xcds + int(block) % xcds, in_unit = at_xcd % unit;
     if (u >= units) return;
     const int seg = u % a.segs, khead = u / a.segs % a.Hk, p = u / a.segs / a.Hk;
-    const int slice = in_unit % slices, oh = KEYS ? khead : khead * group + in_unit / slices / seg_tiles;
-    const int lc = threadIdx.x & 15, lg = threadIdx.x >> 4 & 3, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int s0 = seg * a.seg_tokens, tile = in_unit / slices % seg_tiles, q0 = s0 + (back ? tile : seg_tiles - 1 - tile) * QT, n = lin_valid(a.valid, p, a.T), s1 = min(s0 + a.seg_tokens, n);
-    const int z0 = slice * ZW;
-    if (q0 >= a.T) return;      // (the tiles that see most of their segment come first)
-    const int qw = q0 + wv * 16 * NQ, diag = qw & ~31;     // the wavefront's first token; the 32 tokens that it lies in
+    const int slice = in_unit % slices, oh = KEYS ? khead : khead * group + in_unit / slices / tiles;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int s0 = seg * a.seg_tokens, n = lin_valid(a.valid, p, a.T), s1 = min(s0 + a.seg_tokens, n), z0 = slice * ZW;
     T *out = static_cast<T *>(s.out) + (int64_t(p) * a.T * heads + oh) * Zw + z0;
     const int64_t os = int64_t(heads) * Zw;
-    auto put = [&](int t, int zb, dt4 lo, dt4 hi) {
-        if (t < a.T) eight_store<EVEN>(out + t * os + zb * 32 + lg * 8, Zw - z0 - zb * 32 - lg * 8, lo, hi);
-    };
-    if (q0 >= n) {
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-            for (int zb = 0; zb < ZB; ++zb) put(qw + nq * 16 + lc, zb, dt4{}, dt4{});
-        return;
-    }
-    const bool x_whole = qw + 16 * NQ <= n && XP <= X;
     dt4 acc[ZB][2][NQ];
     auto rows = [&](const Rows &r, int head) { return static_cast<const T *>(r.data) + p * r.sp + head * r.sh; };
-    const int first = KEYS ? oh * group : oh, count = KEYS ? group : 1;
-    for (int h = first; h < first + count; ++h) {
-        const int hk = h / group;
+    // KEYS: the value heads in turn; else tiles, those that see most of their segment first
+    bool gated = false;
+    const int turns = KEYS ? group : seg_tiles / tiles;
+    for (int turn = 0; turn < turns; ++turn) {
+        const int h = KEYS ? oh * group + turn : oh, hk = h / group;
+        const int tile = in_unit / slices % tiles + (KEYS ? 0 : turn), q0 = s0 + (back ? tile : seg_tiles - 1 - tile) * QT;
+        if (q0 >= a.T) continue;
+        const int qw = q0 + wv * 16 * NQ, diag = qw & ~31;     // the wavefront's first token; the 32 tokens that it lies in
+        const bool x_whole = qw + 16 * NQ <= n && XP <= X;
         // The thread's number as a value of its own: addresses made from it stay in this turn of the loop, where the compiler
         // would keep them all in registers through it.
         int tid = threadIdx.x;
         asm volatile("" : "+v"(tid));
         const int lane = tid & 63, lc = lane & 15, lg = lane >> 4;
+        auto put = [&](int t, int zb, dt4 lo, dt4 hi) {
+            if (t < a.T) eight_store<EVEN>(out + t * os + zb * 32 + lg * 8, Zw - z0 - zb * 32 - lg * 8, lo, hi);
+        };
+        if (q0 >= n) {
+            if (KEYS && turn > 0) break;
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                for (int zb = 0; zb < ZB; ++zb) put(qw + nq * 16 + lc, zb, dt4{}, dt4{});
+            continue;
+        }
         // x and y are of one kind (keys or values), z of the other
         const T *xr = rows(s.x, KEYS ? h : hk), *yr = rows(s.y, KEYS ? h : hk), *zr = rows(s.z, KEYS ? hk : h);
-        // everything that is read first is on its way before the gates' sums are waited for (KEYS: where registers allow)
-        Eight<T> ex[NQ][XB];
-        auto bring_x = [&]() {
-#pragma unroll
-            for (int nq = 0; nq < NQ; ++nq) {
-                const T *row = xr + int64_t(min(qw + nq * 16 + lc, n - 1)) * s.x.st;
-#pragma unroll
-                for (int d = 0; d < XB; ++d) ex[nq][d] = eight_load<EVEN>(row, d * 32 + lg * 8, X);
-            }
-        };
-        if (!KEYS) bring_x();
         const float *M = s.M ? s.M + (int64_t(p) * a.Hv + h) * s.M_head + seg * s.M_seg : nullptr;
-        typename C::S tm[C::SD];
+        typename C::S tm;
         auto bring_state = [&](int d) {
             const int V = a.V;
-            if constexpr (KEYS) tm[d % C::SD].load(M + int64_t(z0) * V, V, Zw - z0, d * 32, V, tid);
-            else tm[d % C::SD].load(M + int64_t(min(d * 32, X - 1)) * V, V, max(X - d * 32, 1), z0, V, tid);     // no rows left: x is 0 there
+            if constexpr (KEYS) tm.load(M + int64_t(z0) * V, V, Zw - z0, d * 32, V, tid);
+            else tm.load(M + int64_t(min(d * 32, X - 1)) * V, V, max(X - d * 32, 1), z0, V, tid);     // no rows left: x is 0 there
         };
-        if (M) {
-#pragma unroll
-            for (int d = 0; d < C::SD; ++d) bring_state(d);
-        }
+        if (M) bring_state(0);
         // tiles of the segment, from its far end to the wavefront's own tokens
         const int k0 = back ? (s1 - 1 - s0) / KT : 0, k1 = back ? (q0 - s0) / KT : (min(q0 + QT, s1) - 1 - s0) / KT, step = back ? -1 : 1;
         Y ty;
@@ -138,9 +124,16 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
             ty.load(yr + int64_t(t0) * s.y.st, s.y.st, s1 - t0, 0, X, tid);
             tz.load(zr + int64_t(t0) * s.z.st, s.z.st, s1 - t0, z0, Zw, tid);
         };
-        if (C::kEarly) bring(k0);
-        segment_gates(a.gates, p, h, s0, s1 - s0, G, total_of);
-        if (KEYS) bring_x();
+        const bool new_gates = KEYS || !gated;
+        gated = true;
+        if (new_gates) segment_gates(a.gates, p, h, s0, s1 - s0, G, total_of);
+        Eight<T> ex[NQ][XB];
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            const T *row = xr + int64_t(min(qw + nq * 16 + lc, n - 1)) * s.x.st;
+#pragma unroll
+            for (int d = 0; d < XB; ++d) ex[nq][d] = eight_load<EVEN>(row, d * 32 + lg * 8, X);
+        }
         Frag<NI> fx[NQ][XB];
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq)
@@ -155,38 +148,26 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = dt4{};
-        // the product with the state, 32 SR of its rows (KEYS: columns) at a time
+        // the product with the state, 32 of its rows (KEYS: columns) at a time
         if (M) {
 #pragma unroll
-            for (int d0 = 0; d0 < XB; d0 += C::SR) {
+            for (int d = 0; d < XB; ++d) {
                 lds_barrier();
-#pragma unroll
-                for (int i = 0; i < C::SR; ++i) tm[(d0 + i) % C::SD].store(lds + i * C::kState, tid);
+                tm.store(lds, tid);
                 lds_barrier();
+                if (d + 1 < XB) bring_state(d + 1);
 #pragma unroll
-                for (int i = 0; i < C::SR; ++i)
-                    if (d0 + i + C::SD < XB) bring_state(d0 + i + C::SD);
-                // a step's operands are read from LDS ahead of the products of the step before it
-                Frag<3> f[C::FB][2];
-                auto read = [&](int j) {
-                    const unsigned char *blk = lds + j / ZB * C::kState + j % ZB * kBlk;
+                for (int zb = 0; zb < ZB; ++zb) {
+                    Frag<3> f[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) f[j % C::FB][e] = KEYS ? read_rows<3>(blk, C::S::kPlane, e, lane) : read_cols<3>(blk, C::S::kPlane, e, lane);
-                };
-                if (C::FB == 2) read(0);
-#pragma unroll
-                for (int j = 0; j < C::SR * ZB; ++j) {
-                    if (C::FB == 1) read(j);
-                    else if (j + 1 < C::SR * ZB) read(j + 1);
-                    if (C::FB == 2) lds_point();
-                    const int zb = j % ZB, d = d0 + j / ZB;
+                    for (int e = 0; e < 2; ++e)
+                        f[e] = KEYS ? read_rows<3>(lds + zb * kBlk, C::S::kPlane, e, lane) : read_cols<3>(lds + zb * kBlk, C::S::kPlane, e, lane);
                     each_product<3, 3, NI>([&](int m, int l) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = mma1(f[j % C::FB][e].p[m], fx[nq][d].p[l], acc[zb][e][nq]);
+                            for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = mma1(f[e].p[m], fx[nq][d].p[l], acc[zb][e][nq]);
                     });
-                    if (C::FB == 2) lds_point();
                 }
             }
         } else {
@@ -194,7 +175,7 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
         }
         const double sign = back ? -1.0 : 1.0;
         auto edge_of = [&](int b) { return back ? (b > 0 ? G[b - 1] : 0.0) : G[b + 31]; };    // of the 32 tokens from b on
-        local[threadIdx.x] = exp2_of(sign * (edge_of(threadIdx.x & ~31) - G[threadIdx.x]));
+        if (new_gates) local[threadIdx.x] = exp2_of(sign * (edge_of(threadIdx.x & ~31) - G[threadIdx.x]));
         // Decays are taken relative to a border of the wavefront's tokens until the pairs within its 32: e^{ref - H_b} before it
         // and e^{H_a - ref} after, both at most 1 where the log-decays are (H: G, or -G where b follows a).
         const int border = back ? min(qw + 16 * NQ, s1) - 1 - s0 : qw - 1 - s0;
@@ -210,52 +191,28 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
 #pragma unroll
                 for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] *= ws;
         float self[NQ] = {};     // a1 (x_a . y_a), in the lanes that come upon it
-        if (!C::kEarly) bring(k0);
-        lds_barrier();
-        ty.store(ly, tid);
-        tz.store(lz, tid);
-        if (k0 != k1) bring(k0 + step);
-        for (int kt = k0, turn = 0;; kt += step, ++turn) {
-            // the next tile goes to the other buffer, or to this one once it is free
-            unsigned char *cy = ly + (C::kBufs == 2 && (turn & 1) ? C::kTiles : 0), *cz = cy + (lz - ly);
+        bring(k0);
+        for (int kt = k0;; kt += step) {
             lds_barrier();
-            if (C::kBufs == 2 && kt != k1) {
-                unsigned char *ny = ly + (turn & 1 ? 0 : C::kTiles);
-                ty.store(ny, tid);
-                tz.store(ny + (lz - ly), tid);
-                if (kt + step != k1) bring(kt + 2 * step);
-            }
-            for (int i = 0; i < TB; ++i) {
-                const int tb = back ? TB - 1 - i : i, b0 = s0 + kt * KT + tb * 32;
+            ty.store(ly, tid);
+            tz.store(lz, tid);
+            lds_barrier();
+            if (kt != k1) bring(kt + step);
+            for (int j = 0; j < TB; ++j) {
+                const int tb = back ? TB - 1 - j : j, b0 = s0 + kt * KT + tb * 32;
                 if (qw >= s1 || b0 >= s1 || (back ? b0 < diag : b0 > diag)) continue;
                 dt4 st[2][NQ] = {};
-                Frag<NI> fy[C::FB][C::DY][2], fz[C::FB][2];
-                auto read_y = [&](int j) {
 #pragma unroll
-                    for (int i = 0; i < C::DY; ++i)
+                for (int d = 0; d < XB; ++d) {
+                    Frag<NI> f[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) fy[j % C::FB][i][e] = read_rows<NI>(cy + (tb * XB + j * C::DY + i) * kBlk, Y::kPlane, e, lane);
-                };
-                auto read_z = [&](int zb) {
+                    for (int e = 0; e < 2; ++e) f[e] = read_rows<NI>(ly + (tb * XB + d) * kBlk, Y::kPlane, e, lane);
+                    each_product<3, NI, NI>([&](int m, int l) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) fz[zb % C::FB][e] = read_cols<NI>(cz + (tb * ZB + zb) * kBlk, Z::kPlane, e, lane);
-                };
-                if (C::FB == 2) read_y(0);
+                        for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int j = 0; j < XB / C::DY; ++j) {
-                    if (C::FB == 1) read_y(j);
-                    else if (j + 1 < XB / C::DY) read_y(j + 1);
-                    else read_z(0);
-                    if (C::FB == 2) lds_point();
-#pragma unroll
-                    for (int i = 0; i < C::DY; ++i)
-                        each_product<3, NI, NI>([&](int m, int l) {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                                for (int nq = 0; nq < NQ; ++nq) st[e][nq] = mma1(fy[j % C::FB][i][e].p[m], fx[nq][j * C::DY + i].p[l], st[e][nq]);
-                        });
-                    if (C::FB == 2) lds_point();
+                            for (int nq = 0; nq < NQ; ++nq) st[e][nq] = mma1(f[e].p[m], fx[nq][d].p[l], st[e][nq]);
+                    });
                 }
                 const double *Gb = G + (b0 - s0) + lg * 8;
                 if (b0 != diag) {
@@ -292,29 +249,22 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
                 for (int nq = 0; nq < NQ; ++nq) fp[nq] = split<3>(st[0][nq], st[1][nq]);
 #pragma unroll
                 for (int zb = 0; zb < ZB; ++zb) {
-                    if (C::FB == 1) read_z(zb);
-                    else if (zb + 1 < ZB) read_z(zb + 1);
-                    if (C::FB == 2) lds_point();
+                    Frag<NI> f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) f[e] = read_cols<NI>(lz + (tb * ZB + zb) * kBlk, Z::kPlane, e, lane);
                     each_product<3, NI, 3>([&](int m, int l) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
 #pragma unroll
-                            for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = mma1(fz[zb % C::FB][e].p[m], fp[nq].p[l], acc[zb][e][nq]);
+                            for (int nq = 0; nq < NQ; ++nq) acc[zb][e][nq] = mma1(f[e].p[m], fp[nq].p[l], acc[zb][e][nq]);
                     });
-                    if (C::FB == 2) lds_point();
                 }
             }
             if (kt == k1) break;
-            if (C::kBufs == 1) {
-                lds_barrier();
-                ty.store(ly, tid);
-                tz.store(lz, tid);
-                if (kt + step != k1) bring(kt + 2 * step);
-            }
         }
         if constexpr (KEYS) {
             // The sum over the value heads that share the key head waits in memory for the next one: registers hold one head's alone.
-            const bool begins = h == first, ends = h + 1 == first + count;
+            const bool begins = turn == 0, ends = turn + 1 == turns;
             dt4 *rest = reinterpret_cast<dt4 *>(s.rest) +
                         ((((int64_t(p) * a.segs + seg) * a.Hk + oh) * seg_tiles + (q0 - s0) / QT) * slices + slice) * (2 * ZB * NQ * 256) + tid;
             const T *mine = rows(s.own, oh);
@@ -348,13 +298,14 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
                 if (s.dot && lg == 0 && t < n) s.dot[((int64_t(slice) * a.P + p) * a.Hv + h) * a.T + t] = dot;
             }
             lds_barrier();       // G and the tiles are free
+            if (!ends) continue;
         }
-    }
 #pragma unroll
-    for (int nq = 0; nq < NQ; ++nq) {
-        const int t = qw + nq * 16 + lc;
+        for (int nq = 0; nq < NQ; ++nq) {
+            const int t = qw + nq * 16 + lc;
 #pragma unroll
-        for (int zb = 0; zb < ZB; ++zb) put(t, zb, t < n ? acc[zb][0][nq] : dt4{}, t < n ? acc[zb][1][nq] : dt4{});
+            for (int zb = 0; zb < ZB; ++zb) put(t, zb, t < n ? acc[zb][0][nq] : dt4{}, t < n ? acc[zb][1][nq] : dt4{});
+        }
     }
 }
 
@@ -371,17 +322,22 @@ template <typename T, int XP, int ZW, bool EVEN> __global__ __launch_bounds__(25
 // single: the end states that go with the readings of one segment, or null.
 template <typename T, int XP, int ZW, bool KEYS, bool EVEN> hipError_t attend_go(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
     using C = AttendCfg<T, XP, ZW, KEYS, EVEN>;
-    const int64_t slices = (a.side[0].z.width + ZW - 1) / ZW, unit = slices * (a.seg_tokens / C::QT) * (KEYS ? 1 : a.Hv / a.Hk);
+    // All tiles of a segment in one workgroup where that leaves two to a compute unit: it meets the segment's gates and the kernel's
+    // arguments once (16 heads of 16384 tokens of 128 x 128, bfloat16: 120 us tile by tile, 111 so; 64 heads of 2048: 61 and 56).
+    const int64_t slices = (a.side[0].z.width + ZW - 1) / ZW, all = int64_t(a.P) * a.Hv * a.segs * slices;
+    AttendArgs b = a;
+    b.whole = !KEYS && all >= 2 * kCus;
+    const int64_t unit = slices * (b.whole ? 1 : a.seg_tokens / C::QT) * (KEYS ? 1 : a.Hv / a.Hk);
     const int64_t units = int64_t(a.P) * a.Hk * a.segs, xcds = lin_xcds(units), blocks = (units + xcds - 1) / xcds * xcds * unit;
     if constexpr (!KEYS) {
         if (single) {
             constexpr size_t other = StateCfg<T, XP, ZW, EVEN>::kLds;
             hipLaunchKernelGGL((lin_single_kernel<T, XP, ZW, EVEN>), dim3(unsigned(blocks + slices * a.P * a.Hv)), dim3(256),
-                               C::kLds > other ? C::kLds : other, st, a, *single, int(blocks));
+                               C::kLds > other ? C::kLds : other, st, b, *single, int(blocks));
             return hipGetLastError();
         }
     }
-    hipLaunchKernelGGL((lin_attend_kernel<T, XP, ZW, KEYS, EVEN>), dim3(unsigned(blocks), KEYS ? 2u : 1u), dim3(256), C::kLds, st, a);
+    hipLaunchKernelGGL((lin_attend_kernel<T, XP, ZW, KEYS, EVEN>), dim3(unsigned(blocks), KEYS ? 2u : 1u), dim3(256), C::kLds, st, b);
     return hipGetLastError();
 }
 template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_even(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
