@@ -241,13 +241,13 @@ py::dict la_bwd(const OptTensor &state, const OptTensor &k, const OptTensor &v, 
 
 struct LinearAttention : torch::autograd::Function<LinearAttention> {
     static variable_list forward(AutogradContext *ctx, const OptTensor &state, const Tensor &k, const Tensor &v, const Tensor &g, const Tensor &q,
-                                 std::optional<double> scale, const OptTensor &valid, bool recompute) {
+                                 std::optional<double> scale, const OptTensor &valid, bool keep) {
         const Attention a = attention(k, v, g, q, scale, valid);
         need(state, "state", a.state, at::kFloat, a.dev);
         const Tensor final = make(a.state, at::kFloat, a.dev), out = make(v.sizes(), v.scalar_type(), a.dev);
         const bool wants[5] = {given(state) && state->requires_grad(), k.requires_grad(), v.requires_grad(), g.requires_grad(), q.requires_grad()};
         OptTensor kept;
-        if (!recompute && (wants[0] || wants[1] || wants[2] || wants[3] || wants[4])) kept = scratch(api.la_kept(&a.shape), a.dev);
+        if (keep && (wants[0] || wants[1] || wants[2] || wants[3] || wants[4])) kept = scratch(api.la_kept(&a.shape), a.dev);
         la_values(a, state, final, valid, out, kept, std::nullopt);
         auto some = [](const OptTensor &t) { return given(t) ? *t : Tensor(); };
         ctx->save_for_backward({some(state), k, v, g, q, some(valid), some(kept)});
@@ -274,7 +274,7 @@ struct LinearAttention : torch::autograd::Function<LinearAttention> {
 py::tuple linear_attention(const OptTensor &state, const OptTensor &k, const OptTensor &v, const OptTensor &g, const OptTensor &q, std::optional<double> scale,
                            const OptTensor &valid, bool recompute) {
     if (!given(k) || !given(v) || !given(g) || !given(q)) type_error("k, v, log_decay and q must be torch tensors");
-    const variable_list r = LinearAttention::apply(state, *k, *v, *g, *q, scale, valid, recompute);
+    const variable_list r = LinearAttention::apply(state, *k, *v, *g, *q, scale, valid, !recompute && at::GradMode::is_enabled());
     return py::make_tuple(r[0], r[1]);
 }
 

@@ -11,6 +11,9 @@
 //  - Resident: where a tile's rows fit the registers of a workgroup each element is read once. Several samples share a workgroup
 //    where they are short; their sums meet by shuffles where a group is 8, 16, ... lanes of one wavefront, through LDS elsewhere.
 //  - Split: longer samples are cut into blocks of rows; one kernel leaves each block's sums, the next joins them and reads the rows again.
+// Measured: 8192 tokens of 4096 channels in 32 groups, bfloat16, silu: forward 36 us (134 MB, 3.7 TB/s), backward 52 (201 MB, 3.9 TB/s) and
+// 4 for the sums over workgroups; 64 tokens: 4.3. Split, 8 x 4096 rows of 512 channels: statistics 11, their join 4, values 16 (67 MB,
+// 4.3 TB/s); sums 21 (67 MB), their join 5, gradients 21 (101 MB, 4.7 TB/s), the parameters' sums 4. A large copy: 5.2 TB/s.
 // Statistics: a thread's mean and sum of squared differences from it, joined with their counts (no difference of large sums).
 // All sums run in float32 in a fixed order: results are the same from run to run.
 #include <type_traits>
@@ -70,7 +73,7 @@ template <int V> __device__ __forceinline__ void gn_params(const void *p, bool f
 }
 
 // 1 / (1 + 2^(-z / log 2)): the exponent's rounding, 2^-24 of it, is |z| 2^-24 of a value that falls as e^z: at most 2^-24 in z sigmoid(z).
-// (With expf, whose instructions made the forward's time, 8192 x 4096 took 56 us; so 36.)
+// (With expf and joins by division in each group's lanes the forward of 8192 x 4096 took 56 us; now 36.)
 __device__ __forceinline__ float gn_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z)); }
 __device__ __forceinline__ float gn_phi(float z) { return 0.5f * erfcf(-0.70710678f * z); }
 

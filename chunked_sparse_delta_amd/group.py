@@ -55,7 +55,8 @@ def group_norm_fwd(x: torch.Tensor, groups: int, weight: torch.Tensor | None = N
                    activation: str | None = None, eps: float = 1e-5, valid_rows: torch.Tensor | None = None,
                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Group norm and activation. Returns (y, mean, rstd); mean and rstd float32 [N, groups] are what group_norm_bwd needs.
-    ``workspace`` (uint8, GPU, group_norm_workspace_bytes) is allocated if omitted and needed."""
+    ``out`` may be x where that is contiguous. ``workspace`` (uint8, GPU, group_norm_workspace_bytes) is allocated if
+    omitted and needed."""
     call = _binding().group_norm_fwd
     if stream is not None:
         return _on(stream, call, x, groups, weight, bias, _act(activation), eps, valid_rows, out, workspace)
@@ -75,5 +76,6 @@ def group_norm_bwd(grad_out: torch.Tensor, x: torch.Tensor, groups: int, mean: t
 
 def group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
                activation: str | None = None, eps: float = 1e-5, valid_rows: torch.Tensor | None = None) -> torch.Tensor:
-    """Group norm and activation for autograd (group_norm_fwd, its backward group_norm_bwd)."""
+    """Group norm and activation for autograd (group_norm_fwd, its backward group_norm_bwd). Captured into a graph: see
+    linear_attention."""
     return _binding().group_norm(x, groups, weight, bias, _act(activation), eps, valid_rows)

@@ -140,5 +140,7 @@ def linear_attention(state, k: torch.Tensor, v: torch.Tensor, log_decay: torch.T
                      scale: float | None = None, valid_tokens: torch.Tensor | None = None, recompute: bool = False):
     """Linear attention for autograd: returns (readings, final state); ``state`` (None: zeros) is not changed. Gradients
     reach the state, k, v, log_decay and q through linear_attention_bwd. Until the backward the forward keeps the states
-    between segments of tokens (linear_attention_kept_bytes); ``recompute=True`` keeps the inputs alone."""
+    between segments of tokens (linear_attention_kept_bytes); ``recompute=True`` keeps the inputs alone. Under no_grad
+    nothing is kept. A backward captured into a graph needs leaves that no eager autograd graph holds any longer (autograd would join that one's
+    stream into the capture)."""
     return _binding().linear_attention(state, k, v, log_decay, q, scale, valid_tokens, recompute)

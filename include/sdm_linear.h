@@ -93,7 +93,7 @@ int sdm_linear_attention_bwd(const sdm_delta_shape *shape, const sdm_rows *q, co
  *     float32 parameters, bfloat16 rows either type.
  *   valid_rows: device int32 [samples], or NULL: rows at and past it are padding, which may hold
  *     anything; they do not count and give +0. A sample without a valid row has mean 0 and var 0.
- *   y: dense [samples, rows, channels]; mean, rstd: device float32 [samples, groups], written.
+ *   y: dense [samples, rows, channels], may be x where that is dense, but must not overlap an input otherwise; mean, rstd: device float32 [samples, groups], written.
  *   exec->workspace: sdm_group_norm_workspace_bytes(shape, 0) bytes, 256-byte aligned (where that is
  *     0, none).
  * At most 2^31 - 1 samples and rows of 2^20 channels. Bitwise reproducible.

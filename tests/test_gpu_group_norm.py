@@ -268,3 +268,15 @@ def test_streams_and_graph(gpu, N, L, C, G):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(captured, work())), i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,L,C,G", [(40, 1, 256, 4), (6, 5, 320, 2), (9, 3, 21, 3), (2, 2500, 64, 8)])
+def test_in_place(gpu, N, L, C, G, dtype):
+    """y in x's place: the same bits."""
+    import chunked_sparse_delta_amd as sdm
+    d = {n: t.to(gpu) for n, t in make(N, L, C, DT[dtype]).items()}
+    kw = {"activation": "silu"}
+    first = sdm.group_norm_fwd(d["x"], G, d["weight"], d["bias"], **kw)
+    got = sdm.group_norm_fwd(d["x"], G, d["weight"], d["bias"], out=d["x"], **kw)
+    assert got[0].data_ptr() == d["x"].data_ptr() and all(torch.equal(a, b) for a, b in zip(first, got))

@@ -453,6 +453,56 @@ def test_retained_graph(gpu):
     assert all(torch.equal(s, t) for s, t in zip(a, b))
 
 
+def test_no_grad_keeps_nothing(gpu):
+    """Without autograd: the same bits, no graph, and no memory for a backward."""
+    import chunked_sparse_delta_amd as sdm
+    x = make(4, 100, 8, 8, 128, 128, torch.float32, seed=3)
+    x = {n: None if t is None else t.to(gpu).requires_grad_() for n, t in x.items()}
+    args = [x[n] for n in NAMES]
+    first = [t.detach() for t in sdm.linear_attention(*args)]
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with torch.no_grad():
+        got = sdm.linear_attention(*args)
+    used = torch.cuda.max_memory_allocated() - before
+    assert all(torch.equal(a, b) and not b.requires_grad for a, b in zip(first, got))
+    kept = sdm.linear_attention_kept_bytes(4, 100, 8, 8, 128, 128, torch.float32)
+    assert used < sum(t.nbytes for t in got) + kept // 2
+
+
+def test_graph_of_a_training_step(gpu):
+    """Linear attention, each head's norm with its activation, and all gradients through autograd, captured together: every replay
+    against the eager result."""
+    import chunked_sparse_delta_amd as sdm
+    x = on(make(2, 300, 2, 4, 64, 64, torch.bfloat16, seed=21), gpu)
+    weight = torch.randn(256, device=gpu)
+    go = torch.randn(600, 256, device=gpu).to(torch.bfloat16)
+    leaves = [x[n].requires_grad_() for n in NAMES] + [weight.requires_grad_()]
+
+    def work():
+        out, final = sdm.linear_attention(*leaves[:5])
+        y = sdm.group_norm(out.flatten(2).flatten(0, 1), 4, weight, activation="silu")
+        return [y.detach(), final.detach(), *torch.autograd.grad(y, leaves, go)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = work()
+    for i in range(3):
+        with torch.no_grad():
+            x["v"].copy_(torch.randn(x["v"].shape, device=gpu))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        assert all(torch.equal(a, b) for a, b in zip(got, work())), i
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_terms_that_cancel(gpu, dtype):
     """Readings and gradients whose terms cancel keep float32's bits: every sixteenth value, 2^12 times the others, meets its
