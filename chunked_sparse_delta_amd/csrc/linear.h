@@ -55,7 +55,7 @@ struct LinGrads {
 };
 
 inline int lin_width(int n) { return n <= 64 ? 64 : n <= 128 ? 128 : 256; }   // padded depth of scores
-inline int lin_slice(int n) { return n <= 64 ? 64 : 128; }                    // columns of a workgroup
+__host__ __device__ constexpr int lin_slice(int n) { return n <= 64 ? 64 : 128; }                    // columns of a workgroup
 inline int lin_slices(int n) { return (n + lin_slice(n) - 1) / lin_slice(n); }
 // Over how many XCDs units of workgroups that share their operands are dealt; the grid is padded to as many.
 __host__ __device__ inline int lin_xcds(int64_t units) { return units % kXcds == 0 || units >= 8 * kXcds ? kXcds : 1; }

@@ -227,10 +227,10 @@ int lin_dot_parts(int K, int V) { return (K * V + (K * V % 4 ? 255 : 1023)) / (K
 hipError_t linear_prepare() {
     hipError_t e = state_prepare<bf16>();
     if (e == hipSuccess) e = state_prepare<float>();
-    if (e == hipSuccess) e = attend_prepare_values_bf16();
-    if (e == hipSuccess) e = attend_prepare_values_f32();
-    if (e == hipSuccess) e = attend_prepare_keys_bf16();
-    if (e == hipSuccess) e = attend_prepare_keys_f32();
+    if (e == hipSuccess) e = attend_prepare_bf16();
+    if (e == hipSuccess) e = attend_prepare_f32();
+    if (e == hipSuccess) e = grads_prepare_bf16();
+    if (e == hipSuccess) e = grads_prepare_f32();
     return e;
 }
 
@@ -254,7 +254,7 @@ hipError_t launch_linear_fwd(const LinArgs &a, const LinWs &ws, bool is_bf16, bo
         r.out = a.out;
         r.a0 = r.a1 = a.scale;
         const bool both = !scan && a.state_out && a.state_out != a.state;
-        e = is_bf16 ? attend_values_bf16(t, both ? &s : nullptr, st) : attend_values_f32(t, both ? &s : nullptr, st);
+        e = is_bf16 ? attend_bf16(t, both ? &s : nullptr, st) : attend_f32(t, both ? &s : nullptr, st);
         if (e != hipSuccess || both) return e;
     }
     if (scan || !a.state_out) return hipSuccess;
@@ -277,7 +277,7 @@ hipError_t launch_linear_bwd(const LinArgs &a, const LinWs &ws, const LinGrads &
     if ((e = launch_scan<true>(c, a.P * a.Hv, st)) != hipSuccess) return e;
     if (a.T > 0) {
         AttendArgs t = attend_args(a, ws);
-        AttendSide &q = t.side[0], &k = t.side[1];
+        AttendSide &q = t.side[0], &k = t.side[1], &v = t.side[2];
         q.x = g.go; q.y = a.v; q.z = a.k; q.own = a.q;
         q.M = ws.S; q.M_head = (ws.segs + 1) * KV; q.M_seg = KV;
         q.out = g.q; q.dot = g.g ? ws.rows : nullptr;
@@ -288,12 +288,10 @@ hipError_t launch_linear_bwd(const LinArgs &a, const LinWs &ws, const LinGrads &
         k.out = g.k; k.dot = g.g ? ws.cols : nullptr;
         k.a0 = 1.0f; k.a1 = a.scale; k.back = true;
         k.rest = ws.rest + lin_rest_floats(a.P, a.Hk, a.K, ws.segs, ws.tokens);
-        if ((e = is_bf16 ? attend_keys_bf16(t, st) : attend_keys_f32(t, st)) != hipSuccess) return e;
-        AttendSide v = k;
+        v = k;
         v.x = a.k; v.y = a.q; v.z = g.go;
         v.out = g.v; v.dot = nullptr;
-        t.side[0] = v;
-        if ((e = is_bf16 ? attend_values_bf16(t, nullptr, st) : attend_values_f32(t, nullptr, st)) != hipSuccess) return e;
+        if ((e = is_bf16 ? attend_grads_bf16(t, st) : attend_grads_f32(t, st)) != hipSuccess) return e;
     }
     if (!g.g) return hipSuccess;
     GateGradArgs d{};

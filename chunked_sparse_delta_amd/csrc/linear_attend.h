@@ -38,7 +38,7 @@ struct AttendSide {
     bool back;               // b at or after a
 };
 struct AttendArgs {
-    AttendSide side[2];      // blockIdx.y
+    AttendSide side[3];      // the readings; or dq, dk and dv
     LinGates gates;
     const int32_t *valid;
     int32_t P, T, Hk, Hv, K, V, segs, seg_tokens;
@@ -61,7 +61,7 @@ template <typename T, int XP, int ZW, bool KEYS, bool EVEN> struct AttendCfg {
 };
 
 template <typename T, int XP, int ZW, bool KEYS, bool EVEN>
-__device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block) {
+__device__ __forceinline__ void lin_attend(const AttendArgs &a, const AttendSide &s, const int block) {
     using C = AttendCfg<T, XP, ZW, KEYS, EVEN>;
     constexpr int NI = C::NI, NQ = C::NQ, QT = C::QT, KT = C::KT, XB = XP / 32, ZB = ZW / 32, TB = KT / 32;
     using Y = typename C::Y;
@@ -70,7 +70,6 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
     unsigned char *ly = lds, *lz = lds + NI * Y::kPlane;
     double *total_of = reinterpret_cast<double *>(lds + C::kLds) - 4, *G = total_of - kLinSegMax;
     float *local = reinterpret_cast<float *>(G) - kLinSegMax;     // a token's decay to the edge of its 32 on the side of the a
-    const AttendSide &s = a.side[KEYS ? blockIdx.y : 0];
     const bool back = s.back;
     const int heads = KEYS ? a.Hk : a.Hv, group = a.Hv / a.Hk, X = s.x.width, Zw = s.z.width;
     const int slices = (Zw + ZW - 1) / ZW, seg_tiles = a.seg_tokens / QT;
@@ -318,83 +317,134 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const int block)
     }
 }
 
-template <typename T, int XP, int ZW, bool KEYS, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
-    lin_attend<T, XP, ZW, KEYS, EVEN>(a, blockIdx.x);
+template <typename T, int XP, int ZW, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
+    lin_attend<T, XP, ZW, false, EVEN>(a, a.side[0], blockIdx.x);
 }
 // A sequence of one segment: its readings and, by the workgroups from `attends` on, its end state. (One launch for two: of 200
 // tokens of 4 heads of 64 x 64, 13.6 us and 9 one after the other.)
 template <typename T, int XP, int ZW, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_single_kernel(AttendArgs a, StateArgs s, int attends) {
-    if (int(blockIdx.x) < attends) lin_attend<T, XP, ZW, false, EVEN>(a, blockIdx.x);
+    if (int(blockIdx.x) < attends) lin_attend<T, XP, ZW, false, EVEN>(a, a.side[0], blockIdx.x);
     else lin_state<T, XP, ZW, EVEN>(s, int(blockIdx.x) - attends);
 }
+// dq, dk and dv: `keys` workgroups for each of the first two, then those of dv, which fill the device where the others leave it. The
+// launch begins with workgroup `first`.
+template <typename T, int KP, int VP, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_grads_kernel(AttendArgs a, int keys, int first) {
+    const int b = int(blockIdx.x) + first;
+    if (b < 2 * keys) lin_attend<T, VP, lin_slice(KP), true, EVEN>(a, a.side[b < keys ? 0 : 1], b < keys ? b : b - keys);
+    else lin_attend<T, KP, lin_slice(VP), false, EVEN>(a, a.side[2], b - 2 * keys);
+}
 
-// single: the end states that go with the readings of one segment, or null.
-template <typename T, int XP, int ZW, bool KEYS, bool EVEN> hipError_t attend_go(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
-    using C = AttendCfg<T, XP, ZW, KEYS, EVEN>;
+// Workgroups of a side; sets `whole`.
+template <typename C, bool KEYS> int64_t attend_blocks(AttendArgs &a, const AttendSide &s, int ZW) {
     // All tiles of a segment in one workgroup where that leaves two to a compute unit: it meets the segment's gates and the kernel's
     // arguments once (16 heads of 16384 tokens of 128 x 128, bfloat16: 120 us tile by tile, 111 so; 64 heads of 2048: 61 and 56).
-    const int64_t slices = (a.side[0].z.width + ZW - 1) / ZW, all = int64_t(a.P) * a.Hv * a.segs * slices;
+    const int64_t slices = (s.z.width + ZW - 1) / ZW;
+    if (!KEYS) a.whole = int64_t(a.P) * a.Hv * a.segs * slices >= 2 * kCus;
+    const int64_t unit = slices * (!KEYS && a.whole ? 1 : a.seg_tokens / C::QT) * (KEYS ? 1 : a.Hv / a.Hk);
+    const int64_t units = int64_t(a.P) * a.Hk * a.segs, xcds = lin_xcds(units);
+    return (units + xcds - 1) / xcds * xcds * unit;
+}
+// single: the end states that go with the readings of one segment, or null.
+template <typename T, int XP, int ZW, bool EVEN> hipError_t attend_go(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
+    using C = AttendCfg<T, XP, ZW, false, EVEN>;
     AttendArgs b = a;
-    b.whole = !KEYS && all >= 2 * kCus;
-    const int64_t unit = slices * (b.whole ? 1 : a.seg_tokens / C::QT) * (KEYS ? 1 : a.Hv / a.Hk);
-    const int64_t units = int64_t(a.P) * a.Hk * a.segs, xcds = lin_xcds(units), blocks = (units + xcds - 1) / xcds * xcds * unit;
-    if constexpr (!KEYS) {
-        if (single) {
-            constexpr size_t other = StateCfg<T, XP, ZW, EVEN>::kLds;
-            hipLaunchKernelGGL((lin_single_kernel<T, XP, ZW, EVEN>), dim3(unsigned(blocks + slices * a.P * a.Hv)), dim3(256),
-                               C::kLds > other ? C::kLds : other, st, b, *single, int(blocks));
-            return hipGetLastError();
-        }
+    const int64_t blocks = attend_blocks<C, false>(b, a.side[0], ZW);
+    if (single) {
+        constexpr size_t other = StateCfg<T, XP, ZW, EVEN>::kLds;
+        const int64_t states = (a.V + ZW - 1) / ZW * a.P * a.Hv;
+        hipLaunchKernelGGL((lin_single_kernel<T, XP, ZW, EVEN>), dim3(unsigned(blocks + states)), dim3(256), C::kLds > other ? C::kLds : other, st, b, *single,
+                           int(blocks));
+    } else {
+        hipLaunchKernelGGL((lin_attend_kernel<T, XP, ZW, EVEN>), dim3(unsigned(blocks)), dim3(256), C::kLds, st, b);
     }
-    hipLaunchKernelGGL((lin_attend_kernel<T, XP, ZW, KEYS, EVEN>), dim3(unsigned(blocks), KEYS ? 2u : 1u), dim3(256), C::kLds, st, b);
     return hipGetLastError();
 }
-template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_even(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
-    constexpr int vec = 16 / sizeof(T);
-    return a.K % vec == 0 && a.V % vec == 0 ? attend_go<T, XP, ZW, KEYS, true>(a, single, st) : attend_go<T, XP, ZW, KEYS, false>(a, single, st);
+template <typename T, int KP, int VP, bool EVEN> constexpr size_t grads_lds() {
+    constexpr size_t keys = AttendCfg<T, VP, lin_slice(KP), true, EVEN>::kLds, values = AttendCfg<T, KP, lin_slice(VP), false, EVEN>::kLds;
+    static_assert(keys <= 80 * 1024 && values <= 80 * 1024, "two workgroups to a compute unit");
+    return keys > values ? keys : values;
 }
-template <typename T, int XP, bool KEYS> hipError_t attend_slices(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
-    return lin_slice(a.side[0].z.width) == 64 ? attend_even<T, XP, 64, KEYS>(a, single, st) : attend_even<T, XP, 128, KEYS>(a, single, st);
+template <typename T, int KP, int VP, bool EVEN> hipError_t grads_go(const AttendArgs &a, hipStream_t st) {
+    AttendArgs b = a;
+    const int64_t keys = attend_blocks<AttendCfg<T, VP, lin_slice(KP), true, EVEN>, true>(b, a.side[0], lin_slice(KP));
+    const int64_t values = attend_blocks<AttendCfg<T, KP, lin_slice(VP), false, EVEN>, false>(b, a.side[2], lin_slice(VP));
+    const int64_t all = 2 * keys + values, most = 1 << 23;      // 2^32 threads to a launch
+    for (int64_t first = 0; first < all; first += most)
+        hipLaunchKernelGGL((lin_grads_kernel<T, KP, VP, EVEN>), dim3(unsigned(all - first < most ? all - first : most)), dim3(256),
+                           (grads_lds<T, KP, VP, EVEN>()), st, b, int(keys), int(first));
+    return hipGetLastError();
 }
-template <typename T, bool KEYS> hipError_t attend(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
-    switch (lin_width(a.side[0].x.width)) {
-        case 64: return attend_slices<T, 64, KEYS>(a, single, st);
-        case 128: return attend_slices<T, 128, KEYS>(a, single, st);
-        default: return attend_slices<T, 256, KEYS>(a, single, st);
+
+template <typename T> bool lin_even(int K, int V) { return K % int(16 / sizeof(T)) == 0 && V % int(16 / sizeof(T)) == 0; }
+// f(KP or XP, VP or ZW, EVEN as constants) for the padded widths.
+template <typename F> hipError_t for_width(int width, F f) {
+    switch (width) {
+        case 64: return f(std::integral_constant<int, 64>{});
+        case 128: return f(std::integral_constant<int, 128>{});
+        default: return f(std::integral_constant<int, 256>{});
     }
 }
-template <typename T, int XP, int ZW, bool KEYS> hipError_t attend_attr() {
-    constexpr size_t bytes = AttendCfg<T, XP, ZW, KEYS, true>::kLds, other = StateCfg<T, XP, ZW, true>::kLds;
-    static_assert(bytes <= 80 * 1024 && other <= 80 * 1024, "two workgroups to a compute unit");
-    auto set = [](auto kernel, size_t n) {
-        return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(n));
-    };
-    hipError_t e = set(&lin_attend_kernel<T, XP, ZW, KEYS, true>, bytes);
-    if (e == hipSuccess) e = set(&lin_attend_kernel<T, XP, ZW, KEYS, false>, bytes);
-    if constexpr (!KEYS) {
-        if (e == hipSuccess) e = set(&lin_single_kernel<T, XP, ZW, true>, bytes > other ? bytes : other);
-        if (e == hipSuccess) e = set(&lin_single_kernel<T, XP, ZW, false>, bytes > other ? bytes : other);
-    }
+template <typename T> hipError_t attend(const AttendArgs &a, const StateArgs *single, hipStream_t st) {
+    return for_width(lin_width(a.side[0].x.width), [&](auto xp) {
+        constexpr int XP = decltype(xp)::value;
+        const bool even = lin_even<T>(a.K, a.V);
+        if (lin_slice(a.side[0].z.width) == 64) return even ? attend_go<T, XP, 64, true>(a, single, st) : attend_go<T, XP, 64, false>(a, single, st);
+        return even ? attend_go<T, XP, 128, true>(a, single, st) : attend_go<T, XP, 128, false>(a, single, st);
+    });
+}
+template <typename T> hipError_t attend_grads(const AttendArgs &a, hipStream_t st) {
+    return for_width(lin_width(a.K), [&](auto kp) {
+        return for_width(lin_width(a.V), [&](auto vp) {
+            constexpr int KP = decltype(kp)::value, VP = decltype(vp)::value;
+            return lin_even<T>(a.K, a.V) ? grads_go<T, KP, VP, true>(a, st) : grads_go<T, KP, VP, false>(a, st);
+        });
+    });
+}
+
+template <typename F> hipError_t set_lds(F kernel, size_t bytes) {
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+}
+template <typename T, int XP, int ZW> hipError_t attend_attr() {
+    constexpr size_t bytes = AttendCfg<T, XP, ZW, false, true>::kLds, other = StateCfg<T, XP, ZW, true>::kLds, both = bytes > other ? bytes : other;
+    static_assert(both <= 80 * 1024, "two workgroups to a compute unit");
+    hipError_t e = set_lds(&lin_attend_kernel<T, XP, ZW, true>, bytes);
+    if (e == hipSuccess) e = set_lds(&lin_attend_kernel<T, XP, ZW, false>, bytes);
+    if (e == hipSuccess) e = set_lds(&lin_single_kernel<T, XP, ZW, true>, both);
+    return e == hipSuccess ? set_lds(&lin_single_kernel<T, XP, ZW, false>, both) : e;
+}
+template <typename T> hipError_t attend_prepare() {
+    hipError_t e = hipSuccess;
+    for (int width : {64, 128, 256})
+        if (e == hipSuccess)
+            e = for_width(width, [](auto xp) {
+                const hipError_t r = attend_attr<T, decltype(xp)::value, 64>();
+                return r == hipSuccess ? attend_attr<T, decltype(xp)::value, 128>() : r;
+            });
     return e;
 }
-template <typename T, bool KEYS> hipError_t attend_prepare() {
-    hipError_t e = attend_attr<T, 64, 64, KEYS>();
-    if (e == hipSuccess) e = attend_attr<T, 64, 128, KEYS>();
-    if (e == hipSuccess) e = attend_attr<T, 128, 64, KEYS>();
-    if (e == hipSuccess) e = attend_attr<T, 128, 128, KEYS>();
-    if (e == hipSuccess) e = attend_attr<T, 256, 64, KEYS>();
-    if (e == hipSuccess) e = attend_attr<T, 256, 128, KEYS>();
+template <typename T> hipError_t grads_prepare() {
+    hipError_t e = hipSuccess;
+    for (int k : {64, 128, 256})
+        for (int v : {64, 128, 256})
+            if (e == hipSuccess)
+                e = for_width(k, [&](auto kp) {
+                    return for_width(v, [&](auto vp) {
+                        constexpr int KP = decltype(kp)::value, VP = decltype(vp)::value;
+                        const hipError_t r = set_lds(&lin_grads_kernel<T, KP, VP, true>, grads_lds<T, KP, VP, true>());
+                        return r == hipSuccess ? set_lds(&lin_grads_kernel<T, KP, VP, false>, grads_lds<T, KP, VP, false>()) : r;
+                    });
+                });
     return e;
 }
 
 // One translation unit for each element type and kind (linear_attend_*.hip).
-hipError_t attend_values_bf16(const AttendArgs &a, const StateArgs *single, hipStream_t st);
-hipError_t attend_values_f32(const AttendArgs &a, const StateArgs *single, hipStream_t st);
-hipError_t attend_keys_bf16(const AttendArgs &a, hipStream_t st);
-hipError_t attend_keys_f32(const AttendArgs &a, hipStream_t st);
-hipError_t attend_prepare_values_bf16();
-hipError_t attend_prepare_values_f32();
-hipError_t attend_prepare_keys_bf16();
-hipError_t attend_prepare_keys_f32();
+hipError_t attend_bf16(const AttendArgs &a, const StateArgs *single, hipStream_t st);
+hipError_t attend_f32(const AttendArgs &a, const StateArgs *single, hipStream_t st);
+hipError_t attend_grads_bf16(const AttendArgs &a, hipStream_t st);
+hipError_t attend_grads_f32(const AttendArgs &a, hipStream_t st);
+hipError_t attend_prepare_bf16();
+hipError_t attend_prepare_f32();
+hipError_t grads_prepare_bf16();
+hipError_t grads_prepare_f32();
 
 }  // namespace sdm
