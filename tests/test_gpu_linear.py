@@ -453,6 +453,23 @@ def test_retained_graph(gpu):
     assert all(torch.equal(s, t) for s, t in zip(a, b))
 
 
+@pytest.mark.parametrize("dtype,T", [(torch.float32, t) for t in (127, 128, 129, 192, 193)] + [(torch.bfloat16, t) for t in (255, 256, 257, 384, 385)])
+def test_lengths_around_segments(gpu, dtype, T):
+    """One token less and more than the lengths at which segments' number and length change, forward and backward."""
+    import chunked_sparse_delta_amd as sdm
+    x = make(1, T, 1, 2, 24, 40, dtype, seed=T)
+    out, final = want(x)
+    size, fsize = want(x, absolute=True)
+    d = on(x, gpu)
+    state = torch.empty_like(d["state"])
+    close(sdm.linear_attention_fwd(*(d[n] for n in NAMES), state_out=state), out, size, dtype)
+    close(state, final, fsize, torch.float32)
+    gen = torch.Generator().manual_seed(T)
+    go, gs = torch.randn((1, T, 2, 40), generator=gen).to(dtype), torch.randn((1, 2, 24, 40), generator=gen)
+    got = sdm.linear_attention_bwd(*(d[n] for n in NAMES), go.to(gpu), grad_state=gs.to(gpu))
+    check_grads(got, x, go, gs, dtype)
+
+
 def test_no_grad_keeps_nothing(gpu):
     """Without autograd: the same bits, no graph, and no memory for a backward."""
     import chunked_sparse_delta_amd as sdm
