@@ -15,12 +15,14 @@
 // 32 rows of M, while the next one is on its way through registers; two workgroups share a compute unit.
 // Precision: sums are float32, G float64. M, decayed scores and float32 rows are three bfloat16 pieces each, so that products keep
 // float32's 24 bits; results are rounded once.
-// Measured (bfloat16, 128 x 128, 256 tokens to a segment): the readings of 16 heads of 16384 tokens 110 us. Matrix instructions
-// alone would take 26 (62.9 M cycles on 1024 SIMDs at 2.4 GHz), memory 53 (199 MB read, 66 written). Neither hides the other well. A form that
-// took 120 us took 84 without its matrix instructions and 57 with nothing but the tiles' way through LDS; a workgroup with one tile
-// takes 7. Without effect on that form (2 % at most): tiles or M another step ahead in registers or in a second LDS buffer, operands
-// read from LDS ahead of the products before, 32 tokens of y and z at a time, wavefronts' priorities. With effect: one XCD for what
-// reads the same rows (312 MB read before), all tiles of a segment in one workgroup, loads without branches around them.
+// Measured (bfloat16, 128 x 128, 256 tokens to a segment): the readings of 16 heads of 16384 tokens 108 us; dq, dk and dv of 4 x 16 heads
+// of 2048 tokens, keys shared by two, 200 (of 147 and 55 one after the other). Of the 108: matrix instructions alone would take 26 (62.9 M cycles on
+// 1024 SIMDs at 2.4 GHz), the other vector instructions about 30, a copy of as many bytes 74 (319 MB read, 67 written). None hides
+// the others well. A form that took 120 us took 84 without its matrix instructions and 57 with nothing but the tiles' way through
+// LDS; a workgroup with one tile takes 7. Without effect on that form (2 % at most): tiles or M another step ahead in registers or in a
+// second LDS buffer, operands read from LDS ahead of the products before, 32 tokens of y and z at a time, wavefronts' priorities; eight
+// wavefronts that share a whole segment's tiles, two LDS buffers of them, took 119. With effect: one XCD for what reads
+// the same rows, all tiles of a segment in one workgroup in turn, loads without branches around them.
 #pragma once
 
 #include "linear_state.h"
@@ -326,7 +328,8 @@ template <typename T, int XP, int ZW, bool EVEN> __global__ __launch_bounds__(25
     if (int(blockIdx.x) < attends) lin_attend<T, XP, ZW, false, EVEN>(a, a.side[0], blockIdx.x);
     else lin_state<T, XP, ZW, EVEN>(s, int(blockIdx.x) - attends);
 }
-// dq, dk and dv: `keys` workgroups for each of the first two, then those of dv, which fill the device where the others leave it. The
+// dq, dk and dv: `keys` workgroups for each of the first two, then those of dv, which fill the device where the others leave it (of
+// 3 x 6 heads of 301 float32 tokens of 40 x 72: 36 us in one launch, 34 and 16 in two). The
 // launch begins with workgroup `first`.
 template <typename T, int KP, int VP, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_grads_kernel(AttendArgs a, int keys, int first) {
     const int b = int(blockIdx.x) + first;
