@@ -580,13 +580,23 @@ __global__ __launch_bounds__(64) void gn_join_kernel(GnArgs a, int V) {
     }
 }
 
-// A thread's channels' mean and rstd.
-template <int V> __device__ __forceinline__ void gn_thread_stats(const GnArgs &a, const GnAt &at, int64_t n, float (&mean)[V], float (&rstd)[V]) {
+// The groups of a thread's channels, 0 for those that are not there.
+template <int V> __device__ __forceinline__ void gn_groups(const GnArgs &a, const GnAt &at, int (&g)[V]) {
+    int q = at.c / a.D, r = at.c - q * a.D;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t g = j < at.left ? n * a.G + (at.c + j) / a.D : 0;
-        mean[j] = j < at.left ? a.mean[g] : 0.0f;
-        rstd[j] = j < at.left ? a.rstd[g] : 0.0f;
+        g[j] = j < at.left ? q : 0;
+        const bool ends = ++r == a.D;
+        q += ends;
+        r = ends ? 0 : r;
+    }
+}
+// A thread's channels' mean and rstd.
+template <int V> __device__ __forceinline__ void gn_thread_stats(const GnArgs &a, const int (&g)[V], int64_t n, float (&mean)[V], float (&rstd)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        mean[j] = a.mean[n * a.G + g[j]];
+        rstd[j] = a.rstd[n * a.G + g[j]];
     }
 }
 
@@ -598,7 +608,9 @@ template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_apply_ker
     float w[V], b[V], mean[V], rstd[V];
     gn_params<V>(a.weight, a.w_f32, at.c, at.left, 1.0f, w);
     gn_params<V>(a.bias, a.w_f32, at.c, at.left, 0.0f, b);
-    gn_thread_stats<V>(a, at, n, mean, rstd);
+    int g[V];
+    gn_groups<V>(a, at, g);
+    gn_thread_stats<V>(a, g, n, mean, rstd);
     const T *x = static_cast<const T *>(a.x) + n * a.x_sample + at.c;
     T *y = static_cast<T *>(a.y) + n * a.L * a.C + at.c;
 #pragma unroll 4
@@ -626,7 +638,9 @@ template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_bwd_sums_
         float w[V], b[V], mean[V], rstd[V], c1[V] = {}, c2[V] = {};
         gn_params<V>(a.weight, a.w_f32, at.c, at.left, 1.0f, w);
         gn_params<V>(a.bias, a.w_f32, at.c, at.left, 0.0f, b);
-        gn_thread_stats<V>(a, at, n, mean, rstd);
+        int g[V];
+        gn_groups<V>(a, at, g);
+        gn_thread_stats<V>(a, g, n, mean, rstd);
         const T *x = static_cast<const T *>(a.x) + n * a.x_sample + at.c, *dy = static_cast<const T *>(a.dy) + n * a.L * a.C + at.c;
 #pragma unroll 4
         for (int64_t r = r0 + at.tr; r < r1; r += a.p.rt) {
@@ -726,12 +740,13 @@ template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply
     float w[V], b[V], mean[V], rstd[V], m1[V], m2[V];
     gn_params<V>(a.weight, a.w_f32, at.c, at.left, 1.0f, w);
     gn_params<V>(a.bias, a.w_f32, at.c, at.left, 0.0f, b);
-    gn_thread_stats<V>(a, at, n, mean, rstd);
+    int g[V];
+    gn_groups<V>(a, at, g);
+    gn_thread_stats<V>(a, g, n, mean, rstd);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int64_t g = j < at.left ? (n * a.G + (at.c + j) / a.D) * 2 : 0;
-        m1[j] = j < at.left ? sums[g] * inv : 0.0f;
-        m2[j] = j < at.left ? sums[g + 1] * inv : 0.0f;
+        m1[j] = sums[(n * a.G + g[j]) * 2] * inv;
+        m2[j] = sums[(n * a.G + g[j]) * 2 + 1] * inv;
     }
     const T *x = static_cast<const T *>(a.x) + n * a.x_sample + at.c, *dy = static_cast<const T *>(a.dy) + n * a.L * a.C + at.c;
     T *dx = static_cast<T *>(a.dx) + n * a.L * a.C + at.c;
