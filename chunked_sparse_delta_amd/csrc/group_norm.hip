@@ -12,8 +12,8 @@
 //    where they are short; their sums meet by shuffles where a group is 8, 16, ... lanes of one wavefront, through LDS elsewhere.
 //  - Split: longer samples are cut into blocks of rows; one kernel leaves each block's sums, the next joins them and reads the rows again.
 // Measured: 8192 tokens of 4096 channels in 32 groups, bfloat16, silu: forward 36 us (134 MB, 3.7 TB/s), backward 52 (201 MB, 3.9 TB/s) and
-// 4 for the sums over workgroups; 64 tokens: 4.3. Split, 8 x 4096 rows of 512 channels: statistics 11, their join 4, values 16 (67 MB,
-// 4.3 TB/s); sums 21 (67 MB), their join 5, gradients 21 (101 MB, 4.7 TB/s), the parameters' sums 4. A large copy: 5.2 TB/s.
+// 4 for the sums over workgroups; 64 tokens: 4.3. Split, 8 x 4096 rows of 512 channels: statistics 11, their join 4, values 14 (67 MB,
+// 4.8 TB/s); sums 19 (67 MB), their join 5, gradients 19 (101 MB, 5.3 TB/s), the parameters' sums 4. A large copy: 5.2 TB/s.
 // Statistics: a thread's mean and sum of squared differences from it, joined with their counts (no difference of large sums).
 // All sums run in float32 in a fixed order: results are the same from run to run.
 #include <type_traits>
@@ -485,6 +485,9 @@ template <typename T, int NT, int ITEMS, int MODE> __global__ __launch_bounds__(
 // ---- split -----------------------------------------------------------------------------------------------------------
 
 constexpr int kGnThreads = 256;
+// Rows of a thread on their way at once (one after another the sums of 8 x 4096 x 512 bfloat16 took 21 us, so 19; the gradients' kernel, short of
+// registers, the other way round 19 and 23).
+constexpr int kGnAhead = 4;
 
 // The statistics of the groups of one block of rows: part[sample][block][tile's groups or pieces] as (mean, sum of squares).
 template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
@@ -613,17 +616,27 @@ template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_apply_ker
     gn_thread_stats<V>(a, g, n, mean, rstd);
     const T *x = static_cast<const T *>(a.x) + n * a.x_sample + at.c;
     T *y = static_cast<T *>(a.y) + n * a.L * a.C + at.c;
-#pragma unroll 4
-    for (int64_t r = r0 + at.tr; r < r1; r += a.p.rt) {
-        float z[V] = {};
-        if (r < nv) {
-            float v[V];
-            NormVec<T>::unpack(gn_load<T, V>(x + r * a.x_row, at.left), v);
+    for (int64_t r0t = r0 + at.tr; r0t < r1; r0t += kGnAhead * a.p.rt) {
+        typename NormVec<T>::raw rx[kGnAhead];
 #pragma unroll
-            for (int j = 0; j < V; ++j) z[j] = fmaf((v[j] - mean[j]) * rstd[j], w[j], b[j]);
-            gn_act<V>(a.act, z);
+        for (int u = 0; u < kGnAhead; ++u) {
+            const int64_t r = r0t + u * a.p.rt;
+            rx[u] = gn_load<T, V>(x + r * a.x_row, r < r1 && r < nv ? at.left : 0);
         }
-        norm_put<T, V>(y + r * a.C, 0, at.left, z);
+#pragma unroll
+        for (int u = 0; u < kGnAhead; ++u) {
+            const int64_t r = r0t + u * a.p.rt;
+            if (r >= r1) break;
+            float z[V] = {};
+            if (r < nv) {
+                float v[V];
+                NormVec<T>::unpack(rx[u], v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) z[j] = fmaf((v[j] - mean[j]) * rstd[j], w[j], b[j]);
+                gn_act<V>(a.act, z);
+            }
+            norm_put<T, V>(y + r * a.C, 0, at.left, z);
+        }
     }
 }
 
@@ -642,21 +655,31 @@ template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_bwd_sums_
         gn_groups<V>(a, at, g);
         gn_thread_stats<V>(a, g, n, mean, rstd);
         const T *x = static_cast<const T *>(a.x) + n * a.x_sample + at.c, *dy = static_cast<const T *>(a.dy) + n * a.L * a.C + at.c;
-#pragma unroll 4
-        for (int64_t r = r0 + at.tr; r < r1; r += a.p.rt) {
-            float v[V], d[V], z[V];
-            NormVec<T>::unpack(gn_load<T, V>(x + r * a.x_row, at.left), v);
-            NormVec<T>::unpack(gn_load<T, V>(dy + r * a.C, at.left), d);
+        for (int64_t r0t = r0 + at.tr; r0t < r1; r0t += kGnAhead * a.p.rt) {
+            typename NormVec<T>::raw rx[kGnAhead], rd[kGnAhead];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[j] = (v[j] - mean[j]) * rstd[j];
-                z[j] = fmaf(v[j], w[j], b[j]);
+            for (int u = 0; u < kGnAhead; ++u) {
+                const int64_t r = r0t + u * a.p.rt;
+                rx[u] = gn_load<T, V>(x + r * a.x_row, r < r1 ? at.left : 0);
+                rd[u] = gn_load<T, V>(dy + r * a.C, r < r1 ? at.left : 0);
             }
-            gn_slope<V>(a.act, z, d);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                c1[j] += d[j];
-                c2[j] = fmaf(d[j], v[j], c2[j]);
+            for (int u = 0; u < kGnAhead; ++u) {
+                if (r0t + u * a.p.rt >= r1) break;
+                float v[V], d[V], z[V];
+                NormVec<T>::unpack(rx[u], v);
+                NormVec<T>::unpack(rd[u], d);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    v[j] = (v[j] - mean[j]) * rstd[j];
+                    z[j] = fmaf(v[j], w[j], b[j]);
+                }
+                gn_slope<V>(a.act, z, d);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    c1[j] += d[j];
+                    c2[j] = fmaf(d[j], v[j], c2[j]);
+                }
             }
         }
 #pragma unroll
@@ -852,8 +875,8 @@ GnPlan gn_plan(int64_t N, int64_t L, int C, int G, int V, bool bwd) {
     }
     p.rt = kGnThreads / p.cv;
     p.lanes = pow2_at_most(kGnThreads / (p.gt > 0 ? p.gt : 1) < 64 ? kGnThreads / (p.gt > 0 ? p.gt : 1) : 64);
-    // Blocks of eight rows to a thread, or of four where eight leave the device half empty (8 x 4096 x 512 bfloat16, training: eight
-    // 83 us, four 93, sixteen 81; 5 x 1001 x 320 float32: 51, 46 and 71), at most 2048 workgroups.
+    // Blocks of eight rows to a thread, or of four where eight leave the device half empty (8 x 4096 x 512 bfloat16, training, in a form
+    // that took 83 us with eight: four 93, sixteen 81; 5 x 1001 x 320 float32: 51, 46 and 71), at most 2048 workgroups.
     const int64_t eight = (L + p.rt * 8 - 1) / (p.rt * 8), four = (L + p.rt * 4 - 1) / (p.rt * 4), most_blocks = 2048 / (N * p.tiles < 2048 ? N * p.tiles : 2048);
     const int64_t fit = N * p.tiles * eight >= 512 ? eight : four, blocks = fit < most_blocks ? fit : most_blocks;
     p.block_rows = int((L + blocks - 1) / blocks);
