@@ -6,6 +6,7 @@
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include "sdm_linear.h"
 
@@ -92,6 +93,13 @@ sdm_exec exec_of(int index, const OptTensor &workspace) {
     return e;
 }
 
+// The caller's tensors that a call has written through their pointers: with their versions raised, a backward that saved one of them
+// is refused, as after any other write in place. (Inference tensors have no version.)
+void wrote(std::initializer_list<const OptTensor *> tensors) {
+    for (const OptTensor *t : tensors)
+        if (given(*t) && !(*t)->is_inference()) torch::autograd::impl::bump_version(**t);
+}
+
 // Python's once_differentiable: a gradient of these gradients is an error, not nothing.
 variable_list once(variable_list grads) {
     if (!at::GradMode::is_enabled()) return grads;
@@ -176,7 +184,9 @@ Tensor la_fwd(const OptTensor &state, const OptTensor &k, const OptTensor &v, co
     need(state_out, "state_out", a.state, at::kFloat, a.dev);
     check_kept(a, kept);
     const Tensor out = dense_out(out_, *v);
-    la_values(a, state, given(state_out) ? state_out : state, valid, out, kept, workspace);
+    const OptTensor &final = given(state_out) ? state_out : state;
+    la_values(a, state, final, valid, out, kept, workspace);
+    wrote({&final, &out_, &kept});
     return out;
 }
 
@@ -190,8 +200,10 @@ Tensor la_step(const OptTensor &state, const OptTensor &k, const OptTensor &v, c
     need(ids, "state_ids", {a.state[0]}, at::kInt, a.dev);
     const Tensor out = dense_out(out_, *v);
     const sdm_exec e = exec_of(a.index, std::nullopt);
-    check_rc(api.la_step(&a.shape, &a.q, &a.k, &a.v, a.g, a.per_token, ptr<float>(state), given(state_out) ? ptr<float>(state_out) : ptr<float>(state),
-                         ptr<int32_t>(ids), pool[0], ptr<int32_t>(valid), out.data_ptr(), &e));
+    const OptTensor &final = given(state_out) ? state_out : state;
+    check_rc(api.la_step(&a.shape, &a.q, &a.k, &a.v, a.g, a.per_token, ptr<float>(state), ptr<float>(final), ptr<int32_t>(ids), pool[0],
+                         ptr<int32_t>(valid), out.data_ptr(), &e));
+    wrote({&final, &out_});
     return out;
 }
 
@@ -250,7 +262,8 @@ struct LinearAttention : torch::autograd::Function<LinearAttention> {
         if (keep && (wants[0] || wants[1] || wants[2] || wants[3] || wants[4])) kept = scratch(api.la_kept(&a.shape), a.dev);
         la_values(a, state, final, valid, out, kept, std::nullopt);
         auto some = [](const OptTensor &t) { return given(t) ? *t : Tensor(); };
-        ctx->save_for_backward({some(state), k, v, g, q, some(valid), some(kept)});
+        // (the start state is not read where `kept` is there: the caller may advance it before the backward)
+        ctx->save_for_backward({given(kept) ? Tensor() : some(state), k, v, g, q, some(valid), some(kept)});
         if (scale) ctx->saved_data["scale"] = *scale;
         for (int i = 0; i < 5; ++i) ctx->saved_data[std::string("want") + char('0' + i)] = wants[i];
         ctx->set_materialize_grads(false);
@@ -342,6 +355,7 @@ py::tuple gn_fwd(const Tensor &x, int64_t groups, const OptTensor &weight, const
     const Norm a = norm_of(x, groups, weight, bias, activation, eps, valid);
     need(out, "out", x.sizes(), x.scalar_type(), a.dev);
     const NormValues r = gn_values(a, x, weight, bias, valid, out, workspace);
+    wrote({&out});
     return py::make_tuple(r.y, r.mean, r.rstd);
 }
 
