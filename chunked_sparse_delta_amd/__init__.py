@@ -28,6 +28,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.graph import increment_version
 
 __all__ = ["SdmError", "sdm_fwd", "sdm_fwd_noalloc", "sdm_fwd_phase1", "sdm_fwd_phase2", "sdm_bwd", "sdm_write_read", "bwd_workspace_bytes", "chunk_mats", "chunk_records", "wy_solve", "product_key_topk", "product_key_topk_backward",
            "workspace_bytes", "plan",
@@ -161,6 +162,14 @@ def _expect(t: torch.Tensor, name: str, shape, dtype, device) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+def _wrote(*tensors) -> None:
+    """The caller's tensors (None: not given) that a call has written through their pointers: with their versions raised, a
+    backward that saved one of them is refused, as after any other write in place."""
+    for t in tensors:
+        if t is not None:
+            increment_version(t)
+
+
 def workspace_bytes(P: int, T: int, C: int, W: int, R: int, hd: int, slab_steps: int = 0) -> int:
     """Bytes of scratch sdm_fwd needs for slabs of ``slab_steps`` steps (0: all steps)."""
     return int(_load().sdm_fwd_workspace_bytes(P, T, C, W, R, hd, slab_steps))
@@ -276,6 +285,7 @@ def sdm_fwd(bank: torch.Tensor, k_idx: torch.Tensor, k_val: torch.Tensor, v: tor
     rc = lib.sdm_fwd(P, T, chunk, ctypes.byref(slots), ctypes.byref(weights), _ptr(beta), _ptr(log_decay), G,
                      _ptr(v), ctypes.byref(bk), _ptr(valid_tokens), _ptr(out), ctypes.byref(ex))
     _check_rc(lib, rc)
+    _wrote(bank, out, repeated_writes)
     return out
 
 
@@ -307,6 +317,7 @@ def sdm_fwd_noalloc(bank: torch.Tensor, k_idx: torch.Tensor, k_val: torch.Tensor
     rc = lib.sdm_fwd_noalloc(P, T, chunk, ctypes.byref(slots), ctypes.byref(weights), _ptr(beta), _ptr(log_decay),
                              G, _ptr(v), ctypes.byref(bk), _ptr(valid_tokens), _ptr(out), ctypes.byref(ex))
     _check_rc(lib, rc)
+    _wrote(bank, out, repeated_writes)
     return out
 
 
@@ -374,6 +385,7 @@ def sdm_bwd(bank: torch.Tensor, k_idx: torch.Tensor, k_val: torch.Tensor, v: tor
     rc = lib.sdm_bwd(P, T, ctypes.byref(slots), ctypes.byref(weights), _ptr(beta), _ptr(log_decay), G, _ptr(v),
                      ctypes.byref(bk), _ptr(valid_tokens), _ptr(grad_out), ctypes.byref(gr), mode, ctypes.byref(ex))
     _check_rc(lib, rc)
+    _wrote(grad_bank)      # (the bank is restored)
     return out
 
 
@@ -449,6 +461,7 @@ def _fwd_part(part: int, bank, k_idx, k_val, v, beta, log_decay, q_idx, q_val, *
     rc = fn(P, T, chunk, ctypes.byref(slots), ctypes.byref(weights), _ptr(beta), _ptr(log_decay), G, _ptr(v),
             ctypes.byref(bk), _ptr(valid_tokens), _ptr(out), ctypes.byref(ex))
     _check_rc(lib, rc)
+    _wrote(workspace if part == 1 else bank, out, repeated_writes)
 
 
 def sdm_fwd_phase1(bank, k_idx, k_val, v, beta, log_decay, q_idx, q_val, *, workspace: torch.Tensor, chunk: int = 64,

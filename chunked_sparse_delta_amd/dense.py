@@ -25,7 +25,7 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _DTYPES, _check_rc, _expect, _load, _stream_ptr
+from . import _DTYPES, _check_rc, _expect, _load, _stream_ptr, _wrote
 
 __all__ = ["gated_delta_fwd", "gated_delta_step", "gated_delta_bwd", "gated_delta_rule", "gated_delta_workspace_bytes",
            "layer_norm_fwd", "layer_norm_bwd", "layer_norm"]
@@ -180,7 +180,7 @@ def gated_delta_fwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
         state_out = state
     else:
         _need(state_out, "state_out", full, torch.float32, dev)
-    out = _out(out, v, stream)
+    given, out = out, _out(out, v, stream)
     if workspace is None:
         workspace = _scratch(lib, shape, 0, dev, stream)
     call = lib.sdm_gated_delta_fwd_keep if keep else lib.sdm_gated_delta_fwd
@@ -188,6 +188,7 @@ def gated_delta_fwd(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor,
               out.data_ptr(), _exec(stream, index, workspace))
     if rc:
         _check_rc(lib, rc)
+    _wrote(state_out, given, workspace if keep else None)
     return out
 
 
@@ -213,12 +214,13 @@ def gated_delta_step(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta
         _need(state_out, "state_out", pool, torch.float32, dev)
     if state_ids is not None:
         _need(state_ids, "state_ids", full[:1], torch.int32, dev)
-    out = _out(out, v, stream)
+    given, out = out, _out(out, v, stream)
     rc = lib.sdm_gated_delta_step(shape, qr, kr, vr, beta.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
                                   state_out.data_ptr(), _ptr(state_ids), slots, _ptr(valid_tokens), out.data_ptr(),
                                   _exec(stream, index))
     if rc:
         _check_rc(lib, rc)
+    _wrote(state_out, given)
     return out
 
 
@@ -266,7 +268,8 @@ class _GatedDeltaRule(torch.autograd.Function):
             kept = torch.empty(max(n, 256), dtype=torch.uint8, device=v.device)     # 0: the call itself reports why
         out = gated_delta_fwd(state, k, v, beta, log_decay, q, scale=scale, valid_tokens=valid_tokens, state_out=final,
                               workspace=kept, keep=kept is not None)
-        ctx.save_for_backward(state, k, v, beta, log_decay, q, valid_tokens, kept)
+        # (the start state is not read where `kept` is there: the caller may advance it before the backward)
+        ctx.save_for_backward(None if kept is not None else state, k, v, beta, log_decay, q, valid_tokens, kept)
         ctx.scale = scale
         ctx.set_materialize_grads(False)
         return out, final
@@ -326,6 +329,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     float32, or None. Returns (y, mean, rstd); mean and rstd float32 [rows] are what layer_norm_bwd needs."""
     lib = _load()
     rows, N, code, wdtype, index = _norm_inputs(x, weight, bias)
+    given = out
     if out is None:
         out = torch.empty_like(x) if stream is None else _new(x.shape, x.dtype, x.device, stream)
     else:
@@ -339,6 +343,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
                                 eps, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _exec(stream, index))
     if rc:
         _check_rc(lib, rc)
+    _wrote(given)
     return out, mean, rstd
 
 
