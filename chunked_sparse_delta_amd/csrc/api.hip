@@ -8,6 +8,7 @@
 
 #include <stdlib.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "sdm.h"
@@ -125,6 +126,46 @@ int device_info(DeviceInfo **out) {
 }
 
 }  // namespace
+
+bool sdm::Extent::dense() const {
+    int64_t next = width;
+    for (int i = 2; i >= 0; --i) {
+        if (axis[i].n > 1 && axis[i].stride != next) return false;
+        next *= axis[i].n;
+    }
+    return true;
+}
+
+namespace {
+
+// Whether bytes [from, to), counted from the array's first one, meet its rows of `width` bytes under `count` axes, the longest
+// stride (in bytes) first. Blocks of the first axis that lie in between meet them whole; the first and the last are looked into.
+bool rows_meet(const sdm::Extent::Axis *axis, int count, int64_t width, int64_t from, int64_t to) {
+    int64_t inner = width;      // bytes from a block's first to its last
+    for (int i = 1; i < count; ++i) inner += (axis[i].n - 1) * axis[i].stride;
+    const int64_t step = count > 0 ? axis[0].stride : 0, all = inner + (count > 0 ? (axis[0].n - 1) * step : 0);
+    if (from >= all || to <= 0) return false;
+    if (count == 0 || step < inner) return true;
+    const int64_t first = from < inner ? 0 : (from - inner) / step + 1, last = std::min(axis[0].n - 1, (to - 1) / step);
+    if (first > last) return false;
+    return last - first > 1 || rows_meet(axis + 1, count - 1, width, from - first * step, to - first * step) ||
+           rows_meet(axis + 1, count - 1, width, from - last * step, to - last * step);
+}
+
+}  // namespace
+
+bool sdm::Extent::meets(const void *p, size_t n) const {
+    if (n == 0 || width == 0) return false;
+    Axis real[3];
+    int count = 0;
+    for (const Axis &x : axis) {
+        if (x.n == 0) return false;
+        if (x.n > 1 && x.stride > 0) real[count++] = {x.n, x.stride * es};
+    }
+    std::sort(real, real + count, [](const Axis &a, const Axis &b) { return a.stride > b.stride; });
+    const int64_t from = int64_t(reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(data));
+    return rows_meet(real, count, width * es, from, from + int64_t(n));
+}
 
 int sdm::device_cus(int *cus) {
     DeviceInfo *d = nullptr;

@@ -1001,6 +1001,19 @@ int gn_args(const sdm_group_shape *s, bool bwd, const void *x, int64_t x_sample,
     return SDM_OK;
 }
 
+// Whether an output of n bytes at p (null: not wanted) meets an input. `in_place`: it may be x, where that is dense, or grad_out, whose
+// elements the thread that writes the output's reads before, and no other.
+bool gn_meets(const sdm_group_shape *s, const GnArgs &a, const void *p, size_t n, bool in_place) {
+    if (!p) return false;
+    const int es = s->dtype == SDM_BF16 ? 2 : 4;
+    const Extent x{a.x, {{1, 0}, {a.N, a.x_sample}, {a.L, a.x_row}}, a.C, es};
+    const size_t params = size_t(a.C) * (a.w_f32 ? 4 : 2), groups = a.dy ? size_t(a.N) * size_t(a.G) * 4 : 0;
+    auto dense = [&](const void *q, size_t m) { return q && overlap(p, n, q, m); };
+    return (!(in_place && p == a.x && x.dense()) && x.meets(p, n)) ||
+           (!(in_place && p == a.dy) && dense(a.dy, size_t(a.N) * size_t(a.L) * size_t(a.C) * size_t(es))) || dense(a.weight, params) ||
+           dense(a.bias, params) || dense(a.valid, size_t(a.N) * 4) || dense(a.mean, groups) || dense(a.rstd, groups);
+}
+
 int gn_workspace(const sdm_exec *exec, size_t need, GnArgs *a) {
     if (need == 0) return SDM_OK;
     if (!exec->workspace || exec->workspace_bytes < need)
@@ -1034,6 +1047,10 @@ int sdm_group_norm_fwd(const sdm_group_shape *s, const void *x, int64_t x_sample
     if (!mean || !rstd || (s->rows > 0 && (!x || !y))) return fail(SDM_ERR_NULL, "x, y, mean and rstd must not be NULL");
     if (!aligned(y, s->dtype == SDM_BF16 ? 2 : 4) || !aligned(mean, 4) || !aligned(rstd, 4))
         return fail(SDM_ERR_ALIGN, "y, mean and rstd must be aligned to their element size");
+    const size_t groups = size_t(a.N) * size_t(a.G) * 4;
+    if (gn_meets(s, a, y, size_t(a.N) * size_t(a.L) * size_t(a.C) * (s->dtype == SDM_BF16 ? 2 : 4), true) || gn_meets(s, a, mean, groups, false) ||
+        gn_meets(s, a, rstd, groups, false))
+        return fail(SDM_ERR_SHAPE, "y, mean or rstd overlaps an input (y may be a dense x)");
     if ((rc = gn_workspace(exec, sdm_group_norm_workspace_bytes(s, 0), &a))) return rc;
     a.y = y; a.mean = mean; a.rstd = rstd;
     const hipStream_t st = static_cast<hipStream_t>(exec->stream);
@@ -1054,11 +1071,15 @@ int sdm_group_norm_bwd(const sdm_group_shape *s, const void *grad_out, const voi
         return fail(SDM_ERR_ALIGN, "the gradients, mean and rstd must be aligned to their element size");
     if (s->samples > 0 && (!mean || !rstd || (s->rows > 0 && (!grad_out || !x))))
         return fail(SDM_ERR_NULL, "grad_out, x, mean and rstd must not be NULL");
+    a.dy = grad_out;
+    a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
+    if (gn_meets(s, a, grad_x, size_t(a.N) * size_t(a.L) * size_t(a.C) * es, true) || gn_meets(s, a, grad_weight, size_t(a.C) * ws, false) ||
+        gn_meets(s, a, grad_bias, size_t(a.C) * ws, false))
+        return fail(SDM_ERR_SHAPE, "a gradient overlaps an input (grad_x may be grad_out, or a dense x)");
     const bool sums = grad_weight || grad_bias;
     const bool split = a.p.items == 0;
     if ((sums || split) && (rc = gn_workspace(exec, sdm_group_norm_workspace_bytes(s, 1), &a))) return rc;
-    a.dy = grad_out; a.dx = grad_x;
-    a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
+    a.dx = grad_x;
     const hipStream_t st = static_cast<hipStream_t>(exec->stream);
     const hipError_t e = s->dtype == SDM_BF16 ? gn_bwd<bf16>(a, sums, grad_weight, grad_bias, st) : gn_bwd<float>(a, sums, grad_weight, grad_bias, st);
     return e == hipSuccess ? SDM_OK : hip_fail(e, "group norm backward launch");

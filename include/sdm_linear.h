@@ -93,7 +93,8 @@ int sdm_linear_attention_bwd(const sdm_delta_shape *shape, const sdm_rows *q, co
  *     float32 parameters, bfloat16 rows either type.
  *   valid_rows: device int32 [samples], or NULL: rows at and past it are padding, which may hold
  *     anything; they do not count and give +0. A sample without a valid row has mean 0 and var 0.
- *   y: dense [samples, rows, channels], may be x where that is dense, but must not overlap an input otherwise; mean, rstd: device float32 [samples, groups], written.
+ *   y: dense [samples, rows, channels], may be x where that is dense, but must not overlap an input
+ *     otherwise; mean, rstd: device float32 [samples, groups], written.
  *   exec->workspace: sdm_group_norm_workspace_bytes(shape, 0) bytes, 256-byte aligned (where that is
  *     0, none).
  * At most 2^31 - 1 samples and rows of 2^20 channels. Bitwise reproducible.
@@ -120,8 +121,8 @@ int sdm_group_norm_fwd(const sdm_group_shape *shape, const void *x, int64_t x_sa
 /*
  * Its backward, from the mean and rstd that the forward wrote. grad_out, grad_x: dense
  * [samples, rows, channels] in dtype (padding rows of grad_x: zeros); grad_weight, grad_bias:
- * [channels] in weight_dtype; each gradient may be NULL (not wanted). Sums run in float32 in a
- * fixed order.
+ * [channels] in weight_dtype; each gradient may be NULL (not wanted). grad_x may be grad_out, or x
+ * where that is dense; none may overlap an input otherwise. Sums run in float32 in a fixed order.
  */
 int sdm_group_norm_bwd(const sdm_group_shape *shape, const void *grad_out, const void *x, int64_t x_sample, int64_t x_row,
                        const void *weight, const void *bias, const int32_t *valid_rows, const float *mean,
