@@ -924,7 +924,8 @@ size_t gn_floats(int64_t N, int C, int G, const GnPlan &p, bool bwd) {
     return size_t(N) * (size_t(p.blocks) * size_t(C) * 2 + size_t(G) * 2);
 }
 
-constexpr int64_t kGnGrid = int64_t(1) << 24;     // workgroups of 256 threads of a launch
+// Workgroups of 256 threads stay below 2^24 in a launch (a resident plan's always do).
+bool gn_launches(const GnPlan &p, int64_t N) { return p.items > 0 || N * p.blocks * p.tiles < int64_t(1) << 24; }
 dim3 gn_join_grid(const GnArgs &a) { return dim3(unsigned(a.N * a.G < 65536 ? a.N * a.G : 65536)); }
 
 template <typename T> hipError_t gn_fwd(const GnArgs &a, hipStream_t st) {
@@ -996,7 +997,7 @@ int gn_args(const sdm_group_shape *s, bool bwd, const void *x, int64_t x_sample,
     a->C = s->channels; a->G = s->groups; a->D = s->channels / s->groups;
     a->act = s->activation; a->w_f32 = s->weight_dtype == SDM_F32; a->eps = s->eps;
     a->p = gn_plan(s->samples > 0 ? s->samples : 1, s->rows, s->channels, s->groups, s->dtype == SDM_BF16 ? 8 : 4, bwd);
-    if (a->p.items == 0 && a->N * a->p.blocks * a->p.tiles >= kGnGrid)
+    if (!gn_launches(a->p, a->N))
         return fail(SDM_ERR_RANGE, "%lld samples of %lld rows are too many for a launch", (long long)a->N, (long long)a->L);
     return SDM_OK;
 }
@@ -1034,7 +1035,7 @@ extern "C" {
 size_t sdm_group_norm_workspace_bytes(const sdm_group_shape *s, int32_t backward) {
     if (gn_check(s) != SDM_OK || s->samples == 0) return 0;
     const GnPlan p = gn_plan(s->samples, s->rows, s->channels, s->groups, s->dtype == SDM_BF16 ? 8 : 4, backward != 0);
-    return align256(gn_floats(s->samples, s->channels, s->groups, p, backward != 0) * 4);
+    return gn_launches(p, s->samples) ? align256(gn_floats(s->samples, s->channels, s->groups, p, backward != 0) * 4) : 0;
 }
 
 int sdm_group_norm_fwd(const sdm_group_shape *s, const void *x, int64_t x_sample, int64_t x_row, const void *weight, const void *bias,

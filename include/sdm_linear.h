@@ -97,7 +97,9 @@ int sdm_linear_attention_bwd(const sdm_delta_shape *shape, const sdm_rows *q, co
  *     otherwise; mean, rstd: device float32 [samples, groups], written.
  *   exec->workspace: sdm_group_norm_workspace_bytes(shape, 0) bytes, 256-byte aligned (where that is
  *     0, none).
- * At most 2^31 - 1 samples and rows of 2^20 channels. Bitwise reproducible.
+ * At most 2^31 - 1 samples and rows of 2^20 channels. Samples whose rows a workgroup's registers do
+ * not hold are cut into blocks of rows and tiles of channels: of these there are then less than
+ * 2^24 in all samples (SDM_ERR_RANGE past that). Bitwise reproducible.
  */
 enum { SDM_ACT_NONE = 0, SDM_ACT_SILU = 1, SDM_ACT_GELU = 2 };
 typedef struct {
@@ -111,7 +113,8 @@ typedef struct {
     float eps;
 } sdm_group_shape;
 
-/* Workspace bytes of the forward (backward = 0) or the backward (1). */
+/* Workspace bytes of the forward (backward = 0) or the backward (1); 0 where none are needed, and
+ * for shapes they reject. */
 size_t sdm_group_norm_workspace_bytes(const sdm_group_shape *shape, int32_t backward);
 
 int sdm_group_norm_fwd(const sdm_group_shape *shape, const void *x, int64_t x_sample, int64_t x_row, const void *weight,

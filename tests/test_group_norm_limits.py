@@ -1,9 +1,11 @@
-"""Arrays that overlap in group norm's entry points: refused on the host before any device work. (A call
+"""Arrays that overlap, and shapes past a launch, in group norm's entry points: refused on the host before any device work. (A call
 that passes these checks is let down by its missing workspace here, which is looked at after them: no GPU needed.)"""
+
+import os
 
 import pytest
 
-from tests.test_dense_abi import FAKE, SHAPE, WORKSPACE, lib  # noqa: F401
+from tests.test_dense_abi import FAKE, RANGE, ROOT, SHAPE, WORKSPACE, lib  # noqa: F401
 from tests.test_linear_abi import norm
 
 N, L, C = 4, 5000, 32      # norm()'s sizes, dense rows by default: elements of four bytes
@@ -68,3 +70,16 @@ def test_gradients_in_place(lib):
     for name in ("dw", "db"):
         for at in (X, X + 64, DY, DY + 64, FAKE + (4 << 36), FAKE + (5 << 36)):      # x, grad_out, mean, rstd
             assert bwd(lib, **{name: at}) == SHAPE
+
+
+def test_launches(lib):
+    """Samples that are cut into blocks: samples * blocks * tiles stays below 2^24, the header says so, and what is refused
+    needs a workspace of 0 bytes."""
+    from chunked_sparse_delta_amd import group
+    text = " ".join(open(os.path.join(ROOT, "include", "sdm_linear.h")).read().replace("*", " ").split())
+    assert "2^24" in text[text.index("Group norm with an activation over"):text.index("SDM_ACT_NONE")]
+    for back in (False, True):
+        for samples, code in ((1 << 24, RANGE), ((1 << 24) - 1, WORKSPACE)):
+            assert norm(lib, back, ws_bytes=0, samples=samples, x=FAKE << 4, y=FAKE << 5, dx=FAKE << 5, dy=FAKE << 6) == code
+            size = lib.sdm_group_norm_workspace_bytes(group._SHAPE(samples, 5000, 32, 4, 0, 0, 1, 1e-5), 1 if back else 0)
+            assert (size == 0) == (code == RANGE)
