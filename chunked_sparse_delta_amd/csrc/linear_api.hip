@@ -36,11 +36,6 @@ int check_shape(const sdm_delta_shape *s, bool step) {
     return SDM_OK;
 }
 
-bool overlap(const void *a, const void *b, size_t n) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + n && y < x + n;
-}
-
 size_t state_bytes(const sdm_delta_shape *s, int64_t slots) {
     return size_t(slots) * size_t(s->value_heads) * size_t(s->head_dim) * size_t(s->value_dim) * 4;
 }
@@ -71,6 +66,32 @@ int check_inputs(const sdm_delta_shape *s, bool step, const sdm_rows *q, const s
     a->state = state; a->valid = valid;
     a->P = s->streams; a->T = s->tokens; a->Hk = s->key_heads; a->Hv = s->value_heads;
     a->K = s->head_dim; a->V = s->value_dim; a->scale = s->scale;
+    return SDM_OK;
+}
+
+Extent extent(const sdm_delta_shape *s, const Rows &r, int heads) {
+    return {r.data, {{s->streams, r.sp}, {s->tokens, r.st}, {heads, r.sh}}, r.width, s->dtype == SDM_BF16 ? 2 : 4};
+}
+size_t readings_bytes(const sdm_delta_shape *s) {
+    return size_t(s->streams) * size_t(s->tokens) * size_t(s->value_heads) * size_t(s->value_dim) * (s->dtype == SDM_BF16 ? 2 : 4);
+}
+// Whether the n bytes of a result at p (null: not wanted) meet q, k, v, the log-decays or the counts. over_v: a dense v's own place is
+// allowed.
+bool meets_inputs(const sdm_delta_shape *s, const LinArgs &a, const void *p, size_t n, bool over_v) {
+    if (!p) return false;
+    const Extent v = extent(s, a.v, a.Hv);
+    const size_t gates = size_t(a.Hv) * (a.gates.st ? size_t(a.P) * size_t(a.T) : 1) * 4;
+    return extent(s, a.q, a.Hk).meets(p, n) || extent(s, a.k, a.Hk).meets(p, n) || (!(over_v && p == v.data && v.dense()) && v.meets(p, n)) ||
+           (a.gates.g && overlap(p, n, a.gates.g, gates)) || (a.valid && overlap(p, n, a.valid, size_t(a.P) * 4));
+}
+// The forward's and the step's results: states of `bytes` at a.state (may be null) and a.state_out, readings at a.out.
+int check_apart(const sdm_delta_shape *s, const LinArgs &a, size_t bytes, bool over_v) {
+    const size_t n = readings_bytes(s);
+    if (a.state && a.state_out && a.state != a.state_out && overlap(a.state, bytes, a.state_out, bytes))
+        return fail(SDM_ERR_SHAPE, "state_out overlaps state without being it");
+    if (meets_inputs(s, a, a.out, n, over_v) || (a.state && overlap(a.out, n, a.state, bytes)) || (a.state_out && overlap(a.out, n, a.state_out, bytes)))
+        return fail(SDM_ERR_SHAPE, "out overlaps an input or a state%s", over_v ? " (it may be a dense v)" : "");
+    if (meets_inputs(s, a, a.state_out, bytes, false)) return fail(SDM_ERR_SHAPE, "the state overlaps another input");
     return SDM_OK;
 }
 
@@ -150,15 +171,14 @@ int sdm_linear_attention_fwd(const sdm_delta_shape *s, const sdm_rows *q, const 
     if (!aligned(out, s->dtype == SDM_BF16 ? 2 : 4)) return fail(SDM_ERR_ALIGN, "out must be aligned to its element size");
     if (!aligned(state_out, 4)) return fail(SDM_ERR_ALIGN, "state_out must be 4-byte aligned");
     if (!aligned(kept, 256)) return fail(SDM_ERR_ALIGN, "kept must be 256-byte aligned");
-    if (state && state_out && state != state_out && overlap(state, state_out, state_bytes(s, s->streams)))
-        return fail(SDM_ERR_SHAPE, "state_out overlaps state without being it");
+    a.state_out = state_out;
+    a.out = out;
+    if ((rc = check_apart(s, a, state_bytes(s, s->streams), false))) return rc;
     LinWs ws = segments(s);
     if (kept) layout(s, -1, &ws, kept);
     else if ((rc = take_workspace(s, SDM_LINEAR_FORWARD, exec, &ws))) return rc;
     int cus = 0;
     if ((rc = device_cus(&cus))) return rc;
-    a.state_out = state_out;
-    a.out = out;
     const hipError_t e = launch_linear_fwd(a, ws, s->dtype == SDM_BF16, kept != nullptr, static_cast<hipStream_t>(exec->stream));
     return e == hipSuccess ? SDM_OK : hip_fail(e, "linear attention launch");
 }
@@ -176,8 +196,12 @@ int sdm_linear_attention_step(const sdm_delta_shape *s, const sdm_rows *q, const
         return fail(SDM_ERR_NULL, "state, state_out and out must not be NULL");
     if (!aligned(out, s->dtype == SDM_BF16 ? 2 : 4)) return fail(SDM_ERR_ALIGN, "out must be aligned to its element size");
     if (!aligned(state_out, 4) || !aligned(state_ids, 4)) return fail(SDM_ERR_ALIGN, "state_out and state_ids must be 4-byte aligned");
-    if (state != state_out && overlap(state, state_out, state_bytes(s, slots)))
-        return fail(SDM_ERR_SHAPE, "state_out overlaps state without being it");
+    a.state_out = state_out;
+    a.out = out;
+    const size_t bytes = state_bytes(s, slots);
+    if ((rc = check_apart(s, a, bytes, true))) return rc;
+    if (state_ids && (overlap(out, readings_bytes(s), state_ids, size_t(a.P) * 4) || overlap(state_out, bytes, state_ids, size_t(a.P) * 4)))
+        return fail(SDM_ERR_SHAPE, "out or state_out overlaps state_ids");
     int cus = 0;
     if ((rc = device_cus(&cus))) return rc;
     DeltaArgs d{};
@@ -207,10 +231,19 @@ int sdm_linear_attention_bwd(const sdm_delta_shape *s, const sdm_rows *q, const 
     for (const void *x : f)
         if (!aligned(x, 4)) return fail(SDM_ERR_ALIGN, "float32 gradients must be 4-byte aligned");
     if (!aligned(kept, 256)) return fail(SDM_ERR_ALIGN, "kept must be 256-byte aligned");
-    const size_t bytes = state_bytes(s, s->streams);
-    if (grads->state && ((state && overlap(state, grads->state, bytes)) ||
-                         (grad_state_out && grad_state_out != grads->state && overlap(grad_state_out, grads->state, bytes))))
-        return fail(SDM_ERR_SHAPE, "the state's gradient overlaps an input");
+    const size_t bytes = state_bytes(s, s->streams), readings = readings_bytes(s), keys = size_t(a.P) * a.T * a.Hk * a.K * es;
+    const struct {
+        const void *p;
+        size_t n;
+    } results[] = {{grads->q, keys}, {grads->k, keys}, {grads->v, readings},
+                   {grads->log_decay, size_t(a.Hv) * (per_token ? size_t(a.P) * size_t(a.T) : 1) * 4}, {grads->state, bytes}};
+    for (const auto &r : results) {
+        if (!r.p) continue;
+        const bool own = r.p == grads->state && grads->state == grad_state_out;
+        if (meets_inputs(s, a, r.p, r.n, false) || (state && overlap(r.p, r.n, state, bytes)) || (grad_out && overlap(r.p, r.n, grad_out, readings)) ||
+            (grad_state_out && !own && overlap(r.p, r.n, grad_state_out, bytes)))
+            return fail(SDM_ERR_SHAPE, "a gradient overlaps an input (the state's may be grad_state_out)");
+    }
     LinWs ws = segments(s);
     if (kept) layout(s, -1, &ws, const_cast<void *>(kept));
     if ((rc = take_workspace(s, kept ? SDM_LINEAR_BACKWARD_KEPT : SDM_LINEAR_BACKWARD, exec, &ws))) return rc;

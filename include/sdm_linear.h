@@ -30,7 +30,7 @@ extern "C" {
  *   q, k: [P, T, Hk, K]; v: [P, T, Hv, V] (strided rows, element alignment).
  *   state: device float32 [P, Hv, K, V], or NULL for zeros. state_out: the same shape, or
  *     NULL (not wanted); it may be `state` itself (advanced in place), but must not overlap
- *     it otherwise.
+ *     it, or another input, otherwise.
  *   valid_tokens, out [P, T, Hv, V]: as for sdm_fwd.
  *   kept: NULL, or a device buffer of sdm_linear_attention_kept_bytes(shape) bytes, 256-byte
  *     aligned, in which the call leaves what sdm_linear_attention_bwd then does not compute again.
@@ -55,7 +55,8 @@ int sdm_linear_attention_fwd(const sdm_delta_shape *shape, const sdm_rows *q, co
 /*
  * The same token by token, for single tokens and a few at once: each state is read and
  * written once, whatever T. State, state_out, state_ids, slots: as for sdm_gated_delta_step.
- * No workspace.
+ * out may be v where that is dense, but must not overlap an input or a state otherwise. No
+ * workspace.
  */
 int sdm_linear_attention_step(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
                               const float *log_decay, int32_t decay_per_token, const float *state, float *state_out,
