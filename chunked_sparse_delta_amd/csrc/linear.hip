@@ -14,6 +14,8 @@
 //     dg_m = sum_{i >= m} (r_i - c_i) + <S1, dS1>
 // over the segment: the sums that cancel span one segment, in 64 bits, and leave out what any decay leaves alone. At the segment's
 // start this has to be <S0, dS0>: what it misses, the roundings of all the shares, is spread over the segment, which halves it.
+// Where e^{g_m} is 0 in float32 nothing before m counts after it, and dg_m = e^{g_m} <S, dS> is 0: there the shares cancel, and the 0 is
+// written instead of what their roundings leave (1e-5 of a log-decay of -inf among 400 tokens).
 #include "linear_attend.h"
 #include "linear_state.h"
 
@@ -93,6 +95,7 @@ template <int N, bool BACK> __global__ __launch_bounds__(256) void lin_scan_kern
 }
 
 struct GateGradArgs {
+    LinGates gates;
     const float *rows, *cols, *dots;
     const int32_t *valid;
     float *g;                // [P, T, Hv], or null:
@@ -115,6 +118,7 @@ __global__ __launch_bounds__(256) void lin_gate_grad_kernel(GateGradArgs a) {
     __shared__ double buf[4];
     const int seg = blockIdx.x % a.segs, ph = blockIdx.x / a.segs, h = ph % a.Hv, p = ph / a.Hv, tid = threadIdx.x;
     const int s0 = seg * a.seg_tokens, live = min(a.seg_tokens, lin_valid(a.valid, p, a.T) - s0), t = s0 + tid;
+    const bool counts = tid < live && expf(a.gates.g[p * a.gates.sp + t * a.gates.st + h]) != 0.0f;
     double head = 0.0, tail = 0.0, d = 0.0;     // at the segment's start and end
     if (live > 0)
         for (int i = tid; i < a.parts; i += 256) {
@@ -140,7 +144,7 @@ __global__ __launch_bounds__(256) void lin_gate_grad_kernel(GateGradArgs a) {
     if ((tid & 63) == 63) buf[tid >> 6] = before;
     __syncthreads();
     for (int w = 0; w < tid >> 6; ++w) before += buf[w];
-    const double g = tid < live ? tail + (all - before + d) + (head - (tail + all)) * double(live - tid) / double(live) : 0.0;
+    const double g = counts ? tail + (all - before + d) + (head - (tail + all)) * double(live - tid) / double(live) : 0.0;
     if (a.g) {
         if (tid < a.seg_tokens && t < a.T) a.g[(int64_t(p) * a.T + t) * a.Hv + h] = float(g);
     } else {
@@ -296,6 +300,7 @@ hipError_t launch_linear_bwd(const LinArgs &a, const LinWs &ws, const LinGrads &
     if (!g.g) return hipSuccess;
     GateGradArgs d{};
     const bool per_token = a.gates.st != 0;
+    d.gates = a.gates;
     d.rows = ws.rows; d.cols = ws.cols; d.dots = ws.dots; d.valid = a.valid;
     d.g = per_token ? g.g : nullptr; d.sums = ws.sums;
     d.P = a.P; d.T = a.T; d.Hv = a.Hv; d.segs = ws.segs; d.seg_tokens = ws.tokens;
