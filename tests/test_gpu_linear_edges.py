@@ -6,9 +6,74 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_linear import DT, check_grads, make, on
+from tests.test_gpu_linear import DT, check_grads, close, make, on, run, want
 
 pytestmark = pytest.mark.gpu
+
+
+# At least 512 segments' heads: a workgroup takes all tiles of a segment in turn. P * Hk * segments is a multiple of eight or not
+# (then the grid is padded). T: one segment and several, of two tiles and more (bfloat16 128 tokens to a tile, 64 where a width is above
+# 128; float32 64).
+WHOLE = [
+    # P, T, Hk, Hv, K, V, dtype, decay, start state
+    (33, 200, 8, 16, 16, 16, "bf16", "token", True), (33, 200, 8, 16, 16, 16, "f32", "token", True),
+    (33, 200, 5, 20, 8, 24, "bf16", "head", False), (33, 128, 5, 20, 8, 24, "f32", "head", False),
+    (11, 520, 5, 20, 17, 9, "bf16", "token", True), (11, 520, 5, 20, 17, 9, "f32", "token", True),
+    (33, 180, 8, 16, 136, 16, "bf16", "token", True),
+]
+
+
+@pytest.mark.parametrize("P,T,Hk,Hv,K,V,dtype,decay,start", WHOLE)
+def test_many_segments(gpu, P, T, Hk, Hv, K, V, dtype, decay, start):
+    """Streams that end in every tile of a segment, at its borders, before it and behind it; NaN in the padding."""
+    import chunked_sparse_delta_amd as sdm
+    dt = DT[dtype]
+    counts = [(0, 1, 63, 64, 65, 100, 127, 128, 129, 140, T - 1, T, T + 5)[p % 13] for p in range(P)]
+    x = make(P, T, Hk, Hv, K, V, dt, decay, ragged=counts, seed=P + T, state=start)
+    (o, s), (ao, as_) = want(x), want(x, absolute=True)
+    d = on(x, gpu)
+    for p, n in enumerate(counts):
+        for name in ("q", "k", "v") + (("log_decay",) if decay == "token" else ()):
+            d[name][p, min(n, T):] = math.nan
+    final = torch.full((P, Hv, K, V), math.nan, device=gpu)
+    out = sdm.linear_attention_fwd(d["state"], d["k"], d["v"], d["log_decay"], d["q"], valid_tokens=d["valid"], state_out=final)
+    close(out, o, ao, dt)
+    close(final, s, as_, torch.float32)
+    assert not any(out[p, min(n, T):].any() for p, n in enumerate(counts))
+    if start:       # ... and the state in place
+        close(sdm.linear_attention_fwd(d["state"], d["k"], d["v"], d["log_decay"], d["q"], valid_tokens=d["valid"]), o, ao, dt)
+        close(d["state"], s, as_, torch.float32)
+
+
+@pytest.mark.parametrize("P,T,Hk,Hv,K,V,dtype,decay,start", [WHOLE[i] for i in (0, 1, 2, 5)])
+def test_many_segments_backward(gpu, P, T, Hk, Hv, K, V, dtype, decay, start):
+    import chunked_sparse_delta_amd as sdm
+    dt = DT[dtype]
+    counts = [(0, 1, 63, 64, 65, 100, 127, 128, 129, 140, T - 1, T, T + 5)[p % 13] for p in range(P)]
+    x = make(P, T, Hk, Hv, K, V, dt, decay, ragged=counts, seed=P + T, state=start)
+    gen = torch.Generator().manual_seed(T)
+    go, gs = torch.randn((P, T, Hv, V), generator=gen).to(dt), torch.randn((P, Hv, K, V), generator=gen)
+    d = on(x, gpu)
+    got = sdm.linear_attention_bwd(d["state"], d["k"], d["v"], d["log_decay"], d["q"], go.to(gpu), grad_state=gs.to(gpu), valid_tokens=d["valid"])
+    check_grads(got, x, go, gs, dt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hv", [16, 64])
+def test_many_heads_share_keys(gpu, Hv, dtype):
+    """One key head for 16 and 64 value heads, over several segments: readings, and dq and dk summed over all of them."""
+    import chunked_sparse_delta_amd as sdm
+    dt, T, K, V = DT[dtype], 300, 24, 16
+    x = make(1, T, 1, Hv, K, V, dt, "head", seed=Hv)
+    out, final = run(gpu, x)
+    (o, s), (ao, as_) = want(x), want(x, absolute=True)
+    close(out, o, ao, dt)
+    close(final, s, as_, torch.float32)
+    gen = torch.Generator().manual_seed(Hv)
+    go, gs = torch.randn((1, T, Hv, V), generator=gen).to(dt), torch.randn((1, Hv, K, V), generator=gen)
+    d = on(x, gpu)
+    got = sdm.linear_attention_bwd(d["state"], d["k"], d["v"], d["log_decay"], d["q"], go.to(gpu), grad_state=gs.to(gpu))
+    check_grads(got, x, go, gs, dt)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
