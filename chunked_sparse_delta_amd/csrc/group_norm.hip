@@ -134,9 +134,9 @@ template <typename T, int V> __device__ __forceinline__ typename NormVec<T>::raw
 struct GnStat {
     float n, mean, m2;
     __device__ __forceinline__ void add(const GnStat &o) {
-        const float all = n + o.n, d = o.mean - mean, f = all > 0.0f ? o.n / all : 0.0f;
+        const float all = n + o.n, d = o.mean - mean, f = all > 0.0f ? o.n / all : 0.0f, w = n * f;
         mean = fmaf(d, f, mean);
-        m2 += fmaf(d * d, n * f, o.m2);
+        m2 += w > 0.0f ? fmaf(d * d, w, o.m2) : o.m2;      // beside an empty set d is a mean, whose square may be infinite
         n = all;
     }
 };
