@@ -1,16 +1,41 @@
 """Group norm on the GPU where its sums cancel and where values end, against its definition in 64 bits: bars and helpers of
 test_gpu_group_norm.py."""
 
+import math
+
 import pytest
 import torch
 
-from tests.test_gpu_group_norm import U
+from tests.test_gpu_group_norm import DT, U, bars, close, make
 
 pytestmark = pytest.mark.gpu
 
 # Every way in which a tile's threads meet (test_gpu_group_norm.py names them by their shapes), and blocks of rows: D divided by
 # vectors of a power of two, by others, by none; groups wider than a workgroup.
 FORMS = [(70, 1, 128, 2), (9, 16, 512, 16), (3, 1, 2048, 1), (2, 7, 320, 32), (2, 3000, 32, 4), (1, 3, 20001, 3), (3, 777, 1000, 8)]
+
+
+@pytest.mark.parametrize("N,L,C,G", FORMS)
+def test_means_far_from_zero(gpu, N, L, C, G):
+    """Means a thousand times the spread, of each sample and group its own. With u = 2^-24 and r = |mean| rstd: a mean is right to
+    64 u of itself, so a difference from it, or of two of them, to 64 u r spreads, and the sum of the squares to twice that of
+    itself: rstd to 64 u r beside its own 64 u, 4e-3 here. (Sums of squares less the square of the sum: r^2 u = 6e-2 of the
+    variance for each rounding of the sums.)"""
+    import chunked_sparse_delta_amd as sdm
+    d = make(N, L, C, torch.float32, seed=N + L)
+    gen = torch.Generator().manual_seed(1)
+    d["x"] = 2 * torch.randn((N, L, C), generator=gen) + (2000 + 2 * torch.randn((N, 1, G, 1), generator=gen)).expand(N, 1, G, C // G).reshape(N, 1, C)
+    ref = bars(d["x"], G, d["weight"], d["bias"], "silu", d["go"], None)
+    mean, rstd = ref["mean"][0], ref["rstd"][0]
+    assert bool(((mean * rstd > 500) & (mean * rstd < 2500)).all())
+    d = {n: t.to(gpu) for n, t in d.items()}
+    y, m, r = sdm.group_norm_fwd(d["x"], G, d["weight"], d["bias"], activation="silu")
+    close(m, ref["mean"], torch.float32, "mean")
+    rel = (r.double().cpu() / rstd - 1).abs()
+    assert bool((rel <= U * (65 + 64 * mean * rstd)).all()), f"rstd off by {rel.max():.3g}"
+    close(y, ref["y"], torch.float32, "y")
+    g = sdm.group_norm_bwd(d["go"], d["x"], G, m, r, d["weight"], d["bias"], activation="silu")
+    close(g["x"], ref["grad_x"], torch.float32, "grad_x")
 
 
 @pytest.mark.parametrize("N,L,C,G", FORMS)
@@ -28,3 +53,43 @@ def test_means_whose_squares_overflow(gpu, N, L, C, G):
     assert bool(((m.double().cpu() - mean).abs() <= 64 * U * mean).all())
     rel = (r.double().cpu() / rstd - 1).abs()
     assert bool((rel <= U * (65 + 64 * mean * rstd)).all()), f"rstd off by {rel.max():.3g}"
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,L,C,G", FORMS)
+def test_reach_of_a_live_value(gpu, N, L, C, G, dtype, value):
+    """A NaN or infinity in a live row, or in its gradient, stays in its sample and group: everything else, to the bit, is as it was; the
+    parameters' gradients of that group's channels show it."""
+    import chunked_sparse_delta_amd as sdm
+    d = {n: t.to(gpu) for n, t in make(N, L, C, DT[dtype], seed=3).items()}
+    D, n, row, c = C // G, N - 1, L // 2, (G // 2) * (C // G) + C // G // 3
+    here = slice(c // D * D, (c // D + 1) * D)
+    valid = torch.full((N,), max(1, L - 1), dtype=torch.int32, device=gpu)
+    row = min(row, max(1, L - 1) - 1)
+
+    def work(x, go):
+        y, m, r = sdm.group_norm_fwd(x, G, d["weight"], d["bias"], activation="silu", valid_rows=valid)
+        return [y, m, r, *sdm.group_norm_bwd(go, x, G, m, r, d["weight"], d["bias"], activation="silu", valid_rows=valid).values()]
+
+    clean = work(d["x"], d["go"])
+    for into in ("x", "go"):
+        t = {"x": d["x"].clone(), "go": d["go"].clone()}
+        t[into][n, row, c] = value
+        y, m, r, dx, dw, db = work(t["x"], t["go"])
+        for got, was in ((y, clean[0]), (dx, clean[3])):
+            hit = got != was
+            hit[n, :, here] = False
+            assert not hit.any()
+        for got, was in ((m, clean[1]), (r, clean[2])):
+            hit = got != was
+            hit[n, c // D] = False
+            assert not hit.any()
+        for got, was in ((dw, clean[4]), (db, clean[5])):
+            hit = got != was
+            hit[here] = False
+            assert not hit.any() and not torch.isfinite(got[c])
+        live = int(valid[n])
+        assert not torch.isfinite(dx[n, :live, here]).all() and not y[n, live:].any() and not dx[n, live:].any()
+        if into == "x":
+            assert torch.isnan(y[n, :live, here]).all()
