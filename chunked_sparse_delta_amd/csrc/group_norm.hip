@@ -14,7 +14,8 @@
 // Measured: 8192 tokens of 4096 channels in 32 groups, bfloat16, silu: forward 36 us (134 MB, 3.7 TB/s), backward 52 (201 MB, 3.9 TB/s) and
 // 4 for the sums over workgroups; 64 tokens: 4.3. Split, 8 x 4096 rows of 512 channels: statistics 11, their join 4, values 14 (67 MB,
 // 4.8 TB/s); sums 19 (67 MB), their join 5, gradients 19 (101 MB, 5.3 TB/s), the parameters' sums 4. A large copy: 5.2 TB/s.
-// Statistics: a thread's mean and sum of squared differences from it, joined with their counts (no difference of large sums).
+// Statistics: a thread's mean and sum of squared differences from it, joined with their counts. Split: sums of differences from the first
+// of at most kGnRun rows and of their squares, less the square of the sum, joined likewise.
 // All sums run in float32 in a fixed order: results are the same from run to run.
 #include <type_traits>
 
@@ -485,6 +486,10 @@ template <typename T, int NT, int ITEMS, int MODE> __global__ __launch_bounds__(
 // ---- split -----------------------------------------------------------------------------------------------------------
 
 constexpr int kGnThreads = 256;
+// Rows of a run of the statistics. What cancels between a run's squares and the square of its sum grows with its length: 165 of
+// 2^-24 of the variance at most for 8 rows of which the first lies far off; one run of the 128 rows that a thread had of 2048 x 16384 x 8
+// was off by 4700. (8 rows are a thread's share where blocks are not long.)
+constexpr int kGnRun = 8;
 // Rows of a thread on their way at once (one after another the sums of 8 x 4096 x 512 bfloat16 took 21 us, so 19; the gradients' kernel, short of
 // registers, the other way round 19 and 23).
 constexpr int kGnAhead = 4;
@@ -499,21 +504,36 @@ template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_stats_ker
     const int64_t nv = gn_valid(a, n), r0 = int64_t(block) * a.p.block_rows, r1 = min(r0 + a.p.block_rows, nv);
     const int cw = a.p.cv * V;
     if (at.left > 0) {
-        // sums of differences from the thread's first row
+        // runs of up to kGnRun rows: sums of differences from the run's first one, joined with their counts
         const T *x = static_cast<const T *>(a.x) + n * a.x_sample + at.c;
-        float first[V] = {}, s[V] = {}, q[V] = {};
+        float mean[V] = {}, m2[V] = {};
         int count = 0;
-        int64_t r = r0 + at.tr;
-        if (r < r1) NormVec<T>::unpack(gn_load<T, V>(x + r * a.x_row, at.left), first);
-        constexpr int U = 4;
-        for (; r + (U - 1) * a.p.rt < r1; r += U * a.p.rt) {
-            typename NormVec<T>::raw w[U];
+        for (int64_t r = r0 + at.tr; r < r1;) {
+            float first[V], s[V] = {}, q[V] = {};
+            const int64_t end = min(r1, r + kGnRun * a.p.rt);
+            NormVec<T>::unpack(gn_load<T, V>(x + r * a.x_row, at.left), first);
+            int rows = 0;
+            constexpr int U = 4;
+            for (; r + (U - 1) * a.p.rt < end; r += U * a.p.rt) {
+                typename NormVec<T>::raw w[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) w[u] = gn_load<T, V>(x + (r + u * a.p.rt) * a.x_row, at.left);
+                for (int u = 0; u < U; ++u) w[u] = gn_load<T, V>(x + (r + u * a.p.rt) * a.x_row, at.left);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+                for (int u = 0; u < U; ++u) {
+                    float v[V];
+                    NormVec<T>::unpack(w[u], v);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float d = v[j] - first[j];
+                        s[j] += d;
+                        q[j] = fmaf(d, d, q[j]);
+                    }
+                }
+                rows += U;
+            }
+            for (; r < end; r += a.p.rt, ++rows) {
                 float v[V];
-                NormVec<T>::unpack(w[u], v);
+                NormVec<T>::unpack(gn_load<T, V>(x + r * a.x_row, at.left), v);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float d = v[j] - first[j];
@@ -521,25 +541,22 @@ template <typename T> __global__ __launch_bounds__(kGnThreads) void gn_stats_ker
                     q[j] = fmaf(d, d, q[j]);
                 }
             }
-            count += U;
-        }
-        for (; r < r1; r += a.p.rt, ++count) {
-            float v[V];
-            NormVec<T>::unpack(gn_load<T, V>(x + r * a.x_row, at.left), v);
+            const float inv = 1.0f / float(rows);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float d = v[j] - first[j];
-                s[j] += d;
-                q[j] = fmaf(d, d, q[j]);
+                const float left = fmaf(-s[j] * inv, s[j], q[j]);
+                GnStat t{float(count), mean[j], m2[j]};
+                t.add({float(rows), fmaf(s[j], inv, first[j]), left < 0.0f ? 0.0f : left});
+                mean[j] = t.mean;
+                m2[j] = t.m2;
             }
+            count += rows;
         }
-        const float inv = count > 0 ? 1.0f / float(count) : 0.0f;
         sn[at.tr] = float(count);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float m2 = fmaf(-s[j] * inv, s[j], q[j]);
-            sm[at.tr * cw + at.col * V + j] = fmaf(s[j], inv, first[j]);
-            sq[at.tr * cw + at.col * V + j] = m2 < 0.0f ? 0.0f : m2;
+            sm[at.tr * cw + at.col * V + j] = mean[j];
+            sq[at.tr * cw + at.col * V + j] = m2[j];
         }
     }
     __syncthreads();

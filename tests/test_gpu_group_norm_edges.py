@@ -55,6 +55,28 @@ def test_means_whose_squares_overflow(gpu, N, L, C, G):
     assert bool((rel <= U * (65 + 64 * mean * rstd)).all()), f"rstd off by {rel.max():.3g}"
 
 
+@pytest.mark.parametrize("N,L,C,G", [(2048, 128, 1024, 1), (2048, 16384, 8, 1), (2, 3000, 32, 4), (1024, 600, 64, 64)])
+def test_first_rows_far_from_the_others(gpu, N, L, C, G):
+    """Rows alike but for the first ones, a thousand spreads away (as a first token's large activations): what a thread takes as its
+    origin. With u = 2^-24, sums of at most m = 8 rows' differences and squares from an origin at a distance d are off by
+    u m^2 d / 2 + u m d and u m^2 d^2 / 2 + 2 u m d^2, what is left of the squares by (1.5 m^2 + 6 m) u d^2 = 144 u d^2, of 7/8 d^2:
+    165 u of the variance, 83 u of rstd; with the joins' 64 u below 256 u. All rows but those, and all channels, are the same, so that
+    no roundings average out."""
+    import chunked_sparse_delta_amd as sdm
+    gen = torch.Generator(device=gpu).manual_seed(L)
+    first = min(128, L // 4)
+    x = torch.rand((N, 1, 1), generator=gen, device=gpu).repeat(1, L, 1)
+    x[:, :first] += 1000.1
+    x = x.expand(N, L, C).contiguous()
+    _, m, r = sdm.group_norm_fwd(x, G)
+    one = x[:, :, 0].double()
+    mean = one.mean(1)
+    rstd = 1 / torch.sqrt((one - mean[:, None]).square().mean(1) + 1e-5)
+    assert bool(((m.double() - mean[:, None]).abs() <= 64 * U * 1000).all())
+    rel = (r.double() / rstd[:, None] - 1).abs().max()
+    assert rel <= 256 * U, f"rstd off by {rel / U:.1f} u"
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,L,C,G", FORMS)
