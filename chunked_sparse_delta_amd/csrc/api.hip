@@ -156,15 +156,19 @@ bool rows_meet(const sdm::Extent::Axis *axis, int count, int64_t width, int64_t 
 
 bool sdm::Extent::meets(const void *p, size_t n) const {
     if (n == 0 || width == 0) return false;
-    Axis real[3];
-    int count = 0;
+    int64_t all = width;
     for (const Axis &x : axis) {
         if (x.n == 0) return false;
-        if (x.n > 1 && x.stride > 0) real[count++] = {x.n, x.stride * es};
+        all += (x.n - 1) * x.stride;
     }
+    const int64_t from = int64_t(reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(data)), to = from + int64_t(n);
+    if (from >= all * es || to <= 0) return false;      // as a rule
+    Axis real[3];
+    int count = 0;
+    for (const Axis &x : axis)
+        if (x.n > 1 && x.stride > 0) real[count++] = {x.n, x.stride * es};
     std::sort(real, real + count, [](const Axis &a, const Axis &b) { return a.stride > b.stride; });
-    const int64_t from = int64_t(reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(data));
-    return rows_meet(real, count, width * es, from, from + int64_t(n));
+    return rows_meet(real, count, width * es, from, to);
 }
 
 int sdm::device_cus(int *cus) {
