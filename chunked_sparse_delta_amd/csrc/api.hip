@@ -15,7 +15,7 @@
 #include "common.h"
 #include "wy_impl.h"
 #include "backward.h"
-#include "linear.h"
+#include "delta.h"
 #include "host.h"
 
 namespace sdm {
@@ -112,7 +112,6 @@ int device_info(DeviceInfo **out) {
         if ((e = bwd_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (backward)");
         if ((e = delta_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (gated delta)");
         if ((e = delta_bwd_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (gated delta backward)");
-        if ((e = linear_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (linear attention)");
         void *sp = nullptr;
         if ((e = hipGetSymbolAddress(&sp, HIP_SYMBOL(scratch))) != hipSuccess)
             return hip_fail(e, "hipGetSymbolAddress (static scratch)");

@@ -1,4 +1,6 @@
 // Host entry points of linear attention with a decay: argument checks, workspace layout, launches.
+#include <mutex>
+
 #include "linear.h"
 #include "host.h"
 
@@ -95,6 +97,24 @@ int check_apart(const sdm_delta_shape *s, const LinArgs &a, size_t bytes, bool o
     return SDM_OK;
 }
 
+// The device's setup, and that of the sequences' kernels, which may take more LDS than by default: once a device, by the first call of
+// theirs. (As a part of the device's setup it cost the first call of every other entry point 5 ms beside its 34.)
+int prepare_once() {
+    static std::mutex mu;
+    static bool ready[64];      // device_cus refuses devices past these
+    int cus = 0, dev = 0;
+    const int rc = device_cus(&cus);
+    if (rc) return rc;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    std::lock_guard<std::mutex> lk(mu);
+    if (!ready[dev]) {
+        if ((e = linear_prepare()) != hipSuccess) return hip_fail(e, "hipFuncSetAttribute (linear attention)");
+        ready[dev] = true;
+    }
+    return SDM_OK;
+}
+
 // Takes arrays from a buffer in order (from NULL: only the size counts).
 struct Taker {
     char *base;
@@ -177,8 +197,7 @@ int sdm_linear_attention_fwd(const sdm_delta_shape *s, const sdm_rows *q, const 
     LinWs ws = segments(s);
     if (kept) layout(s, -1, &ws, kept);
     else if ((rc = take_workspace(s, SDM_LINEAR_FORWARD, exec, &ws))) return rc;
-    int cus = 0;
-    if ((rc = device_cus(&cus))) return rc;
+    if ((rc = prepare_once())) return rc;
     const hipError_t e = launch_linear_fwd(a, ws, s->dtype == SDM_BF16, kept != nullptr, static_cast<hipStream_t>(exec->stream));
     return e == hipSuccess ? SDM_OK : hip_fail(e, "linear attention launch");
 }
@@ -247,8 +266,7 @@ int sdm_linear_attention_bwd(const sdm_delta_shape *s, const sdm_rows *q, const 
     LinWs ws = segments(s);
     if (kept) layout(s, -1, &ws, const_cast<void *>(kept));
     if ((rc = take_workspace(s, kept ? SDM_LINEAR_BACKWARD_KEPT : SDM_LINEAR_BACKWARD, exec, &ws))) return rc;
-    int cus = 0;
-    if ((rc = device_cus(&cus))) return rc;
+    if ((rc = prepare_once())) return rc;
     const LinGrads g{{grad_out, int64_t(a.T) * a.Hv * a.V, int64_t(a.Hv) * a.V, a.V, a.V}, grad_state_out,
                      grads->q, grads->k, grads->v, grads->log_decay, grads->state};
     const hipError_t e = launch_linear_bwd(a, ws, g, s->dtype == SDM_BF16, kept != nullptr, static_cast<hipStream_t>(exec->stream));
