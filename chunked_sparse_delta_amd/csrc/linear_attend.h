@@ -9,6 +9,10 @@
 // KEYS: dq and dk, which sum over the value heads of a key head and also give each head's share of the log-decays' gradient
 // (linear.hip): the row's own q or k times the sum above without b = a.
 //
+// CAUSAL, the readings: no infinity or NaN in a z behind a reaches it, though a's scores with the 32 tokens around it are zeros in a product
+// with all of their z. Tiles that may lie behind some of the a are sifted on their way to LDS: such values go in as zeros, and the a at or behind
+// the first one of a column read NaN there. (1 % of the time: 16384 tokens of 16 heads 180.5 us of all kernels, 178.5 without.)
+//
 // A workgroup takes 64 NQ tokens a, 16 NQ to a wavefront, and ZW columns. Scores are computed transposed: with y as the A operand a lane's
 // accumulators are eight neighbouring b of one a, a B operand as they stand (delta_tile.h), so decayed scores go from registers
 // into the product with z. The outcome is transposed too: a lane holds eight neighbouring columns of its token. LDS holds a tile of y and z, or
@@ -37,7 +41,7 @@ struct AttendSide {
     float *dot;              // KEYS: [slices][ph][T], or null
     float *rest;             // KEYS with shared key heads: lin_rest_floats
     float a0, a1;
-    bool back;               // b at or after a
+    bool back;               // b at or after a (not CAUSAL)
 };
 struct AttendArgs {
     AttendSide side[3];      // the readings; or dq, dk and dv
@@ -57,12 +61,12 @@ template <typename T, int XP, int ZW, bool KEYS, bool EVEN> struct AttendCfg {
     using Z = Tile<T, KT, ZW, EVEN>;
     using S = Tile<float, KEYS ? ZW : 32, KEYS ? 32 : ZW, EVEN>;
     static constexpr size_t kTiles = size_t(NI) * (Y::kPlane + Z::kPlane), kState = 3 * size_t(S::kPlane);
-    static constexpr size_t kGates = (kLinSegMax + 4) * sizeof(double) + kLinSegMax * sizeof(float);
+    static constexpr size_t kGates = (kLinSegMax + 4) * sizeof(double) + kLinSegMax * sizeof(float) + (ZW + 4) * sizeof(int);
     static constexpr size_t kLds = (kTiles > kState ? kTiles : kState) + kGates;
     static_assert(kLinSegMax % QT == 0, "a query tile lies in one segment");
 };
 
-template <typename T, int XP, int ZW, bool KEYS, bool EVEN>
+template <typename T, int XP, int ZW, bool KEYS, bool EVEN, bool CAUSAL>
 __device__ __forceinline__ void lin_attend(const AttendArgs &a, const AttendSide &s, const int block) {
     using C = AttendCfg<T, XP, ZW, KEYS, EVEN>;
     constexpr int NI = C::NI, NQ = C::NQ, QT = C::QT, KT = C::KT, XB = XP / 32, ZB = ZW / 32, TB = KT / 32;
@@ -72,6 +76,8 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const AttendSide
     unsigned char *ly = lds, *lz = lds + NI * Y::kPlane;
     double *total_of = reinterpret_cast<double *>(lds + C::kLds) - 4, *G = total_of - kLinSegMax;
     float *local = reinterpret_cast<float *>(G) - kLinSegMax;     // a token's decay to the edge of its 32 on the side of the a
+    int *first = reinterpret_cast<int *>(local) - (ZW + 4);       // CAUSAL: see Tile::sift
+    if (CAUSAL && threadIdx.x <= ZW) first[threadIdx.x] = INT_MAX;
     const bool back = s.back;
     const int heads = KEYS ? a.Hk : a.Hv, group = a.Hv / a.Hk, X = s.x.width, Zw = s.z.width;
     const int slices = (Zw + ZW - 1) / ZW, seg_tiles = a.seg_tokens / QT;
@@ -205,6 +211,7 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const AttendSide
         for (int kt = k0;; kt += step) {
             lds_barrier();
             ty.store(ly, tid);
+            if (CAUSAL && s0 + (kt + 1) * KT > q0) tz.sift(tid, kt * KT, first);      // (what lies before all of the a reaches them all)
             tz.store(lz, tid);
             lds_barrier();
             if (kt != k1) bring(kt + step);
@@ -310,6 +317,19 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const AttendSide
             lds_barrier();       // G and the tiles are free
             if (!ends) continue;
         }
+        if (CAUSAL && __builtin_amdgcn_readfirstlane(first[ZW]) < qw + 16 * NQ - s0) {
+#pragma unroll
+            for (int zb = 0; zb < ZB; ++zb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int from = first[zb * 32 + lg * 8 + e * 4 + r];
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq)
+                            if (qw - s0 + nq * 16 + lc >= from) acc[zb][e][nq][r] = __builtin_nanf("");
+                    }
+        }
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
             const int t = qw + nq * 16 + lc;
@@ -320,12 +340,12 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const AttendSide
 }
 
 template <typename T, int XP, int ZW, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_attend_kernel(AttendArgs a) {
-    lin_attend<T, XP, ZW, false, EVEN>(a, a.side[0], blockIdx.x);
+    lin_attend<T, XP, ZW, false, EVEN, true>(a, a.side[0], blockIdx.x);
 }
 // A sequence of one segment: its readings and, by the workgroups from `attends` on, its end state. (One launch for two: of 200
 // tokens of 4 heads of 64 x 64, 13.6 us and 9 one after the other.)
 template <typename T, int XP, int ZW, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_single_kernel(AttendArgs a, StateArgs s, int attends) {
-    if (int(blockIdx.x) < attends) lin_attend<T, XP, ZW, false, EVEN>(a, a.side[0], blockIdx.x);
+    if (int(blockIdx.x) < attends) lin_attend<T, XP, ZW, false, EVEN, true>(a, a.side[0], blockIdx.x);
     else lin_state<T, XP, ZW, EVEN>(s, int(blockIdx.x) - attends);
 }
 // dq, dk and dv: `keys` workgroups for each of the first two, then those of dv, which fill the device where the others leave it (of
@@ -333,8 +353,8 @@ template <typename T, int XP, int ZW, bool EVEN> __global__ __launch_bounds__(25
 // launch begins with workgroup `first`.
 template <typename T, int KP, int VP, bool EVEN> __global__ __launch_bounds__(256, 2) void lin_grads_kernel(AttendArgs a, int keys, int first) {
     const int b = int(blockIdx.x) + first;
-    if (b < 2 * keys) lin_attend<T, VP, lin_slice(KP), true, EVEN>(a, a.side[b < keys ? 0 : 1], b < keys ? b : b - keys);
-    else lin_attend<T, KP, lin_slice(VP), false, EVEN>(a, a.side[2], b - 2 * keys);
+    if (b < 2 * keys) lin_attend<T, VP, lin_slice(KP), true, EVEN, false>(a, a.side[b < keys ? 0 : 1], b < keys ? b : b - keys);
+    else lin_attend<T, KP, lin_slice(VP), false, EVEN, false>(a, a.side[2], b - 2 * keys);
 }
 
 // Workgroups of a side; sets `whole`.

@@ -1,6 +1,8 @@
 // What linear attention's kernels share: rows brought from memory to LDS blocks, and a segment's gates.
 #pragma once
 
+#include <limits.h>
+
 #include <type_traits>
 
 #include "linear.h"
@@ -83,6 +85,41 @@ __device__ __forceinline__ void eight_values(const Eight<float> &x, dt4 &a, dt4 
     a = x.a;
     b = x.b;
 }
+// NaN where an infinity or NaN is among the eight, else 0: a sum of them times 0.
+__device__ __forceinline__ float eight_seen(const Eight<bf16> &x) {
+    float seen = 0.0f;
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) seen = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, uint32_t(x.w[j])), b2{}, seen, false);
+    return seen;
+}
+__device__ __forceinline__ float eight_seen(const Eight<float> &x) {
+    float seen = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) seen = fmaf(x.b[j], 0.0f, fmaf(x.a[j], 0.0f, seen));
+    return seen;
+}
+// Infinities and NaN to zeros, f(j) for each of them.
+template <typename F> __device__ __forceinline__ void eight_sift(Eight<bf16> &x, F f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t bits = 0x7F80u << (j & 1 ? 16 : 0), all = j & 1 ? 0xFFFF0000u : 0xFFFFu;
+        if ((x.w[j / 2] & bits) == bits) {
+            x.w[j / 2] &= ~all;
+            f(j);
+        }
+    }
+}
+template <typename F> __device__ __forceinline__ void eight_sift(Eight<float> &x, F f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        float y = j < 4 ? x.a[j % 4] : x.b[j % 4];
+        if ((__float_as_uint(y) & 0x7F800000u) == 0x7F800000u) {
+            (j < 4 ? x.a : x.b)[j % 4] = 0.0f;
+            f(j);
+        }
+    }
+}
 // split<3>, each value on its own: there an infinity or NaN would reach the other value of its pair, here another column.
 __device__ __forceinline__ Frag<3> split_apart(dt4 a, dt4 b) {
     Frag<3> f;
@@ -148,6 +185,25 @@ template <typename T, int ROWS, int W, bool EVEN> struct Tile {
         for (int i = 0; i < N; ++i) {
             const int slot = tid + 256 * i;
             x[i] = eight_load<EVEN>(rows + min(row_of(slot), live - 1) * st, c0 + col_of(slot), width);
+        }
+    }
+    // Infinities and NaN to zeros; `first` (LDS) keeps the least row, counted from `row0`, with one in each of the W columns, behind them in any.
+    __device__ __forceinline__ void sift(int tid, int row0, int *first) {
+        float seen = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int slot = tid + 256 * i;
+            if (live < ROWS || c0 + W > width) eight_mask(x[i], c0 + col_of(slot), width, row_of(slot) < live);
+            seen += eight_seen(x[i]);
+        }
+        if (seen == seen) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int slot = tid + 256 * i, row = row0 + row_of(slot), col = col_of(slot);
+            eight_sift(x[i], [&](int j) {
+                atomicMin(first + col + j, row);
+                atomicMin(first + W, row);
+            });
         }
     }
     template <int NP, typename F> __device__ __forceinline__ void put(unsigned char *lds, int tid, F cut) {

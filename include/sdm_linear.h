@@ -38,9 +38,9 @@ extern "C" {
  *     256-byte aligned (not used where `kept` is given).
  * Arithmetic: products of the inputs and of float32 quantities (24 bits, to 2^-23) accumulate
  * in float32; the state stays float32; out is rounded once. Bitwise reproducible.
- * Tokens are taken 32 at once: an infinity or NaN in a live token's k or v may reach readings
- * of up to 31 tokens before it, of the heads that read it (from v or a state: its own column
- * alone); what an infinity reaches may be NaN. Padding tokens may hold anything.
+ * An infinity or NaN in a live token's inputs reaches the readings of that token and later ones
+ * of its stream, of the heads that read it (from v or a state: its own column alone), and the
+ * states after it; what an infinity reaches may be NaN. Padding tokens may hold anything.
  */
 enum { SDM_LINEAR_FORWARD = 0, SDM_LINEAR_BACKWARD = 1, SDM_LINEAR_BACKWARD_KEPT = 2 };
 
@@ -76,7 +76,11 @@ int sdm_linear_attention_step(const sdm_delta_shape *shape, const sdm_rows *q, c
  *     overlap an input, except that grads->state may be grad_state_out.
  *   exec->workspace: sdm_linear_attention_workspace_bytes(shape, SDM_LINEAR_BACKWARD, or
  *     SDM_LINEAR_BACKWARD_KEPT with `kept`) bytes, 256-byte aligned.
- * The log-decays' gradient gathers differences over up to 256 tokens, in 64 bits.
+ * The log-decays' gradient gathers differences over up to 256 tokens, in 64 bits; it is 0 where the
+ * log-decay's exponential is 0 in float32.
+ * Tokens are taken 32 at once here, and up to 256 for the log-decays: an infinity or NaN in a live
+ * token's inputs or readings' gradient may reach gradients of as many tokens around those that
+ * depend on it, never other streams or heads that do not share keys.
  */
 int sdm_linear_attention_bwd(const sdm_delta_shape *shape, const sdm_rows *q, const sdm_rows *k, const sdm_rows *v,
                              const float *log_decay, int32_t decay_per_token, const float *state,

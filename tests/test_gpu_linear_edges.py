@@ -113,3 +113,43 @@ def test_backward_head_that_forgets(gpu, dtype):
     got = sdm.linear_attention_bwd(d["state"], d["k"], d["v"], d["log_decay"], d["q"], go.to(gpu), grad_state=gs.to(gpu))
     check_grads(got, x, go, gs, dt)
     assert got["log_decay"][0] == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [24, 130])
+@pytest.mark.parametrize("name,value", [("v", math.inf), ("v", -math.inf), ("v", math.nan), ("k", math.nan), ("k", math.inf), ("log_decay", math.nan)])
+def test_readings_do_not_look_ahead(gpu, dtype, K, name, value):
+    """An infinity or NaN in a live token's k, v or log-decay leaves the readings of every earlier token, of other heads and of other
+    streams, to the bit, as they are; one in v stays in its column."""
+    x = make(2, 300, 2, 2, K, 40, DT[dtype], seed=17)
+    clean, clean_final = run(gpu, x)
+    for t in (0, 1, 31, 32, 63, 64, 100, 128, 170, 255, 256, 298, 299):
+        y = {n: None if a is None else a.clone() for n, a in x.items()}
+        if name == "log_decay":
+            y[name][1, t, 1] = value
+        else:
+            y[name][1, t, 1, 7] = value
+        out, final = run(gpu, y)
+        hit, hit_final = ~torch.eq(out, clean), ~torch.eq(final, clean_final)
+        assert not hit[0].any() and not hit[1, :, 0].any() and not hit[1, :t].any(), t
+        assert not hit_final[0].any() and not hit_final[1, 0].any(), t
+        if name == "v":
+            assert not torch.isfinite(out[1, t:, 1, 7]).any() and not torch.isfinite(final[1, 1, :, 7]).any()
+            hit[1, :, 1, 7], hit_final[1, 1, :, 7] = False, False
+            assert not hit.any() and not hit_final.any(), t
+        else:
+            assert not torch.isfinite(out[1, t, 1]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_segments_do_not_look_ahead(gpu, dtype):
+    """The same where a workgroup takes a segment's tiles in turn: NaN in v of one token of every stream and head."""
+    x = make(33, 250, 8, 16, 16, 40, DT[dtype], "head", seed=18)
+    clean, clean_final = run(gpu, x)
+    for t in (0, 40, 63, 64, 127, 128, 200, 249):
+        y = {n: None if a is None else a.clone() for n, a in x.items()}
+        y["v"][:, t, :, 30] = math.nan
+        out, final = run(gpu, y)
+        assert torch.equal(out[:, :t], clean[:, :t]) and torch.isnan(out[:, t:, :, 30]).all() and torch.isnan(final[..., 30]).all()
+        rest = [c for c in range(40) if c != 30]
+        assert torch.equal(out[..., rest], clean[..., rest]) and torch.equal(final[..., rest], clean_final[..., rest])
