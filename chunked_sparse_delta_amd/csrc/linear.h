@@ -44,7 +44,7 @@ struct LinWs {
     float *decay;      // [ph][segs]: exp of a segment's summed log-decays
     float *dS;         // [ph][segs][K][V]: the same for the state's gradient: a segment's end (backward)
     float *dots;       // [ph][segs + 1][lin_dot_parts]: <state, its gradient> at each segment's start and at the end, by wavefronts (backward)
-    float *rows, *cols;  // [slices][ph][T]: the gates' shares through dq and dk, a slice of K each (backward)
+    float *rows, *cols;  // [slices][ph][T]: the gates' shares through dq and, negative, through dk, a slice of K each (backward)
     float *rest;       // dq's and dk's sums between the value heads that share a key head, lin_rest_floats each (backward)
     double *sums;      // [ph][segs]: a segment's sum of log-decay gradients (backward, a decay for each head)
     int32_t segs, tokens;

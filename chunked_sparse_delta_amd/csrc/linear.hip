@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256) void lin_gate_grad_kernel(GateGradArgs a) {
     if (tid < live)
         for (int s = 0; s < a.slices; ++s) {
             const int64_t at = (int64_t(s) * a.P * a.Hv + ph) * a.T + t;
-            d += double(a.rows[at]) - double(a.cols[at]);
+            d += double(a.rows[at]) + double(a.cols[at]);
         }
     head = block_sum(head, buf);
     tail = block_sum(tail, buf);

@@ -17,6 +17,10 @@
 // accumulators are eight neighbouring b of one a, a B operand as they stand (delta_tile.h), so decayed scores go from registers
 // into the product with z. The outcome is transposed too: a lane holds eight neighbouring columns of its token. LDS holds a tile of y and z, or
 // 32 rows of M, while the next one is on its way through registers; two workgroups share a compute unit.
+// dk is summed with its sign turned. The matrix instruction's sums come out low on average, whatever their sign, and so did a token's shares
+// as query and as key, in which q and k of one sign are common: their difference, summed over a segment, was off by as much in all heads. So
+// the one is low and the other high, by as much for every token together, which the correction at the segment's ends takes out (a head's
+// log-decay gradient, 2 x 128 float32 tokens of 64 x 64: 7.1e-7 off on average, now 2.0e-7; a token's 3.6e-7 and 1.9e-7).
 // Precision: sums are float32, G float64. M, decayed scores and float32 rows are three bfloat16 pieces each, so that products keep
 // float32's 24 bits; results are rounded once.
 // Measured (bfloat16, 128 x 128, 256 tokens to a segment): the readings of 16 heads of 16384 tokens 108 us; dq, dk and dv of 4 x 16 heads
@@ -38,7 +42,7 @@ struct AttendSide {
     const float *M;          // [ph][..] + a segment's, [K][V], or null
     int64_t M_head, M_seg;
     void *out;               // dense [P, T, heads, width of z]
-    float *dot;              // KEYS: [slices][ph][T], or null
+    float *dot;              // KEYS: [slices][ph][T], or null (dk: negative)
     float *rest;             // KEYS with shared key heads: lin_rest_floats
     float a0, a1;
     bool back;               // b at or after a (not CAUSAL)
@@ -156,6 +160,7 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const AttendSide
 #pragma unroll
             for (int d = 0; d < XB; ++d) {
                 if (!x_whole) eight_mask(ex[nq][d], d * 32 + lg * 8, X, qw + nq * 16 + lc < n);
+                if (KEYS && back) eight_negate(ex[nq][d]);
                 fx[nq][d] = pieces(ex[nq][d]);
             }
 #pragma unroll
@@ -334,7 +339,13 @@ __device__ __forceinline__ void lin_attend(const AttendArgs &a, const AttendSide
         for (int nq = 0; nq < NQ; ++nq) {
             const int t = qw + nq * 16 + lc;
 #pragma unroll
-            for (int zb = 0; zb < ZB; ++zb) put(t, zb, t < n ? acc[zb][0][nq] : dt4{}, t < n ? acc[zb][1][nq] : dt4{});
+            for (int zb = 0; zb < ZB; ++zb) {
+                if (KEYS && back) {
+                    acc[zb][0][nq] = -acc[zb][0][nq];
+                    acc[zb][1][nq] = -acc[zb][1][nq];
+                }
+                put(t, zb, t < n ? acc[zb][0][nq] : dt4{}, t < n ? acc[zb][1][nq] : dt4{});
+            }
         }
     }
 }

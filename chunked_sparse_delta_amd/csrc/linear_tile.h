@@ -67,6 +67,11 @@ __device__ __forceinline__ void eight_mask(Eight<float> &o, int c, int width, bo
         o.b[j] = more ? o.b[j] : 0.0f;
     }
 }
+__device__ __forceinline__ void eight_negate(Eight<bf16> &o) { o.w ^= 0x80008000u; }
+__device__ __forceinline__ void eight_negate(Eight<float> &o) {
+    o.a = -o.a;
+    o.b = -o.b;
+}
 template <bool EVEN, typename T> __device__ __forceinline__ Eight<T> eight(const T *p, int c, int width, bool live) {
     Eight<T> o = eight_load<EVEN>(p, c, width);
     eight_mask(o, c, width, live);

@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_linear import DT, check_grads, close, make, on, run, want
+from tests.test_gpu_linear import DT, check_grads, close, grads_of, make, on, run, want
 
 pytestmark = pytest.mark.gpu
 
@@ -153,3 +153,23 @@ def test_many_segments_do_not_look_ahead(gpu, dtype):
         assert torch.equal(out[:, :t], clean[:, :t]) and torch.isnan(out[:, t:, :, 30]).all() and torch.isnan(final[..., 30]).all()
         rest = [c for c in range(40) if c != 30]
         assert torch.equal(out[..., rest], clean[..., rest]) and torch.equal(final[..., rest], clean_final[..., rest])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_log_decay_errors_have_no_sign(gpu, dtype):
+    """The errors of log-decays' gradients in the middle of a segment, where their sums cancel, are of either sign, for long
+    memories and keys and queries that are mostly positive: over 64 streams' heads, relative to their gradients' size, the mean of errors without
+    a common sign is within 4 / sqrt(64) of their root mean square; of ones with a common sign it is nearer to that."""
+    import chunked_sparse_delta_amd as sdm
+    P, T, H, W, dt = 4, 128, 16, 64, DT[dtype]
+    x = make(P, T, H, H, W, W, dt, seed=23)
+    for n in ("q", "k"):
+        x[n] = torch.nn.functional.silu(x[n].float()).to(dt)
+    x["log_decay"] = (-0.003 - 0.01 * torch.rand(H, generator=torch.Generator().manual_seed(3))).expand(P, T, H).contiguous()
+    gen = torch.Generator().manual_seed(9)
+    go, gs = torch.randn((P, T, H, W), generator=gen).to(dt), torch.randn((P, H, W, W), generator=gen)
+    d = on(x, gpu)
+    got = sdm.linear_attention_bwd(d["state"], d["k"], d["v"], d["log_decay"], d["q"], go.to(gpu), grad_state=gs.to(gpu))["log_decay"]
+    ref = grads_of(x, go, gs)["log_decay"]
+    off = (got.double().cpu() - ref)[:, 32:96].mean(1) / ref.square().mean(1).sqrt()
+    assert off.mean().abs() <= 0.5 * off.square().mean().sqrt(), f"mean {off.mean():.3g} of {off.square().mean().sqrt():.3g}"
