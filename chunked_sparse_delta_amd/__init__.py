@@ -11,7 +11,8 @@ cannot be loaded, every call raises.
 
 mirrors sdm_write_read's no-grad forward (memory_ops.py, sparse-delta-memory 2.0.0
 wheel, diffend page 21) with per-stream banks: bank [P, M, hd] is advanced in place and
-the readings [P, T, hd] are returned.
+the readings [P, T, hd] are returned. Given tensors that a call writes (the bank, out) count
+as written to autograd: a backward that saved one of them is refused.
 
     grads = sdm_bwd(bank0, k_idx, k_val, v, beta, log_decay, q_idx, q_val, grad_out)
 

@@ -6,14 +6,15 @@
 // and with dz = dy act'(z), h = dz w:
 //     dx = rstd (h - sum(h) / m - xh sum(h xh) / m),  dw = sum over samples and rows (dz xh),  db = the same of dz
 //
-// Bound by memory. A thread owns a vector of 16 bytes of channels and takes rows of it; neighbouring threads take neighbouring
-// vectors, so that rows are read whole whatever the groups. A workgroup takes a tile: whole groups side by side.
+// Bound by memory where samples are long, by the issue of instructions where they are short and many. A thread owns a vector of 16 bytes
+// of channels and takes rows of it; neighbouring threads take neighbouring vectors, so that rows are read whole whatever the groups. A workgroup takes a tile: whole groups side by side.
 //  - Resident: where a tile's rows fit the registers of a workgroup each element is read once. Several samples share a workgroup
-//    where they are short; their sums meet by shuffles where a group is 8, 16, ... lanes of one wavefront, through LDS elsewhere.
+//    where they are short; their sums meet by shuffles where a group is 1, 2, 4, ... lanes of one wavefront, through LDS elsewhere.
 //  - Split: longer samples are cut into blocks of rows; one kernel leaves each block's sums, the next joins them and reads the rows again.
-// Measured: 8192 tokens of 4096 channels in 32 groups, bfloat16, silu: forward 36 us (134 MB, 3.7 TB/s), backward 52 (201 MB, 3.9 TB/s) and
-// 4 for the sums over workgroups; 64 tokens: 4.3. Split, 8 x 4096 rows of 512 channels: statistics 11, their join 4, values 14 (67 MB,
-// 4.8 TB/s); sums 19 (67 MB), their join 5, gradients 19 (101 MB, 5.3 TB/s), the parameters' sums 4. A large copy: 5.2 TB/s.
+// Measured: 8192 tokens of 4096 channels in 32 groups, bfloat16, silu: forward 37 us (134 MB, 26 us at a copy's rate; 17.6 M vector
+// instructions, 29 us at four cycles each on 1024 SIMDs at 2.4 GHz), backward 53 (201 MB, 39; 22.9 M, 37) and 4 for the sums over workgroups; 64
+// tokens: 4.4. Split, 8 x 4096 rows of 512 channels: statistics 12 to 13, their join 4, values 13.5 (67 MB, 5.0 TB/s); sums 20 (67 MB),
+// their join 5, gradients 19 (101 MB, 5.3 TB/s), the parameters' sums 4. A large copy: 5.2 TB/s.
 // Statistics: a thread's mean and sum of squared differences from it, joined with their counts. Split: sums of differences from the first
 // of at most kGnRun rows and of their squares, less the square of the sum, joined likewise.
 // All sums run in float32 in a fixed order: results are the same from run to run.

@@ -23,10 +23,11 @@
 // log-decay gradient, 2 x 128 float32 tokens of 64 x 64: 7.1e-7 off on average, now 2.0e-7; a token's 3.6e-7 and 1.9e-7).
 // Precision: sums are float32, G float64. M, decayed scores and float32 rows are three bfloat16 pieces each, so that products keep
 // float32's 24 bits; results are rounded once.
-// Measured (bfloat16, 128 x 128, 256 tokens to a segment): the readings of 16 heads of 16384 tokens 108 us; dq, dk and dv of 4 x 16 heads
-// of 2048 tokens, keys shared by two, 200 (of 147 and 55 one after the other). Of the 108: matrix instructions alone would take 26 (62.9 M cycles on
-// 1024 SIMDs at 2.4 GHz), the other vector instructions about 30, a copy of as many bytes 74 (319 MB read, 67 written). None hides
-// the others well. A form that took 120 us took 84 without its matrix instructions and 57 with nothing but the tiles' way through
+// Measured (bfloat16, 128 x 128, 256 tokens to a segment): the readings of 16 heads of 16384 tokens 109 us; dq, dk and dv of 4 x 16 heads
+// of 2048 tokens, keys shared by two, 199 (of 147 and 55 one after the other). Of the 109: matrix instructions alone would take 26 (62.9 M cycles on
+// 1024 SIMDs at 2.4 GHz), the other vector instructions about 32, a copy of as many bytes 74 (319 MB read, 67 written). None hides
+// the others well. Of the 199: 38, 55 and 154 (655 MB read, 143 written): a workgroup takes one tile and reads its segment's rows and state again, and
+// sums over sharing heads go through memory. A form that took 120 us took 84 without its matrix instructions and 57 with nothing but the tiles' way through
 // LDS; a workgroup with one tile takes 7. Without effect on that form (2 % at most): tiles or M another step ahead in registers or in a
 // second LDS buffer, operands read from LDS ahead of the products before, 32 tokens of y and z at a time, wavefronts' priorities; eight
 // wavefronts that share a whole segment's tiles, two LDS buffers of them, took 119. With effect: one XCD for what reads

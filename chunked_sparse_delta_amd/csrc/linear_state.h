@@ -1,7 +1,7 @@
 // Linear attention with a decay for each head: the sum of decayed products k v over a segment (and of q and the readings' gradient).
 //
-// Bound by memory: 16 heads of 16384 tokens of 128 x 128, bfloat16, in segments of 256 tokens: 50 us for 98 MB read and 67 MB of
-// sums written (a copy's rate: 32 us; its matrix instructions 12). The product's accumulators are the sum, a wavefront's ZW / 4 columns of it,
+// Bound by memory: 16 heads of 16384 tokens of 128 x 128, bfloat16, in segments of 256 tokens: 50 us for 101 MB read and 85 written, 67 of
+// them the sums, stored 64 bytes in a row (at a copy's rate 36 us; its matrix instructions 10, the others 13). The product's accumulators are the sum, a wavefront's ZW / 4 columns of it,
 // so that nothing is added up across wavefronts.
 #pragma once
 

@@ -15,6 +15,8 @@ Shapes: k, q [P, T, Hk, K]; v, out [P, T, Hv, V]; beta, log_decay float32 [P, T,
 Value head h reads key head h // (Hv // Hk). k, q and v are float32 or bfloat16 and may be strided views whose last axis
 is dense (slices of one projection); everything else is contiguous. ``valid_tokens`` (int32 [P] on the GPU): tokens at and
 past it are padding, they leave the state alone and read 0. ``scale`` defaults to K ** -0.5.
+Given tensors that a call writes (``state``, ``state_out``, ``out``) count as written to autograd: a backward that saved one of them is
+refused.
 """
 
 from __future__ import annotations
@@ -292,7 +294,7 @@ def gated_delta_rule(state, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor
                      recompute: bool = False):
     """The rule for autograd: returns (readings, final state); ``state`` (None: zeros) is not changed. Gradients reach
     the state, k, v, beta, log_decay and q through gated_delta_bwd. Until the backward the forward keeps what it computed
-    per chunk (gated_delta_workspace_bytes(..., backward=True)); ``recompute=True`` keeps the inputs alone and computes the
+    per chunk (gated_delta_workspace_bytes(..., backward=True); the start state may then be advanced before it); ``recompute=True`` keeps the inputs alone and computes the
     forward again, for less memory and about a sixth more time."""
     return _GatedDeltaRule.apply(state, k, v, beta, log_decay, q, scale, valid_tokens, recompute)
 

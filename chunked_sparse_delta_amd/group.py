@@ -46,7 +46,8 @@ def _act(activation) -> int:
 
 
 def group_norm_workspace_bytes(N: int, rows: int, channels: int, groups: int, dtype: torch.dtype, backward: bool = False) -> int:
-    """Bytes of scratch that group_norm_fwd (or group_norm_bwd) needs; 0 where none, and for shapes they reject."""
+    """Bytes of scratch that group_norm_fwd (or group_norm_bwd) needs; 0 where none, and for shapes they reject (samples cut
+    into 2^24 blocks or more among them)."""
     shape = _SHAPE(N, rows, channels, groups, _DTYPES.get(dtype, -1), 0, 0, 0.0)
     return _load().sdm_group_norm_workspace_bytes(shape, 1 if backward else 0)
 
@@ -55,7 +56,7 @@ def group_norm_fwd(x: torch.Tensor, groups: int, weight: torch.Tensor | None = N
                    activation: str | None = None, eps: float = 1e-5, valid_rows: torch.Tensor | None = None,
                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Group norm and activation. Returns (y, mean, rstd); mean and rstd float32 [N, groups] are what group_norm_bwd needs.
-    ``out`` may be x where that is contiguous. ``workspace`` (uint8, GPU, group_norm_workspace_bytes) is allocated if
+    ``out`` may be x where that is contiguous (autograd counts it as written), and must not overlap an input otherwise. ``workspace`` (uint8, GPU, group_norm_workspace_bytes) is allocated if
     omitted and needed."""
     call = _binding().group_norm_fwd
     if stream is not None:

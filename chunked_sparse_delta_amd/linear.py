@@ -11,6 +11,8 @@ Shapes: k, q [P, T, Hk, K]; v, out [P, T, Hv, V]; state float32 [P, Hv, K, V]; l
 head, or [P, T, Hv], one for each token. Value head h reads key head h // (Hv // Hk). k, q and v are float32 or bfloat16
 and may be strided views whose last axis is dense; everything else is contiguous. ``valid_tokens`` (int32 [P] on the GPU):
 tokens at and past it are padding, they leave the state alone and read 0. ``scale`` defaults to K ** -0.5.
+Given tensors that a call writes (``state``, ``state_out``, ``out``, ``kept``) count as written to autograd: a backward that saved one
+of them is refused. They must not overlap an input but where it is said.
 """
 
 from __future__ import annotations
@@ -114,7 +116,7 @@ def linear_attention_step(state: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Linear attention for one token of each stream, or a few (T small): every state is read and written once. ``state``
     [slots, Hv, K, V] is a pool; ``state_ids`` (int32 [P], distinct) names each stream's slot, an id outside the pool an
     idle stream, which reads 0; without it stream p has slot p. The states are advanced in place, or written to
-    ``state_out`` (the same shape; slots that no stream names are left alone there)."""
+    ``state_out`` (the same shape; slots that no stream names are left alone there). ``out`` may be v where that is dense."""
     call = _binding().linear_attention_step
     if stream is not None:
         return _on(stream, call, state, k, v, log_decay, q, state_ids, scale, valid_tokens, state_out, out)
@@ -140,7 +142,7 @@ def linear_attention(state, k: torch.Tensor, v: torch.Tensor, log_decay: torch.T
                      scale: float | None = None, valid_tokens: torch.Tensor | None = None, recompute: bool = False):
     """Linear attention for autograd: returns (readings, final state); ``state`` (None: zeros) is not changed. Gradients
     reach the state, k, v, log_decay and q through linear_attention_bwd. Until the backward the forward keeps the states
-    between segments of tokens (linear_attention_kept_bytes); ``recompute=True`` keeps the inputs alone. Under no_grad
-    nothing is kept. A backward captured into a graph needs leaves that no eager autograd graph holds any longer (autograd would join that one's
-    stream into the capture)."""
+    between segments of tokens (linear_attention_kept_bytes; the start state may then be advanced before the backward);
+    ``recompute=True`` keeps the inputs alone. Under no_grad nothing is kept. A backward captured into a graph needs leaves that
+    no eager autograd graph holds any longer (autograd would join that one's stream into the capture)."""
     return _binding().linear_attention(state, k, v, log_decay, q, scale, valid_tokens, recompute)
