@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_group_norm import DT, U, bars, close, make
+from tests.test_gpu_group_norm import DT, U, bars, check, close, make
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,23 @@ def test_reach_of_a_live_value(gpu, N, L, C, G, dtype, value):
         assert not torch.isfinite(dx[n, :live, here]).all() and not y[n, live:].any() and not dx[n, live:].any()
         if into == "x":
             assert torch.isnan(y[n, :live, here]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,L,C,G", [(3000, 1, 1024, 8), (5000, 40, 24, 2), (3000, 2, 640, 2)])
+def test_workgroups_take_samples_in_turn(gpu, N, L, C, G, dtype):
+    """More samples than workgroups, whose threads meet in each way: by shuffles, by vectors and by channels."""
+    check(gpu, N, L, C, G, dtype, "silu", seed=N)
+
+
+def test_no_eps(gpu):
+    """eps 0: a sample without a valid row, whose rstd is infinite, reads 0 and has gradients of 0; the others are as ever."""
+    import chunked_sparse_delta_amd as sdm
+    for N, L, C, G in ((3, 4, 64, 4), (3, 5, 30, 3), (3, 3000, 32, 4)):
+        d = {n: t.to(gpu) for n, t in make(N, L, C, torch.float32, seed=2).items()}
+        valid = torch.tensor([L, 0, L - 1], dtype=torch.int32, device=gpu)
+        kw = {"activation": "silu", "eps": 0.0, "valid_rows": valid}
+        y, m, r = sdm.group_norm_fwd(d["x"], G, d["weight"], d["bias"], **kw)
+        g = sdm.group_norm_bwd(d["go"], d["x"], G, m, r, d["weight"], d["bias"], **kw)
+        assert torch.isinf(r[1]).all() and not y[1].any() and not g["x"][1].any()
+        assert all(torch.isfinite(t).all() for t in (y, m, g["x"], g["weight"], g["bias"]))

@@ -43,3 +43,19 @@ def test_norm_across_its_input(gpu, L):
     for out in (room[:3 * L * 32], room[16:16 + 3 * L * 32]):
         with pytest.raises(sdm.SdmError, match="overlap"):
             sdm.group_norm_fwd(x, 4, out=out.view(3, L, 32))
+
+
+@pytest.mark.parametrize("L,G", [(130, 2), (3000, 2)])
+def test_rows_far_apart(gpu, L, G):
+    """Rows so far apart that the last lies past 2^32 elements: the bits of a dense copy."""
+    import chunked_sparse_delta_amd as sdm
+    C = 24
+    far = (1 << 32) // (L - 2)
+    x = torch.empty((L - 1) * far + C, dtype=torch.bfloat16, device=gpu).as_strided((1, L, C), (0, far, 1))
+    x.copy_(torch.randn((1, L, C), generator=torch.Generator().manual_seed(1)))
+    go = torch.randn((1, L, C), device=gpu).bfloat16()
+    got = []
+    for t in (x, x.contiguous()):
+        y, m, r = sdm.group_norm_fwd(t, G, activation="silu")
+        got.append([y, m, r, *sdm.group_norm_bwd(go, t, G, m, r, activation="silu").values()])
+    assert all(torch.equal(a, b) for a, b in zip(*got))

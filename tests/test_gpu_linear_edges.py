@@ -173,3 +173,27 @@ def test_log_decay_errors_have_no_sign(gpu, dtype):
     ref = grads_of(x, go, gs)["log_decay"]
     off = (got.double().cpu() - ref)[:, 32:96].mean(1) / ref.square().mean(1).sqrt()
     assert off.mean().abs() <= 0.5 * off.square().mean().sqrt(), f"mean {off.mean():.3g} of {off.square().mean().sqrt():.3g}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("decay", ["head", "token"])
+def test_states_that_grow(gpu, dtype, decay):
+    """Log-decays above zero, sums of up to 75 over a segment, and ones that fall by 70 and rise again: decays are then of up to
+    e^75, their exponents rounded to 75 / log 2 u = 108 * 2^-24, under the bar's 64 * 2^-23."""
+    import chunked_sparse_delta_amd as sdm
+    dt, T = DT[dtype], 256
+    x = make(2, T, 1, 3, 40, 24, dt, decay, seed=31)
+    rate = 75.0 / T
+    if decay == "head":
+        x["log_decay"] = torch.tensor([rate, -rate, 0.01])
+    else:
+        x["log_decay"] = torch.stack([torch.full((T,), rate), torch.linspace(-2.2, 2.2, T) * 0.5, -rate * torch.rand(T)], -1).expand(2, T, 3).contiguous()
+    out, final = run(gpu, x)
+    (o, s), (ao, as_) = want(x), want(x, absolute=True)
+    close(out, o, ao, dt)
+    close(final, s, as_, torch.float32)
+    gen = torch.Generator().manual_seed(4)
+    go, gs = torch.randn((2, T, 3, 24), generator=gen).to(dt), torch.randn((2, 3, 40, 24), generator=gen)
+    d = on(x, gpu)
+    got = sdm.linear_attention_bwd(d["state"], d["k"], d["v"], d["log_decay"], d["q"], go.to(gpu), grad_state=gs.to(gpu))
+    check_grads(got, x, go, gs, dt)
